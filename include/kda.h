@@ -285,6 +285,139 @@ KDA_API kda_status kda_decode_multi(const void* q, const void* k, const void* v,
                             kda_dtype dtype, void* o, cudaStream_t stream);
 
 /*
+ * ---------------------------------------------------------------------------
+ * Serving step of a model that mixes KDA layers with softmax-attention layers.
+ * The attention layers keep keys and values in a paged cache:
+ *
+ *   k_cache, v_cache  [n_pages, H_kv, page_size, d] dtype, 16-byte aligned
+ *   slot              page * page_size + (place inside the page)
+ *   block_table       [N, max_blocks] int32: page of every page_size tokens of
+ *                     each request, in order
+ *
+ * page_size is 16, 32, 64, 128 or 256; N is at most KDA_MAX_STEP_REQUESTS.
+ * The order of a step: kda_build_block_tables once, then per attention layer
+ * kda_cache_append and kda_paged_attention; with drafted tokens,
+ * kda_verify_draft at the end, whose commit_len is what kda_decode_multi takes
+ * for the KDA layers.  Every length is read on the device, so a captured graph
+ * serves any lengths that its buffers hold.
+ */
+#define KDA_MAX_STEP_REQUESTS 8192
+
+/*
+ * Block tables and slot map of one step.  Request n holds ctx_len[n] cached
+ * tokens and adds new_len[n] (negative lengths count as 0).  Its table already
+ * names the pages of the cached tokens; the pages for the new ones,
+ * ceil((ctx + new) / page_size) - ceil(ctx / page_size) of them, are taken from
+ * free_pages in request order and written into its row.
+ *
+ * ctx_len, new_len [N] int32
+ * free_pages       [n_free] int32 (may be NULL when n_free is 0)
+ * block_table      [N, max_blocks] int32, updated in place; only the entries
+ *                  of newly taken pages are written
+ * cu_seqlens       [N + 1] int32, written: offsets of each request's new tokens
+ *                  (the packed batch of kda_prefill and kda_paged_attention)
+ * seq_len          [N] int32, written: ctx + new
+ * slot_map         [n_tokens] int64, written: slot of each new token; -1 for
+ *                  the padding behind the last one, and where there is no page
+ * positions        [n_tokens] int32 or NULL, written: position of each new
+ *                  token in its request; 0 for the padding
+ * n_taken          [1] int32, written: pages needed.  More than n_free means
+ *                  that the free list ran out: the entries without a page are
+ *                  -1, and the calls below leave their tokens out.
+ * n_tokens is the size of slot_map; new tokens past it get no slot.  Tokens
+ * past max_blocks * page_size get no page.  The new tokens of all requests
+ * together must stay below 2^31.
+ */
+KDA_API kda_status kda_build_block_tables(const int32_t* ctx_len, const int32_t* new_len,
+                                  const int32_t* free_pages, int n_free, int N, int max_blocks,
+                                  int page_size, int n_tokens, int32_t* block_table,
+                                  int32_t* cu_seqlens, int32_t* seq_len, int64_t* slot_map,
+                                  int32_t* positions, int32_t* n_taken, cudaStream_t stream);
+
+/*
+ * Writes the keys and values of T new tokens into the paged cache: row t goes
+ * to slot_map[t]; slots below 0 or at and past n_pages * page_size are skipped.
+ *
+ * k, v      [T, H_kv, d] dtype; consecutive tokens are k_stride and v_stride
+ *           elements apart (at least H_kv * d, so that both may be slices of a
+ *           fused projection); any alignment of the elements
+ * slot_map  [T] int64.  Two tokens with one slot leave either's row there.
+ */
+KDA_API kda_status kda_cache_append(const void* k, const void* v, const int64_t* slot_map,
+                            int64_t k_stride, int64_t v_stride, int T, int H_kv, int d, int page_size,
+                            int n_pages, kda_dtype dtype, void* k_cache, void* v_cache,
+                            cudaStream_t stream);
+
+/* Bytes of device workspace kda_paged_attention needs for T new tokens. */
+KDA_API size_t kda_paged_attention_workspace_size(int T, int H_q, int H_kv, int d, kda_dtype dtype);
+
+/*
+ * Attention of new tokens over a paged cache that holds their own keys and
+ * values already.  Token i of the m = cu_seqlens[n + 1] - cu_seqlens[n] new
+ * tokens of request n stands at position p = seq_len[n] - m + i and sees the
+ * keys j <= p, with window > 0 only those with j > p - window.  Per query head
+ * h, over the head h / (H_q / H_kv) of the cache:
+ *
+ *     o = sum_j exp(scale q.k_j - lse) v_j,   lse = ln sum_j exp(scale q.k_j)
+ *
+ * One call serves any mix of single tokens (decode), a few tokens (verify) and
+ * long chunks (prefill).  A row that sees no key gives o = 0, lse = -inf.
+ * Keys whose block_table entry names no page of the cache (below 0, n_pages or
+ * more) are left out, as are keys past max_blocks * page_size.  What stands in
+ * the cache at places that a row does not see, NaN among it, does not reach
+ * that row.
+ *
+ * q           [T, H_q, d] dtype, consecutive tokens q_stride elements apart
+ * cu_seqlens  [N + 1] int32 device array, 0 = cu[0] <= ... <= cu[N] <= T;
+ *             rows of q at and past cu[N] are padding, their o is not written
+ * seq_len     [N] int32 device array
+ * scale       finite and > 0
+ * window      0: no window
+ * o           [T, H_q, d] dtype;  lse [T, H_q] float or NULL
+ * workspace   kda_paged_attention_workspace_size bytes, 256-byte aligned
+ * d is 32, 64 or 128; H_q a multiple of H_kv.  The scores, their statistics and
+ * the sums are fp32; on the tensor-core path (bf16, d = 64 or 128, q 16-byte
+ * aligned with a stride that is a multiple of 8) the weights enter the second
+ * product as bf16.  Every other combination runs in fp32 on CUDA cores.
+ */
+KDA_API kda_status kda_paged_attention(const void* q, const void* k_cache, const void* v_cache,
+                               const int32_t* block_table, const int32_t* cu_seqlens,
+                               const int32_t* seq_len, int64_t q_stride, int N, int T, int H_q,
+                               int H_kv, int d, int page_size, int max_blocks, int n_pages,
+                               float scale, int window, kda_dtype dtype, void* o, float* lse,
+                               void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/*
+ * Verification of drafted tokens against the target's probabilities.  Request
+ * n has L = draft_len[n] drafted tokens x_0 ... (at most K).  With p_i the
+ * target's and q_i the draft's distribution at draft i, x_i stands while
+ * u_i q_i(x_i) < p_i(x_i); with a the number of tokens that stand, one more
+ * token is drawn with u_K: from max(p_a - q_a, 0) if a < L, from p_a if a = L
+ * (and from p_a where max(p_a - q_a, 0) is zero everywhere).  The drawn token
+ * is the first one at which the running sum exceeds u_K times the whole sum.
+ *
+ * target        [N, K + 1, V] dtype, probabilities in [0, 1], each row summing
+ *               to about 1 (less than 4)
+ * draft         [N, K, V] dtype, likewise; NULL for tokens proposed with
+ *               certainty (q_i = 1 at x_i, 0 elsewhere)
+ * draft_tokens  [N, K] int32; a token outside [0, V) does not stand
+ * uniforms      [N, K + 1] float in [0, 1)
+ * draft_len     [N] int32 clamped to [0, K], or NULL (= K)
+ * tokens        [N, K + 1] int32, written: the tokens that stand, the drawn
+ *               one, then -1
+ * commit_len    [N] int32, written: a + 1, the number of tokens to commit when
+ *               the request's last token and its drafts were run through
+ *               kda_decode_multi as K + 1 tokens
+ * Sums are exact to 2^-60 of a probability, in integers: no order of summation
+ * enters the result.  Negative and NaN probabilities count as 0.  A target row
+ * without a positive entry draws V - 1.  K is at most 16.
+ */
+KDA_API kda_status kda_verify_draft(const void* target, const void* draft, const int32_t* draft_tokens,
+                            const float* uniforms, const int32_t* draft_len, int N, int K, int V,
+                            kda_dtype dtype, int32_t* tokens, int32_t* commit_len,
+                            cudaStream_t stream);
+
+/*
  * Synchronises `stream`, then returns and clears the device status word:
  * KDA_OK, or KDA_ERR_TIMEOUT if a kernel since the last call gave up waiting
  * (its outputs are then incomplete), or KDA_ERR_CUDA if the synchronisation

@@ -23,7 +23,8 @@ KDA_FP32, KDA_BF16 = 0, 1
 SYMBOLS = ("kda_prefill_workspace_size", "kda_prefill", "kda_prefill_ckpt", "kda_prefill_fused",
            "kda_prefill_noalloc", "kda_decode", "kda_decode_fused", "kda_decode_multi",
            "kda_get_last_device_status", "kda_check_wait_timeout", "kda_set_trace_events", "kda_debug_build",
-           "kda_status_string")
+           "kda_status_string", "kda_build_block_tables", "kda_cache_append", "kda_paged_attention_workspace_size",
+           "kda_paged_attention", "kda_verify_draft")
 NOALLOC_SCRATCH_BYTES = 64 << 20
 
 _lock = threading.Lock()
@@ -80,6 +81,17 @@ def _open(path):
     lib.kda_decode.restype = I
     lib.kda_decode_multi.argtypes = [P, P, P, P, P, P, P, I, I, I, I, I, I, P, P]
     lib.kda_decode_multi.restype = I
+    L, F = ctypes.c_longlong, ctypes.c_float
+    lib.kda_build_block_tables.argtypes = [P, P, P, I, I, I, I, I, P, P, P, P, P, P, P]
+    lib.kda_build_block_tables.restype = I
+    lib.kda_cache_append.argtypes = [P, P, P, L, L, I, I, I, I, I, I, P, P, P]
+    lib.kda_cache_append.restype = I
+    lib.kda_paged_attention_workspace_size.argtypes = [I, I, I, I, I]
+    lib.kda_paged_attention_workspace_size.restype = Z
+    lib.kda_paged_attention.argtypes = [P, P, P, P, P, P, L, I, I, I, I, I, I, I, I, F, I, I, P, P, P, Z, P]
+    lib.kda_paged_attention.restype = I
+    lib.kda_verify_draft.argtypes = [P, P, P, P, P, I, I, I, I, P, P, P]
+    lib.kda_verify_draft.restype = I
     lib.kda_get_last_device_status.argtypes = [P]
     lib.kda_get_last_device_status.restype = I
     lib.kda_check_wait_timeout.argtypes = [ctypes.c_longlong, P]

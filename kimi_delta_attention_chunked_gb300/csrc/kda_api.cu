@@ -87,6 +87,7 @@ long long chunk_upper_bound(int n_seq, int T_total, int chunk) {
 }  // namespace
 
 namespace kda_host {
+int* status_word() { return status_ptr(); }
 void trace_reset() { t_next = 0; }
 void trace_mark(cudaStream_t stream) {
     if (t_events && t_next < t_n_events) {

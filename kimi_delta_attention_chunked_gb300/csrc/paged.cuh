@@ -1,0 +1,380 @@
+// paged.cuh -- what the operators of a serving step share: the checked view of
+// a step's lengths, and the division of paged attention's work over the grid.
+//
+// Attention work comes in units: up to U new tokens of one request, with the
+// Gv query heads that share a cache head, against the 128- or 64-key tiles that
+// any of their rows sees.  The tiles of all units, in the order request, head,
+// unit, tile, are one line, and CTA c of C takes the c-th of C equal pieces of
+// it: every CTA has the same number of tiles whatever the lengths are.  A unit
+// that a border cuts is finished by each of its CTAs into fp32 partial rows,
+// which the merge kernel joins.  A CTA finds its piece itself, from the lengths
+// on the device: no plan is made on the host, and no extra launch is needed.
+#pragma once
+
+#include "common.cuh"
+
+namespace kda_paged {
+
+constexpr int kMaxRequests = KDA_MAX_STEP_REQUESTS;
+constexpr int kMaxCtas = 512;                      // most CTAs an attention launch uses
+
+// Sizes of one attention call.
+struct Shape {
+    int n_req, T;                                  // requests, rows of q
+    int Hq, Hkv, Hv, Gv, sub;                      // Hv = Hkv * sub groups of Gv query heads
+    int blocks, page_log2, n_pages, window;
+    int U, tile_log2;                              // tokens per unit, keys per tile
+};
+
+// One request's lengths, inside the buffers whatever the device arrays hold.
+struct Req {
+    int tok0, len;                                 // first row of q, new tokens
+    int pos0;                                      // position of the first new token (may be negative)
+    int kend;                                      // keys below it exist
+};
+
+__device__ __forceinline__ Req load_req(const Shape& s, const int32_t* __restrict__ cu,
+                                        const int32_t* __restrict__ seq_len, int n) {
+    Req r;
+    r.tok0 = min(max(cu[n], 0), s.T);
+    const int end = min(max(cu[n + 1], r.tok0), s.T);
+    r.len = end - r.tok0;
+    const int seq = max(seq_len[n], 0);
+    r.pos0 = seq - r.len;
+    const long long cap = (long long)s.blocks << s.page_log2;
+    r.kend = (int)min((long long)seq, cap);
+    return r;
+}
+
+__device__ __forceinline__ int n_units(const Shape& s, const Req& r) { return (r.len + s.U - 1) / s.U; }
+
+// Tiles [tb, te) of unit i: those that hold a key some row sees, and one tile
+// where no row sees any (its rows are written as empty).
+__device__ __forceinline__ void unit_span(const Shape& s, const Req& r, int i, int& tb, int& te) {
+    const int first = i * s.U, last = min(r.len, first + s.U);
+    const int hi = min(max(r.pos0 + last, 0), r.kend);
+    int lo = s.window > 0 ? max(0, r.pos0 + first - s.window + 1) : 0;
+    lo = min(lo, hi);
+    tb = lo >> s.tile_log2;
+    te = (hi + (1 << s.tile_log2) - 1) >> s.tile_log2;
+    if (te <= tb) te = tb + 1;
+}
+
+// Tiles of all units of a request, for one head.  A thread counts a request of
+// few units by itself; the lanes of a warp share out one of many.
+__device__ __forceinline__ unsigned long long request_tiles(const Shape& s, const int32_t* __restrict__ cu,
+                                                            const int32_t* __restrict__ seq_len, int n, bool valid) {
+    constexpr int kAlone = 8;
+    Req r{0, 0, 0, 0};
+    if (valid) r = load_req(s, cu, seq_len, n);
+    const int units = n_units(s, r);
+    unsigned long long cost = 0;
+    if (units <= kAlone) {
+        for (int i = 0; i < units; ++i) {
+            int tb, te;
+            unit_span(s, r, i, tb, te);
+            cost += te - tb;
+        }
+    }
+    unsigned many = __ballot_sync(0xffffffffu, units > kAlone);
+    while (many) {
+        const int src = __ffs(many) - 1;
+        many &= many - 1;
+        Req q;
+        q.tok0 = 0;
+        q.len = __shfl_sync(0xffffffffu, r.len, src);
+        q.pos0 = __shfl_sync(0xffffffffu, r.pos0, src);
+        q.kend = __shfl_sync(0xffffffffu, r.kend, src);
+        const int total = n_units(s, q);
+        unsigned long long part = 0;
+        for (int i = threadIdx.x & 31; i < total; i += 32) {
+            int tb, te;
+            unit_span(s, q, i, tb, te);
+            part += te - tb;
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) part += __shfl_xor_sync(0xffffffffu, part, o);
+        if ((int)(threadIdx.x & 31) == src) cost = part;
+    }
+    return cost;
+}
+
+// Where a CTA's piece begins and ends on the line of tiles.
+struct Piece {
+    unsigned long long begin, end, total;          // tiles [begin, end) of `total`
+    unsigned long long off;                        // begin - first tile of request n
+    unsigned long long tiles;                      // tiles of request n for one head
+    int n, ctas;                                   // first request; CTAs that have a piece
+};
+
+// Finds the piece of CTA `c` of `C`.  Every thread of the block (NT of them)
+// calls it; `cost` holds n_req words and `red` NT / 32, of 64 bits, and free again after the block's next barrier.
+template <int NT>
+__device__ __forceinline__ Piece find_piece(const Shape& s, const int32_t* __restrict__ cu,
+                                            const int32_t* __restrict__ seq_len, int c, int C,
+                                            unsigned long long* cost,
+                                            unsigned long long* red, Piece* shared) {
+    constexpr int NW = NT / 32;
+    const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
+    for (int base = 0; base < s.n_req; base += NT) {
+        const int n = base + tid;
+        const unsigned long long x = request_tiles(s, cu, seq_len, n, n < s.n_req);
+        if (n < s.n_req) cost[n] = x;
+    }
+    if (tid == 0) *shared = Piece{0, 0, 0, 0, 0, 0, 0};
+    __syncthreads();
+    // each thread takes `per` consecutive requests of the running sum
+    const int per = (s.n_req + NT - 1) / NT, n0 = min(tid * per, s.n_req), n1 = min(n0 + per, s.n_req);
+    unsigned long long mine = 0;
+    for (int n = n0; n < n1; ++n) mine += cost[n];
+    mine *= (unsigned)s.Hv;
+    unsigned long long incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const unsigned long long t = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += t;
+    }
+    if (lane == 31) red[w] = incl;
+    __syncthreads();
+    unsigned long long before = 0, total = 0;
+#pragma unroll
+    for (int i = 0; i < NW; ++i) {
+        const unsigned long long t = red[i];
+        if (i < w) before += t;
+        total += t;
+    }
+    incl += before;
+    const int ctas = (int)min((unsigned long long)C, total);
+    if (c < ctas) {
+        const unsigned long long begin = total * (unsigned)c / (unsigned)ctas;
+        const unsigned long long excl = incl - mine;
+        if (excl <= begin && begin < incl) {
+            unsigned long long at = excl;
+            int n = n0;
+            for (; n < n1; ++n) {
+                const unsigned long long x = cost[n] * (unsigned)s.Hv;
+                if (begin < at + x) break;
+                at += x;
+            }
+            shared->begin = begin;
+            shared->end = total * (unsigned)(c + 1) / (unsigned)ctas;
+            shared->total = total;
+            shared->off = begin - at;
+            shared->tiles = cost[n];
+            shared->n = n;
+            shared->ctas = ctas;
+        }
+    }
+    __syncthreads();
+    return *shared;
+}
+
+// One unit, or the part of it that a CTA's piece holds.
+struct Unit {
+    int n, kvh, qh0;                               // request, cache head, first query head
+    int tok0, ntok;                                // rows of q: tokens tok0 .. tok0 + ntok - 1
+    int pos, kend;                                 // position of token tok0; keys below kend exist
+    int tb, te;                                    // tiles of this part
+    int first, last;                               // the part holds the unit's first / last tile
+    int parts;                                     // CTAs that share the unit, from this one on (first && !last)
+};
+
+// Walks the units of a CTA's piece.  Used by all lanes of one warp together.
+struct Walker {
+    unsigned long long at, end, total;
+    int ctas;
+    int n, h, i, skip;                             // next unit; tiles of it that lie before the piece
+    Req r;
+    int units;
+
+    __device__ __forceinline__ void start(const Shape& s, const int32_t* cu, const int32_t* seq_len, const Piece& p) {
+        at = p.begin;
+        end = p.end;
+        total = p.total;
+        ctas = p.ctas;
+        n = p.n;
+        h = i = skip = 0;
+        r = Req{0, 0, 0, 0};
+        units = 0;
+        if (at >= end) return;
+        r = load_req(s, cu, seq_len, n);
+        units = n_units(s, r);
+        h = (int)(p.off / p.tiles);
+        unsigned long long left = p.off - (unsigned long long)h * p.tiles;
+        const int lane = threadIdx.x & 31;
+        for (int base = 0; base < units; base += 32) {         // the unit that holds tile `left` of this head
+            unsigned x = 0;
+            if (base + lane < units) {
+                int tb, te;
+                unit_span(s, r, base + lane, tb, te);
+                x = te - tb;
+            }
+            unsigned incl = x;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const unsigned t = __shfl_up_sync(0xffffffffu, incl, o);
+                if (lane >= o) incl += t;
+            }
+            const unsigned hit = __ballot_sync(0xffffffffu, left < incl);
+            if (hit) {
+                const int src = __ffs(hit) - 1;
+                i = base + src;
+                skip = (int)(left - __shfl_sync(0xffffffffu, incl - x, src));
+                break;
+            }
+            left -= __shfl_sync(0xffffffffu, incl, 31);
+        }
+    }
+
+    // The next part, or false at the end of the piece.
+    __device__ __forceinline__ bool next(const Shape& s, const int32_t* cu, const int32_t* seq_len, Unit& u) {
+        if (at >= end) return false;
+        while (i >= units) {
+            i = 0;
+            if (units == 0 || ++h >= s.Hv) {
+                h = 0;
+                if (++n >= s.n_req) return false;
+                r = load_req(s, cu, seq_len, n);
+                units = n_units(s, r);
+            }
+        }
+        int tb, te;
+        unit_span(s, r, i, tb, te);
+        const int full_end = te;
+        tb += skip;
+        const unsigned long long fin = at + (unsigned)(te - tb);
+        if (fin > end) te = tb + (int)(end - at);
+        u.n = n;
+        u.kvh = h / s.sub;
+        u.qh0 = h * s.Gv;
+        u.tok0 = r.tok0 + i * s.U;
+        u.ntok = min(s.U, r.len - i * s.U);
+        u.pos = r.pos0 + i * s.U;
+        u.kend = r.kend;
+        u.tb = tb;
+        u.te = te;
+        u.first = skip == 0;
+        u.last = te == full_end;
+        u.parts = 1;
+        if (u.first && !u.last) {
+            // CTA c begins at total * c / ctas, so the last one that has a tile below `fin` is
+            // ceil(fin * ctas / total) - 1; likewise this one, from its first tile
+            const unsigned long long hi = (fin * (unsigned)ctas + total - 1) / total;
+            const unsigned long long lo = ((at + 1) * (unsigned)ctas + total - 1) / total;
+            u.parts = (int)(hi - lo) + 1;
+        }
+        at += (unsigned)(te - tb);
+        skip = 0;
+        ++i;
+        return true;
+    }
+};
+
+// Partial rows of cut units in the workspace: CTA c's slot 0 holds a part that
+// goes on from CTA c - 1, slot 1 one that begins in CTA c and goes on in c + 1.
+// A slot is rows x d unnormalised sums, then rows x (reference, sum of weights),
+// the reference in units of log2.  `meta[c]` describes slot 1: (first token,
+// first query head, tokens, parts), parts = 0 where nothing begins and goes on.
+struct Partials {
+    int4* meta;
+    float* rows;
+    int cap;                                       // rows of a slot
+    int d;
+    __device__ __forceinline__ size_t slot(int c, int which) const {
+        return ((size_t)c * 2 + which) * (size_t)cap * (d + 2);
+    }
+    __device__ __forceinline__ float* sums(int c, int which) const { return rows + slot(c, which); }
+    __device__ __forceinline__ float2* stats(int c, int which) const {
+        return reinterpret_cast<float2*>(rows + slot(c, which) + (size_t)cap * d);
+    }
+};
+
+}  // namespace kda_paged
+
+namespace kda_host {
+
+struct PagedArgs {
+    const void* q;
+    const void* k_cache;
+    const void* v_cache;
+    const int32_t* block_table;
+    const int32_t* cu_seqlens;
+    const int32_t* seq_len;
+    int64_t q_stride;
+    int N, T, Hq, Hkv, d, page_size, blocks, n_pages;
+    float scale;
+    int window;
+    kda_dtype dtype;
+    void* o;
+    float* lse;
+    void* workspace;
+    cudaStream_t stream;
+    int* status;
+};
+
+struct TablesArgs {
+    const int32_t* ctx_len;
+    const int32_t* new_len;
+    const int32_t* free_pages;
+    int n_free, N, blocks, page_size, n_tokens;
+    int32_t* block_table;
+    int32_t* cu_seqlens;
+    int32_t* seq_len;
+    int64_t* slot_map;
+    int32_t* positions;
+    int32_t* n_taken;
+    cudaStream_t stream;
+};
+
+struct AppendArgs {
+    const void* k;
+    const void* v;
+    const int64_t* slot_map;
+    int64_t k_stride, v_stride;
+    int T, H, d, page_size, n_pages, esize;
+    void* k_cache;
+    void* v_cache;
+    cudaStream_t stream;
+};
+
+struct VerifyArgs {
+    const void* target;
+    const void* draft;
+    const int32_t* draft_tokens;
+    const float* uniforms;
+    const int32_t* draft_len;
+    int N, K, V;
+    kda_dtype dtype;
+    int32_t* tokens;
+    int32_t* commit_len;
+    cudaStream_t stream;
+};
+
+int* status_word();                                // the device status word (kda_api.cu)
+int sm_count();                                    // SMs of the current device
+
+// Query heads of one unit's rows, and how many such groups share a cache head:
+// the most heads that divide the group evenly and fit `most` rows.
+inline int heads_per_unit(int group, int most) {
+    int g = group < most ? group : most;
+    while (group % g != 0) --g;
+    return g;
+}
+
+// Partial-row geometry of an attention call: rows of a slot, most CTAs.
+struct PagedPlan {
+    int Gv, U, rows, tile_log2, max_ctas;
+};
+PagedPlan paged_plan_simt(int T, int Hq, int Hkv, int d);
+int paged_slot_rows(int U, int T, int Gv);
+size_t paged_plan_bytes(const PagedPlan& p, int d);
+
+cudaError_t launch_build_tables(const TablesArgs& a);
+cudaError_t launch_cache_append(const AppendArgs& a);
+cudaError_t launch_verify_draft(const VerifyArgs& a);
+cudaError_t launch_paged_attention_simt(const PagedArgs& a);
+cudaError_t launch_paged_merge(const PagedArgs& a, const PagedPlan& p, int ctas);
+kda_paged::Shape paged_shape(const PagedArgs& a, const PagedPlan& p);
+kda_paged::Partials paged_partials(const PagedArgs& a, const PagedPlan& p);
+
+}  // namespace kda_host

@@ -1,0 +1,427 @@
+// paged_attention.cu -- attention over a paged cache on CUDA cores in fp32, and
+// the merge of units that were cut between CTAs (paged.cuh).
+//
+// Per row (a new token and query head), over the keys it sees, in one pass:
+//     m' = max(m, max_j s_j),  l' = l 2^(m - m') + sum_j 2^(s_j - m'),
+//     o' = o 2^(m - m') + sum_j 2^(s_j - m') v_j,   s_j = scale log2(e) q.k_j
+// and o / l at the end; lse = (m + log2 l) ln 2.
+//
+// This path is for fp32 (whose accuracy the tensor cores' 16-bit operands do
+// not reach), head dimension 32, and rows of q that TMA cannot fetch.  A unit
+// has up to 32 rows; a tile of 64 keys and values is brought to shared memory
+// as fp32 and each of 256 threads forms 2 x 4 scores, then 4 rows x d / 32
+// columns of the weighted sum.  Bound: fp32 issue (one shared-memory load per
+// 2 to 4 multiply-adds) for many rows, the latency of a tile's loads for few.
+#include <algorithm>
+
+#include "paged.cuh"
+
+namespace {
+
+using kda_paged::Partials;
+using kda_paged::Piece;
+using kda_paged::Shape;
+using kda_paged::Unit;
+using kda_paged::Walker;
+
+constexpr int kThreads = 256;
+constexpr int kRows = 32;                              // rows of a unit
+constexpr int kTileLog2 = 6;
+constexpr int kTile = 1 << kTileLog2;
+constexpr float kLn2 = 0.69314718055994531f;
+constexpr float kLog2e = 1.44269504088896341f;
+
+template <int D>
+struct SimtSmem {
+    float q[kRows][D];
+    float k[kTile][D + 4];
+    float v[kTile][D];
+    float p[kRows][kTile + 4];                         // weights; -1 where the row does not see the key
+    float scale[kRows];                                // factor of the earlier sums
+};
+
+template <int D, typename T>
+__global__ void __launch_bounds__(kThreads)
+kda_paged_attention_simt_kernel(const T* __restrict__ q, const T* __restrict__ kc, const T* __restrict__ vc,
+                                const int32_t* __restrict__ table, const int32_t* __restrict__ cu,
+                                const int32_t* __restrict__ seq_len, long long q_stride, Shape s, float scale_log2,
+                                T* __restrict__ o, float* __restrict__ lse, Partials parts) {
+    extern __shared__ __align__(16) unsigned char smem_raw[];
+    SimtSmem<D>& sm = *reinterpret_cast<SimtSmem<D>*>(smem_raw);
+    __shared__ unsigned long long s_red[kThreads / 32];
+    __shared__ Piece s_piece;
+    __shared__ Unit s_unit;
+    __shared__ int s_more;
+    const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
+
+    const Piece piece = kda_paged::find_piece<kThreads>(s, cu, seq_len, blockIdx.x, gridDim.x,
+                                                        reinterpret_cast<unsigned long long*>(smem_raw), s_red,
+                                                        &s_piece);
+    Walker walk;
+    if (w == 0) walk.start(s, cu, seq_len, piece);
+    if (tid == 0) parts.meta[blockIdx.x] = make_int4(0, 0, 0, 0);
+
+    constexpr int VC = D / 32;                         // value columns per thread
+    for (;;) {
+        __syncthreads();                               // the unit before is done with shared memory
+        if (w == 0) {
+            Unit nu;
+            const bool more = walk.next(s, cu, seq_len, nu);
+            if (lane == 0) {
+                s_unit = nu;
+                s_more = more;
+            }
+        }
+        __syncthreads();
+        if (!s_more) break;
+        const Unit u = s_unit;
+        const int rows = u.ntok * s.Gv;
+        for (int e = tid; e < kRows * D; e += kThreads) {
+            const int r = e / D, c = e % D;
+            float x = 0.f;
+            if (r < rows)
+                x = kda::io<T>::ld(q + (long long)(u.tok0 + r / s.Gv) * q_stride + (long long)(u.qh0 + r % s.Gv) * D + c);
+            sm.q[r][c] = x * scale_log2;
+        }
+        // softmax state: 8 threads share a row
+        const int sr = tid >> 3, sx = tid & 7;
+        const int my_pos = u.pos + sr / s.Gv;
+        const int my_hi = sr < rows ? min(my_pos + 1, u.kend) : 0;
+        const int my_lo = s.window > 0 ? max(0, my_pos - s.window + 1) : 0;
+        float m = -INFINITY, l = 0.f;
+        float acc[4][VC];
+#pragma unroll
+        for (int a = 0; a < 4; ++a)
+#pragma unroll
+            for (int c = 0; c < VC; ++c) acc[a][c] = 0.f;
+
+        for (int t = u.tb; t < u.te; ++t) {
+            const int key0 = t << kTileLog2;
+            __syncthreads();                           // q stored; the tile before is consumed
+            // keys and values of the tile; places without a key become zero
+            constexpr int VEC = 16 / sizeof(T);        // the cache is 16-byte aligned
+            int ok_page = 0;                           // this thread's view of key `lane + 32 * half`, below
+            for (int e = tid; e < kTile * (D / VEC); e += kThreads) {
+                const int j = e / (D / VEC), c = (e % (D / VEC)) * VEC, key = key0 + j;
+                int page = -1;
+                if (key < u.kend) page = table[(size_t)u.n * s.blocks + (key >> s.page_log2)];
+                float kx[VEC], vx[VEC];
+#pragma unroll
+                for (int x = 0; x < VEC; ++x) kx[x] = vx[x] = 0.f;
+                if (page >= 0 && page < s.n_pages) {
+                    const size_t off = ((((size_t)page * s.Hkv + u.kvh) << s.page_log2) + (key & ((1 << s.page_log2) - 1))) * D + c;
+                    const uint4 ka = *reinterpret_cast<const uint4*>(kc + off), va = *reinterpret_cast<const uint4*>(vc + off);
+                    const T* kt = reinterpret_cast<const T*>(&ka);
+                    const T* vt = reinterpret_cast<const T*>(&va);
+#pragma unroll
+                    for (int x = 0; x < VEC; ++x) {
+                        kx[x] = kda::io<T>::ld(kt + x);
+                        vx[x] = kda::io<T>::ld(vt + x);
+                    }
+                }
+#pragma unroll
+                for (int x = 0; x < VEC; x += 4) {
+                    *reinterpret_cast<float4*>(&sm.k[j][c + x]) = make_float4(kx[x], kx[x + 1], kx[x + 2], kx[x + 3]);
+                    *reinterpret_cast<float4*>(&sm.v[j][c + x]) = make_float4(vx[x], vx[x + 1], vx[x + 2], vx[x + 3]);
+                }
+            }
+            // pages that exist, for the keys this thread judges below (sx + 8 i)
+            unsigned exists = 0;
+            ok_page = -1;
+            int last_block = -1;
+#pragma unroll
+            for (int i = 0; i < kTile / 8; ++i) {
+                const int key = key0 + sx + 8 * i;
+                if (key >= u.kend) continue;
+                const int b = key >> s.page_log2;
+                if (b != last_block) {
+                    ok_page = table[(size_t)u.n * s.blocks + b];
+                    last_block = b;
+                }
+                if (ok_page >= 0 && ok_page < s.n_pages) exists |= 1u << i;
+            }
+            __syncthreads();
+            // scores: rows 2 ty, 2 ty + 1, keys tx + 16 i
+            {
+                const int ty = tid >> 4, tx = tid & 15;
+                float a[2][4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) a[0][i] = a[1][i] = 0.f;
+                for (int c = 0; c < D; c += 4) {
+                    const float4 q0 = *reinterpret_cast<const float4*>(&sm.q[2 * ty][c]);
+                    const float4 q1 = *reinterpret_cast<const float4*>(&sm.q[2 * ty + 1][c]);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float4 kk = *reinterpret_cast<const float4*>(&sm.k[tx + 16 * i][c]);
+                        a[0][i] = fmaf(q0.x, kk.x, fmaf(q0.y, kk.y, fmaf(q0.z, kk.z, fmaf(q0.w, kk.w, a[0][i]))));
+                        a[1][i] = fmaf(q1.x, kk.x, fmaf(q1.y, kk.y, fmaf(q1.z, kk.z, fmaf(q1.w, kk.w, a[1][i]))));
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    sm.p[2 * ty][tx + 16 * i] = a[0][i];
+                    sm.p[2 * ty + 1][tx + 16 * i] = a[1][i];
+                }
+            }
+            __syncthreads();
+            // softmax statistics of row sr
+            {
+                float x[kTile / 8];
+                float top = -INFINITY;
+                unsigned seen = 0;
+#pragma unroll
+                for (int i = 0; i < kTile / 8; ++i) {
+                    const int key = key0 + sx + 8 * i;
+                    x[i] = sm.p[sr][sx + 8 * i];
+                    if (((exists >> i) & 1) && key >= my_lo && key < my_hi) {
+                        seen |= 1u << i;
+                        top = fmaxf(top, x[i]);
+                    }
+                }
+#pragma unroll
+                for (int d = 4; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+                const float mn = fmaxf(m, top), ref = mn == -INFINITY ? 0.f : mn;
+                const float f = m == -INFINITY ? (l == 0.f ? 0.f : 1.f) : exp2f(m - ref);
+                float sum = 0.f;
+#pragma unroll
+                for (int i = 0; i < kTile / 8; ++i) {
+                    const float p = (seen >> i) & 1 ? exp2f(x[i] - ref) : -1.f;
+                    if ((seen >> i) & 1) sum += p;
+                    sm.p[sr][sx + 8 * i] = p;
+                }
+#pragma unroll
+                for (int d = 4; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+                l = fmaf(l, f, sum);
+                m = mn;
+                if (sx == 0) sm.scale[sr] = f;
+            }
+            __syncthreads();
+            // weighted sums: rows 4 w .. 4 w + 3, columns lane + 32 c; a masked key is
+            // passed over, not multiplied by zero, so that what stands there stays out
+#pragma unroll
+            for (int a = 0; a < 4; ++a) {
+                const float f = sm.scale[4 * w + a];
+#pragma unroll
+                for (int c = 0; c < VC; ++c) acc[a][c] *= f;
+            }
+            if (4 * w < rows) {
+                for (int j = 0; j < kTile; j += 4) {
+                    float4 p[4];
+#pragma unroll
+                    for (int a = 0; a < 4; ++a) p[a] = *reinterpret_cast<const float4*>(&sm.p[4 * w + a][j]);
+#pragma unroll
+                    for (int jj = 0; jj < 4; ++jj) {
+                        float vv[VC];
+#pragma unroll
+                        for (int c = 0; c < VC; ++c) vv[c] = sm.v[j + jj][lane + 32 * c];
+#pragma unroll
+                        for (int a = 0; a < 4; ++a) {
+                            const float pj = jj == 0 ? p[a].x : jj == 1 ? p[a].y : jj == 2 ? p[a].z : p[a].w;
+                            if (pj != -1.f) {
+#pragma unroll
+                                for (int c = 0; c < VC; ++c) acc[a][c] = fmaf(pj, vv[c], acc[a][c]);
+                            }
+                        }
+                    }
+                }
+            }
+        }
+        // the row's statistics to the threads that hold its sums
+        __syncthreads();
+        if (sx == 0) {
+            sm.p[sr][0] = m;
+            sm.p[sr][1] = l;
+        }
+        __syncthreads();
+        const bool whole = u.first && u.last;
+        const int which = u.first ? 1 : 0;
+#pragma unroll
+        for (int a = 0; a < 4; ++a) {
+            const int r = 4 * w + a;
+            if (r >= rows) continue;
+            const float rm = sm.p[r][0], rl = sm.p[r][1];
+            if (whole) {
+                const float inv = rl == 0.f ? 0.f : 1.f / rl;
+                const size_t at = (size_t)(u.tok0 + r / s.Gv) * s.Hq + u.qh0 + r % s.Gv;
+#pragma unroll
+                for (int c = 0; c < VC; ++c) kda::io<T>::st(o + at * D + lane + 32 * c, acc[a][c] * inv);
+                if (lse && lane == 0) lse[at] = rl == 0.f ? -INFINITY : (rm + log2f(rl)) * kLn2;
+            } else {
+                float* dst = parts.sums(blockIdx.x, which) + (size_t)r * D;
+#pragma unroll
+                for (int c = 0; c < VC; ++c) dst[lane + 32 * c] = acc[a][c];
+                if (lane == 0) parts.stats(blockIdx.x, which)[r] = make_float2(rm, rl);
+            }
+        }
+        if (!whole && u.first && tid == 0) parts.meta[blockIdx.x] = make_int4(u.tok0, u.qh0, u.ntok, u.parts);
+    }
+}
+
+// Joins the parts of each cut unit: with M = max of the parts' references,
+//     o = sum_i 2^(m_i - M) o_i / sum_i 2^(m_i - M) l_i.
+// blockIdx.x names the CTA in which the unit begins, blockIdx.y the block's
+// rows; D / 4 threads take a row.  Reads each partial row once.
+template <int D, typename T>
+__global__ void __launch_bounds__(256)
+kda_paged_merge_kernel(Partials parts, int Gv, int Hq, T* __restrict__ o, float* __restrict__ lse) {
+    constexpr int TPR = D / 4, RPB = 256 / TPR;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int c0 = blockIdx.x;
+    const int4 me = parts.meta[c0];
+    if (me.w == 0) return;
+    const int rows = me.z * Gv, n = me.w;
+    const int x = threadIdx.x % TPR;
+    for (int r = blockIdx.y * RPB + threadIdx.x / TPR; r < rows; r += gridDim.y * RPB) {
+        float top = -INFINITY;
+#pragma unroll 4
+        for (int i = 0; i < n; ++i) top = fmaxf(top, parts.stats(c0 + i, i == 0 ? 1 : 0)[r].x);
+        const float ref = top == -INFINITY ? 0.f : top;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        float l = 0.f;
+#pragma unroll 4
+        for (int i = 0; i < n; ++i) {
+            const float2 st = parts.stats(c0 + i, i == 0 ? 1 : 0)[r];
+            const float4 v = reinterpret_cast<const float4*>(parts.sums(c0 + i, i == 0 ? 1 : 0) + (size_t)r * D)[x];
+            if (st.y == 0.f) continue;                 // the part saw no key of this row
+            const float f = st.x == -INFINITY ? 1.f : exp2f(st.x - ref);
+            l = fmaf(f, st.y, l);
+            acc.x = fmaf(f, v.x, acc.x); acc.y = fmaf(f, v.y, acc.y);
+            acc.z = fmaf(f, v.z, acc.z); acc.w = fmaf(f, v.w, acc.w);
+        }
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        const size_t at = (size_t)(me.x + r / Gv) * Hq + me.y + r % Gv;
+        T* dst = o + at * D + 4 * x;
+        kda::io<T>::st(dst + 0, acc.x * inv);
+        kda::io<T>::st(dst + 1, acc.y * inv);
+        kda::io<T>::st(dst + 2, acc.z * inv);
+        kda::io<T>::st(dst + 3, acc.w * inv);
+        if (lse && x == 0) lse[at] = l == 0.f ? -INFINITY : (top + log2f(l)) * kLn2;
+    }
+}
+
+template <int D, typename T>
+cudaError_t launch_merge(const kda_host::PagedArgs& a, const kda_host::PagedPlan& p, int ctas) {
+    const int rows_per_block = 256 / (D / 4);
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(ctas, std::max(1, std::min(4, (p.rows + rows_per_block - 1) / rows_per_block)));
+    cfg.blockDim = dim3(256);
+    cfg.stream = a.stream;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kda_paged_merge_kernel<D, T>, kda_host::paged_partials(a, p), p.Gv, a.Hq,
+                              static_cast<T*>(a.o), a.lse);
+}
+
+template <int D, typename T>
+cudaError_t launch_simt(const kda_host::PagedArgs& a) {
+    const kda_host::PagedPlan p = kda_host::paged_plan_simt(a.T, a.Hq, a.Hkv, a.d);
+    const size_t smem = std::max(sizeof(SimtSmem<D>), (size_t)a.N * sizeof(unsigned long long));
+    auto kern = kda_paged_attention_simt_kernel<D, T>;
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    const int ctas = std::min(p.max_ctas, 2 * kda_host::sm_count());
+    kern<<<ctas, kThreads, smem, a.stream>>>(
+        static_cast<const T*>(a.q), static_cast<const T*>(a.k_cache), static_cast<const T*>(a.v_cache), a.block_table,
+        a.cu_seqlens, a.seq_len, a.q_stride, kda_host::paged_shape(a, p), a.scale * kLog2e, static_cast<T*>(a.o), a.lse,
+        kda_host::paged_partials(a, p));
+    const cudaError_t err = cudaGetLastError();
+    if (err != cudaSuccess) return err;
+    return kda_host::launch_paged_merge(a, p, ctas);
+}
+
+size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
+
+}  // namespace
+
+namespace kda_host {
+
+int sm_count() {
+    constexpr int kMaxDevices = 64;
+    static int counts[kMaxDevices] = {};               // 0: not asked yet; every writer stores the same value
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) {
+        (void)cudaGetLastError();
+        return 148;
+    }
+    if (counts[dev] == 0) {
+        int n = 0;
+        if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) {
+            (void)cudaGetLastError();
+            return 148;
+        }
+        counts[dev] = n;
+    }
+    return counts[dev];
+}
+
+PagedPlan paged_plan_simt(int T, int Hq, int Hkv, int d) {
+    PagedPlan p;
+    (void)d;
+    p.Gv = heads_per_unit(Hq / Hkv, kRows);
+    p.U = kRows / p.Gv;
+    p.rows = kda_host::paged_slot_rows(p.U, T, p.Gv);
+    p.tile_log2 = kTileLog2;
+    p.max_ctas = 304;
+    return p;
+}
+
+// A multiple of 4, so that every slot and its statistics start on a 16-byte
+// boundary (a row has d + 2 floats).
+int paged_slot_rows(int U, int T, int Gv) { return (std::min(U, std::max(T, 1)) * Gv + 3) & ~3; }
+
+size_t paged_plan_bytes(const PagedPlan& p, int d) {
+    return up256((size_t)p.max_ctas * sizeof(int4)) + up256((size_t)p.max_ctas * 2 * p.rows * (d + 2) * sizeof(float));
+}
+
+kda_paged::Shape paged_shape(const PagedArgs& a, const PagedPlan& p) {
+    Shape s;
+    s.n_req = a.N;
+    s.T = a.T;
+    s.Hq = a.Hq;
+    s.Hkv = a.Hkv;
+    s.Gv = p.Gv;
+    s.Hv = a.Hq / p.Gv;
+    s.sub = s.Hv / a.Hkv;
+    s.blocks = a.blocks;
+    s.page_log2 = 0;
+    while ((1 << s.page_log2) < a.page_size) ++s.page_log2;
+    s.n_pages = a.n_pages;
+    s.window = a.window;
+    s.U = p.U;
+    s.tile_log2 = p.tile_log2;
+    return s;
+}
+
+kda_paged::Partials paged_partials(const PagedArgs& a, const PagedPlan& p) {
+    Partials x;
+    x.meta = static_cast<int4*>(a.workspace);
+    x.rows = reinterpret_cast<float*>(static_cast<char*>(a.workspace) + up256((size_t)p.max_ctas * sizeof(int4)));
+    x.cap = p.rows;
+    x.d = a.d;
+    return x;
+}
+
+cudaError_t launch_paged_merge(const PagedArgs& a, const PagedPlan& p, int ctas) {
+    const bool wide = a.dtype == KDA_BF16;
+    switch (a.d) {
+        case 32: return wide ? launch_merge<32, __nv_bfloat16>(a, p, ctas) : launch_merge<32, float>(a, p, ctas);
+        case 64: return wide ? launch_merge<64, __nv_bfloat16>(a, p, ctas) : launch_merge<64, float>(a, p, ctas);
+        case 128: return wide ? launch_merge<128, __nv_bfloat16>(a, p, ctas) : launch_merge<128, float>(a, p, ctas);
+    }
+    return cudaErrorNotSupported;
+}
+
+cudaError_t launch_paged_attention_simt(const PagedArgs& a) {
+    const bool wide = a.dtype == KDA_BF16;
+    switch (a.d) {
+        case 32: return wide ? launch_simt<32, __nv_bfloat16>(a) : launch_simt<32, float>(a);
+        case 64: return wide ? launch_simt<64, __nv_bfloat16>(a) : launch_simt<64, float>(a);
+        case 128: return wide ? launch_simt<128, __nv_bfloat16>(a) : launch_simt<128, float>(a);
+    }
+    return cudaErrorNotSupported;
+}
+
+}  // namespace kda_host
