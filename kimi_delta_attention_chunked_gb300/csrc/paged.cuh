@@ -365,6 +365,8 @@ inline int heads_per_unit(int group, int most) {
 struct PagedPlan {
     int Gv, U, rows, tile_log2, max_ctas;
 };
+bool paged_tc_supported(int d, kda_dtype dt);
+PagedPlan paged_plan_tc(int T, int Hq, int Hkv);
 PagedPlan paged_plan_simt(int T, int Hq, int Hkv, int d);
 int paged_slot_rows(int U, int T, int Gv);
 size_t paged_plan_bytes(const PagedPlan& p, int d);
@@ -372,6 +374,7 @@ size_t paged_plan_bytes(const PagedPlan& p, int d);
 cudaError_t launch_build_tables(const TablesArgs& a);
 cudaError_t launch_cache_append(const AppendArgs& a);
 cudaError_t launch_verify_draft(const VerifyArgs& a);
+cudaError_t launch_paged_attention_tc(const PagedArgs& a);
 cudaError_t launch_paged_attention_simt(const PagedArgs& a);
 cudaError_t launch_paged_merge(const PagedArgs& a, const PagedPlan& p, int ctas);
 kda_paged::Shape paged_shape(const PagedArgs& a, const PagedPlan& p);

@@ -1,5 +1,6 @@
 // paged_api.cu -- C entry points of the serving-step operators: argument
 // checks, path selection, launches.  See include/kda.h for their contracts.
+#include <algorithm>
 #include <cmath>
 
 #include "paged.cuh"
@@ -17,8 +18,11 @@ bool dim_ok(int d) { return d == 32 || d == 64 || d == 128; }
 bool dtype_ok(kda_dtype t) { return t == KDA_FP32 || t == KDA_BF16; }
 bool aligned(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
 
-size_t attention_workspace(int T, int Hq, int Hkv, int d, kda_dtype) {
-    return kda_host::paged_plan_bytes(kda_host::paged_plan_simt(T, Hq, Hkv, d), d);
+// Enough for either path: which one runs also depends on the alignment of q.
+size_t attention_workspace(int T, int Hq, int Hkv, int d, kda_dtype dt) {
+    const size_t simt = kda_host::paged_plan_bytes(kda_host::paged_plan_simt(T, Hq, Hkv, d), d);
+    if (!kda_host::paged_tc_supported(d, dt)) return simt;
+    return std::max(simt, kda_host::paged_plan_bytes(kda_host::paged_plan_tc(T, Hq, Hkv), d));
 }
 
 }  // namespace
@@ -88,7 +92,11 @@ kda_status kda_paged_attention(const void* q, const void* k_cache, const void* v
     kda_host::PagedArgs a{q, k_cache, v_cache, block_table, cu_seqlens, seq_len, q_stride, N, T, H_q, H_kv, d,
                           page_size, max_blocks, n_pages, scale, window, dtype, o, lse, workspace, stream,
                           kda_host::status_word()};
-    return from_cuda(kda_host::launch_paged_attention_simt(a));
+    // the tensor-core path fetches q by TMA, whose rows start on 16-byte boundaries, and
+    // describes the cache to it, which an empty one cannot be
+    const bool tc = kda_host::paged_tc_supported(d, dtype) && aligned(q, 16) && q_stride % 8 == 0 && n_pages > 0 &&
+                    max_blocks > 0;
+    return from_cuda(tc ? kda_host::launch_paged_attention_tc(a) : kda_host::launch_paged_attention_simt(a));
 }
 
 kda_status kda_verify_draft(const void* target, const void* draft, const int32_t* draft_tokens,

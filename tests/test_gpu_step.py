@@ -289,7 +289,8 @@ def test_attention_strided_q(dtype, d, qpad):
     c = make([(100, 2), (3, 9)], 4, 2, d, 16, dtype, dev, qpad=qpad)
     check(c, dev)
     args = on(c, dev)
-    q = torch.cat([args[0], torch.full_like(args[0][:5], math.nan)])
+    wide = c["wide"].to(dev)                               # the same strides and alignment, with rows behind the last token
+    q = torch.cat([wide, torch.full_like(wide[:5], math.nan)])[:, qpad:].unflatten(1, (4, d))
     o = torch.full(tuple(q.shape), 7.0, dtype=dtype, device=dev)
     kda.kda_paged_attention(q, *args[1:], o=o)
     assert bool((o[-5:] == 7).all())
