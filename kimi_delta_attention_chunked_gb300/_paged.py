@@ -9,6 +9,8 @@ when it is another one.
 """
 from __future__ import annotations
 
+import functools
+
 import torch
 
 from . import _lib
@@ -16,52 +18,55 @@ from ._lib import KDA_BF16, KDA_FP32, KDA_OK, KDAError
 
 _CODE = {torch.bfloat16: KDA_BF16, torch.float32: KDA_FP32}
 _I32, _I64, _F32 = torch.int32, torch.int64, torch.float32
+# the current stream's handle without a Stream object around it, where torch has it
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _call(entry, dev, stream, args):
-    """Calls C entry ``entry`` on ``stream`` with ``dev`` current; raises on an error code."""
+def _call(entry, idx, stream, args):
+    """Calls C entry ``entry`` on ``stream`` with device ``idx`` current; raises on an error code."""
     fn = getattr(_lib._lib or _lib.load(), entry)
     if stream is None:
-        handle = torch.cuda.current_stream(dev).cuda_stream
+        handle = _raw_stream(idx) if _raw_stream else torch.cuda.current_stream(idx).cuda_stream
     else:
         handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-    if dev.index == torch.cuda.current_device():
+    if idx == torch.cuda.current_device():
         st = fn(*args, handle)
     else:
-        with torch.cuda.device(dev):
+        with torch.cuda.device(idx):
             st = fn(*args, handle)
     if st != KDA_OK:
         raise KDAError(st, entry)
 
 
 def _device(name, t):
-    dev = t.device
-    if dev.type != "cuda":
+    """Index of the CUDA device that holds t."""
+    idx = t.get_device()
+    if idx < 0:
         raise ValueError(f"{name} must be on a CUDA device")
-    return dev
+    return idx
 
 
-def _need(name, t, dev, dtype, shape):
-    if tuple(t.shape) != shape:
-        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
+def _refuse(name, t, idx, dtype, shape):
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.device != dev:
-        raise ValueError(f"{name} must be on {dev}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
+    if t.get_device() != idx:
+        raise ValueError(f"{name} must be on cuda:{idx}")
+    raise ValueError(f"{name} must be contiguous")
+
+
+def _need(name, t, idx, dtype, shape):
+    if t.shape != shape or t.dtype != dtype or t.get_device() != idx or not t.is_contiguous():
+        _refuse(name, t, idx, dtype, shape)
     return t.data_ptr()
 
 
-def _rows(name, t, dev, dtype, shape):
+def _rows(name, t, idx, dtype, shape):
     """A [tokens, heads, d] tensor whose tokens may lie further apart than heads * d
     (a slice of a fused projection): (pointer, elements between tokens)."""
-    if tuple(t.shape) != shape:
-        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.device != dev:
-        raise ValueError(f"{name} must be on {dev}")
+    if t.shape != shape or t.dtype != dtype or t.get_device() != idx:
+        _refuse(name, t, idx, dtype, shape)
     row = shape[1] * shape[2]
     if t.is_contiguous():
         return t.data_ptr(), row
@@ -93,7 +98,7 @@ def kda_build_block_tables(ctx_len, new_len, free_pages, block_table, page_size,
     if new_len.shape != ctx_len.shape:
         raise ValueError(f"new_len must have shape {(n,)}, got {tuple(new_len.shape)}")
     dev = _device("ctx_len", ctx_len)
-    new = lambda shape, dt: torch.empty(shape, dtype=dt, device=dev)  # noqa: E731
+    new = lambda shape, dt: torch.empty(shape, dtype=dt, device=ctx_len.device)  # noqa: E731
     n_tokens = int(n_tokens)
     if cu_seqlens is None:
         cu_seqlens = new(n + 1, _I32)
@@ -119,7 +124,7 @@ def _cache_shape(name, k_cache, v_cache):
     if k_cache.dim() != 4 or v_cache.shape != k_cache.shape:
         raise ValueError(f"{name}: k_cache and v_cache must have one shape [n_pages, H_kv, page_size, d], "
                          f"got {tuple(k_cache.shape)} and {tuple(v_cache.shape)}")
-    return tuple(k_cache.shape)
+    return k_cache.shape
 
 
 def kda_cache_append(k, v, k_cache, v_cache, slot_map, stream=None):
@@ -131,7 +136,7 @@ def kda_cache_append(k, v, k_cache, v_cache, slot_map, stream=None):
         raise ValueError(f"k must have 3 dims, got {k.dim()}")
     rows = (k.shape[0], heads, d)
     code, dt = _code(k_cache), k_cache.dtype
-    if tuple(k.shape) != rows or tuple(v.shape) != rows:
+    if k.shape != rows or v.shape != rows:
         raise ValueError(f"k and v must have shape {rows}, got {tuple(k.shape)} and {tuple(v.shape)}")
     dev = _device("k_cache", k_cache)
     kp, ks = _rows("k", k, dev, dt, rows)
@@ -139,6 +144,11 @@ def kda_cache_append(k, v, k_cache, v_cache, slot_map, stream=None):
     args = (kp, vp, _need("slot_map", slot_map, dev, _I64, (rows[0],)), ks, vs, rows[0], heads, d, page, n_pages, code,
             _need("k_cache", k_cache, dev, dt, shape), _need("v_cache", v_cache, dev, dt, shape))
     _call("kda_cache_append", dev, stream, args)
+
+
+@functools.lru_cache(maxsize=256)
+def _workspace_size(T, heads, kv_heads, d, code):
+    return int(_lib.load().kda_paged_attention_workspace_size(T, heads, kv_heads, d, code))
 
 
 def kda_paged_attention_workspace_size(T: int, H_q: int, H_kv: int, d: int, dtype: torch.dtype) -> int:
@@ -156,30 +166,29 @@ def kda_paged_attention(q, k_cache, v_cache, block_table, cu_seqlens, seq_len, s
     n_pages, kv_heads, page, d = shape
     if q.dim() != 3 or block_table.dim() != 2:
         raise ValueError(f"q must have 3 dims and block_table 2, got {q.dim()} and {block_table.dim()}")
-    rows = tuple(q.shape)
+    rows = q.shape
     T, heads, qd = rows
     if qd != d or heads % kv_heads != 0:
-        raise ValueError(f"q {rows} does not match caches of {kv_heads} heads of {d}")
+        raise ValueError(f"q {tuple(rows)} does not match caches of {kv_heads} heads of {d}")
     n, blocks = block_table.shape
     code, dt = _code(q), q.dtype
-    if tuple(cu_seqlens.shape) != (n + 1,) or tuple(seq_len.shape) != (n,):
+    if cu_seqlens.shape != (n + 1,) or seq_len.shape != (n,):
         raise ValueError(f"cu_seqlens and seq_len must have shapes {(n + 1,)} and {(n,)}, got "
                          f"{tuple(cu_seqlens.shape)} and {tuple(seq_len.shape)}")
-    if o is not None and tuple(o.shape) != rows:
-        raise ValueError(f"o must have shape {rows}, got {tuple(o.shape)}")
-    if lse is not None and tuple(lse.shape) != rows[:2]:
-        raise ValueError(f"lse must have shape {rows[:2]}, got {tuple(lse.shape)}")
+    if o is not None and o.shape != rows:
+        raise ValueError(f"o must have shape {tuple(rows)}, got {tuple(o.shape)}")
+    if lse is not None and lse.shape != rows[:2]:
+        raise ValueError(f"lse must have shape {tuple(rows[:2])}, got {tuple(lse.shape)}")
     dev = _device("q", q)
     qp, qs = _rows("q", q, dev, dt, rows)
     if o is None:
-        o = torch.empty(rows, dtype=dt, device=dev)
+        o = torch.empty(rows, dtype=dt, device=q.device)
     if lse is None and want_lse:
-        lse = torch.empty(rows[:2], dtype=_F32, device=dev)
+        lse = torch.empty(rows[:2], dtype=_F32, device=q.device)
     if workspace is None:
-        size = (_lib._lib or _lib.load()).kda_paged_attention_workspace_size(T, heads, kv_heads, d, code)
-        workspace = torch.empty(size, dtype=torch.uint8, device=dev)
-    elif workspace.device != dev or not workspace.is_contiguous():
-        raise ValueError(f"workspace must be contiguous and on {dev}")
+        workspace = torch.empty(_workspace_size(T, heads, kv_heads, d, code), dtype=torch.uint8, device=q.device)
+    elif workspace.get_device() != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be contiguous and on cuda:{dev}")
     args = (qp, _need("k_cache", k_cache, dev, dt, shape), _need("v_cache", v_cache, dev, dt, shape),
             _need("block_table", block_table, dev, _I32, (n, blocks)),
             _need("cu_seqlens", cu_seqlens, dev, _I32, (n + 1,)), _need("seq_len", seq_len, dev, _I32, (n,)), qs, n, T,
@@ -200,17 +209,17 @@ def kda_verify_draft(target, draft, draft_tokens, uniforms, draft_len=None, toke
         raise ValueError(f"target must have 3 dims and draft_tokens 2, got {target.dim()} and {draft_tokens.dim()}")
     n, k = draft_tokens.shape
     vocab = target.shape[2]
-    if tuple(target.shape) != (n, k + 1, vocab) or (draft is not None and tuple(draft.shape) != (n, k, vocab)):
+    if target.shape != (n, k + 1, vocab) or (draft is not None and draft.shape != (n, k, vocab)):
         raise ValueError(f"target and draft must have shapes {(n, k + 1, vocab)} and {(n, k, vocab)}, got "
                          f"{tuple(target.shape)} and {None if draft is None else tuple(draft.shape)}")
-    if tuple(uniforms.shape) != (n, k + 1):
+    if uniforms.shape != (n, k + 1):
         raise ValueError(f"uniforms must have shape {(n, k + 1)}, got {tuple(uniforms.shape)}")
     code, dt = _code(target), target.dtype
     dev = _device("target", target)
     if tokens is None:
-        tokens = torch.empty((n, k + 1), dtype=_I32, device=dev)
+        tokens = torch.empty((n, k + 1), dtype=_I32, device=target.device)
     if commit_len is None:
-        commit_len = torch.empty((n,), dtype=_I32, device=dev)
+        commit_len = torch.empty((n,), dtype=_I32, device=target.device)
     args = (_need("target", target, dev, dt, (n, k + 1, vocab)),
             None if draft is None else _need("draft", draft, dev, dt, (n, k, vocab)),
             _need("draft_tokens", draft_tokens, dev, _I32, (n, k)), _need("uniforms", uniforms, dev, _F32, (n, k + 1)),

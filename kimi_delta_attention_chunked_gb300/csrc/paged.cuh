@@ -11,6 +11,8 @@
 // on the device: no plan is made on the host, and no extra launch is needed.
 #pragma once
 
+#include <atomic>
+
 #include "common.cuh"
 
 namespace kda_paged {
@@ -107,6 +109,62 @@ struct Piece {
     int n, ctas;                                   // first request; CTAs that have a piece
 };
 
+// x * y / z; a 64-bit division takes several times the cycles of a 32-bit one,
+// and all but the longest calls stay below its limit.
+__device__ __forceinline__ unsigned long long mul_div(unsigned long long x, unsigned y, unsigned z) {
+    if (x < (1u << 22) && y <= (unsigned)kMaxCtas) return (unsigned)x * y / z;
+    return x * y / z;
+}
+
+// A few requests: one warp finds the piece by itself, `kPerLane` consecutive
+// requests a lane.  No shared memory and no barrier, so the rest of the block
+// can set up meanwhile.
+constexpr int kPerLane = 8;
+constexpr int kWarpRequests = 32 * kPerLane;
+__device__ __forceinline__ Piece find_piece_warp(const Shape& s, const int32_t* __restrict__ cu,
+                                                 const int32_t* __restrict__ seq_len, int c, int C) {
+    const int lane = threadIdx.x & 31, per = (s.n_req + 31) / 32;
+    unsigned long long cost[kPerLane], mine = 0;
+#pragma unroll
+    for (int i = 0; i < kPerLane; ++i) {
+        cost[i] = 0;
+        if (i < per) cost[i] = request_tiles(s, cu, seq_len, lane * per + i, lane * per + i < s.n_req) * (unsigned)s.Hv;
+        mine += cost[i];
+    }
+    unsigned long long incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const unsigned long long t = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += t;
+    }
+    Piece p{0, 0, 0, 0, 0, 0, 0};
+    p.total = __shfl_sync(0xffffffffu, incl, 31);
+    p.ctas = (int)min((unsigned long long)C, p.total);
+    if (c >= p.ctas) return p;
+    p.begin = mul_div(p.total, (unsigned)c, (unsigned)p.ctas);
+    p.end = mul_div(p.total, (unsigned)(c + 1), (unsigned)p.ctas);
+    // the lane whose requests hold tile `begin`, and the request among them
+    const int src = __ffs((int)__ballot_sync(0xffffffffu, p.begin < incl)) - 1;
+    unsigned long long at = incl - mine, tiles = 0;
+    int n = lane * per;
+    bool found = false;
+#pragma unroll
+    for (int i = 0; i < kPerLane; ++i) {
+        if (found || i >= per) continue;
+        if (p.begin < at + cost[i]) {
+            found = true;
+            tiles = cost[i];
+            n = lane * per + i;
+        } else {
+            at += cost[i];
+        }
+    }
+    p.n = __shfl_sync(0xffffffffu, n, src);
+    p.off = p.begin - __shfl_sync(0xffffffffu, at, src);
+    p.tiles = __shfl_sync(0xffffffffu, tiles, src) / (unsigned)s.Hv;
+    return p;
+}
+
 // Finds the piece of CTA `c` of `C`.  Every thread of the block (NT of them)
 // calls it; `cost` holds n_req words and `red` NT / 32, of 64 bits, and free again after the block's next barrier.
 template <int NT>
@@ -146,7 +204,7 @@ __device__ __forceinline__ Piece find_piece(const Shape& s, const int32_t* __res
     incl += before;
     const int ctas = (int)min((unsigned long long)C, total);
     if (c < ctas) {
-        const unsigned long long begin = total * (unsigned)c / (unsigned)ctas;
+        const unsigned long long begin = mul_div(total, (unsigned)c, (unsigned)ctas);
         const unsigned long long excl = incl - mine;
         if (excl <= begin && begin < incl) {
             unsigned long long at = excl;
@@ -157,7 +215,7 @@ __device__ __forceinline__ Piece find_piece(const Shape& s, const int32_t* __res
                 at += x;
             }
             shared->begin = begin;
-            shared->end = total * (unsigned)(c + 1) / (unsigned)ctas;
+            shared->end = mul_div(total, (unsigned)(c + 1), (unsigned)ctas);
             shared->total = total;
             shared->off = begin - at;
             shared->tiles = cost[n];
@@ -199,7 +257,8 @@ struct Walker {
         if (at >= end) return;
         r = load_req(s, cu, seq_len, n);
         units = n_units(s, r);
-        h = (int)(p.off / p.tiles);
+        const bool small = p.off <= 0xffffffffu && p.tiles <= 0xffffffffu;
+        h = small ? (int)((unsigned)p.off / (unsigned)p.tiles) : (int)(p.off / p.tiles);
         unsigned long long left = p.off - (unsigned long long)h * p.tiles;
         const int lane = threadIdx.x & 31;
         for (int base = 0; base < units; base += 32) {         // the unit that holds tile `left` of this head
@@ -259,9 +318,14 @@ struct Walker {
         if (u.first && !u.last) {
             // CTA c begins at total * c / ctas, so the last one that has a tile below `fin` is
             // ceil(fin * ctas / total) - 1; likewise this one, from its first tile
-            const unsigned long long hi = (fin * (unsigned)ctas + total - 1) / total;
-            const unsigned long long lo = ((at + 1) * (unsigned)ctas + total - 1) / total;
-            u.parts = (int)(hi - lo) + 1;
+            if (total < (1u << 22)) {
+                const unsigned z = (unsigned)total;
+                u.parts = (int)(((unsigned)fin * (unsigned)ctas + z - 1) / z - (((unsigned)at + 1) * (unsigned)ctas + z - 1) / z) + 1;
+            } else {
+                const unsigned long long hi = (fin * (unsigned)ctas + total - 1) / total;
+                const unsigned long long lo = ((at + 1) * (unsigned)ctas + total - 1) / total;
+                u.parts = (int)(hi - lo) + 1;
+            }
         }
         at += (unsigned)(te - tb);
         skip = 0;
@@ -348,6 +412,22 @@ struct VerifyArgs {
     int32_t* tokens;
     int32_t* commit_len;
     cudaStream_t stream;
+};
+
+// Runs a device's one-time set-up (function attributes) on its first call there.
+struct OncePerDevice {
+    std::atomic<unsigned long long> done{0};
+    template <typename F>
+    cudaError_t run(F f) {
+        int dev = 0;
+        cudaError_t e = cudaGetDevice(&dev);
+        if (e != cudaSuccess) return e;
+        const unsigned long long bit = 1ull << (dev & 63);
+        if (dev < 64 && (done.load(std::memory_order_acquire) & bit)) return cudaSuccess;
+        e = f();                                       // twice is harmless
+        if (e == cudaSuccess && dev < 64) done.fetch_or(bit, std::memory_order_release);
+        return e;
+    }
 };
 
 int* status_word();                                // the device status word (kda_api.cu)

@@ -301,6 +301,14 @@ kda_paged_merge_kernel(Partials parts, int Gv, int Hq, T* __restrict__ o, float*
 
 template <int D, typename T>
 cudaError_t launch_merge(const kda_host::PagedArgs& a, const kda_host::PagedPlan& p, int ctas) {
+    // the same split of L1 and shared memory as the attention kernel before it: an SM
+    // must run dry to change it
+    static kda_host::OncePerDevice once;
+    const cudaError_t e = once.run([] {
+        return cudaFuncSetAttribute(kda_paged_merge_kernel<D, T>, cudaFuncAttributePreferredSharedMemoryCarveout,
+                                    cudaSharedmemCarveoutMaxShared);
+    });
+    if (e != cudaSuccess) return e;
     const int rows_per_block = 256 / (D / 4);
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(ctas, std::max(1, std::min(4, (p.rows + rows_per_block - 1) / rows_per_block)));
@@ -320,7 +328,11 @@ cudaError_t launch_simt(const kda_host::PagedArgs& a) {
     const kda_host::PagedPlan p = kda_host::paged_plan_simt(a.T, a.Hq, a.Hkv, a.d);
     const size_t smem = std::max(sizeof(SimtSmem<D>), (size_t)a.N * sizeof(unsigned long long));
     auto kern = kda_paged_attention_simt_kernel<D, T>;
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    static kda_host::OncePerDevice once;
+    const cudaError_t e = once.run([&] {
+        constexpr size_t most = std::max(sizeof(SimtSmem<D>), (size_t)kda_paged::kMaxRequests * 8);
+        return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
+    });
     if (e != cudaSuccess) return e;
     const int ctas = std::min(p.max_ctas, 2 * kda_host::sm_count());
     kern<<<ctas, kThreads, smem, a.stream>>>(

@@ -202,15 +202,7 @@ kda_paged_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __
     Tail& tl = *reinterpret_cast<Tail*>(sm + C::TAIL);
     const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
 
-    // ---- this CTA's piece of the work
-    auto* cost = reinterpret_cast<unsigned long long*>(sm + C::KV0);
-    auto* red = cost + kda_paged::kMaxRequests;
-    auto* shared_piece = reinterpret_cast<Piece*>(red + kThreads / 32);
-    const Piece piece = kda_paged::find_piece<kThreads>(s, cu, seq_len, blockIdx.x, gridDim.x, cost, red, shared_piece);
-    if (piece.begin >= piece.end) {
-        if (tid == 0) parts.meta[blockIdx.x] = make_int4(0, 0, 0, 0);
-        return;
-    }
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the merge may be set up; it waits for this grid
     if (w == kIssueWarp) {
         kda::tmem_alloc(&tl.tmem, 512);
         kda::tmem_relinquish();
@@ -237,7 +229,19 @@ kda_paged_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __
         kda::fence_barrier_init();
         tl.abort = 0;
     }
-    kda::fence_proxy_async_smem();                     // the scratch above becomes the target of copies
+    if (w == kCopyWarp && lane < 3) {
+        const CUtensorMap* m = lane == 0 ? &qmap : lane == 1 ? &kmap : &vmap;
+        asm volatile("prefetch.tensormap [%0];" ::"l"(m) : "memory");
+    }
+    // this CTA's piece of the work: by the walking warp alone where it can
+    Piece piece{0, 0, 0, 0, 0, 0, 0};
+    if (s.n_req > kda_paged::kWarpRequests) {
+        auto* cost = reinterpret_cast<unsigned long long*>(sm + C::KV0);
+        auto* red = cost + kda_paged::kMaxRequests;
+        auto* shared_piece = reinterpret_cast<Piece*>(red + kThreads / 32);
+        piece = kda_paged::find_piece<kThreads>(s, cu, seq_len, blockIdx.x, gridDim.x, cost, red, shared_piece);
+        kda::fence_proxy_async_smem();                 // the scratch becomes the target of copies
+    }
     kda::tc_fence_before();
     __syncthreads();
     kda::tc_fence_after();
@@ -266,6 +270,8 @@ kda_paged_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __
 
     if (w == kWalkWarp) {
         // ---------------- unit descriptions
+        if (s.n_req <= kda_paged::kWarpRequests)
+            piece = kda_paged::find_piece_warp(s, cu, seq_len, blockIdx.x, gridDim.x);
         Walker walk;
         walk.start(s, cu, seq_len, piece);
         int4 meta = make_int4(0, 0, 0, 0);
@@ -288,8 +294,8 @@ kda_paged_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __
         // g - 2, then the keys of step g, each when first needed
         const int pieces = s.page_log2 >= kKeysLog2 ? 1 : kKeys >> s.page_log2;   // pages of a tile
         const int box_rows = min(1 << s.page_log2, kKeys);
-        int g = 0;
-        struct { int load, page, y, kvh; } pend[2] = {};
+        struct Values { int load, page, y, kvh; };
+        Values older{0, 0, 0, 0}, newer{0, 0, 0, 0};   // of steps g - 2 and g - 1
         auto page_of = [&](const Unit& u, int tile) {  // lane's page of the tile; n_pages reads as zeros
             const int key = (tile << kKeysLog2) + lane * box_rows;
             int page = -1;
@@ -318,21 +324,21 @@ kda_paged_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __
             const bool two = u.ntok > BT;
             const int steps = (u.te - u.tb) << (two ? 1 : 0);
             int next_page = page_of(u, u.tb);
-            for (int t = 0; ok && t < steps; ++t, ++g) {
-                auto& pv = pend[g & 1];
-                if (pv.load) ok = load(&vmap, pv.page, pv.y, pv.kvh);
+            for (int t = 0; ok && t < steps; ++t) {
+                if (older.load) ok = load(&vmap, older.page, older.y, older.kvh);
+                older = newer;
                 const bool first_use = !two || (t & 1) == 0;
+                newer.load = first_use;
                 if (ok && first_use) {
                     const int tile = u.tb + (two ? t >> 1 : t);
                     const int page = next_page;
                     if (tile + 1 < u.te) next_page = page_of(u, tile + 1);
                     const int y = (tile << kKeysLog2) & ((1 << s.page_log2) - 1) & ~(box_rows - 1);
                     ok = load(&kmap, page, y, u.kvh);
-                    pv.page = page;
-                    pv.y = y;
-                    pv.kvh = u.kvh;
+                    newer.page = page;
+                    newer.y = y;
+                    newer.kvh = u.kvh;
                 }
-                pv.load = first_use;
                 if (ok && t == 0) {
                     ok = k == 0 || wait(&tl.q_empty, (k - 1) & 1);
                     if (ok) {
@@ -349,57 +355,73 @@ kda_paged_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __
                 }
             }
         }
-        for (int e = 0; ok && e < 2; ++e, ++g)
-            if (pend[g & 1].load) ok = load(&vmap, pend[g & 1].page, pend[g & 1].y, pend[g & 1].kvh);
+        if (ok && older.load) ok = load(&vmap, older.page, older.y, older.kvh);
+        if (ok && newer.load) ok = load(&vmap, newer.page, newer.y, newer.kvh);
     } else if (w == kIssueWarp) {
         // ---------------- products.  All lanes wait, lane 0 issues
         const uint32_t id_s = kda::idesc_bf16(128, 128, 0, 0), id_o = kda::idesc_bf16(128, D, 0, 1);
         const uint64_t q_desc = kda::sw128_desc(kda::smem_u32(sm), 16, 1024);
         const uint64_t k_desc = kda::sw128_desc(kda::smem_u32(sm + C::KV0), 16, 1024);
         const uint64_t v_desc = kda::sw128_desc(kda::smem_u32(sm + C::KV0), kPanel, 1024);
-        int n_p[2] = {0, 0}, g = 0, v_stage = 0, k_stage = 0;
+        int g = 0, v_stage = 0, k_stage = 0;
+        uint32_t p_phase = 0;                          // bit h: parity of the next P_h
         bool issued = false;
-        struct Pending { int valid, first_use, last_use, accumulate, final, tile, slot; Sight si; } pend[2];
-        pend[0].valid = pend[1].valid = 0;
+        // a step whose second product is due: flags, key tile, and what its unit's rows see
+        enum { kFirstUse = 1, kLastUse = 2, kAdd = 4, kFinal = 8, kDue = 16 };
+        struct Pending { int flags, tile, slot, kend; Sight si; };
+        Pending older, newer;                          // of steps g - 2 and g - 1
+        older.flags = newer.flags = 0;
 
-        // values that must not meet a zero weight (see the header); all lanes
-        auto clean = [&](unsigned char* v, int tile, const Sight& si, int slot) {
-            const int k0 = tile << kKeysLog2;
-            if (k0 >= si.all_lo && k0 + kKeys <= si.all_hi) return;
-            constexpr int CH = D / 8;                  // 16-byte chunks of a row
+        // takes the elements that are not finite out of rows [a, b) of a value tile; all lanes
+        constexpr int CH = D / 8, RPI = 32 / CH;       // 16-byte chunks of a row, rows a warp handles at once
+        const int my_row = lane / CH, my_off = ((lane % CH) >> 3) * kPanel + (lane & 7) * 16;
+        auto zero_rows = [&](unsigned char* v, int a, int b) {
+            for (int r = a + my_row; r < b; r += RPI)
+                *reinterpret_cast<uint4*>(v + my_off + r * 128) = make_uint4(0, 0, 0, 0);
+        };
+        auto finite_rows = [&](unsigned char* v, int a, int b) -> int {
             int odd = 0;
-            for (int e = lane; e < kKeys * CH; e += 32) {
-                const int r = e / CH, c = e % CH, key = k0 + r;
-                if (key >= si.all_lo && key < si.all_hi) continue;
-                uint4* p = reinterpret_cast<uint4*>(v + (c >> 3) * kPanel + r * 128 + (c & 7) * 16);
-                uint4 x = make_uint4(0, 0, 0, 0);
-                if (key >= si.lo && key < si.hi) {
-                    x = *p;
-                    uint32_t* u = reinterpret_cast<uint32_t*>(&x);
-                    int found = 0;
+#pragma unroll 4
+            for (int r = a + my_row; r < b; r += RPI) {
+                uint4* p = reinterpret_cast<uint4*>(v + my_off + r * 128);
+                uint4 x = *p;
+                uint32_t* u = reinterpret_cast<uint32_t*>(&x);
+                int found = 0;
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        if ((u[i] & 0x7f80u) == 0x7f80u) { u[i] &= 0xffff0000u; found = 1; }
-                        if ((u[i] & 0x7f800000u) == 0x7f800000u) { u[i] &= 0x0000ffffu; found = 1; }
-                    }
-                    if (!found) continue;
-                    odd = 1;
+                for (int i = 0; i < 4; ++i) {
+                    if ((u[i] & 0x7f80u) == 0x7f80u) { u[i] &= 0xffff0000u; found = 1; }
+                    if ((u[i] & 0x7f800000u) == 0x7f800000u) { u[i] &= 0x0000ffffu; found = 1; }
                 }
-                *p = x;
+                if (found) { *p = x; odd = 1; }
             }
-            if (odd) tl.odd_values[slot] = 1;
+            return odd;
+        };
+        // values that must not meet a zero weight (see the header).  Pages that hold no
+        // key below kend were filled with zeros by the copy
+        auto clean = [&](unsigned char* v, const Pending& pv) {
+            const int k0 = pv.tile << kKeysLog2;
+            const Sight& si = pv.si;
+            if (k0 >= si.all_lo && k0 + kKeys <= si.all_hi) return;
+            const int page = 1 << s.page_log2;
+            auto in = [&](int key) { return min(max(key - k0, 0), kKeys); };
+            const int filled = in((pv.kend + page - 1) & ~(page - 1));
+            zero_rows(v, 0, in(si.lo));
+            zero_rows(v, in(si.hi), filled);
+            const int mid = min(si.all_lo, si.hi);
+            int odd = finite_rows(v, in(si.lo), in(mid));
+            odd |= finite_rows(v, in(max(si.all_hi, mid)), in(si.hi));
+            if (odd) tl.odd_values[pv.slot] = 1;
             kda::fence_proxy_async_smem();
             __syncwarp();
         };
-        auto values_step = [&](int h) -> bool {        // O_h += P_h V
-            Pending& pv = pend[h];
-            if (!wait(&tl.p_full[h], n_p[h] & 1)) return false;
-            ++n_p[h];
-            if (pv.first_use) {
+        auto values_step = [&](int h, const Pending& pv) -> bool {   // O_h += P_h V
+            if (!wait(&tl.p_full[h], (p_phase >> h) & 1)) return false;
+            p_phase ^= 1u << h;
+            if (pv.flags & kFirstUse) {
                 v_stage = n_ld % C::STAGES;
                 if (!wait(&tl.kv_full[v_stage], (n_ld / C::STAGES) & 1)) return false;
                 ++n_ld;
-                clean(sm + C::KV0 + v_stage * C::TILE, pv.tile, pv.si, pv.slot);
+                clean(sm + C::KV0 + v_stage * C::TILE, pv);
             }
             kda::tc_fence_after();
             if (lane == 0) {
@@ -407,12 +429,11 @@ kda_paged_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __
                 const uint32_t d = tmem + C::TMEM_O + h * D, a = tmem + h * 128;
 #pragma unroll
                 for (int i = 0; i < kKeys / 16; ++i)
-                    umma_bf16_ta(d, a + 8 * i, b + kda::desc_step(i * 2048), id_o, i > 0 ? 1u : (uint32_t)pv.accumulate);
-                if (pv.last_use) kda::umma_commit(&tl.kv_empty[v_stage]);
-                if (pv.final) kda::umma_commit(&tl.o_full[h]);
+                    umma_bf16_ta(d, a + 8 * i, b + kda::desc_step(i * 2048), id_o, (i > 0 || (pv.flags & kAdd)) ? 1u : 0u);
+                if (pv.flags & kLastUse) kda::umma_commit(&tl.kv_empty[v_stage]);
+                if (pv.flags & kFinal) kda::umma_commit(&tl.o_full[h]);
             }
             __syncwarp();
-            pv.valid = 0;
             return true;
         };
         bool ok = true;
@@ -424,8 +445,9 @@ kda_paged_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __
             const Sight si = sight(u, s.window, 0, u.ntok - 1);
             for (int t = 0; ok && t < steps; ++t, ++g) {
                 const int h = g & 1;
-                if (pend[h].valid) ok = values_step(h);
+                if (older.flags & kDue) ok = values_step(h, older);
                 if (!ok) break;
+                older = newer;
                 const bool first_use = !two || (t & 1) == 0;
                 if (first_use) {
                     k_stage = n_ld % C::STAGES;
@@ -452,20 +474,17 @@ kda_paged_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __
                 }
                 __syncwarp();
                 issued = true;
-                Pending& pv = pend[h];
-                pv.valid = 1;
-                pv.first_use = first_use;
-                pv.last_use = !two || (t & 1);
-                pv.accumulate = t >= 2;
-                pv.final = t >= steps - 2;
-                pv.tile = u.tb + (two ? t >> 1 : t);
-                pv.slot = k & 3;
-                pv.si = si;
+                newer.flags = kDue | (first_use ? kFirstUse : 0) | (!two || (t & 1) ? kLastUse : 0) | (t >= 2 ? kAdd : 0) |
+                              (t >= steps - 2 ? kFinal : 0);
+                newer.tile = u.tb + (two ? t >> 1 : t);
+                newer.slot = k & 3;
+                newer.kend = u.kend;
+                newer.si = si;
                 if (t == 0 && lane == 0) tl.odd_values[k & 3] = 0;
             }
         }
-        for (int e = 0; ok && e < 2; ++e, ++g)
-            if (pend[g & 1].valid) ok = values_step(g & 1);
+        if (ok && (older.flags & kDue)) ok = values_step(g & 1, older);
+        if (ok && (newer.flags & kDue)) ok = values_step((g + 1) & 1, newer);
         if (issued) {                                  // no product in flight when TMEM is freed
             if (lane == 0) kda::umma_commit(&tl.drain);
             __syncwarp();
@@ -480,7 +499,8 @@ kda_paged_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __
         const int tok_in = row / s.Gv, head_in = row % s.Gv;
         const int pieces = s.page_log2 >= kKeysLog2 ? 1 : kKeys >> s.page_log2;
         const int piece_log2 = min(s.page_log2, kKeysLog2);
-        int n_s = 0, n_o[2] = {0, 0}, n_j = 0, g = 0;
+        int n_s = 0, n_j = 0, g = 0;
+        uint32_t o_phase = 0;                          // bit h: parity of the next O_h
         bool ok = true;
         for (int k = 0; ok; ++k) {
             Unit u;
@@ -617,9 +637,8 @@ kda_paged_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __
                 }
             };
             if (two) {
-                ok = wait(&tl.o_full[h], n_o[h] & 1);
-                ++n_o[0];
-                ++n_o[1];
+                ok = wait(&tl.o_full[h], (o_phase >> h) & 1);
+                o_phase ^= 3;
                 if (!ok) break;
                 kda::tc_fence_after();
                 if (busy) {
@@ -639,10 +658,11 @@ kda_paged_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __
                 __syncwarp();
                 if (lane == 0) kda::mbar_arrive(&tl.join_a);
                 ok = wait(&tl.join_a, n_j & 1);
+#pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     if (!has[e]) continue;
-                    ok = ok && wait(&tl.o_full[e], n_o[e] & 1);
-                    ++n_o[e];
+                    ok = ok && wait(&tl.o_full[e], (o_phase >> e) & 1);
+                    o_phase ^= 1u << e;
                 }
                 if (!ok) break;
                 kda::tc_fence_after();
@@ -742,7 +762,10 @@ cudaError_t launch_tc(const kda_host::PagedArgs& a) {
     if (!make_q_map(&qm, a, p.Gv, BT) || !make_cache_map(&km, a.k_cache, a) || !make_cache_map(&vm, a.v_cache, a))
         return cudaErrorInvalidValue;
     auto kern = kda_paged_attention_tc_kernel<D>;
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::SMEM);
+    static kda_host::OncePerDevice once;
+    const cudaError_t e = once.run([&] {
+        return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::SMEM);
+    });
     if (e != cudaSuccess) return e;
     const int ctas = std::min(p.max_ctas, kda_host::sm_count());
     kern<<<ctas, kThreads, Cfg<D>::SMEM, a.stream>>>(

@@ -228,8 +228,11 @@ cudaError_t launch_build_tables(const TablesArgs& a) {
     const size_t smem = ((size_t)3 * a.N + 2) * sizeof(int);
     static_assert(((size_t)3 * kMaxRequests + 2) * sizeof(int) <= 100 * 1024, "shared memory of the running sums");
     if (smem > 47 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(kda_build_tables_kernel,
-                                                   cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        static OncePerDevice once;
+        const cudaError_t e = once.run([] {
+            return cudaFuncSetAttribute(kda_build_tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                        (int)(((size_t)3 * kMaxRequests + 2) * sizeof(int)));
+        });
         if (e != cudaSuccess) return e;
     }
     const long long work = std::max<long long>(((long long)a.n_tokens + kTokensPerThread - 1) / kTokensPerThread, 1);

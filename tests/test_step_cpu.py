@@ -182,7 +182,7 @@ def test_binding_attention():
 def test_binding_strided_rows():
     from kimi_delta_attention_chunked_gb300 import _paged
     t = torch.zeros(5, 12, 32)
-    cpu = torch.device("cpu")
+    cpu = -1                                                   # get_device() of a CPU tensor
     ptr, stride = _paged._rows("q", t[:, 4:8], cpu, torch.float32, (5, 4, 32))
     assert ptr == t.data_ptr() + 4 * 32 * 4 and stride == 12 * 32
     with pytest.raises(ValueError, match="contiguous"):
