@@ -116,52 +116,51 @@ __device__ __forceinline__ unsigned long long mul_div(unsigned long long x, unsi
     return x * y / z;
 }
 
-// A few requests: one warp finds the piece by itself, `kPerLane` consecutive
-// requests a lane.  No shared memory and no barrier, so the rest of the block
-// can set up meanwhile.
-constexpr int kPerLane = 8;
-constexpr int kWarpRequests = 32 * kPerLane;
+// A few requests: one warp finds the piece by itself, 32 requests at a time.  No
+// shared memory and no barrier, so the rest of the block can set up meanwhile.
+// The counting is one function, not inlined: a short call spends much of its time
+// on fetching instructions.
+constexpr int kWarpRequests = 256;
+static __device__ __noinline__ unsigned long long count_tiles(const Shape* s, const int32_t* cu, const int32_t* seq_len, int n) {
+    return request_tiles(*s, cu, seq_len, n, n < s->n_req);
+}
 __device__ __forceinline__ Piece find_piece_warp(const Shape& s, const int32_t* __restrict__ cu,
                                                  const int32_t* __restrict__ seq_len, int c, int C) {
-    const int lane = threadIdx.x & 31, per = (s.n_req + 31) / 32;
-    unsigned long long cost[kPerLane], mine = 0;
-#pragma unroll
-    for (int i = 0; i < kPerLane; ++i) {
-        cost[i] = 0;
-        if (i < per) cost[i] = request_tiles(s, cu, seq_len, lane * per + i, lane * per + i < s.n_req) * (unsigned)s.Hv;
-        mine += cost[i];
-    }
-    unsigned long long incl = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const unsigned long long t = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += t;
-    }
+    const int lane = threadIdx.x & 31;
     Piece p{0, 0, 0, 0, 0, 0, 0};
-    p.total = __shfl_sync(0xffffffffu, incl, 31);
+    unsigned long long x = 0, sum = 0;
+#pragma unroll 1
+    for (int base = 0; base < s.n_req; base += 32) {
+        x = count_tiles(&s, cu, seq_len, base + lane);
+        sum += x;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    p.total = sum * (unsigned)s.Hv;
     p.ctas = (int)min((unsigned long long)C, p.total);
     if (c >= p.ctas) return p;
     p.begin = mul_div(p.total, (unsigned)c, (unsigned)p.ctas);
     p.end = mul_div(p.total, (unsigned)(c + 1), (unsigned)p.ctas);
-    // the lane whose requests hold tile `begin`, and the request among them
-    const int src = __ffs((int)__ballot_sync(0xffffffffu, p.begin < incl)) - 1;
-    unsigned long long at = incl - mine, tiles = 0;
-    int n = lane * per;
-    bool found = false;
+    unsigned long long at = 0;
+#pragma unroll 1
+    for (int base = 0; base < s.n_req; base += 32) {
+        if (s.n_req > 32) x = count_tiles(&s, cu, seq_len, base + lane);
+        unsigned long long incl = x * (unsigned)s.Hv;
 #pragma unroll
-    for (int i = 0; i < kPerLane; ++i) {
-        if (found || i >= per) continue;
-        if (p.begin < at + cost[i]) {
-            found = true;
-            tiles = cost[i];
-            n = lane * per + i;
-        } else {
-            at += cost[i];
+        for (int o = 1; o < 32; o <<= 1) {
+            const unsigned long long t = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += t;
         }
+        const unsigned hit = __ballot_sync(0xffffffffu, p.begin < at + incl);
+        if (hit) {
+            const int src = __ffs((int)hit) - 1;
+            p.n = base + src;
+            p.tiles = __shfl_sync(0xffffffffu, x, src);
+            p.off = p.begin - at - (__shfl_sync(0xffffffffu, incl, src) - p.tiles * (unsigned)s.Hv);
+            break;
+        }
+        at += __shfl_sync(0xffffffffu, incl, 31);
     }
-    p.n = __shfl_sync(0xffffffffu, n, src);
-    p.off = p.begin - __shfl_sync(0xffffffffu, at, src);
-    p.tiles = __shfl_sync(0xffffffffu, tiles, src) / (unsigned)s.Hv;
     return p;
 }
 

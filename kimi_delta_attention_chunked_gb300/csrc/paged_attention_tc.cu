@@ -127,6 +127,19 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* u) {
         : "memory");
 }
 
+// One lane of the (converged) warp.  Unlike `lane == 0`, the compiler keeps what
+// is the same for the whole warp in uniform registers across this branch, where
+// the operands of tcgen05.mma have to be.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(p));
+    return p != 0;
+}
+
 __device__ __forceinline__ float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -424,7 +437,7 @@ kda_paged_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __
                 clean(sm + C::KV0 + v_stage * C::TILE, pv);
             }
             kda::tc_fence_after();
-            if (lane == 0) {
+            if (elect_one()) {
                 const uint64_t b = v_desc + kda::desc_step(v_stage * C::TILE);
                 const uint32_t d = tmem + C::TMEM_O + h * D, a = tmem + h * 128;
 #pragma unroll
@@ -460,7 +473,7 @@ kda_paged_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __
                     if (!ok) break;
                 }
                 kda::tc_fence_after();
-                if (lane == 0) {                       // S_h = Q K^T
+                if (elect_one()) {                     // S_h = Q K^T
                     const uint64_t a = q_desc + kda::desc_step((two && (t & 1)) ? C::TILE : 0);
                     const uint64_t b = k_desc + kda::desc_step(k_stage * C::TILE);
 #pragma unroll
@@ -486,7 +499,7 @@ kda_paged_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __
         if (ok && (older.flags & kDue)) ok = values_step(g & 1, older);
         if (ok && (newer.flags & kDue)) ok = values_step((g + 1) & 1, newer);
         if (issued) {                                  // no product in flight when TMEM is freed
-            if (lane == 0) kda::umma_commit(&tl.drain);
+            if (elect_one()) kda::umma_commit(&tl.drain);
             __syncwarp();
             (void)kda::mbar_wait(&tl.drain, 0, kda::kWaitCycles);
         }
@@ -530,24 +543,29 @@ kda_paged_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __
                 ++n_s;
                 kda::tc_fence_after();
                 if (busy) {
+                    if (k0 < mine.all_lo || k0 + kKeys > mine.all_hi || missing) {
+                        // scores of keys this row does not see become -inf, in place.  Rolled: these
+                        // tiles are few, and a short call's time goes into fetching instructions
+#pragma unroll 1
+                        for (int c = 0; c < kKeys; c += 32) {
+                            const int a = max(lo - k0 - c, 0), b = hi - k0 - c;
+                            uint32_t seen = a >= 32 || b <= a ? 0u : 0xffffffffu << a;
+                            if (b < 32) seen &= (1u << max(b, 0)) - 1u;
+                            if ((missing >> (c >> piece_log2)) & 1) seen &= piece_log2 == 4 ? 0xffff0000u : 0u;
+                            if (piece_log2 == 4 && ((missing >> ((c >> 4) + 1)) & 1)) seen &= 0x0000ffffu;
+                            float y[32];
+                            kda::tmem_ld32(tS + c, y);
+                            kda::tmem_wait_ld();
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) y[e] = (seen >> e) & 1 ? y[e] : -INFINITY;
+                            tmem_st32(tS + c, reinterpret_cast<const uint32_t*>(y));
+                        }
+                        kda::tmem_wait_st();
+                    }
                     float x[128];
 #pragma unroll
                     for (int c = 0; c < 128; c += 32) kda::tmem_ld32(tS + c, x + c);
                     kda::tmem_wait_ld();
-                    if (k0 < mine.all_lo || k0 + kKeys > mine.all_hi || missing) {
-                        const int a = lo - k0, b = hi - k0;
-#pragma unroll
-                        for (int c = 0; c < 128; ++c)
-                            if (c < a || c >= b) x[c] = -INFINITY;
-                        if (missing) {
-#pragma unroll
-                            for (int c = 0; c < 128; c += 16)
-                                if ((missing >> (c >> piece_log2)) & 1) {
-#pragma unroll
-                                    for (int e = 0; e < 16; ++e) x[c + e] = -INFINITY;
-                                }
-                        }
-                    }
                     float top[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
                     for (int c = 4; c < 128; c += 4)
@@ -562,7 +580,7 @@ kda_paged_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __
                         if (__any_sync(0xffffffffu, grow)) {
                             const float f = grow ? ex2((m - big) * scale_log2) : 1.f;
                             const uint32_t tO = tmem + lane_off + C::TMEM_O + h * D;
-#pragma unroll
+#pragma unroll 1
                             for (int c = 0; c < D; c += 16) {
                                 float y[16];
                                 kda::tmem_ld16(tO + c, y);
