@@ -140,6 +140,9 @@ __device__ __forceinline__ bool elect_one() {
     return p != 0;
 }
 
+// A value that is the same in all lanes, in a form the compiler knows to be so.
+__device__ __forceinline__ int uniform(int x) { return __reduce_max_sync(0xffffffffu, x); }
+
 __device__ __forceinline__ float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -258,7 +261,7 @@ kda_paged_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __
     kda::tc_fence_before();
     __syncthreads();
     kda::tc_fence_after();
-    const uint32_t tmem = tl.tmem;
+    const uint32_t tmem = (uint32_t)uniform((int)tl.tmem);
     volatile int* abort_f = &tl.abort;
     // true once the phase is complete; false when this CTA gives up.  Called by all
     // lanes of a warp, with one answer for all of them, so that none leaves a loop alone
@@ -377,6 +380,14 @@ kda_paged_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __
         const uint64_t k_desc = kda::sw128_desc(kda::smem_u32(sm + C::KV0), 16, 1024);
         const uint64_t v_desc = kda::sw128_desc(kda::smem_u32(sm + C::KV0), kPanel, 1024);
         int g = 0, v_stage = 0, k_stage = 0;
+        int stage = 0;                                 // next stage of the ring, and its parity
+        uint32_t ring = 0;
+        auto take_stage = [&](int& at) -> bool {
+            at = stage;
+            if (!wait(&tl.kv_full[stage], ring)) return false;
+            if (++stage == C::STAGES) { stage = 0; ring ^= 1; }
+            return true;
+        };
         uint32_t p_phase = 0;                          // bit h: parity of the next P_h
         bool issued = false;
         // a step whose second product is due: flags, key tile, and what its unit's rows see
@@ -427,25 +438,42 @@ kda_paged_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __
             kda::fence_proxy_async_smem();
             __syncwarp();
         };
-        auto values_step = [&](int h, const Pending& pv) -> bool {   // O_h += P_h V
+        // the values of a step are there and clean
+        auto take_values = [&](const Pending& pv) -> bool {
+            if (!(pv.flags & kFirstUse)) return true;
+            if (!take_stage(v_stage)) return false;
+            clean(sm + C::KV0 + v_stage * C::TILE, pv);
+            return true;
+        };
+        auto take_weights = [&](int h) -> bool {
             if (!wait(&tl.p_full[h], (p_phase >> h) & 1)) return false;
             p_phase ^= 1u << h;
-            if (pv.flags & kFirstUse) {
-                v_stage = n_ld % C::STAGES;
-                if (!wait(&tl.kv_full[v_stage], (n_ld / C::STAGES) & 1)) return false;
-                ++n_ld;
-                clean(sm + C::KV0 + v_stage * C::TILE, pv);
-            }
-            kda::tc_fence_after();
-            if (elect_one()) {
-                const uint64_t b = v_desc + kda::desc_step(v_stage * C::TILE);
-                const uint32_t d = tmem + C::TMEM_O + h * D, a = tmem + h * 128;
+            return true;
+        };
+        auto issue_values = [&](int h, int flags) {    // O_h += P_h V; one lane
+            const uint64_t b = v_desc + kda::desc_step(v_stage * C::TILE);
+            const uint32_t d = tmem + C::TMEM_O + h * D, a = tmem + h * 128;
 #pragma unroll
-                for (int i = 0; i < kKeys / 16; ++i)
-                    umma_bf16_ta(d, a + 8 * i, b + kda::desc_step(i * 2048), id_o, (i > 0 || (pv.flags & kAdd)) ? 1u : 0u);
-                if (pv.flags & kLastUse) kda::umma_commit(&tl.kv_empty[v_stage]);
-                if (pv.flags & kFinal) kda::umma_commit(&tl.o_full[h]);
+            for (int i = 0; i < kKeys / 16; ++i)
+                umma_bf16_ta(d, a + 8 * i, b + kda::desc_step(i * 2048), id_o, (i > 0 || (flags & kAdd)) ? 1u : 0u);
+            if (flags & kLastUse) kda::umma_commit(&tl.kv_empty[v_stage]);
+            if (flags & kFinal) kda::umma_commit(&tl.o_full[h]);
+        };
+        auto issue_scores = [&](int h, int tile, int flags) {        // S_h = Q_tile K^T; one lane
+            const uint64_t a = q_desc + kda::desc_step(tile * C::TILE), b = k_desc + kda::desc_step(k_stage * C::TILE);
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i) {
+                const uint64_t at = kda::desc_step((i >> 2) * kPanel + (i & 3) * 32);
+                kda::umma_bf16(tmem + h * 128, a + at, b + at, id_s, i > 0 ? 1u : 0u);
             }
+            kda::umma_commit(&tl.s_full[h]);
+            if (flags & kLastUse) kda::umma_commit(&tl.kv_empty[k_stage]);
+            if (flags & kFinal) kda::umma_commit(&tl.q_empty);
+        };
+        auto values_step = [&](int h, const Pending& pv) -> bool {
+            if (!take_values(pv) || !take_weights(h)) return false;
+            kda::tc_fence_after();
+            if (elect_one()) issue_values(h, pv.flags);
             __syncwarp();
             return true;
         };
@@ -453,48 +481,63 @@ kda_paged_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __
         for (int k = 0; ok; ++k) {
             Unit u;
             if (!read_unit(k, u)) break;
-            const bool two = u.ntok > BT;
-            const int steps = (u.te - u.tb) << (two ? 1 : 0);
+            const int two = uniform(u.ntok > BT), tiles = uniform(u.te - u.tb), steps = tiles << two, tb = uniform(u.tb);
             const Sight si = sight(u, s.window, 0, u.ntok - 1);
-            for (int t = 0; ok && t < steps; ++t, ++g) {
+            auto due_after = [&](int t) {              // the second product of step t
+                Pending pv;
+                const int lone = !two || (t & 1);
+                pv.flags = kDue | (!two || !(t & 1) ? kFirstUse : 0) | (lone ? kLastUse : 0) | (t >= 2 ? kAdd : 0) |
+                           (t >= steps - 2 ? kFinal : 0);
+                pv.tile = tb + (t >> two);
+                pv.slot = k & 3;
+                pv.kend = u.kend;
+                pv.si = si;
+                return pv;
+            };
+            if (lane == 0) tl.odd_values[k & 3] = 0;
+            // a unit of two row tiles past its first key tile goes through the loop below this one
+            const int slow = two ? 2 : steps;
+            for (int t = 0; t < slow; ++t, ++g) {
                 const int h = g & 1;
                 if (older.flags & kDue) ok = values_step(h, older);
+                if (ok && (!two || t == 0)) ok = take_stage(k_stage);
+                if (ok && t == 0) ok = wait(&tl.q_full, k & 1);
                 if (!ok) break;
-                older = newer;
-                const bool first_use = !two || (t & 1) == 0;
-                if (first_use) {
-                    k_stage = n_ld % C::STAGES;
-                    ok = wait(&tl.kv_full[k_stage], (n_ld / C::STAGES) & 1);
-                    if (!ok) break;
-                    ++n_ld;
-                }
-                if (t == 0) {
-                    ok = wait(&tl.q_full, k & 1);
-                    if (!ok) break;
-                }
                 kda::tc_fence_after();
-                if (elect_one()) {                     // S_h = Q K^T
-                    const uint64_t a = q_desc + kda::desc_step((two && (t & 1)) ? C::TILE : 0);
-                    const uint64_t b = k_desc + kda::desc_step(k_stage * C::TILE);
-#pragma unroll
-                    for (int i = 0; i < D / 16; ++i) {
-                        const uint64_t at = kda::desc_step((i >> 2) * kPanel + (i & 3) * 32);
-                        kda::umma_bf16(tmem + h * 128, a + at, b + at, id_s, i > 0 ? 1u : 0u);
-                    }
-                    kda::umma_commit(&tl.s_full[h]);
-                    if (!two || (t & 1)) kda::umma_commit(&tl.kv_empty[k_stage]);
-                    if (t == steps - 1) kda::umma_commit(&tl.q_empty);
-                }
+                if (elect_one())
+                    issue_scores(h, two & t, (!two || t == 1 ? kLastUse : 0) | (t == steps - 1 ? kFinal : 0));
                 __syncwarp();
                 issued = true;
-                newer.flags = kDue | (first_use ? kFirstUse : 0) | (!two || (t & 1) ? kLastUse : 0) | (t >= 2 ? kAdd : 0) |
-                              (t >= steps - 2 ? kFinal : 0);
-                newer.tile = u.tb + (two ? t >> 1 : t);
-                newer.slot = k & 3;
-                newer.kend = u.kend;
-                newer.si = si;
-                if (t == 0 && lane == 0) tl.odd_values[k & 3] = 0;
+                older = newer;
+                newer = due_after(t);
             }
+            if (!ok || slow == steps) continue;
+            // the tensor cores' time is here: as few instructions between products as can be
+            const int h0 = g & 1, h1 = h0 ^ 1;
+            Pending pv = older;                        // values of the tile before
+            for (int j = 1; j < tiles; ++j) {
+                pv.tile = tb + j - 1;
+                pv.flags = kDue | kFirstUse;
+                ok = take_values(pv) && take_weights(h0);
+                if (!ok) break;
+                kda::tc_fence_after();
+                const int add = j > 1 ? kAdd : 0;
+                if (elect_one()) issue_values(h0, add);
+                ok = take_stage(k_stage);
+                if (!ok) break;
+                if (elect_one()) issue_scores(h0, 0, 0);
+                ok = take_weights(h1);
+                if (!ok) break;
+                kda::tc_fence_after();
+                if (elect_one()) {
+                    issue_values(h1, add | kLastUse);
+                    issue_scores(h1, 1, kLastUse | (j == tiles - 1 ? kFinal : 0));
+                }
+            }
+            __syncwarp();
+            g += steps - 2;
+            older = due_after(steps - 2);
+            newer = due_after(steps - 1);
         }
         if (ok && (older.flags & kDue)) ok = values_step(g & 1, older);
         if (ok && (newer.flags & kDue)) ok = values_step((g + 1) & 1, newer);
