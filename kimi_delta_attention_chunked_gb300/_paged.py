@@ -22,7 +22,7 @@ _I32, _I64, _F32 = torch.int32, torch.int64, torch.float32
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _call(entry, idx, stream, args):
+def _call(entry, idx, stream, *args):
     """Calls C entry ``entry`` on ``stream`` with device ``idx`` current; raises on an error code."""
     fn = getattr(_lib._lib or _lib.load(), entry)
     if stream is None:
@@ -57,9 +57,18 @@ def _refuse(name, t, idx, dtype, shape):
 
 
 def _need(name, t, idx, dtype, shape):
+    """Pointer of a contiguous tensor of that dtype and shape on that device."""
     if t.shape != shape or t.dtype != dtype or t.get_device() != idx or not t.is_contiguous():
         _refuse(name, t, idx, dtype, shape)
     return t.data_ptr()
+
+
+def _out(name, t, like, idx, dtype, shape):
+    """The caller's output tensor, checked, or a new one: (tensor, pointer)."""
+    if t is None:
+        t = torch.empty(shape, dtype=dtype, device=like.device)
+        return t, t.data_ptr()
+    return t, _need(name, t, idx, dtype, shape)
 
 
 def _rows(name, t, idx, dtype, shape):
@@ -98,25 +107,16 @@ def kda_build_block_tables(ctx_len, new_len, free_pages, block_table, page_size,
     if new_len.shape != ctx_len.shape:
         raise ValueError(f"new_len must have shape {(n,)}, got {tuple(new_len.shape)}")
     dev = _device("ctx_len", ctx_len)
-    new = lambda shape, dt: torch.empty(shape, dtype=dt, device=ctx_len.device)  # noqa: E731
     n_tokens = int(n_tokens)
-    if cu_seqlens is None:
-        cu_seqlens = new(n + 1, _I32)
-    if seq_len is None:
-        seq_len = new(n, _I32)
-    if slot_map is None:
-        slot_map = new(n_tokens, _I64)
-    if positions is None:
-        positions = new(n_tokens, _I32)
-    if n_taken is None:
-        n_taken = new(1, _I32)
-    args = (_need("ctx_len", ctx_len, dev, _I32, (n,)), _need("new_len", new_len, dev, _I32, (n,)),
-            _need("free_pages", free_pages, dev, _I32, (n_free,)), n_free, n, blocks, int(page_size), n_tokens,
-            _need("block_table", block_table, dev, _I32, (n, blocks)),
-            _need("cu_seqlens", cu_seqlens, dev, _I32, (n + 1,)), _need("seq_len", seq_len, dev, _I32, (n,)),
-            _need("slot_map", slot_map, dev, _I64, (n_tokens,)),
-            _need("positions", positions, dev, _I32, (n_tokens,)), _need("n_taken", n_taken, dev, _I32, (1,)))
-    _call("kda_build_block_tables", dev, stream, args)
+    cu_seqlens, cu_ptr = _out("cu_seqlens", cu_seqlens, ctx_len, dev, _I32, (n + 1,))
+    seq_len, seq_ptr = _out("seq_len", seq_len, ctx_len, dev, _I32, (n,))
+    slot_map, slot_ptr = _out("slot_map", slot_map, ctx_len, dev, _I64, (n_tokens,))
+    positions, pos_ptr = _out("positions", positions, ctx_len, dev, _I32, (n_tokens,))
+    n_taken, taken_ptr = _out("n_taken", n_taken, ctx_len, dev, _I32, (1,))
+    _call("kda_build_block_tables", dev, stream, _need("ctx_len", ctx_len, dev, _I32, (n,)),
+          _need("new_len", new_len, dev, _I32, (n,)), _need("free_pages", free_pages, dev, _I32, (n_free,)), n_free, n,
+          blocks, page_size, n_tokens, _need("block_table", block_table, dev, _I32, (n, blocks)), cu_ptr, seq_ptr,
+          slot_ptr, pos_ptr, taken_ptr)
     return cu_seqlens, seq_len, slot_map, positions, n_taken
 
 
@@ -136,14 +136,16 @@ def kda_cache_append(k, v, k_cache, v_cache, slot_map, stream=None):
         raise ValueError(f"k must have 3 dims, got {k.dim()}")
     rows = (k.shape[0], heads, d)
     code, dt = _code(k_cache), k_cache.dtype
-    if k.shape != rows or v.shape != rows:
+    if k.shape != rows:
+        raise ValueError(f"k and v must have shape {rows}, got {tuple(k.shape)} and {tuple(v.shape)}")
+    if v.shape != rows:
         raise ValueError(f"k and v must have shape {rows}, got {tuple(k.shape)} and {tuple(v.shape)}")
     dev = _device("k_cache", k_cache)
     kp, ks = _rows("k", k, dev, dt, rows)
     vp, vs = _rows("v", v, dev, dt, rows)
-    args = (kp, vp, _need("slot_map", slot_map, dev, _I64, (rows[0],)), ks, vs, rows[0], heads, d, page, n_pages, code,
-            _need("k_cache", k_cache, dev, dt, shape), _need("v_cache", v_cache, dev, dt, shape))
-    _call("kda_cache_append", dev, stream, args)
+    _call("kda_cache_append", dev, stream, kp, vp, _need("slot_map", slot_map, dev, _I64, (rows[0],)), ks, vs, rows[0],
+          heads, d, page, n_pages, code, _need("k_cache", k_cache, dev, dt, shape),
+          _need("v_cache", v_cache, dev, dt, shape))
 
 
 @functools.lru_cache(maxsize=256)
@@ -181,21 +183,22 @@ def kda_paged_attention(q, k_cache, v_cache, block_table, cu_seqlens, seq_len, s
         raise ValueError(f"lse must have shape {tuple(rows[:2])}, got {tuple(lse.shape)}")
     dev = _device("q", q)
     qp, qs = _rows("q", q, dev, dt, rows)
-    if o is None:
-        o = torch.empty(rows, dtype=dt, device=q.device)
-    if lse is None and want_lse:
-        lse = torch.empty(rows[:2], dtype=_F32, device=q.device)
+    k_ptr, v_ptr = _need("k_cache", k_cache, dev, dt, shape), _need("v_cache", v_cache, dev, dt, shape)
+    table = _need("block_table", block_table, dev, _I32, (n, blocks))
+    cu, seq = _need("cu_seqlens", cu_seqlens, dev, _I32, (n + 1,)), _need("seq_len", seq_len, dev, _I32, (n,))
+    o, o_ptr = _out("o", o, q, dev, dt, rows)
+    lse_ptr = None
+    if lse is not None or want_lse:
+        lse, lse_ptr = _out("lse", lse, q, dev, _F32, rows[:2])
     if workspace is None:
-        workspace = torch.empty(_workspace_size(T, heads, kv_heads, d, code), dtype=torch.uint8, device=q.device)
+        size = _workspace_size(T, heads, kv_heads, d, code)
+        workspace = torch.empty(size, dtype=torch.uint8, device=q.device)
     elif workspace.get_device() != dev or not workspace.is_contiguous():
         raise ValueError(f"workspace must be contiguous and on cuda:{dev}")
-    args = (qp, _need("k_cache", k_cache, dev, dt, shape), _need("v_cache", v_cache, dev, dt, shape),
-            _need("block_table", block_table, dev, _I32, (n, blocks)),
-            _need("cu_seqlens", cu_seqlens, dev, _I32, (n + 1,)), _need("seq_len", seq_len, dev, _I32, (n,)), qs, n, T,
-            heads, kv_heads, d, page, blocks, n_pages, d ** -0.5 if scale is None else scale, window, code,
-            _need("o", o, dev, dt, rows), None if lse is None else _need("lse", lse, dev, _F32, rows[:2]),
-            workspace.data_ptr(), workspace.numel() * workspace.element_size())
-    _call("kda_paged_attention", dev, stream, args)
+    else:
+        size = workspace.numel() * workspace.element_size()
+    _call("kda_paged_attention", dev, stream, qp, k_ptr, v_ptr, table, cu, seq, qs, n, T, heads, kv_heads, d, page, blocks,
+          n_pages, d ** -0.5 if scale is None else scale, window, code, o_ptr, lse_ptr, workspace.data_ptr(), size)
     return o if lse is None else (o, lse)
 
 
@@ -216,14 +219,11 @@ def kda_verify_draft(target, draft, draft_tokens, uniforms, draft_len=None, toke
         raise ValueError(f"uniforms must have shape {(n, k + 1)}, got {tuple(uniforms.shape)}")
     code, dt = _code(target), target.dtype
     dev = _device("target", target)
-    if tokens is None:
-        tokens = torch.empty((n, k + 1), dtype=_I32, device=target.device)
-    if commit_len is None:
-        commit_len = torch.empty((n,), dtype=_I32, device=target.device)
-    args = (_need("target", target, dev, dt, (n, k + 1, vocab)),
+    ptrs = (_need("target", target, dev, dt, (n, k + 1, vocab)),
             None if draft is None else _need("draft", draft, dev, dt, (n, k, vocab)),
             _need("draft_tokens", draft_tokens, dev, _I32, (n, k)), _need("uniforms", uniforms, dev, _F32, (n, k + 1)),
-            None if draft_len is None else _need("draft_len", draft_len, dev, _I32, (n,)), n, k, vocab, code,
-            _need("tokens", tokens, dev, _I32, (n, k + 1)), _need("commit_len", commit_len, dev, _I32, (n,)))
-    _call("kda_verify_draft", dev, stream, args)
+            None if draft_len is None else _need("draft_len", draft_len, dev, _I32, (n,)))
+    tokens, tokens_ptr = _out("tokens", tokens, target, dev, _I32, (n, k + 1))
+    commit_len, commit_ptr = _out("commit_len", commit_len, target, dev, _I32, (n,))
+    _call("kda_verify_draft", dev, stream, *ptrs, n, k, vocab, code, tokens_ptr, commit_ptr)
     return tokens, commit_len

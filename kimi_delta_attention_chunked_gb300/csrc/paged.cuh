@@ -26,6 +26,7 @@ struct Shape {
     int Hq, Hkv, Hv, Gv, sub;                      // Hv = Hkv * sub groups of Gv query heads
     int blocks, page_log2, n_pages, window;
     int U, tile_log2;                              // tokens per unit, keys per tile
+    int narrow;                                    // few requests and tiles: see Walker::start_narrow
 };
 
 // One request's lengths, inside the buffers whatever the device arrays hold.
@@ -64,13 +65,11 @@ __device__ __forceinline__ void unit_span(const Shape& s, const Req& r, int i, i
 
 // Tiles of all units of a request, for one head.  A thread counts a request of
 // few units by itself; the lanes of a warp share out one of many.
-__device__ __forceinline__ unsigned long long request_tiles(const Shape& s, const int32_t* __restrict__ cu,
-                                                            const int32_t* __restrict__ seq_len, int n, bool valid) {
+template <typename I>
+__device__ __forceinline__ I request_tiles(const Shape& s, const Req& r) {
     constexpr int kAlone = 8;
-    Req r{0, 0, 0, 0};
-    if (valid) r = load_req(s, cu, seq_len, n);
     const int units = n_units(s, r);
-    unsigned long long cost = 0;
+    I cost = 0;
     if (units <= kAlone) {
         for (int i = 0; i < units; ++i) {
             int tb, te;
@@ -88,7 +87,7 @@ __device__ __forceinline__ unsigned long long request_tiles(const Shape& s, cons
         q.pos0 = __shfl_sync(0xffffffffu, r.pos0, src);
         q.kend = __shfl_sync(0xffffffffu, r.kend, src);
         const int total = n_units(s, q);
-        unsigned long long part = 0;
+        I part = 0;
         for (int i = threadIdx.x & 31; i < total; i += 32) {
             int tb, te;
             unit_span(s, q, i, tb, te);
@@ -109,61 +108,6 @@ struct Piece {
     int n, ctas;                                   // first request; CTAs that have a piece
 };
 
-// x * y / z; a 64-bit division takes several times the cycles of a 32-bit one,
-// and all but the longest calls stay below its limit.
-__device__ __forceinline__ unsigned long long mul_div(unsigned long long x, unsigned y, unsigned z) {
-    if (x < (1u << 22) && y <= (unsigned)kMaxCtas) return (unsigned)x * y / z;
-    return x * y / z;
-}
-
-// A few requests: one warp finds the piece by itself, 32 requests at a time.  No
-// shared memory and no barrier, so the rest of the block can set up meanwhile.
-// The counting is one function, not inlined: a short call spends much of its time
-// on fetching instructions.
-constexpr int kWarpRequests = 256;
-static __device__ __noinline__ unsigned long long count_tiles(const Shape* s, const int32_t* cu, const int32_t* seq_len, int n) {
-    return request_tiles(*s, cu, seq_len, n, n < s->n_req);
-}
-__device__ __forceinline__ Piece find_piece_warp(const Shape& s, const int32_t* __restrict__ cu,
-                                                 const int32_t* __restrict__ seq_len, int c, int C) {
-    const int lane = threadIdx.x & 31;
-    Piece p{0, 0, 0, 0, 0, 0, 0};
-    unsigned long long x = 0, sum = 0;
-#pragma unroll 1
-    for (int base = 0; base < s.n_req; base += 32) {
-        x = count_tiles(&s, cu, seq_len, base + lane);
-        sum += x;
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    p.total = sum * (unsigned)s.Hv;
-    p.ctas = (int)min((unsigned long long)C, p.total);
-    if (c >= p.ctas) return p;
-    p.begin = mul_div(p.total, (unsigned)c, (unsigned)p.ctas);
-    p.end = mul_div(p.total, (unsigned)(c + 1), (unsigned)p.ctas);
-    unsigned long long at = 0;
-#pragma unroll 1
-    for (int base = 0; base < s.n_req; base += 32) {
-        if (s.n_req > 32) x = count_tiles(&s, cu, seq_len, base + lane);
-        unsigned long long incl = x * (unsigned)s.Hv;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const unsigned long long t = __shfl_up_sync(0xffffffffu, incl, o);
-            if (lane >= o) incl += t;
-        }
-        const unsigned hit = __ballot_sync(0xffffffffu, p.begin < at + incl);
-        if (hit) {
-            const int src = __ffs((int)hit) - 1;
-            p.n = base + src;
-            p.tiles = __shfl_sync(0xffffffffu, x, src);
-            p.off = p.begin - at - (__shfl_sync(0xffffffffu, incl, src) - p.tiles * (unsigned)s.Hv);
-            break;
-        }
-        at += __shfl_sync(0xffffffffu, incl, 31);
-    }
-    return p;
-}
-
 // Finds the piece of CTA `c` of `C`.  Every thread of the block (NT of them)
 // calls it; `cost` holds n_req words and `red` NT / 32, of 64 bits, and free again after the block's next barrier.
 template <int NT>
@@ -175,7 +119,9 @@ __device__ __forceinline__ Piece find_piece(const Shape& s, const int32_t* __res
     const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
     for (int base = 0; base < s.n_req; base += NT) {
         const int n = base + tid;
-        const unsigned long long x = request_tiles(s, cu, seq_len, n, n < s.n_req);
+        Req r{0, 0, 0, 0};
+        if (n < s.n_req) r = load_req(s, cu, seq_len, n);
+        const unsigned long long x = request_tiles<unsigned long long>(s, r);
         if (n < s.n_req) cost[n] = x;
     }
     if (tid == 0) *shared = Piece{0, 0, 0, 0, 0, 0, 0};
@@ -203,7 +149,7 @@ __device__ __forceinline__ Piece find_piece(const Shape& s, const int32_t* __res
     incl += before;
     const int ctas = (int)min((unsigned long long)C, total);
     if (c < ctas) {
-        const unsigned long long begin = mul_div(total, (unsigned)c, (unsigned)ctas);
+        const unsigned long long begin = total * (unsigned)c / (unsigned)ctas;
         const unsigned long long excl = incl - mine;
         if (excl <= begin && begin < incl) {
             unsigned long long at = excl;
@@ -214,7 +160,7 @@ __device__ __forceinline__ Piece find_piece(const Shape& s, const int32_t* __res
                 at += x;
             }
             shared->begin = begin;
-            shared->end = mul_div(total, (unsigned)(c + 1), (unsigned)ctas);
+            shared->end = total * (unsigned)(c + 1) / (unsigned)ctas;
             shared->total = total;
             shared->off = begin - at;
             shared->tiles = cost[n];
@@ -236,31 +182,93 @@ struct Unit {
     int parts;                                     // CTAs that share the unit, from this one on (first && !last)
 };
 
-// Walks the units of a CTA's piece.  Used by all lanes of one warp together.
+// Walks the units of a CTA's piece.  Used by all lanes of one warp together.  I:
+// 64 bits, or 32 where the products below stay under 2^32 (Shape::narrow).
+constexpr int kNarrowRequests = 256;
+constexpr long long kNarrowTiles = 1 << 22;            // times kMaxCtas: 2^31
+template <typename I>
 struct Walker {
-    unsigned long long at, end, total;
+    I at, end, total;
     int ctas;
     int n, h, i, skip;                             // next unit; tiles of it that lie before the piece
     Req r;
     int units;
 
+    // From the piece that the whole block found.
     __device__ __forceinline__ void start(const Shape& s, const int32_t* cu, const int32_t* seq_len, const Piece& p) {
-        at = p.begin;
-        end = p.end;
-        total = p.total;
+        at = (I)p.begin;
+        end = (I)p.end;
+        total = (I)p.total;
         ctas = p.ctas;
         n = p.n;
-        h = i = skip = 0;
-        r = Req{0, 0, 0, 0};
-        units = 0;
         if (at >= end) return;
         r = load_req(s, cu, seq_len, n);
-        units = n_units(s, r);
-        const bool small = p.off <= 0xffffffffu && p.tiles <= 0xffffffffu;
-        h = small ? (int)((unsigned)p.off / (unsigned)p.tiles) : (int)(p.off / p.tiles);
-        unsigned long long left = p.off - (unsigned long long)h * p.tiles;
+        first_unit(s, (I)p.off, (I)p.tiles);
+    }
+
+    // A step of few requests and tiles: this warp finds the piece of CTA `c` of `C` by
+    // itself, 32 requests at a time, in 32 bits, while the rest of the block sets
+    // up.  Kept short: a small call spends more on fetching instructions than on
+    // running them.
+    __device__ __forceinline__ void start_narrow(const Shape& s, const int32_t* cu, const int32_t* seq_len, int c, int C) {
         const int lane = threadIdx.x & 31;
-        for (int base = 0; base < units; base += 32) {         // the unit that holds tile `left` of this head
+        Req q{0, 0, 0, 0};
+        unsigned x = 0, sum = 0;
+#pragma unroll 1
+        for (int base = 0; base < s.n_req; base += 32) {
+            q = Req{0, 0, 0, 0};
+            if (base + lane < s.n_req) q = load_req(s, cu, seq_len, base + lane);
+            x = request_tiles<unsigned>(s, q);
+            sum += x;
+        }
+        total = __reduce_add_sync(0xffffffffu, sum) * (unsigned)s.Hv;
+        ctas = (int)min((unsigned)C, (unsigned)total);
+        at = end = 0;
+        if (c >= ctas) return;
+        at = total * (unsigned)c / (unsigned)ctas;
+        end = total * (unsigned)(c + 1) / (unsigned)ctas;
+        unsigned before = 0;
+#pragma unroll 1
+        for (int base = 0; base < s.n_req; base += 32) {
+            if (s.n_req > 32) {
+                q = Req{0, 0, 0, 0};
+                if (base + lane < s.n_req) q = load_req(s, cu, seq_len, base + lane);
+                x = request_tiles<unsigned>(s, q);
+            }
+            unsigned incl = x * (unsigned)s.Hv;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const unsigned t = __shfl_up_sync(0xffffffffu, incl, o);
+                if (lane >= o) incl += t;
+            }
+            const unsigned hit = __ballot_sync(0xffffffffu, (unsigned)at < before + incl);
+            if (hit) {
+                const int src = __ffs((int)hit) - 1;
+                n = base + src;
+                r.tok0 = __shfl_sync(0xffffffffu, q.tok0, src);
+                r.len = __shfl_sync(0xffffffffu, q.len, src);
+                r.pos0 = __shfl_sync(0xffffffffu, q.pos0, src);
+                r.kend = __shfl_sync(0xffffffffu, q.kend, src);
+                const unsigned tiles = __shfl_sync(0xffffffffu, x, src);
+                const unsigned to_n = before + __shfl_sync(0xffffffffu, incl, src) - tiles * (unsigned)s.Hv;
+                first_unit(s, (I)at - to_n, tiles);
+                return;
+            }
+            before += __shfl_sync(0xffffffffu, incl, 31);
+        }
+    }
+
+    // Head, unit and tile that lie `off` tiles behind the start of request n, whose heads have `tiles` each.
+    __device__ __forceinline__ void first_unit(const Shape& s, I off, I tiles) {
+        units = n_units(s, r);
+        h = (int)(off / tiles);
+        I left = off - (I)h * tiles;
+        i = 0;
+        skip = (int)left;
+        if (units <= 1) return;
+        const int lane = threadIdx.x & 31;
+#pragma unroll 1
+        for (int base = 0; base < units; base += 32) {
             unsigned x = 0;
             if (base + lane < units) {
                 int tb, te;
@@ -275,10 +283,10 @@ struct Walker {
             }
             const unsigned hit = __ballot_sync(0xffffffffu, left < incl);
             if (hit) {
-                const int src = __ffs(hit) - 1;
+                const int src = __ffs((int)hit) - 1;
                 i = base + src;
                 skip = (int)(left - __shfl_sync(0xffffffffu, incl - x, src));
-                break;
+                return;
             }
             left -= __shfl_sync(0xffffffffu, incl, 31);
         }
@@ -300,7 +308,7 @@ struct Walker {
         unit_span(s, r, i, tb, te);
         const int full_end = te;
         tb += skip;
-        const unsigned long long fin = at + (unsigned)(te - tb);
+        const I fin = at + (unsigned)(te - tb);
         if (fin > end) te = tb + (int)(end - at);
         u.n = n;
         u.kvh = h / s.sub;
@@ -317,14 +325,9 @@ struct Walker {
         if (u.first && !u.last) {
             // CTA c begins at total * c / ctas, so the last one that has a tile below `fin` is
             // ceil(fin * ctas / total) - 1; likewise this one, from its first tile
-            if (total < (1u << 22)) {
-                const unsigned z = (unsigned)total;
-                u.parts = (int)(((unsigned)fin * (unsigned)ctas + z - 1) / z - (((unsigned)at + 1) * (unsigned)ctas + z - 1) / z) + 1;
-            } else {
-                const unsigned long long hi = (fin * (unsigned)ctas + total - 1) / total;
-                const unsigned long long lo = ((at + 1) * (unsigned)ctas + total - 1) / total;
-                u.parts = (int)(hi - lo) + 1;
-            }
+            const I hi = (fin * (unsigned)ctas + total - 1) / total;
+            const I lo = ((at + 1) * (unsigned)ctas + total - 1) / total;
+            u.parts = (int)(hi - lo) + 1;
         }
         at += (unsigned)(te - tb);
         skip = 0;

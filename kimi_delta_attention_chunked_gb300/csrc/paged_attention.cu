@@ -53,12 +53,18 @@ kda_paged_attention_simt_kernel(const T* __restrict__ q, const T* __restrict__ k
     __shared__ Unit s_unit;
     __shared__ int s_more;
     const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the merge may be set up; it waits for this grid
 
-    const Piece piece = kda_paged::find_piece<kThreads>(s, cu, seq_len, blockIdx.x, gridDim.x,
-                                                        reinterpret_cast<unsigned long long*>(smem_raw), s_red,
-                                                        &s_piece);
-    Walker walk;
-    if (w == 0) walk.start(s, cu, seq_len, piece);
+    Walker<unsigned> walk_narrow;
+    Walker<unsigned long long> walk;
+    if (s.narrow) {
+        if (w == 0) walk_narrow.start_narrow(s, cu, seq_len, blockIdx.x, gridDim.x);
+    } else {
+        const Piece piece = kda_paged::find_piece<kThreads>(s, cu, seq_len, blockIdx.x, gridDim.x,
+                                                            reinterpret_cast<unsigned long long*>(smem_raw), s_red,
+                                                            &s_piece);
+        if (w == 0) walk.start(s, cu, seq_len, piece);
+    }
     if (tid == 0) parts.meta[blockIdx.x] = make_int4(0, 0, 0, 0);
 
     constexpr int VC = D / 32;                         // value columns per thread
@@ -66,7 +72,7 @@ kda_paged_attention_simt_kernel(const T* __restrict__ q, const T* __restrict__ k
         __syncthreads();                               // the unit before is done with shared memory
         if (w == 0) {
             Unit nu;
-            const bool more = walk.next(s, cu, seq_len, nu);
+            const bool more = s.narrow ? walk_narrow.next(s, cu, seq_len, nu) : walk.next(s, cu, seq_len, nu);
             if (lane == 0) {
                 s_unit = nu;
                 s_more = more;
@@ -259,42 +265,85 @@ kda_paged_attention_simt_kernel(const T* __restrict__ q, const T* __restrict__ k
 
 // Joins the parts of each cut unit: with M = max of the parts' references,
 //     o = sum_i 2^(m_i - M) o_i / sum_i 2^(m_i - M) l_i.
-// blockIdx.x names the CTA in which the unit begins, blockIdx.y the block's
-// rows; D / 4 threads take a row.  Reads each partial row once.
+// blockIdx.x names the CTA in which the unit begins.  D / 4 threads take the
+// columns of a row; up to eight such groups share out a row's parts, as many as
+// there are parts, so that a unit cut many times costs a few load latencies and
+// one cut once gives every group a row of its own.  Reads each partial row once.
+constexpr int kMergeThreads = 256;
 template <int D, typename T>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(kMergeThreads)
 kda_paged_merge_kernel(Partials parts, int Gv, int Hq, T* __restrict__ o, float* __restrict__ lse) {
-    constexpr int TPR = D / 4, RPB = 256 / TPR;
+    constexpr int TPR = D / 4, GROUPS = kMergeThreads / TPR;
+    __shared__ float4 s_acc[kMergeThreads];
+    __shared__ float2 s_st[GROUPS];
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int c0 = blockIdx.x;
     const int4 me = parts.meta[c0];
     if (me.w == 0) return;
     const int rows = me.z * Gv, n = me.w;
-    const int x = threadIdx.x % TPR;
-    for (int r = blockIdx.y * RPB + threadIdx.x / TPR; r < rows; r += gridDim.y * RPB) {
-        float top = -INFINITY;
-#pragma unroll 4
-        for (int i = 0; i < n; ++i) top = fmaxf(top, parts.stats(c0 + i, i == 0 ? 1 : 0)[r].x);
-        const float ref = top == -INFINITY ? 0.f : top;
+    int share = 1;                                     // groups that share a row
+    while (share < n && share < 8 && share < GROUPS) share <<= 1;
+    const int x = threadIdx.x % TPR, grp = threadIdx.x / TPR, y = grp % share;
+    const int per_pass = GROUPS / share;
+    for (int r0 = blockIdx.y * per_pass; r0 < rows; r0 += gridDim.y * per_pass) {
+        const int r = r0 + grp / share;
+        float top = -INFINITY, l = 0.f;
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-        float l = 0.f;
-#pragma unroll 4
-        for (int i = 0; i < n; ++i) {
-            const float2 st = parts.stats(c0 + i, i == 0 ? 1 : 0)[r];
-            const float4 v = reinterpret_cast<const float4*>(parts.sums(c0 + i, i == 0 ? 1 : 0) + (size_t)r * D)[x];
-            if (st.y == 0.f) continue;                 // the part saw no key of this row
-            const float f = st.x == -INFINITY ? 1.f : exp2f(st.x - ref);
-            l = fmaf(f, st.y, l);
-            acc.x = fmaf(f, v.x, acc.x); acc.y = fmaf(f, v.y, acc.y);
-            acc.z = fmaf(f, v.z, acc.z); acc.w = fmaf(f, v.w, acc.w);
+        if (r < rows) {
+            constexpr int kU = 4;
+            for (int i0 = y; i0 < n; i0 += kU * share) {
+                float2 st[kU];
+                float4 v[kU];
+#pragma unroll
+                for (int e = 0; e < kU; ++e) {
+                    const int i = i0 + e * share;
+                    st[e] = make_float2(-INFINITY, 0.f);
+                    v[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (i < n) {
+                        st[e] = parts.stats(c0 + i, i == 0 ? 1 : 0)[r];
+                        v[e] = reinterpret_cast<const float4*>(parts.sums(c0 + i, i == 0 ? 1 : 0) + (size_t)r * D)[x];
+                    }
+                }
+#pragma unroll
+                for (int e = 0; e < kU; ++e) {
+                    if (st[e].y == 0.f) continue;      // the part saw no key of this row
+                    const float m = fmaxf(top, st[e].x), ref = m == -INFINITY ? 0.f : m;
+                    const float fo = exp2f(top - ref), fn = st[e].x == -INFINITY ? 1.f : exp2f(st[e].x - ref);
+                    top = m;
+                    l = fmaf(l, fo, fn * st[e].y);
+                    acc.x = fmaf(acc.x, fo, fn * v[e].x); acc.y = fmaf(acc.y, fo, fn * v[e].y);
+                    acc.z = fmaf(acc.z, fo, fn * v[e].z); acc.w = fmaf(acc.w, fo, fn * v[e].w);
+                }
+            }
         }
+        if (share > 1) {
+            __syncthreads();                           // the pass before has been read
+            s_acc[threadIdx.x] = acc;
+            if (x == 0) s_st[grp] = make_float2(top, l);
+            __syncthreads();
+            if (y != 0) continue;
+            for (int g = 1; g < share; ++g) {
+                const float2 st = s_st[grp + g];
+                const float4 v = s_acc[threadIdx.x + g * TPR];
+                if (st.y == 0.f) continue;
+                const float m = fmaxf(top, st.x), ref = m == -INFINITY ? 0.f : m;
+                const float fo = exp2f(top - ref), fn = st.x == -INFINITY ? 1.f : exp2f(st.x - ref);
+                top = m;
+                l = fmaf(l, fo, fn * st.y);
+                acc.x = fmaf(acc.x, fo, fn * v.x); acc.y = fmaf(acc.y, fo, fn * v.y);
+                acc.z = fmaf(acc.z, fo, fn * v.z); acc.w = fmaf(acc.w, fo, fn * v.w);
+            }
+        }
+        if (r >= rows) continue;
         const float inv = l == 0.f ? 0.f : 1.f / l;
         const size_t at = (size_t)(me.x + r / Gv) * Hq + me.y + r % Gv;
         T* dst = o + at * D + 4 * x;
-        kda::io<T>::st(dst + 0, acc.x * inv);
-        kda::io<T>::st(dst + 1, acc.y * inv);
-        kda::io<T>::st(dst + 2, acc.z * inv);
-        kda::io<T>::st(dst + 3, acc.w * inv);
+        if constexpr (sizeof(T) == 2) {
+            *reinterpret_cast<uint2*>(dst) =
+                make_uint2(kda::pack_bf16x2(acc.x * inv, acc.y * inv), kda::pack_bf16x2(acc.z * inv, acc.w * inv));
+        } else {
+            *reinterpret_cast<float4*>(dst) = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+        }
         if (lse && x == 0) lse[at] = l == 0.f ? -INFINITY : (top + log2f(l)) * kLn2;
     }
 }
@@ -309,10 +358,9 @@ cudaError_t launch_merge(const kda_host::PagedArgs& a, const kda_host::PagedPlan
                                     cudaSharedmemCarveoutMaxShared);
     });
     if (e != cudaSuccess) return e;
-    const int rows_per_block = 256 / (D / 4);
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(ctas, std::max(1, std::min(4, (p.rows + rows_per_block - 1) / rows_per_block)));
-    cfg.blockDim = dim3(256);
+    cfg.gridDim = dim3(ctas, std::min(16, p.rows));
+    cfg.blockDim = dim3(kMergeThreads);
     cfg.stream = a.stream;
     cudaLaunchAttribute attr{};
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -404,6 +452,11 @@ kda_paged::Shape paged_shape(const PagedArgs& a, const PagedPlan& p) {
     s.window = a.window;
     s.U = p.U;
     s.tile_log2 = p.tile_log2;
+    // the most tiles any lengths can give: each unit sees the whole table at most
+    const long long units = (long long)s.Hv * (a.T / p.U + a.N);
+    const long long tiles = ((long long)a.blocks * a.page_size >> p.tile_log2) + 2;
+    s.narrow = a.N <= kda_paged::kNarrowRequests && units < kda_paged::kNarrowTiles &&
+               units * tiles < kda_paged::kNarrowTiles;
     return s;
 }
 

@@ -251,7 +251,7 @@ kda_paged_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __
     }
     // this CTA's piece of the work: by the walking warp alone where it can
     Piece piece{0, 0, 0, 0, 0, 0, 0};
-    if (s.n_req > kda_paged::kWarpRequests) {
+    if (!s.narrow) {
         auto* cost = reinterpret_cast<unsigned long long*>(sm + C::KV0);
         auto* red = cost + kda_paged::kMaxRequests;
         auto* shared_piece = reinterpret_cast<Piece*>(red + kThreads / 32);
@@ -286,23 +286,30 @@ kda_paged_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __
 
     if (w == kWalkWarp) {
         // ---------------- unit descriptions
-        if (s.n_req <= kda_paged::kWarpRequests)
-            piece = kda_paged::find_piece_warp(s, cu, seq_len, blockIdx.x, gridDim.x);
-        Walker walk;
-        walk.start(s, cu, seq_len, piece);
         int4 meta = make_int4(0, 0, 0, 0);
-        for (int k = 0;; ++k) {
-            Unit u;
-            const bool more = walk.next(s, cu, seq_len, u);
-            if (k >= kUnits && !wait(&tl.u_empty[k % kUnits], (k / kUnits - 1) & 1)) break;
-            __syncwarp();
-            if (lane == 0) {
-                if (more) tl.units[k % kUnits].u = u;
-                tl.units[k % kUnits].more = more;
-                kda::mbar_arrive(&tl.u_full[k % kUnits]);
+        auto publish = [&](auto& walk) {
+            for (int k = 0;; ++k) {
+                Unit u;
+                const bool more = walk.next(s, cu, seq_len, u);
+                if (k >= kUnits && !wait(&tl.u_empty[k % kUnits], (k / kUnits - 1) & 1)) break;
+                __syncwarp();
+                if (lane == 0) {
+                    if (more) tl.units[k % kUnits].u = u;
+                    tl.units[k % kUnits].more = more;
+                    kda::mbar_arrive(&tl.u_full[k % kUnits]);
+                }
+                if (!more) break;
+                if (u.first && !u.last) meta = make_int4(u.tok0, u.qh0, u.ntok, u.parts);
             }
-            if (!more) break;
-            if (u.first && !u.last) meta = make_int4(u.tok0, u.qh0, u.ntok, u.parts);
+        };
+        if (s.narrow) {
+            Walker<unsigned> walk;
+            walk.start_narrow(s, cu, seq_len, blockIdx.x, gridDim.x);
+            publish(walk);
+        } else {
+            Walker<unsigned long long> walk;
+            walk.start(s, cu, seq_len, piece);
+            publish(walk);
         }
         if (lane == 0) parts.meta[blockIdx.x] = meta;
     } else if (w == kCopyWarp) {
@@ -333,6 +340,16 @@ kda_paged_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __
             ++n_ld;
             return true;
         };
+        auto load_q = [&](const Unit& u, bool two) {
+            __syncwarp();
+            if (lane == 0) {
+                kda::mbar_arrive_expect_tx(&tl.q_full, (two ? 2 : 1) * C::PANELS * BT * s.Gv * 128);
+                for (int i = 0; i < (two ? 2 : 1); ++i)
+                    for (int c = 0; c < C::PANELS; ++c)
+                        kda::tma_load_3d(sm + i * C::TILE + c * kPanel, &qmap, c * 64, u.qh0, u.tok0 + i * BT, &tl.q_full);
+            }
+            ++n_q;
+        };
         bool ok = true;
         for (int k = 0; ok; ++k) {
             Unit u;
@@ -343,6 +360,7 @@ kda_paged_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __
             for (int t = 0; ok && t < steps; ++t) {
                 if (older.load) ok = load(&vmap, older.page, older.y, older.kvh);
                 older = newer;
+                if (k == 0 && t == 0) load_q(u, two);
                 const bool first_use = !two || (t & 1) == 0;
                 newer.load = first_use;
                 if (ok && first_use) {
@@ -355,19 +373,9 @@ kda_paged_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __
                     newer.y = y;
                     newer.kvh = u.kvh;
                 }
-                if (ok && t == 0) {
-                    ok = k == 0 || wait(&tl.q_empty, (k - 1) & 1);
-                    if (ok) {
-                        __syncwarp();
-                        if (lane == 0) {
-                            kda::mbar_arrive_expect_tx(&tl.q_full, (two ? 2 : 1) * C::PANELS * BT * s.Gv * 128);
-                            for (int i = 0; i < (two ? 2 : 1); ++i)
-                                for (int c = 0; c < C::PANELS; ++c)
-                                    kda::tma_load_3d(sm + i * C::TILE + c * kPanel, &qmap, c * 64, u.qh0,
-                                                     u.tok0 + i * BT, &tl.q_full);
-                        }
-                        ++n_q;
-                    }
+                if (ok && t == 0 && k > 0) {
+                    ok = wait(&tl.q_empty, (k - 1) & 1);
+                    if (ok) load_q(u, two);
                 }
             }
         }
@@ -502,6 +510,7 @@ kda_paged_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __
                 if (older.flags & kDue) ok = values_step(h, older);
                 if (ok && (!two || t == 0)) ok = take_stage(k_stage);
                 if (ok && t == 0) ok = wait(&tl.q_full, k & 1);
+                if (ok && g < 2) ok = take_weights(h);       // the softmax warps' round -1
                 if (!ok) break;
                 kda::tc_fence_after();
                 if (elect_one())
@@ -558,9 +567,12 @@ kda_paged_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __
         int n_s = 0, n_j = 0, g = 0;
         uint32_t o_phase = 0;                          // bit h: parity of the next O_h
         bool ok = true;
-        for (int k = 0; ok; ++k) {
-            Unit u;
-            if (!read_unit(k, u)) break;
+        // Round -1 takes one step over whatever TMEM holds, for the sake of its instructions:
+        // fetching them for the first time takes thousands of cycles, and these warps wait that
+        // long for the first keys anyway.  Its arrival tells the issuing warp that S is free
+        for (int k = -1; ok; ++k) {
+            Unit u{0, 0, 0, 0, 2 * BT, 0, 0, 0, 1, 0, 0, 0};
+            if (k >= 0 && !read_unit(k, u)) break;
             const bool two = u.ntok > BT;
             const int steps = (u.te - u.tb) << (two ? 1 : 0);
             const int t0 = (h ^ g) & 1;                // this half's first step
@@ -582,8 +594,10 @@ kda_paged_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __
                 const int tile = u.tb + (two ? t >> 1 : t), k0 = tile << kKeysLog2;
                 const unsigned missing = __ballot_sync(0xffffffffu, page < 0 || page >= s.n_pages);
                 if (busy && t + 2 < steps) page = page_of(tile + (two ? 1 : 2));
-                if (!wait(&tl.s_full[h], n_s & 1)) { ok = false; break; }
-                ++n_s;
+                if (k >= 0) {
+                    if (!wait(&tl.s_full[h], n_s & 1)) { ok = false; break; }
+                    ++n_s;
+                }
                 kda::tc_fence_after();
                 if (busy) {
                     if (k0 < mine.all_lo || k0 + kKeys > mine.all_hi || missing) {
@@ -663,6 +677,7 @@ kda_paged_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __
                 if (lane == 0) kda::mbar_arrive(&tl.p_full[h]);
             }
             if (!ok) break;
+            if (k < 0) continue;
             // ---- output
             const bool whole = u.first && u.last;
             const int which = u.first ? 1 : 0;

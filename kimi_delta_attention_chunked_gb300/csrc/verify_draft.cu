@@ -30,13 +30,9 @@ constexpr int kWarps = kThreads / 32;
 
 // floor(min(max(p, 0), 1) 2^60); NaN counts as 0
 __device__ __forceinline__ unsigned long long fixed60(float p) {
-    p = fminf(fmaxf(p, 0.f), 1.f);
-    const unsigned b = __float_as_uint(p);
-    const int e = (int)(b >> 23);                          // p = 1.m 2^(e - 127); denormals are below 2^-60
-    if (e == 0) return 0;
-    const unsigned long long m = (b & 0x7fffffu) | 0x800000u;
-    const int s = e - 90;                                  // m 2^(e - 150) 2^60
-    return s >= 0 ? m << s : (s > -24 ? m >> -s : 0);
+    const unsigned b = __float_as_uint(__saturatef(p));    // 0 ... 1, NaN becomes 0
+    const unsigned long long m = (unsigned long long)((b & 0x7fffffu) | 0x800000u) << 37;
+    return m >> min(127u - (b >> 23), 63u);                // p = 1.m 2^(e - 127), e <= 127; below 2^-60: 0
 }
 
 template <typename T>
@@ -62,15 +58,14 @@ template <typename T>
 __device__ __forceinline__ long long part_sum(const Row<T>& row, int lo, int hi) {
     const int lane = threadIdx.x & 31;
     long long s = 0;
-    int v = lo + lane;
-    constexpr int kU = 8;
-    for (; v + 32 * (kU - 1) < hi; v += 32 * kU) {
+    constexpr int kU = 4;
+    for (int v = lo + lane; v < hi; v += 32 * kU) {
         float a[kU], b[kU];
 #pragma unroll
-        for (int e = 0; e < kU; ++e) a[e] = kda::io<T>::ld(row.p + v + 32 * e);
+        for (int e = 0; e < kU; ++e) a[e] = v + 32 * e < hi ? kda::io<T>::ld(row.p + v + 32 * e) : 0.f;
         if (row.q) {
 #pragma unroll
-            for (int e = 0; e < kU; ++e) b[e] = kda::io<T>::ld(row.q + v + 32 * e);
+            for (int e = 0; e < kU; ++e) b[e] = v + 32 * e < hi ? kda::io<T>::ld(row.q + v + 32 * e) : 0.f;
 #pragma unroll
             for (int e = 0; e < kU; ++e) s += max((long long)fixed60(a[e]) - (long long)fixed60(b[e]), 0ll);
         } else {
@@ -78,12 +73,11 @@ __device__ __forceinline__ long long part_sum(const Row<T>& row, int lo, int hi)
             for (int e = 0; e < kU; ++e) s += v + 32 * e == row.masked ? 0ll : (long long)fixed60(a[e]);
         }
     }
-    for (; v < hi; v += 32) s += row.at(v);
     return warp_sum(s);
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 4)
 kda_verify_draft_kernel(const T* __restrict__ target, const T* __restrict__ draft,
                         const int32_t* __restrict__ draft_tokens, const float* __restrict__ uniforms,
                         const int32_t* __restrict__ draft_len, int K, int V, int32_t* __restrict__ tokens,
