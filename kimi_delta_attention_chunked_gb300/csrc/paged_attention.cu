@@ -266,12 +266,26 @@ kda_paged_attention_simt_kernel(const T* __restrict__ q, const T* __restrict__ k
 // Joins the parts of each cut unit: with M = max of the parts' references,
 //     o = sum_i 2^(m_i - M) o_i / sum_i 2^(m_i - M) l_i.
 // blockIdx.x names the CTA in which the unit begins.  D / 4 threads take the
-// columns of a row; up to eight such groups share out a row's parts, as many as
-// there are parts, so that a unit cut many times costs a few load latencies and
-// one cut once gives every group a row of its own.  Reads each partial row once.
+// columns of a row.  A unit cut once or twice gives each such group rows of its
+// own, four at a time; the parts of one cut more often are shared out among up
+// to eight groups, so that it costs a few load latencies too.  Reads each
+// partial row once.
 constexpr int kMergeThreads = 256;
+struct Merged {
+    float top = -INFINITY, l = 0.f;
+    float4 acc = {0.f, 0.f, 0.f, 0.f};
+    __device__ __forceinline__ void add(const float2& st, const float4& v) {
+        if (st.y == 0.f) return;                       // the part saw no key of this row
+        const float m = fmaxf(top, st.x), ref = m == -INFINITY ? 0.f : m;
+        const float fo = exp2f(top - ref), fn = st.x == -INFINITY ? 1.f : exp2f(st.x - ref);
+        top = m;
+        l = fmaf(l, fo, fn * st.y);
+        acc.x = fmaf(acc.x, fo, fn * v.x); acc.y = fmaf(acc.y, fo, fn * v.y);
+        acc.z = fmaf(acc.z, fo, fn * v.z); acc.w = fmaf(acc.w, fo, fn * v.w);
+    }
+};
 template <int D, typename T>
-__global__ void __launch_bounds__(kMergeThreads)
+__global__ void __launch_bounds__(kMergeThreads, 4)
 kda_paged_merge_kernel(Partials parts, int Gv, int Hq, T* __restrict__ o, float* __restrict__ lse) {
     constexpr int TPR = D / 4, GROUPS = kMergeThreads / TPR;
     __shared__ float4 s_acc[kMergeThreads];
@@ -281,70 +295,70 @@ kda_paged_merge_kernel(Partials parts, int Gv, int Hq, T* __restrict__ o, float*
     const int4 me = parts.meta[c0];
     if (me.w == 0) return;
     const int rows = me.z * Gv, n = me.w;
-    int share = 1;                                     // groups that share a row
-    while (share < n && share < 8 && share < GROUPS) share <<= 1;
-    const int x = threadIdx.x % TPR, grp = threadIdx.x / TPR, y = grp % share;
-    const int per_pass = GROUPS / share;
+    const int x = threadIdx.x % TPR, grp = threadIdx.x / TPR;
+    auto part = [&](int i, int r, float2& st, float4& v) {
+        st = parts.stats(c0 + i, i == 0 ? 1 : 0)[r];
+        v = reinterpret_cast<const float4*>(parts.sums(c0 + i, i == 0 ? 1 : 0) + (size_t)r * D)[x];
+    };
+    auto put = [&](const Merged& m, int r) {
+        const float inv = m.l == 0.f ? 0.f : 1.f / m.l;
+        const size_t at = (size_t)(me.x + r / Gv) * Hq + me.y + r % Gv;
+        T* dst = o + at * D + 4 * x;
+        if constexpr (sizeof(T) == 2) {
+            *reinterpret_cast<uint2*>(dst) =
+                make_uint2(kda::pack_bf16x2(m.acc.x * inv, m.acc.y * inv), kda::pack_bf16x2(m.acc.z * inv, m.acc.w * inv));
+        } else {
+            *reinterpret_cast<float4*>(dst) = make_float4(m.acc.x * inv, m.acc.y * inv, m.acc.z * inv, m.acc.w * inv);
+        }
+        if (lse && x == 0) lse[at] = m.l == 0.f ? -INFINITY : (m.top + log2f(m.l)) * kLn2;
+    };
+    if (n <= 3) {
+        constexpr int kR = 4;
+        const int step = gridDim.y * GROUPS;
+        for (int r0 = blockIdx.y * GROUPS + grp; r0 < rows; r0 += kR * step) {
+            Merged m[kR];
+            for (int i = 0; i < n; ++i) {
+                float2 st[kR];
+                float4 v[kR];
+#pragma unroll
+                for (int e = 0; e < kR; ++e) part(i, min(r0 + e * step, rows - 1), st[e], v[e]);
+#pragma unroll
+                for (int e = 0; e < kR; ++e) m[e].add(st[e], v[e]);
+            }
+#pragma unroll
+            for (int e = 0; e < kR; ++e)
+                if (r0 + e * step < rows) put(m[e], r0 + e * step);
+        }
+        return;
+    }
+    constexpr int kU = 2;                              // parts a group has in flight
+    int share = 2;                                     // groups that share a row
+    while (share * kU < n && share < 8 && share < GROUPS) share <<= 1;
+    const int y = grp % share, per_pass = GROUPS / share;
     for (int r0 = blockIdx.y * per_pass; r0 < rows; r0 += gridDim.y * per_pass) {
         const int r = r0 + grp / share;
-        float top = -INFINITY, l = 0.f;
-        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        Merged m;
         if (r < rows) {
-            constexpr int kU = 4;
             for (int i0 = y; i0 < n; i0 += kU * share) {
                 float2 st[kU];
                 float4 v[kU];
 #pragma unroll
                 for (int e = 0; e < kU; ++e) {
-                    const int i = i0 + e * share;
                     st[e] = make_float2(-INFINITY, 0.f);
                     v[e] = make_float4(0.f, 0.f, 0.f, 0.f);
-                    if (i < n) {
-                        st[e] = parts.stats(c0 + i, i == 0 ? 1 : 0)[r];
-                        v[e] = reinterpret_cast<const float4*>(parts.sums(c0 + i, i == 0 ? 1 : 0) + (size_t)r * D)[x];
-                    }
+                    if (i0 + e * share < n) part(i0 + e * share, r, st[e], v[e]);
                 }
 #pragma unroll
-                for (int e = 0; e < kU; ++e) {
-                    if (st[e].y == 0.f) continue;      // the part saw no key of this row
-                    const float m = fmaxf(top, st[e].x), ref = m == -INFINITY ? 0.f : m;
-                    const float fo = exp2f(top - ref), fn = st[e].x == -INFINITY ? 1.f : exp2f(st[e].x - ref);
-                    top = m;
-                    l = fmaf(l, fo, fn * st[e].y);
-                    acc.x = fmaf(acc.x, fo, fn * v[e].x); acc.y = fmaf(acc.y, fo, fn * v[e].y);
-                    acc.z = fmaf(acc.z, fo, fn * v[e].z); acc.w = fmaf(acc.w, fo, fn * v[e].w);
-                }
+                for (int e = 0; e < kU; ++e) m.add(st[e], v[e]);
             }
         }
-        if (share > 1) {
-            __syncthreads();                           // the pass before has been read
-            s_acc[threadIdx.x] = acc;
-            if (x == 0) s_st[grp] = make_float2(top, l);
-            __syncthreads();
-            if (y != 0) continue;
-            for (int g = 1; g < share; ++g) {
-                const float2 st = s_st[grp + g];
-                const float4 v = s_acc[threadIdx.x + g * TPR];
-                if (st.y == 0.f) continue;
-                const float m = fmaxf(top, st.x), ref = m == -INFINITY ? 0.f : m;
-                const float fo = exp2f(top - ref), fn = st.x == -INFINITY ? 1.f : exp2f(st.x - ref);
-                top = m;
-                l = fmaf(l, fo, fn * st.y);
-                acc.x = fmaf(acc.x, fo, fn * v.x); acc.y = fmaf(acc.y, fo, fn * v.y);
-                acc.z = fmaf(acc.z, fo, fn * v.z); acc.w = fmaf(acc.w, fo, fn * v.w);
-            }
-        }
-        if (r >= rows) continue;
-        const float inv = l == 0.f ? 0.f : 1.f / l;
-        const size_t at = (size_t)(me.x + r / Gv) * Hq + me.y + r % Gv;
-        T* dst = o + at * D + 4 * x;
-        if constexpr (sizeof(T) == 2) {
-            *reinterpret_cast<uint2*>(dst) =
-                make_uint2(kda::pack_bf16x2(acc.x * inv, acc.y * inv), kda::pack_bf16x2(acc.z * inv, acc.w * inv));
-        } else {
-            *reinterpret_cast<float4*>(dst) = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
-        }
-        if (lse && x == 0) lse[at] = l == 0.f ? -INFINITY : (top + log2f(l)) * kLn2;
+        __syncthreads();                               // the pass before has been read
+        s_acc[threadIdx.x] = m.acc;
+        if (x == 0) s_st[grp] = make_float2(m.top, m.l);
+        __syncthreads();
+        if (y != 0) continue;
+        for (int g = 1; g < share; ++g) m.add(s_st[grp + g], s_acc[threadIdx.x + g * TPR]);
+        if (r < rows) put(m, r);
     }
 }
 
@@ -359,7 +373,7 @@ cudaError_t launch_merge(const kda_host::PagedArgs& a, const kda_host::PagedPlan
     });
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(ctas, std::min(16, p.rows));
+    cfg.gridDim = dim3(ctas, std::min(4, p.rows));
     cfg.blockDim = dim3(kMergeThreads);
     cfg.stream = a.stream;
     cudaLaunchAttribute attr{};

@@ -510,7 +510,6 @@ kda_paged_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __
                 if (older.flags & kDue) ok = values_step(h, older);
                 if (ok && (!two || t == 0)) ok = take_stage(k_stage);
                 if (ok && t == 0) ok = wait(&tl.q_full, k & 1);
-                if (ok && g < 2) ok = take_weights(h);       // the softmax warps' round -1
                 if (!ok) break;
                 kda::tc_fence_after();
                 if (elect_one())
@@ -570,9 +569,9 @@ kda_paged_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __
         // Round -1 takes one step over whatever TMEM holds, for the sake of its instructions:
         // fetching them for the first time takes thousands of cycles, and these warps wait that
         // long for the first keys anyway.  Its arrival tells the issuing warp that S is free
-        for (int k = -1; ok; ++k) {
-            Unit u{0, 0, 0, 0, 2 * BT, 0, 0, 0, 1, 0, 0, 0};
-            if (k >= 0 && !read_unit(k, u)) break;
+        for (int k = 0; ok; ++k) {
+            Unit u;
+            if (!read_unit(k, u)) break;
             const bool two = u.ntok > BT;
             const int steps = (u.te - u.tb) << (two ? 1 : 0);
             const int t0 = (h ^ g) & 1;                // this half's first step
@@ -594,10 +593,8 @@ kda_paged_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __
                 const int tile = u.tb + (two ? t >> 1 : t), k0 = tile << kKeysLog2;
                 const unsigned missing = __ballot_sync(0xffffffffu, page < 0 || page >= s.n_pages);
                 if (busy && t + 2 < steps) page = page_of(tile + (two ? 1 : 2));
-                if (k >= 0) {
-                    if (!wait(&tl.s_full[h], n_s & 1)) { ok = false; break; }
-                    ++n_s;
-                }
+                if (!wait(&tl.s_full[h], n_s & 1)) { ok = false; break; }
+                ++n_s;
                 kda::tc_fence_after();
                 if (busy) {
                     if (k0 < mine.all_lo || k0 + kKeys > mine.all_hi || missing) {
@@ -677,7 +674,6 @@ kda_paged_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __
                 if (lane == 0) kda::mbar_arrive(&tl.p_full[h]);
             }
             if (!ok) break;
-            if (k < 0) continue;
             // ---- output
             const bool whole = u.first && u.last;
             const int which = u.first ? 1 : 0;
