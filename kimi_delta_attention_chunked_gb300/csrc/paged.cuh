@@ -20,6 +20,13 @@ namespace kda_paged {
 constexpr int kMaxRequests = KDA_MAX_STEP_REQUESTS;
 constexpr int kMaxCtas = 512;                      // most CTAs an attention launch uses
 
+// The kernels before this one on the stream are complete and their writes seen;
+// the kernel behind it may be set up from here on.
+__device__ __forceinline__ void wait_for_stream() {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
 // Sizes of one attention call.
 struct Shape {
     int n_req, T;                                  // requests, rows of q
@@ -431,6 +438,28 @@ struct OncePerDevice {
         return e;
     }
 };
+
+// Launches `kern` so that it may be set up while the kernel before it on the stream
+// still runs: every thread of such a kernel calls kda_paged::wait_for_stream()
+// before it touches global memory.
+template <typename... P, typename... A>
+cudaError_t launch_overlapped(void (*kern)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream, int cluster,
+                              A&&... args) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2]{};
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = cluster;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kern, static_cast<P>(args)...);
+}
 
 int* status_word();                                // the device status word (kda_api.cu)
 int sm_count();                                    // SMs of the current device

@@ -53,7 +53,7 @@ kda_paged_attention_simt_kernel(const T* __restrict__ q, const T* __restrict__ k
     __shared__ Unit s_unit;
     __shared__ int s_more;
     const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the merge may be set up; it waits for this grid
+    kda_paged::wait_for_stream();
 
     Walker<unsigned> walk_narrow;
     Walker<unsigned long long> walk;
@@ -290,7 +290,7 @@ kda_paged_merge_kernel(Partials parts, int Gv, int Hq, T* __restrict__ o, float*
     constexpr int TPR = D / 4, GROUPS = kMergeThreads / TPR;
     __shared__ float4 s_acc[kMergeThreads];
     __shared__ float2 s_st[GROUPS];
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    kda_paged::wait_for_stream();
     const int c0 = blockIdx.x;
     const int4 me = parts.meta[c0];
     if (me.w == 0) return;
@@ -372,17 +372,9 @@ cudaError_t launch_merge(const kda_host::PagedArgs& a, const kda_host::PagedPlan
                                     cudaSharedmemCarveoutMaxShared);
     });
     if (e != cudaSuccess) return e;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(ctas, std::min(4, p.rows));
-    cfg.blockDim = dim3(kMergeThreads);
-    cfg.stream = a.stream;
-    cudaLaunchAttribute attr{};
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kda_paged_merge_kernel<D, T>, kda_host::paged_partials(a, p), p.Gv, a.Hq,
-                              static_cast<T*>(a.o), a.lse);
+    return kda_host::launch_overlapped(kda_paged_merge_kernel<D, T>, dim3(ctas, std::min(4, p.rows)), kMergeThreads, 0,
+                                       a.stream, 1, kda_host::paged_partials(a, p), p.Gv, a.Hq, static_cast<T*>(a.o),
+                                       a.lse);
 }
 
 template <int D, typename T>
@@ -397,11 +389,10 @@ cudaError_t launch_simt(const kda_host::PagedArgs& a) {
     });
     if (e != cudaSuccess) return e;
     const int ctas = std::min(p.max_ctas, 2 * kda_host::sm_count());
-    kern<<<ctas, kThreads, smem, a.stream>>>(
-        static_cast<const T*>(a.q), static_cast<const T*>(a.k_cache), static_cast<const T*>(a.v_cache), a.block_table,
+    const cudaError_t err = kda_host::launch_overlapped(
+        kern, ctas, kThreads, smem, a.stream, 1, static_cast<const T*>(a.q), static_cast<const T*>(a.k_cache), static_cast<const T*>(a.v_cache), a.block_table,
         a.cu_seqlens, a.seq_len, a.q_stride, kda_host::paged_shape(a, p), a.scale * kLog2e, static_cast<T*>(a.o), a.lse,
         kda_host::paged_partials(a, p));
-    const cudaError_t err = cudaGetLastError();
     if (err != cudaSuccess) return err;
     return kda_host::launch_paged_merge(a, p, ctas);
 }

@@ -206,6 +206,16 @@ __device__ __forceinline__ void add_odd_values(float* o, int c0, const Unit& u, 
     }
 }
 
+// The rest of a wait that did not succeed at once.  One copy of it for the whole
+// kernel: its many inlined ones would be most of what a short call fetches.
+__device__ __noinline__ bool wait_longer(uint64_t* b, uint32_t parity, volatile int* abort, int* status) {
+    const bool done = kda::mbar_wait_or_abort(b, parity, kda::kWaitCycles, abort);
+    if (__all_sync(0xffffffffu, done)) return true;
+    if (!*abort) kda::record_status(status, kda::kDevTimeout);
+    *abort = 1;
+    return false;
+}
+
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
 kda_paged_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
@@ -266,11 +276,8 @@ kda_paged_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __
     // true once the phase is complete; false when this CTA gives up.  Called by all
     // lanes of a warp, with one answer for all of them, so that none leaves a loop alone
     auto wait = [&](uint64_t* b, uint32_t parity) -> bool {
-        const bool done = kda::mbar_wait_or_abort(b, parity, kda::kWaitCycles, abort_f);
-        if (__all_sync(0xffffffffu, done)) return true;
-        if (!*abort_f) kda::record_status(status, kda::kDevTimeout);
-        *abort_f = 1;
-        return false;
+        if (__all_sync(0xffffffffu, kda::mbar_try_wait(b, parity))) return true;
+        return wait_longer(b, parity, &tl.abort, status);
     };
     int n_ld = 0, n_q = 0;                             // copies issued (copy warp) or taken (issuing warp)
     // reads unit description k; every lane of the calling warp gets it
@@ -360,7 +367,6 @@ kda_paged_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __
             for (int t = 0; ok && t < steps; ++t) {
                 if (older.load) ok = load(&vmap, older.page, older.y, older.kvh);
                 older = newer;
-                if (k == 0 && t == 0) load_q(u, two);
                 const bool first_use = !two || (t & 1) == 0;
                 newer.load = first_use;
                 if (ok && first_use) {
@@ -373,8 +379,8 @@ kda_paged_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __
                     newer.y = y;
                     newer.kvh = u.kvh;
                 }
-                if (ok && t == 0 && k > 0) {
-                    ok = wait(&tl.q_empty, (k - 1) & 1);
+                if (ok && t == 0) {
+                    ok = k == 0 || wait(&tl.q_empty, (k - 1) & 1);
                     if (ok) load_q(u, two);
                 }
             }

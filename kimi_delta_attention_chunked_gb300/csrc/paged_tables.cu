@@ -40,6 +40,7 @@ kda_build_tables_kernel(const int32_t* __restrict__ ctx_len, const int32_t* __re
     int* s_page = s_first + N + 1;                         // [N + 1] first new page of each request
     int* s_ctx = s_page + N + 1;                           // [N] cached tokens
     __shared__ unsigned long long s_red[kTableThreads / 32];
+    kda_paged::wait_for_stream();
 
     const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
     const int page = 1 << page_log2;
@@ -164,6 +165,7 @@ __global__ void __launch_bounds__(kAppendThreads)
 kda_cache_append_kernel(const U* __restrict__ k, const U* __restrict__ v, const int64_t* __restrict__ slot_map,
                         long long k_stride, long long v_stride, long long total, int per_head, int per_row, int H,
                         int page_log2, long long n_slots, U* __restrict__ k_cache, U* __restrict__ v_cache) {
+    kda_paged::wait_for_stream();
     const long long step = (long long)gridDim.x * kAppendThreads;
     for (long long u0 = (long long)blockIdx.x * kAppendThreads + threadIdx.x; u0 < total; u0 += step * kAppendUnroll) {
         U a[kAppendUnroll], b[kAppendUnroll];
@@ -213,11 +215,10 @@ cudaError_t append(const kda_host::AppendArgs& a) {
     const long long total = (long long)a.T * per_row;
     const long long want = (total + kAppendThreads - 1) / kAppendThreads;
     const int grid = (int)std::min<long long>(want, (long long)kda_host::sm_count() * 8);
-    kda_cache_append_kernel<U><<<grid, kAppendThreads, 0, a.stream>>>(
-        static_cast<const U*>(a.k), static_cast<const U*>(a.v), a.slot_map, a.k_stride / ratio, a.v_stride / ratio,
+    return kda_host::launch_overlapped(
+        kda_cache_append_kernel<U>, grid, kAppendThreads, 0, a.stream, 1, static_cast<const U*>(a.k), static_cast<const U*>(a.v), a.slot_map, a.k_stride / ratio, a.v_stride / ratio,
         total, per_head, per_row, a.H, log2_of(a.page_size), (long long)a.n_pages * a.page_size,
         static_cast<U*>(a.k_cache), static_cast<U*>(a.v_cache));
-    return cudaGetLastError();
 }
 
 }  // namespace
@@ -237,10 +238,9 @@ cudaError_t launch_build_tables(const TablesArgs& a) {
     }
     const long long work = std::max<long long>(((long long)a.n_tokens + kTokensPerThread - 1) / kTokensPerThread, 1);
     const int grid = (int)std::min<long long>((work + kTableThreads - 1) / kTableThreads, (long long)sm_count() * 2);
-    kda_build_tables_kernel<<<grid, kTableThreads, smem, a.stream>>>(
-        a.ctx_len, a.new_len, a.free_pages, a.n_free, a.N, a.blocks, log2_of(a.page_size), a.n_tokens, a.block_table,
+    return launch_overlapped(
+        kda_build_tables_kernel, grid, kTableThreads, smem, a.stream, 1, a.ctx_len, a.new_len, a.free_pages, a.n_free, a.N, a.blocks, log2_of(a.page_size), a.n_tokens, a.block_table,
         a.cu_seqlens, a.seq_len, a.slot_map, a.positions, a.n_taken);
-    return cudaGetLastError();
 }
 
 cudaError_t launch_cache_append(const AppendArgs& a) {

@@ -25,8 +25,9 @@ namespace cg = cooperative_groups;
 
 namespace {
 
-constexpr int kThreads = 512;
+constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
+constexpr int kPerSm = 6;                              // CTAs of an SM
 
 // floor(min(max(p, 0), 1) 2^60); NaN counts as 0
 __device__ __forceinline__ unsigned long long fixed60(float p) {
@@ -58,26 +59,35 @@ template <typename T>
 __device__ __forceinline__ long long part_sum(const Row<T>& row, int lo, int hi) {
     const int lane = threadIdx.x & 31;
     long long s = 0;
-    constexpr int kU = 4;
-    for (int v = lo + lane; v < hi; v += 32 * kU) {
-        float a[kU], b[kU];
+    constexpr int kU = 4, kStep = 32 * kU;
+    float a[kU], b[kU];
+    // four numbers of either row in registers while the four behind them are on their way
+    auto load = [&](int v, float* x, float* y) {
 #pragma unroll
-        for (int e = 0; e < kU; ++e) a[e] = v + 32 * e < hi ? kda::io<T>::ld(row.p + v + 32 * e) : 0.f;
+        for (int e = 0; e < kU; ++e) x[e] = v + 32 * e < hi ? kda::io<T>::ld(row.p + v + 32 * e) : 0.f;
         if (row.q) {
 #pragma unroll
-            for (int e = 0; e < kU; ++e) b[e] = v + 32 * e < hi ? kda::io<T>::ld(row.q + v + 32 * e) : 0.f;
+            for (int e = 0; e < kU; ++e) y[e] = v + 32 * e < hi ? kda::io<T>::ld(row.q + v + 32 * e) : 0.f;
+        }
+    };
+    load(lo + lane, a, b);
+    for (int v = lo + lane; v < hi; v += kStep) {
+        float an[kU], bn[kU];
+        load(v + kStep, an, bn);
 #pragma unroll
-            for (int e = 0; e < kU; ++e) s += max((long long)fixed60(a[e]) - (long long)fixed60(b[e]), 0ll);
-        } else {
-#pragma unroll
-            for (int e = 0; e < kU; ++e) s += v + 32 * e == row.masked ? 0ll : (long long)fixed60(a[e]);
+        for (int e = 0; e < kU; ++e) {
+            const long long x = (long long)fixed60(a[e]);
+            if (row.q) s += max(x - (long long)fixed60(b[e]), 0ll);
+            else s += v + 32 * e == row.masked ? 0ll : x;
+            a[e] = an[e];
+            b[e] = bn[e];
         }
     }
     return warp_sum(s);
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads, 4)
+__global__ void __launch_bounds__(kThreads, kPerSm)
 kda_verify_draft_kernel(const T* __restrict__ target, const T* __restrict__ draft,
                         const int32_t* __restrict__ draft_tokens, const float* __restrict__ uniforms,
                         const int32_t* __restrict__ draft_len, int K, int V, int32_t* __restrict__ tokens,
@@ -86,6 +96,7 @@ kda_verify_draft_kernel(const T* __restrict__ target, const T* __restrict__ draf
     const int ranks = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
     const int n = blockIdx.x / ranks;
     const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
+    kda_paged::wait_for_stream();
     cluster.barrier_arrive();                              // waited for before the first remote store: by then all CTAs run
     __shared__ int s_count, s_len;
     __shared__ long long s_cta[2][8];                      // each CTA's sum, pushed by it; one row per attempt
@@ -200,23 +211,12 @@ kda_verify_draft_kernel(const T* __restrict__ target, const T* __restrict__ draf
 
 template <typename T>
 cudaError_t verify(const kda_host::VerifyArgs& a) {
-    // CTAs per request: enough to fill the GPU when there are few requests, but
-    // no part of a row below 4096 numbers
-    int ranks = 8;
-    while (ranks > 1 && ((long long)a.N * ranks > 4ll * kda_host::sm_count() || a.V / ranks < 4096)) ranks >>= 1;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)a.N * ranks);
-    cfg.blockDim = dim3(kThreads);
-    cfg.stream = a.stream;
-    cudaLaunchAttribute attr{};
-    attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim.x = ranks;
-    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kda_verify_draft_kernel<T>, static_cast<const T*>(a.target),
-                              static_cast<const T*>(a.draft), a.draft_tokens, a.uniforms, a.draft_len, a.K, a.V,
-                              a.tokens, a.commit_len);
+    // CTAs per request: as many as the GPU holds at once, but no part of a row below 4096 numbers
+    const long long fit = (long long)kPerSm * kda_host::sm_count() / a.N;
+    const int ranks = (int)std::max<long long>(1, std::min<long long>({8, fit, a.V / 4096}));
+    return kda_host::launch_overlapped(kda_verify_draft_kernel<T>, dim3((unsigned)a.N * ranks), kThreads, 0, a.stream,
+                                       ranks, static_cast<const T*>(a.target), static_cast<const T*>(a.draft),
+                                       a.draft_tokens, a.uniforms, a.draft_len, a.K, a.V, a.tokens, a.commit_len);
 }
 
 }  // namespace
