@@ -6,7 +6,9 @@ objects are linked into one shared library next to this file.  The debug
 variant recompiles the files that hold KDA_DEBUG code with ``-DKDA_DEBUG``
 (input precondition and device index checks, see include/kda.h) and shares
 the other objects.  The CUDA runtime is linked statically, so the libraries
-need only the driver at run time.  Run
+need only the driver at run time.  Beside them, g++ compiles the Python binding
+of the serving-step operators (``_step_binding.so``, against the torch it is
+built under).  Run
 ``python -m kimi_delta_attention_chunked_gb300.build``.
 """
 from __future__ import annotations
@@ -18,6 +20,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -26,6 +29,8 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(ROOT, "_build")
 LIB_PATH = os.path.join(PKG, "libkda.so")
 LIB_DEBUG_PATH = os.path.join(PKG, "libkda_debug.so")
+BINDING_SOURCE = os.path.join(CSRC, "step_binding.cpp")
+BINDING_PATH = os.path.join(PKG, "_step_binding.so")
 DEBUG_SOURCES = ("kda_api.cu", "prefill_tc.cu")      # the files with KDA_DEBUG code
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
@@ -49,16 +54,37 @@ def _fingerprint() -> str:
         h.update(f.encode())
         with open(f, "rb") as fh:
             h.update(fh.read())
-    h.update(" ".join(ARCH + NVCC_FLAGS).encode())
+    with open(BINDING_SOURCE, "rb") as fh:
+        h.update(fh.read())
+    import torch
+    h.update((" ".join(ARCH + NVCC_FLAGS) + torch.__version__ + sys.version).encode())
     return h.hexdigest()
 
 
+def _compile_binding() -> None:
+    """step_binding.cpp -> _step_binding.so, an extension module against this Python's torch."""
+    import torch
+    base = os.path.dirname(os.path.abspath(torch.__file__))
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
+    tmp = BINDING_PATH + f".tmp{os.getpid()}"
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           "-I", INCLUDE, "-isystem", os.path.join(base, "include"),
+           "-isystem", os.path.join(base, "include", "torch", "csrc", "api", "include"),
+           "-isystem", os.path.join(cuda, "include"), "-isystem", sysconfig.get_paths()["include"], BINDING_SOURCE,
+           "-L", os.path.join(base, "lib"), "-ltorch_python", "-ltorch_cpu", "-ltorch", "-lc10_cuda", "-lc10", "-o", tmp]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"compiling {os.path.basename(BINDING_SOURCE)} failed:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, BINDING_PATH)
+
+
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
-    """Compile every .cu file under csrc/ and link libkda.so and libkda_debug.so;
-    returns libkda.so's path."""
+    """Compile every .cu file under csrc/, link libkda.so and libkda_debug.so, and
+    compile the Python binding of the step operators; returns libkda.so's path."""
     fp = _fingerprint()
     stamp = LIB_PATH + ".sha256"
-    if (not force and all(os.path.exists(p) for p in (LIB_PATH, LIB_DEBUG_PATH, stamp))
+    if (not force and all(os.path.exists(p) for p in (LIB_PATH, LIB_DEBUG_PATH, BINDING_PATH, stamp))
             and open(stamp).read() == fp):
         return LIB_PATH
     os.makedirs(os.path.join(BUILD_DIR, "debug"), exist_ok=True)
@@ -82,8 +108,10 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
     # the two slowest files first, so that they start at once
     jobs = sorted([(f, False) for f in srcs] + [(f, True) for f in srcs if os.path.basename(f) in DEBUG_SOURCES],
                   key=lambda j: os.path.basename(j[0]) != "prefill_tc.cu")
-    with cf.ThreadPoolExecutor(max_workers=min(len(jobs), os.cpu_count() or 4)) as ex:
+    with cf.ThreadPoolExecutor(max_workers=min(len(jobs) + 1, os.cpu_count() or 4)) as ex:
+        binding = ex.submit(_compile_binding)
         objs = dict(zip(jobs, ex.map(compile_one, jobs)))
+        binding.result()
 
     def link(path, debug):
         members = [objs[(f, debug and os.path.basename(f) in DEBUG_SOURCES)] for f in srcs]

@@ -297,6 +297,48 @@ def test_attention_strided_q(dtype, d, qpad):
     assert torch.equal(o[:-5], kda.kda_paged_attention(*args))
 
 
+def test_binding_refuses_layouts_the_kernels_cannot_read():
+    """What only shows past the device check: strides, devices and dtypes."""
+    dev = need_gpu()
+    c = make([(20, 3)], 4, 2, 32, 16, F32, dev)
+    args = on(c, dev)
+    wide = torch.zeros(3, 8, 32, device=dev)
+    for q in (wide[:, ::2], torch.zeros(3, 32, 4, device=dev).transpose(1, 2)):
+        with pytest.raises(ValueError, match="contiguous"):
+            kda.kda_paged_attention(q, *args[1:])
+    with pytest.raises(ValueError, match="overlap"):
+        kda.kda_paged_attention(torch.zeros(1, 4, 32, device=dev).expand(3, 4, 32), *args[1:])
+    for i, word in ((1, "one shape|contiguous|k_cache"), (3, "block_table"), (4, "cu_seqlens"), (5, "seq_len")):
+        bad = list(args)
+        bad[i] = bad[i].cpu()
+        with pytest.raises(ValueError, match=word):
+            kda.kda_paged_attention(*bad)
+    bad = list(args)
+    bad[3] = bad[3].long()
+    with pytest.raises(TypeError, match="block_table must be torch.int32, got torch.int64"):
+        kda.kda_paged_attention(*bad)
+    bad = list(args)
+    bad[1] = bad[1].transpose(1, 2).contiguous().transpose(1, 2)
+    with pytest.raises(ValueError, match="k_cache must be contiguous"):
+        kda.kda_paged_attention(*bad)
+    with pytest.raises(kda.KDAError, match="KDA_ERR_WORKSPACE"):
+        kda.kda_paged_attention(*args, workspace=torch.empty(16, dtype=torch.uint8, device=dev))
+    with pytest.raises(kda.KDAError, match="KDA_ERR_INVALID_ARG"):
+        kda.kda_paged_attention(*args, scale=-1.0)
+    slot = torch.zeros(3, dtype=torch.int64, device=dev)
+    kv = torch.zeros(3, 4, 32, device=dev)
+    with pytest.raises(ValueError, match="v: the heads of a token must be contiguous"):
+        kda.kda_cache_append(kv[:, :2], kv[:, ::2], args[1], args[2], slot)
+    with pytest.raises(TypeError, match="slot_map must be torch.int64"):
+        kda.kda_cache_append(kv[:, :2], kv[:, :2], args[1], args[2], slot.int())
+    with pytest.raises(TypeError, match="draft_len must be torch.int32"):
+        p = torch.zeros(2, 2, 10, device=dev)
+        kda.kda_verify_draft(p, None, torch.zeros(2, 1, dtype=torch.int32, device=dev), torch.zeros(2, 2, device=dev),
+                             torch.zeros(2, device=dev))
+    with pytest.raises(TypeError, match="must be a tensor"):
+        kda.kda_verify_draft(None, None, None, None)
+
+
 def test_attention_far_offsets():
     """A page whose element offset passes 32 bits, on both paths."""
     dev = need_gpu()

@@ -179,20 +179,6 @@ def test_binding_attention():
         call(q=z(5, 4, 32, dt=torch.float16))
 
 
-def test_binding_strided_rows():
-    from kimi_delta_attention_chunked_gb300 import _paged
-    t = torch.zeros(5, 12, 32)
-    cpu = -1                                                   # get_device() of a CPU tensor
-    ptr, stride = _paged._rows("q", t[:, 4:8], cpu, torch.float32, (5, 4, 32))
-    assert ptr == t.data_ptr() + 4 * 32 * 4 and stride == 12 * 32
-    with pytest.raises(ValueError, match="contiguous"):
-        _paged._rows("q", t[:, ::2][:, :4], cpu, torch.float32, (5, 4, 32))
-    with pytest.raises(ValueError, match="contiguous"):
-        _paged._rows("q", torch.zeros(5, 32, 4).transpose(1, 2), cpu, torch.float32, (5, 4, 32))
-    with pytest.raises(ValueError, match="overlap"):
-        _paged._rows("q", torch.zeros(1, 4, 32).expand(5, 4, 32), cpu, torch.float32, (5, 4, 32))
-
-
 def test_binding_verify():
     ok = dict(target=z(2, 4, 10), draft=z(2, 3, 10), draft_tokens=i32(2, 3), uniforms=z(2, 4))
     call = lambda **kw: kda.kda_verify_draft(**{**ok, **kw})  # noqa: E731
