@@ -5,9 +5,12 @@
 // Gv query heads that share a cache head, against the 128- or 64-key tiles that
 // any of their rows sees.  The tiles of all units, in the order request, head,
 // unit, tile, are one line, and CTA c of C takes the c-th of C equal pieces of
-// it: every CTA has the same number of tiles whatever the lengths are.  A unit
-// that a border cuts is finished by each of its CTAs into fp32 partial rows,
-// which the merge kernel joins.  A CTA finds its piece itself, from the lengths
+// it: every CTA has the same work whatever the lengths are.  Before a unit's
+// tiles the line has `extra` places that stand for its fixed cost (the pipeline
+// drains and the output is written, 2 to 4 us, the time of one to two tiles); without
+// them the CTAs of a decode batch's short requests finished 20 % behind the others.
+// A unit that a border cuts is finished by each of its CTAs into fp32 partial
+// rows, which the merge kernel joins.  A CTA finds its piece itself, from the lengths
 // on the device: no plan is made on the host, and no extra launch is needed.
 #pragma once
 
@@ -54,6 +57,13 @@ __device__ __forceinline__ Req load_req(const Shape& s, const int32_t* __restric
     const long long cap = (long long)s.blocks << s.page_log2;
     r.kend = (int)min((long long)seq, cap);
     return r;
+}
+
+// Places before a unit's tiles, for so many tiles and CTAs: none in a short call, where a
+// CTA without tiles would leave another with two.
+template <typename I>
+__device__ __forceinline__ int unit_extra(I tiles, int C) {
+    return tiles >= (I)(8 * C) ? 2 : tiles >= (I)(2 * C) ? 1 : 0;
 }
 
 __device__ __forceinline__ int n_units(const Shape& s, const Req& r) { return (r.len + s.U - 1) / s.U; }
@@ -111,8 +121,9 @@ __device__ __forceinline__ I request_tiles(const Shape& s, const Req& r) {
 struct Piece {
     unsigned long long begin, end, total;          // tiles [begin, end) of `total`
     unsigned long long off;                        // begin - first tile of request n
-    unsigned long long tiles;                      // tiles of request n for one head
+    unsigned long long tiles;                      // length of request n for one head
     int n, ctas;                                   // first request; CTAs that have a piece
+    int extra;                                     // places before a unit's tiles
 };
 
 // Finds the piece of CTA `c` of `C`.  Every thread of the block (NT of them)
@@ -122,16 +133,16 @@ __device__ __forceinline__ Piece find_piece(const Shape& s, const int32_t* __res
                                             const int32_t* __restrict__ seq_len, int c, int C,
                                             unsigned long long* cost,
                                             unsigned long long* red, Piece* shared) {
-    constexpr int NW = NT / 32;
+    constexpr int NW = NT / 32, kExtra = 2;            // a large step
     const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
     for (int base = 0; base < s.n_req; base += NT) {
         const int n = base + tid;
         Req r{0, 0, 0, 0};
         if (n < s.n_req) r = load_req(s, cu, seq_len, n);
-        const unsigned long long x = request_tiles<unsigned long long>(s, r);
+        const unsigned long long x = request_tiles<unsigned long long>(s, r) + (unsigned)(kExtra * n_units(s, r));
         if (n < s.n_req) cost[n] = x;
     }
-    if (tid == 0) *shared = Piece{0, 0, 0, 0, 0, 0, 0};
+    if (tid == 0) *shared = Piece{0, 0, 0, 0, 0, 0, 0, 0};
     __syncthreads();
     // each thread takes `per` consecutive requests of the running sum
     const int per = (s.n_req + NT - 1) / NT, n0 = min(tid * per, s.n_req), n1 = min(n0 + per, s.n_req);
@@ -173,6 +184,7 @@ __device__ __forceinline__ Piece find_piece(const Shape& s, const int32_t* __res
             shared->tiles = cost[n];
             shared->n = n;
             shared->ctas = ctas;
+            shared->extra = kExtra;
         }
     }
     __syncthreads();
@@ -196,13 +208,16 @@ constexpr long long kNarrowTiles = 1 << 22;            // times kMaxCtas: 2^31
 template <typename I>
 struct Walker {
     I at, end, total;
-    int ctas;
-    int n, h, i, skip;                             // next unit; tiles of it that lie before the piece
+    int ctas, c, extra;
+    int n, h, i, in;                               // next unit; places of it that lie before the piece
     Req r;
     int units;
 
     // From the piece that the whole block found.
-    __device__ __forceinline__ void start(const Shape& s, const int32_t* cu, const int32_t* seq_len, const Piece& p) {
+    __device__ __forceinline__ void start(const Shape& s, const int32_t* cu, const int32_t* seq_len, const Piece& p,
+                                          int cta) {
+        c = cta;
+        extra = p.extra;
         at = (I)p.begin;
         end = (I)p.end;
         total = (I)p.total;
@@ -217,18 +232,22 @@ struct Walker {
     // itself, 32 requests at a time, in 32 bits, while the rest of the block sets
     // up.  Kept short: a small call spends more on fetching instructions than on
     // running them.
-    __device__ __forceinline__ void start_narrow(const Shape& s, const int32_t* cu, const int32_t* seq_len, int c, int C) {
+    __device__ __forceinline__ void start_narrow(const Shape& s, const int32_t* cu, const int32_t* seq_len, int cta, int C) {
         const int lane = threadIdx.x & 31;
+        c = cta;
         Req q{0, 0, 0, 0};
-        unsigned x = 0, sum = 0;
+        unsigned x = 0, sum = 0, units_sum = 0;
 #pragma unroll 1
         for (int base = 0; base < s.n_req; base += 32) {
             q = Req{0, 0, 0, 0};
             if (base + lane < s.n_req) q = load_req(s, cu, seq_len, base + lane);
             x = request_tiles<unsigned>(s, q);
             sum += x;
+            units_sum += n_units(s, q);
         }
         total = __reduce_add_sync(0xffffffffu, sum) * (unsigned)s.Hv;
+        extra = unit_extra(total, C);
+        total += (I)extra * __reduce_add_sync(0xffffffffu, units_sum) * (unsigned)s.Hv;
         ctas = (int)min((unsigned)C, (unsigned)total);
         at = end = 0;
         if (c >= ctas) return;
@@ -242,6 +261,7 @@ struct Walker {
                 if (base + lane < s.n_req) q = load_req(s, cu, seq_len, base + lane);
                 x = request_tiles<unsigned>(s, q);
             }
+            x += extra * n_units(s, q);
             unsigned incl = x * (unsigned)s.Hv;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -265,13 +285,13 @@ struct Walker {
         }
     }
 
-    // Head, unit and tile that lie `off` tiles behind the start of request n, whose heads have `tiles` each.
-    __device__ __forceinline__ void first_unit(const Shape& s, I off, I tiles) {
+    // Head, unit and place that lie `off` places behind the start of request n, whose heads have `len` each.
+    __device__ __forceinline__ void first_unit(const Shape& s, I off, I len) {
         units = n_units(s, r);
-        h = (int)(off / tiles);
-        I left = off - (I)h * tiles;
+        h = (int)(off / len);
+        I left = off - (I)h * len;
         i = 0;
-        skip = (int)left;
+        in = (int)left;
         if (units <= 1) return;
         const int lane = threadIdx.x & 31;
 #pragma unroll 1
@@ -280,7 +300,7 @@ struct Walker {
             if (base + lane < units) {
                 int tb, te;
                 unit_span(s, r, base + lane, tb, te);
-                x = te - tb;
+                x = te - tb + extra;
             }
             unsigned incl = x;
 #pragma unroll
@@ -292,7 +312,7 @@ struct Walker {
             if (hit) {
                 const int src = __ffs((int)hit) - 1;
                 i = base + src;
-                skip = (int)(left - __shfl_sync(0xffffffffu, incl - x, src));
+                in = (int)(left - __shfl_sync(0xffffffffu, incl - x, src));
                 return;
             }
             left -= __shfl_sync(0xffffffffu, incl, 31);
@@ -301,45 +321,43 @@ struct Walker {
 
     // The next part, or false at the end of the piece.
     __device__ __forceinline__ bool next(const Shape& s, const int32_t* cu, const int32_t* seq_len, Unit& u) {
-        if (at >= end) return false;
-        while (i >= units) {
-            i = 0;
-            if (units == 0 || ++h >= s.Hv) {
-                h = 0;
-                if (++n >= s.n_req) return false;
-                r = load_req(s, cu, seq_len, n);
-                units = n_units(s, r);
+        while (at < end) {
+            while (i >= units) {
+                i = 0;
+                if (units == 0 || ++h >= s.Hv) {
+                    h = 0;
+                    if (++n >= s.n_req) return false;
+                    r = load_req(s, cu, seq_len, n);
+                    units = n_units(s, r);
+                }
             }
+            int tb, te;
+            unit_span(s, r, i, tb, te);
+            const int len = extra + te - tb;
+            const int take = (int)min((I)(len - in), (I)(end - at));
+            const int t0 = max(in - extra, 0), t1 = max(in + take - extra, 0);     // tiles of this part
+            const I fin = at - (unsigned)in + (unsigned)len;                       // the unit's end
+            u.n = n;
+            u.kvh = h / s.sub;
+            u.qh0 = h * s.Gv;
+            u.tok0 = r.tok0 + i * s.U;
+            u.ntok = min(s.U, r.len - i * s.U);
+            u.pos = r.pos0 + i * s.U;
+            u.kend = r.kend;
+            u.tb = tb + t0;
+            u.te = tb + t1;
+            u.first = t0 == 0;
+            u.last = u.te == te;
+            // CTA c begins at total * c / ctas, so the last one that has a place below `fin` is
+            // ceil(fin * ctas / total) - 1
+            u.parts = 1;
+            if (!u.last) u.parts = (int)((fin * (unsigned)ctas + total - 1) / total) - c;
+            at += (unsigned)take;
+            in = 0;
+            ++i;
+            if (t1 > t0) return true;
         }
-        int tb, te;
-        unit_span(s, r, i, tb, te);
-        const int full_end = te;
-        tb += skip;
-        const I fin = at + (unsigned)(te - tb);
-        if (fin > end) te = tb + (int)(end - at);
-        u.n = n;
-        u.kvh = h / s.sub;
-        u.qh0 = h * s.Gv;
-        u.tok0 = r.tok0 + i * s.U;
-        u.ntok = min(s.U, r.len - i * s.U);
-        u.pos = r.pos0 + i * s.U;
-        u.kend = r.kend;
-        u.tb = tb;
-        u.te = te;
-        u.first = skip == 0;
-        u.last = te == full_end;
-        u.parts = 1;
-        if (u.first && !u.last) {
-            // CTA c begins at total * c / ctas, so the last one that has a tile below `fin` is
-            // ceil(fin * ctas / total) - 1; likewise this one, from its first tile
-            const I hi = (fin * (unsigned)ctas + total - 1) / total;
-            const I lo = ((at + 1) * (unsigned)ctas + total - 1) / total;
-            u.parts = (int)(hi - lo) + 1;
-        }
-        at += (unsigned)(te - tb);
-        skip = 0;
-        ++i;
-        return true;
+        return false;
     }
 };
 

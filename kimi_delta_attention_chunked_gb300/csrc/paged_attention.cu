@@ -63,7 +63,7 @@ kda_paged_attention_simt_kernel(const T* __restrict__ q, const T* __restrict__ k
         const Piece piece = kda_paged::find_piece<kThreads>(s, cu, seq_len, blockIdx.x, gridDim.x,
                                                             reinterpret_cast<unsigned long long*>(smem_raw), s_red,
                                                             &s_piece);
-        if (w == 0) walk.start(s, cu, seq_len, piece);
+        if (w == 0) walk.start(s, cu, seq_len, piece, blockIdx.x);
     }
     if (tid == 0) parts.meta[blockIdx.x] = make_int4(0, 0, 0, 0);
 
@@ -459,7 +459,7 @@ kda_paged::Shape paged_shape(const PagedArgs& a, const PagedPlan& p) {
     s.tile_log2 = p.tile_log2;
     // the most tiles any lengths can give: each unit sees the whole table at most
     const long long units = (long long)s.Hv * (a.T / p.U + a.N);
-    const long long tiles = ((long long)a.blocks * a.page_size >> p.tile_log2) + 2;
+    const long long tiles = ((long long)a.blocks * a.page_size >> p.tile_log2) + 4;
     s.narrow = a.N <= kda_paged::kNarrowRequests && units < kda_paged::kNarrowTiles &&
                units * tiles < kda_paged::kNarrowTiles;
     return s;

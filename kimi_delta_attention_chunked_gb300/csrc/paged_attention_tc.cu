@@ -260,7 +260,7 @@ kda_paged_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __
         asm volatile("prefetch.tensormap [%0];" ::"l"(m) : "memory");
     }
     // this CTA's piece of the work: by the walking warp alone where it can
-    Piece piece{0, 0, 0, 0, 0, 0, 0};
+    Piece piece{0, 0, 0, 0, 0, 0, 0, 0};
     if (!s.narrow) {
         auto* cost = reinterpret_cast<unsigned long long*>(sm + C::KV0);
         auto* red = cost + kda_paged::kMaxRequests;
@@ -315,17 +315,16 @@ kda_paged_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __
             publish(walk);
         } else {
             Walker<unsigned long long> walk;
-            walk.start(s, cu, seq_len, piece);
+            walk.start(s, cu, seq_len, piece, blockIdx.x);
             publish(walk);
         }
         if (lane == 0) parts.meta[blockIdx.x] = meta;
     } else if (w == kCopyWarp) {
-        // ---------------- copies.  Order of the ring: at step g the values of step
-        // g - 2, then the keys of step g, each when first needed
+        // ---------------- copies: the keys, then the values of each tile.  (With the values two
+        // steps behind, in the order of the products, a unit's last ones came behind the next unit's
+        // first keys, and its output held up the ring.)
         const int pieces = s.page_log2 >= kKeysLog2 ? 1 : kKeys >> s.page_log2;   // pages of a tile
         const int box_rows = min(1 << s.page_log2, kKeys);
-        struct Values { int load, page, y, kvh; };
-        Values older{0, 0, 0, 0}, newer{0, 0, 0, 0};   // of steps g - 2 and g - 1
         auto page_of = [&](const Unit& u, int tile) {  // lane's page of the tile; n_pages reads as zeros
             const int key = (tile << kKeysLog2) + lane * box_rows;
             int page = -1;
@@ -362,31 +361,19 @@ kda_paged_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __
             Unit u;
             if (!read_unit(k, u)) break;
             const bool two = u.ntok > BT;
-            const int steps = (u.te - u.tb) << (two ? 1 : 0);
             int next_page = page_of(u, u.tb);
-            for (int t = 0; ok && t < steps; ++t) {
-                if (older.load) ok = load(&vmap, older.page, older.y, older.kvh);
-                older = newer;
-                const bool first_use = !two || (t & 1) == 0;
-                newer.load = first_use;
-                if (ok && first_use) {
-                    const int tile = u.tb + (two ? t >> 1 : t);
-                    const int page = next_page;
-                    if (tile + 1 < u.te) next_page = page_of(u, tile + 1);
-                    const int y = (tile << kKeysLog2) & ((1 << s.page_log2) - 1) & ~(box_rows - 1);
-                    ok = load(&kmap, page, y, u.kvh);
-                    newer.page = page;
-                    newer.y = y;
-                    newer.kvh = u.kvh;
-                }
-                if (ok && t == 0) {
+            for (int tile = u.tb; ok && tile < u.te; ++tile) {
+                const int page = next_page;
+                if (tile + 1 < u.te) next_page = page_of(u, tile + 1);
+                const int y = (tile << kKeysLog2) & ((1 << s.page_log2) - 1) & ~(box_rows - 1);
+                ok = load(&kmap, page, y, u.kvh);
+                if (ok && tile == u.tb) {
                     ok = k == 0 || wait(&tl.q_empty, (k - 1) & 1);
                     if (ok) load_q(u, two);
                 }
+                if (ok) ok = load(&vmap, page, y, u.kvh);
             }
         }
-        if (ok && older.load) ok = load(&vmap, older.page, older.y, older.kvh);
-        if (ok && newer.load) ok = load(&vmap, newer.page, newer.y, newer.kvh);
     } else if (w == kIssueWarp) {
         // ---------------- products.  All lanes wait, lane 0 issues
         const uint32_t id_s = kda::idesc_bf16(128, 128, 0, 0), id_o = kda::idesc_bf16(128, D, 0, 1);
@@ -394,19 +381,26 @@ kda_paged_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __
         const uint64_t k_desc = kda::sw128_desc(kda::smem_u32(sm + C::KV0), 16, 1024);
         const uint64_t v_desc = kda::sw128_desc(kda::smem_u32(sm + C::KV0), kPanel, 1024);
         int g = 0, v_stage = 0, k_stage = 0;
-        int stage = 0;                                 // next stage of the ring, and its parity
+        // the next tile's keys, and the parity of their stage; its values have the stage behind
+        int stage = 0;
         uint32_t ring = 0;
-        auto take_stage = [&](int& at) -> bool {
-            at = stage;
+        auto advance = [&](int& at, uint32_t& parity) {
+            if (++at == C::STAGES) { at = 0; parity ^= 1; }
+        };
+        auto take_keys = [&](int& v_at, uint32_t& v_ring) -> bool {
+            k_stage = stage;
             if (!wait(&tl.kv_full[stage], ring)) return false;
-            if (++stage == C::STAGES) { stage = 0; ring ^= 1; }
+            advance(stage, ring);
+            v_at = stage;
+            v_ring = ring;
+            advance(stage, ring);
             return true;
         };
         uint32_t p_phase = 0;                          // bit h: parity of the next P_h
         bool issued = false;
         // a step whose second product is due: flags, key tile, and what its unit's rows see
         enum { kFirstUse = 1, kLastUse = 2, kAdd = 4, kFinal = 8, kDue = 16 };
-        struct Pending { int flags, tile, slot, kend; Sight si; };
+        struct Pending { int flags, tile, slot, kend, v_at; uint32_t v_ring; Sight si; };
         Pending older, newer;                          // of steps g - 2 and g - 1
         older.flags = newer.flags = 0;
 
@@ -455,7 +449,8 @@ kda_paged_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __
         // the values of a step are there and clean
         auto take_values = [&](const Pending& pv) -> bool {
             if (!(pv.flags & kFirstUse)) return true;
-            if (!take_stage(v_stage)) return false;
+            v_stage = pv.v_at;
+            if (!wait(&tl.kv_full[v_stage], pv.v_ring)) return false;
             clean(sm + C::KV0 + v_stage * C::TILE, pv);
             return true;
         };
@@ -497,8 +492,12 @@ kda_paged_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __
             if (!read_unit(k, u)) break;
             const int two = uniform(u.ntok > BT), tiles = uniform(u.te - u.tb), steps = tiles << two, tb = uniform(u.tb);
             const Sight si = sight(u, s.window, 0, u.ntok - 1);
+            int v_at = 0;                              // stage of the current tile's values, its parity
+            uint32_t v_ring = 0;
             auto due_after = [&](int t) {              // the second product of step t
                 Pending pv;
+                pv.v_at = v_at;
+                pv.v_ring = v_ring;
                 const int lone = !two || (t & 1);
                 pv.flags = kDue | (!two || !(t & 1) ? kFirstUse : 0) | (lone ? kLastUse : 0) | (t >= 2 ? kAdd : 0) |
                            (t >= steps - 2 ? kFinal : 0);
@@ -514,7 +513,7 @@ kda_paged_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __
             for (int t = 0; t < slow; ++t, ++g) {
                 const int h = g & 1;
                 if (older.flags & kDue) ok = values_step(h, older);
-                if (ok && (!two || t == 0)) ok = take_stage(k_stage);
+                if (ok && (!two || t == 0)) ok = take_keys(v_at, v_ring);
                 if (ok && t == 0) ok = wait(&tl.q_full, k & 1);
                 if (!ok) break;
                 kda::tc_fence_after();
@@ -532,12 +531,14 @@ kda_paged_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __
             for (int j = 1; j < tiles; ++j) {
                 pv.tile = tb + j - 1;
                 pv.flags = kDue | kFirstUse;
+                pv.v_at = v_at;
+                pv.v_ring = v_ring;
                 ok = take_values(pv) && take_weights(h0);
                 if (!ok) break;
                 kda::tc_fence_after();
                 const int add = j > 1 ? kAdd : 0;
                 if (elect_one()) issue_values(h0, add);
-                ok = take_stage(k_stage);
+                ok = take_keys(v_at, v_ring);
                 if (!ok) break;
                 if (elect_one()) issue_scores(h0, 0, 0);
                 ok = take_weights(h1);
