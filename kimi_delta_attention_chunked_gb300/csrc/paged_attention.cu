@@ -267,7 +267,7 @@ kda_paged_attention_simt_kernel(const T* __restrict__ q, const T* __restrict__ k
 //     o = sum_i 2^(m_i - M) o_i / sum_i 2^(m_i - M) l_i.
 // blockIdx.x names the CTA in which the unit begins.  D / 4 threads take the
 // columns of a row.  A unit cut once or twice gives each such group rows of its
-// own, four at a time; the parts of one cut more often are shared out among up
+// own, two at a time; the parts of one cut more often are shared out among up
 // to eight groups, so that it costs a few load latencies too.  Reads each
 // partial row once.
 constexpr int kMergeThreads = 256;
@@ -313,21 +313,23 @@ kda_paged_merge_kernel(Partials parts, int Gv, int Hq, T* __restrict__ o, float*
         if (lse && x == 0) lse[at] = m.l == 0.f ? -INFINITY : (m.top + log2f(m.l)) * kLn2;
     };
     if (n <= 3) {
-        constexpr int kR = 4;
+        constexpr int kR = 2;                          // rows a group has in flight
         const int step = gridDim.y * GROUPS;
         for (int r0 = blockIdx.y * GROUPS + grp; r0 < rows; r0 += kR * step) {
-            Merged m[kR];
-            for (int i = 0; i < n; ++i) {
-                float2 st[kR];
-                float4 v[kR];
-#pragma unroll
-                for (int e = 0; e < kR; ++e) part(i, min(r0 + e * step, rows - 1), st[e], v[e]);
-#pragma unroll
-                for (int e = 0; e < kR; ++e) m[e].add(st[e], v[e]);
-            }
+            float2 st[kR][3];
+            float4 v[kR][3];
 #pragma unroll
             for (int e = 0; e < kR; ++e)
-                if (r0 + e * step < rows) put(m[e], r0 + e * step);
+#pragma unroll
+                for (int i = 0; i < 3; ++i) part(min(i, n - 1), min(r0 + e * step, rows - 1), st[e][i], v[e][i]);
+#pragma unroll
+            for (int e = 0; e < kR; ++e) {
+                Merged m;
+#pragma unroll
+                for (int i = 0; i < 3; ++i)
+                    if (i < n) m.add(st[e][i], v[e][i]);
+                if (r0 + e * step < rows) put(m, r0 + e * step);
+            }
         }
         return;
     }

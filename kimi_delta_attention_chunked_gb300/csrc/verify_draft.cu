@@ -7,15 +7,28 @@
 //
 // The drawn index is a whole number that must not depend on how the sum was
 // cut up, and in fp32 the running sum of 10^5 probabilities is off by more than
-// many of them.  So probabilities become integers, p -> floor(p 2^60), and
-// every sum is exact in 64 bits.  The conversion is a shift of the mantissa (the
-// fp64 units and 64-bit conversions of this GPU are far slower than its memory).
+// many of them.  So the sums are in integers, which no order of summation
+// changes, in two forms:
+//   exact  p -> floor(p 2^60), the mantissa shifted in 64 bits: 12 integer
+//          instructions a number, more than the memory gives time for;
+//   quick  p -> round(p 2^46), from the bits of two fp32 sums: with x = fl(p + 1),
+//          bits(x) - bits(1) = round(p 2^23), and with l = p - (x - 1) (exact),
+//          bits(l 2^23 + 1.5) - bits(1.5) = round(l 2^46): 5 fp32 instructions.
+// A quick sum of V terms is off by at most V.  Where that could decide the index
+// (the threshold within 2 V + 2 of a border of the element found, or so small a
+// sum; about once in a thousand draws at V = 160,000) one CTA does the row again
+// in the exact form.
 //
-// A cluster of CTAs takes one request: each sums its part of the row (16 bytes
-// of p and q of it per thread and step where the row is aligned), the parts are
-// exchanged through distributed shared memory, and the CTA that holds the
+// A cluster of CTAs takes one request: each sums its part of the row, the parts
+// are exchanged through distributed shared memory, and the CTA that holds the
 // crossing finds the warp's part, then the element, by scanning again what is
 // by then in L2.  Only row a is read: bound by HBM, 2 V numbers a request.
+// 128 requests, V = 160,001, fp32 (164 MB, floor 24.5 us), GPU time: 47 us with
+// the exact form throughout (issue bound), 37 us with the quick one.  Then three
+// CTAs of 512 threads an SM, 8 numbers of each row in flight a thread: 43 us with six of 256 (more,
+// smaller clusters wait longer for each other), 39 us with 4 numbers, 47 us with two of 1024.
+// What is left of it: the chain before the row (length, token, two probabilities: three
+// dependent reads) and behind it (cluster barrier, second scan), in which nothing streams.
 #include <algorithm>
 #include <cooperative_groups.h>
 
@@ -25,26 +38,48 @@ namespace cg = cooperative_groups;
 
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
-constexpr int kPerSm = 6;                              // CTAs of an SM
+constexpr int kPerSm = 3;                              // CTAs of an SM
 
-// floor(min(max(p, 0), 1) 2^60); NaN counts as 0
+// A probability as it counts: 0 ... 1, NaN as 0.
+__device__ __forceinline__ float clean(float p) { return __saturatef(p); }
+
+// floor(p 2^60) of a clean p
 __device__ __forceinline__ unsigned long long fixed60(float p) {
-    const unsigned b = __float_as_uint(__saturatef(p));    // 0 ... 1, NaN becomes 0
+    const unsigned b = __float_as_uint(p);
     const unsigned long long m = (unsigned long long)((b & 0x7fffffu) | 0x800000u) << 37;
     return m >> min(127u - (b >> 23), 63u);                // p = 1.m 2^(e - 127), e <= 127; below 2^-60: 0
 }
+
+// The two words of a clean p in the quick form, each with the bits of its constant added.
+__device__ __forceinline__ void quick_words(float p, int& hi, int& lo) {
+    const float x = __fadd_rn(p, 1.f);
+    hi = __float_as_int(x);
+    lo = __float_as_int(__fmaf_rn(__fadd_rn(p, -__fadd_rn(x, -1.f)), 8388608.f, 1.5f));
+}
+constexpr int kHiBits = 0x3f800000, kLoBits = 0x3fc00000;  // of 1 and 1.5
 
 template <typename T>
 struct Row {
     const T* p;
     const T* q;                                            // nullptr: no draft row
     int masked;                                            // index with q = 1 (a token drafted with certainty), or -1
+    // element v, in units of 2^-60 (exact) or 2^-46
+    template <bool kExact>
     __device__ __forceinline__ long long at(int v) const {
-        const long long a = (long long)fixed60(kda::io<T>::ld(p + v));
-        if (q) return max(a - (long long)fixed60(kda::io<T>::ld(q + v)), 0ll);
-        return v == masked ? 0ll : a;
+        const float a = clean(kda::io<T>::ld(p + v));
+        if (!q && v == masked) return 0;
+        const float b = q ? clean(kda::io<T>::ld(q + v)) : 0.f;
+        if (!(a > b)) return 0;
+        if constexpr (kExact) {
+            return (long long)(fixed60(a) - fixed60(b));
+        } else {
+            int ah, al, bh, bl;
+            quick_words(a, ah, al);
+            quick_words(b, bh, bl);
+            return ((long long)(ah - bh) << 23) + (al - bl);
+        }
     }
 };
 
@@ -54,36 +89,120 @@ __device__ __forceinline__ long long warp_sum(long long x) {
     return x;
 }
 
-// Sum over [lo, hi), a warp's part, lanes side by side.
+// Quick sum over [lo, hi), a warp's part, lanes side by side.
 template <typename T>
-__device__ __forceinline__ long long part_sum(const Row<T>& row, int lo, int hi) {
+__device__ __forceinline__ long long quick_sum(const Row<T>& row, int lo, int hi) {
     const int lane = threadIdx.x & 31;
+    constexpr int kU = 8;
     long long s = 0;
-    constexpr int kU = 4, kStep = 32 * kU;
-    float a[kU], b[kU];
-    // four numbers of either row in registers while the four behind them are on their way
-    auto load = [&](int v, float* x, float* y) {
+    int v = lo + lane;
+    for (; v + 32 * (kU - 1) < hi; v += 32 * kU) {
+        float a[kU], b[kU];
 #pragma unroll
-        for (int e = 0; e < kU; ++e) x[e] = v + 32 * e < hi ? kda::io<T>::ld(row.p + v + 32 * e) : 0.f;
+        for (int e = 0; e < kU; ++e) a[e] = kda::io<T>::ld(row.p + v + 32 * e);
+        int h = 0, l = 0;                                  // of 8 numbers: |h| <= 2^26, |l| <= 2^26
         if (row.q) {
 #pragma unroll
-            for (int e = 0; e < kU; ++e) y[e] = v + 32 * e < hi ? kda::io<T>::ld(row.q + v + 32 * e) : 0.f;
-        }
-    };
-    load(lo + lane, a, b);
-    for (int v = lo + lane; v < hi; v += kStep) {
-        float an[kU], bn[kU];
-        load(v + kStep, an, bn);
+            for (int e = 0; e < kU; ++e) b[e] = kda::io<T>::ld(row.q + v + 32 * e);
 #pragma unroll
-        for (int e = 0; e < kU; ++e) {
-            const long long x = (long long)fixed60(a[e]);
-            if (row.q) s += max(x - (long long)fixed60(b[e]), 0ll);
-            else s += v + 32 * e == row.masked ? 0ll : x;
-            a[e] = an[e];
-            b[e] = bn[e];
+            for (int e = 0; e < kU; ++e) {
+                const float x = clean(a[e]), y = clean(b[e]);
+                int xh, xl, yh, yl;
+                quick_words(x, xh, xl);
+                quick_words(y, yh, yl);
+                if (x > y) {
+                    h += xh - yh;
+                    l += xl - yl;
+                }
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < kU; ++e) {
+                int xh, xl;
+                quick_words(clean(a[e]), xh, xl);
+                if (v + 32 * e != row.masked) {
+                    h += xh - kHiBits;
+                    l += xl - kLoBits;
+                }
+            }
         }
+        s += ((long long)h << 23) + l;
     }
+#pragma unroll 4
+    for (; v < hi; v += 32) s += row.template at<false>(v);
     return warp_sum(s);
+}
+
+// floor(u total), inside [0, total - 1]: u at or above 1 takes the last positive
+// element, u below 0 or NaN the first
+__device__ __forceinline__ long long threshold(float u, long long total) {
+    const double want = (double)u * (double)total;
+    const long long thr = want > 0.0 ? (want < 9.0e18 ? (long long)want : total) : 0;
+    return min(thr, total - 1);
+}
+
+// The element of [c0, c1) at which the running sum passes `thr`, given its warps'
+// parts in s_warp; the sum before it in `before`, its own value in `value`.  All threads of the
+// block call it; the one that finds it gets the index, the others -1.
+template <bool kExact, typename T, typename F>
+__device__ __forceinline__ int locate(const Row<T>& row, F part_lo, long long thr, const long long* s_warp,
+                                      long long* s_scan, long long& before, long long& value) {
+    const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
+    long long base = 0;
+    int part = 0;
+    for (; part < kWarps - 1 && thr >= base + s_warp[part]; ++part) base += s_warp[part];
+    // every thread takes `per` consecutive elements of that warp's part
+    const int lo = part_lo(part), hi = part_lo(part + 1), per = (hi - lo + kThreads - 1) / kThreads;
+    const int v0 = min(lo + tid * per, hi), v1 = min(v0 + per, hi);
+    long long mine = 0;
+    for (int v = v0; v < v1; ++v) mine += row.template at<kExact>(v);
+    long long incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long t = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += t;
+    }
+    if (lane == 31) s_scan[w] = incl;
+    __syncthreads();
+    incl += base;
+    for (int i = 0; i < w; ++i) incl += s_scan[i];
+    before = incl - mine;
+    if (thr < before || thr >= incl) return -1;
+    for (int v = v0; v < v1; ++v) {
+        value = row.template at<kExact>(v);
+        if (thr < before + value) return v;
+        before += value;
+    }
+    return -1;
+}
+
+// The whole draw in the exact form, by one CTA.
+template <typename T>
+__device__ __noinline__ void draw_exact(Row<T> row, int V, float u, int32_t* out, long long* s_warp, long long* s_scan) {
+    const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
+    auto part_lo = [&](int i) { return (int)((long long)V * i / kWarps); };
+    long long total = 0;
+    for (int attempt = 0; attempt < 2; ++attempt) {
+        long long s = 0;
+#pragma unroll 4
+        for (int v = part_lo(w) + lane; v < part_lo(w + 1); v += 32) s += row.template at<true>(v);
+        s = warp_sum(s);
+        __syncthreads();
+        if (lane == 0) s_warp[w] = s;
+        __syncthreads();
+        total = 0;
+        for (int i = 0; i < kWarps; ++i) total += s_warp[i];
+        if (total > 0 || (!row.q && row.masked < 0)) break;
+        row.q = nullptr;                                   // nothing is left of the row: draw from the target itself
+        row.masked = -1;
+    }
+    if (total <= 0) {
+        if (tid == 0) *out = V - 1;
+        return;
+    }
+    long long before, value;
+    const int v = locate<true>(row, part_lo, threshold(u, total), s_warp, s_scan, before, value);
+    if (v >= 0) *out = v;
 }
 
 template <typename T>
@@ -98,8 +217,8 @@ kda_verify_draft_kernel(const T* __restrict__ target, const T* __restrict__ draf
     const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
     kda_paged::wait_for_stream();
     cluster.barrier_arrive();                              // waited for before the first remote store: by then all CTAs run
-    __shared__ int s_count, s_len;
-    __shared__ long long s_cta[2][8];                      // each CTA's sum, pushed by it; one row per attempt
+    __shared__ int s_count, s_len, s_unsure;
+    __shared__ long long s_cta[8];                         // each CTA's sum, pushed by it
     __shared__ long long s_warp[kWarps];
     __shared__ long long s_scan[kWarps];
 
@@ -121,6 +240,7 @@ kda_verify_draft_kernel(const T* __restrict__ target, const T* __restrict__ draf
         if (lane == 0) {
             s_count = min(__ffs((int)fail) - 1, len);      // bits at and past len are set in `fail`
             s_len = len;
+            s_unsure = 0;
         }
     }
     __syncthreads();
@@ -133,80 +253,43 @@ kda_verify_draft_kernel(const T* __restrict__ target, const T* __restrict__ draf
 
     // ---- sums: CTA `rank` has [c0, c1), its warps equal parts of that
     const int c0 = (int)((long long)V * rank / ranks), c1 = (int)((long long)V * (rank + 1) / ranks);
-    auto warp_lo = [&](int i) { return c0 + (int)((long long)(c1 - c0) * i / kWarps); };
-    long long total = 0, before = 0, own = 0;
-    for (int attempt = 0; attempt < 2; ++attempt) {
-        const long long ws = part_sum(row, warp_lo(w), warp_lo(w + 1));
-        if (lane == 0) s_warp[w] = ws;
-        __syncthreads();
-        if (attempt == 0) cluster.barrier_wait();
-        if (w == 0) {
-            long long c = lane < kWarps ? s_warp[lane] : 0;
-            c = warp_sum(c);
-            if (lane < ranks) *cluster.map_shared_rank(&s_cta[attempt][rank], lane) = c;
-        }
-        cluster.sync();
-        total = before = 0;
-        for (int r = 0; r < ranks; ++r) {
-            const long long c = s_cta[attempt][r];
-            if (r < rank) before += c;
-            if (r == rank) own = c;
-            total += c;
-        }
-        if (total > 0 || (!row.q && row.masked < 0)) break;
-        row.q = nullptr;                                   // nothing is left of the row: draw from the target itself
-        row.masked = -1;
-        __syncthreads();
+    auto part_lo = [&](int i) { return c0 + (int)((long long)(c1 - c0) * i / kWarps); };
+    const long long ws = quick_sum(row, part_lo(w), part_lo(w + 1));
+    if (lane == 0) s_warp[w] = ws;
+    __syncthreads();
+    cluster.barrier_wait();
+    if (w == 0) {
+        const long long c = warp_sum(lane < kWarps ? s_warp[lane] : 0);
+        if (lane < ranks) *cluster.map_shared_rank(&s_cta[rank], lane) = c;
     }
+    cluster.sync();
     // no CTA touches another's shared memory past this point
-
+    long long total = 0, before = 0;
+    for (int r = 0; r < ranks; ++r) {
+        if (r < rank) before += s_cta[r];
+        total += s_cta[r];
+    }
     int32_t* out = tokens + (size_t)n * (K + 1);
     if (rank == 0) {
         if (tid <= K && tid != a) out[tid] = tid < a ? draft_tokens[(size_t)n * K + tid] : -1;
-        if (tid == 0) {
-            commit_len[n] = a + 1;
-            if (total <= 0) out[a] = V - 1;
-        }
+        if (tid == 0) commit_len[n] = a + 1;
     }
-    if (total <= 0) return;
-    // ---- the first element whose running sum exceeds thr = floor(u total); u at
-    // or above 1 takes the last positive one, u below 0 or NaN the first
     const float u = uniforms[(size_t)n * (K + 1) + K];
-    const double want = (double)u * (double)total;
-    long long thr = want > 0.0 ? (want < 9.0e18 ? (long long)want : total) : 0;
-    thr = min(thr, total - 1);
-    if (thr < before || thr >= before + own) return;
-    thr -= before;
-    int part = 0;
-    for (; part < kWarps - 1; ++part) {
-        const long long c = s_warp[part];
-        if (thr < c) break;
-        thr -= c;
+    const long long margin = 2ll * V + 2;
+    if (total <= margin) {                                 // next to nothing is left of the row
+        if (rank == 0) draw_exact(row, V, u, out + a, s_warp, s_scan);
+        return;
     }
-    // every thread takes `per` consecutive elements of that warp's part
-    const int lo = warp_lo(part), hi = warp_lo(part + 1), per = (hi - lo + kThreads - 1) / kThreads;
-    const int v0 = min(lo + tid * per, hi), v1 = min(v0 + per, hi);
-    long long mine = 0;
-    for (int v = v0; v < v1; ++v) mine += row.at(v);
-    long long incl = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const long long t = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += t;
+    const long long thr = threshold(u, total) - before;
+    if (thr < 0 || thr >= s_cta[rank]) return;
+    long long sum, value;
+    const int v = locate<false>(row, part_lo, thr, s_warp, s_scan, sum, value);
+    if (v >= 0) {
+        if (thr - sum >= margin && sum + value - thr > margin) out[a] = v;
+        else s_unsure = 1;
     }
-    if (lane == 31) s_scan[w] = incl;
     __syncthreads();
-    for (int i = 0; i < w; ++i) incl += s_scan[i];
-    if (thr >= incl - mine && thr < incl) {
-        long long at = incl - mine;
-        for (int v = v0; v < v1; ++v) {
-            at += row.at(v);
-            if (thr < at) {
-                out[a] = v;
-                break;
-            }
-        }
-    }
+    if (s_unsure) draw_exact(row, V, u, out + a, s_warp, s_scan);
 }
 
 template <typename T>
