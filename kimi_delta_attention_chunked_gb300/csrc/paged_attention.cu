@@ -41,7 +41,7 @@ struct SimtSmem {
 };
 
 template <int D, typename T>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 2)
 kda_paged_attention_simt_kernel(const T* __restrict__ q, const T* __restrict__ kc, const T* __restrict__ vc,
                                 const int32_t* __restrict__ table, const int32_t* __restrict__ cu,
                                 const int32_t* __restrict__ seq_len, long long q_stride, Shape s, float scale_log2,
@@ -52,6 +52,7 @@ kda_paged_attention_simt_kernel(const T* __restrict__ q, const T* __restrict__ k
     __shared__ Piece s_piece;
     __shared__ Unit s_unit;
     __shared__ int s_more;
+    __shared__ int s_page[2][kTile / 16];              // pages of a tile, 16 keys each; -1: none
     const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
     kda_paged::wait_for_stream();
 
@@ -101,51 +102,61 @@ kda_paged_attention_simt_kernel(const T* __restrict__ q, const T* __restrict__ k
 #pragma unroll
             for (int c = 0; c < VC; ++c) acc[a][c] = 0.f;
 
+        // the pages of a tile are looked up a tile ahead, so that its loads wait for one read, not two
+        auto page_of = [&](int t) {
+            const int key = (t << kTileLog2) + 16 * tid;
+            int page = -1;
+            if (key < u.kend) page = table[(size_t)u.n * s.blocks + (key >> s.page_log2)];
+            return page < s.n_pages ? page : -1;
+        };
+        if (tid < kTile / 16) s_page[u.tb & 1][tid] = page_of(u.tb);
         for (int t = u.tb; t < u.te; ++t) {
             const int key0 = t << kTileLog2;
-            __syncthreads();                           // q stored; the tile before is consumed
+            __syncthreads();                           // q and the pages stored; the tile before is consumed
+            const int* pages = s_page[t & 1];
+            int next_page = -1;
+            if (tid < kTile / 16 && t + 1 < u.te) next_page = page_of(t + 1);
             // keys and values of the tile; places without a key become zero
-            constexpr int VEC = 16 / sizeof(T);        // the cache is 16-byte aligned
-            int ok_page = 0;                           // this thread's view of key `lane + 32 * half`, below
-            for (int e = tid; e < kTile * (D / VEC); e += kThreads) {
-                const int j = e / (D / VEC), c = (e % (D / VEC)) * VEC, key = key0 + j;
-                int page = -1;
-                if (key < u.kend) page = table[(size_t)u.n * s.blocks + (key >> s.page_log2)];
-                float kx[VEC], vx[VEC];
+            constexpr int VEC = 16 / sizeof(T), CH = D / VEC;        // the cache is 16-byte aligned
+            constexpr int kIter = kTile * CH / kThreads, kBatch = kIter < 4 ? kIter : 4;
+            static_assert(kIter >= 1 && kIter % kBatch == 0, "tile");
 #pragma unroll
-                for (int x = 0; x < VEC; ++x) kx[x] = vx[x] = 0.f;
-                if (page >= 0 && page < s.n_pages) {
-                    const size_t off = ((((size_t)page * s.Hkv + u.kvh) << s.page_log2) + (key & ((1 << s.page_log2) - 1))) * D + c;
-                    const uint4 ka = *reinterpret_cast<const uint4*>(kc + off), va = *reinterpret_cast<const uint4*>(vc + off);
-                    const T* kt = reinterpret_cast<const T*>(&ka);
-                    const T* vt = reinterpret_cast<const T*>(&va);
+            for (int i0 = 0; i0 < kIter; i0 += kBatch) {
+                uint4 ka[kBatch], va[kBatch];
 #pragma unroll
-                    for (int x = 0; x < VEC; ++x) {
-                        kx[x] = kda::io<T>::ld(kt + x);
-                        vx[x] = kda::io<T>::ld(vt + x);
+                for (int i = 0; i < kBatch; ++i) {
+                    const int e = tid + (i0 + i) * kThreads, j = e / CH, c = (e % CH) * VEC, key = key0 + j;
+                    const int page = pages[j >> 4];
+                    ka[i] = va[i] = make_uint4(0, 0, 0, 0);
+                    if (page >= 0 && key < u.kend) {
+                        const size_t off =
+                            ((((size_t)page * s.Hkv + u.kvh) << s.page_log2) + (key & ((1 << s.page_log2) - 1))) * D + c;
+                        ka[i] = *reinterpret_cast<const uint4*>(kc + off);
+                        va[i] = *reinterpret_cast<const uint4*>(vc + off);
                     }
                 }
 #pragma unroll
-                for (int x = 0; x < VEC; x += 4) {
-                    *reinterpret_cast<float4*>(&sm.k[j][c + x]) = make_float4(kx[x], kx[x + 1], kx[x + 2], kx[x + 3]);
-                    *reinterpret_cast<float4*>(&sm.v[j][c + x]) = make_float4(vx[x], vx[x + 1], vx[x + 2], vx[x + 3]);
-                }
-            }
-            // pages that exist, for the keys this thread judges below (sx + 8 i)
-            unsigned exists = 0;
-            ok_page = -1;
-            int last_block = -1;
+                for (int i = 0; i < kBatch; ++i) {
+                    const int e = tid + (i0 + i) * kThreads, j = e / CH, c = (e % CH) * VEC;
+                    const T* kt = reinterpret_cast<const T*>(&ka[i]);
+                    const T* vt = reinterpret_cast<const T*>(&va[i]);
 #pragma unroll
-            for (int i = 0; i < kTile / 8; ++i) {
-                const int key = key0 + sx + 8 * i;
-                if (key >= u.kend) continue;
-                const int b = key >> s.page_log2;
-                if (b != last_block) {
-                    ok_page = table[(size_t)u.n * s.blocks + b];
-                    last_block = b;
+                    for (int x = 0; x < VEC; x += 4) {
+                        *reinterpret_cast<float4*>(&sm.k[j][c + x]) =
+                            make_float4(kda::io<T>::ld(kt + x), kda::io<T>::ld(kt + x + 1), kda::io<T>::ld(kt + x + 2),
+                                        kda::io<T>::ld(kt + x + 3));
+                        *reinterpret_cast<float4*>(&sm.v[j][c + x]) =
+                            make_float4(kda::io<T>::ld(vt + x), kda::io<T>::ld(vt + x + 1), kda::io<T>::ld(vt + x + 2),
+                                        kda::io<T>::ld(vt + x + 3));
+                    }
                 }
-                if (ok_page >= 0 && ok_page < s.n_pages) exists |= 1u << i;
             }
+            if (tid < kTile / 16 && t + 1 < u.te) s_page[(t + 1) & 1][tid] = next_page;
+            // which of the keys this thread judges below (sx + 8 i) exist
+            unsigned exists = 0;
+#pragma unroll
+            for (int i = 0; i < kTile / 8; ++i)
+                if (key0 + sx + 8 * i < u.kend && pages[i >> 1] >= 0) exists |= 1u << i;
             __syncthreads();
             // scores: rows 2 ty, 2 ty + 1, keys tx + 16 i
             {

@@ -227,13 +227,13 @@ kda_verify_draft_kernel(const T* __restrict__ target, const T* __restrict__ draf
         int len = K;
         if (draft_len) len = min(max(draft_len[n], 0), K);
         bool stands = false;
-        if (lane < len) {
+        if (lane < K) {                                    // not `len`: the two reads go out together
             const int x = draft_tokens[(size_t)n * K + lane];
             if (x >= 0 && x < V) {
                 const float p = kda::io<T>::ld(target + ((size_t)n * (K + 1) + lane) * V + x);
                 const float q = draft ? kda::io<T>::ld(draft + ((size_t)n * K + lane) * V + x) : 1.f;
                 const float u = uniforms[(size_t)n * (K + 1) + lane];
-                stands = (double)u * (double)q < (double)p;
+                stands = lane < len && (double)u * (double)q < (double)p;
             }
         }
         const unsigned fail = ~__ballot_sync(0xffffffffu, stands);
