@@ -10,6 +10,7 @@
 
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
+#include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -108,22 +109,38 @@ const void* rows(const char* name, const Tensor& t, int dev, ScalarType dtype, a
     stride = std::max(t.stride(0), row);
     return t.data_ptr();
 }
-// the caller's output tensor, checked, or a new one (None)
-Tensor out(const char* name, PyObject* o, const Tensor& like, int dev, ScalarType dtype, at::IntArrayRef shape) {
-    if (o == Py_None) return at::empty(shape, like.options().dtype(dtype).requires_grad(false));
-    const Tensor& t = tensor(name, o);
-    need(name, t, dev, dtype, shape);
-    return t;
-}
-
-cudaStream_t stream_of(PyObject* o, int dev) {
-    if (o == Py_None) return c10::cuda::getCurrentCUDAStream(dev).stream();
+// The stream of a call.  Tensors made here belong to the current stream; used on another
+// one, the allocator must not hand their memory out again before that stream is done.
+struct Stream {
+    cudaStream_t handle;
+    int dev;
+    bool other;
+    Tensor make(const Tensor& like, ScalarType dtype, at::IntArrayRef shape) const {
+        Tensor t = at::empty(shape, like.options().dtype(dtype).requires_grad(false));
+        if (other && t.numel() > 0) {
+            const auto s = c10::cuda::getStreamFromExternal(handle, (c10::DeviceIndex)dev);
+            c10::cuda::CUDACachingAllocator::recordStream(t.storage().data_ptr(), s);
+        }
+        return t;
+    }
+};
+Stream stream_of(PyObject* o, int dev) {
+    const cudaStream_t current = c10::cuda::getCurrentCUDAStream(dev).stream();
+    if (o == Py_None) return {current, dev, false};
     PyObject* handle = PyObject_HasAttrString(o, "cuda_stream") ? PyObject_GetAttrString(o, "cuda_stream") : PyNumber_Long(o);
     if (!handle) throw Refused{};
     void* p = PyLong_AsVoidPtr(handle);
     Py_DECREF(handle);
     if (!p && PyErr_Occurred()) throw Refused{};
-    return static_cast<cudaStream_t>(p);
+    return {static_cast<cudaStream_t>(p), dev, p != current};
+}
+
+// the caller's output tensor, checked, or a new one (None)
+Tensor out(const char* name, PyObject* o, const Stream& s, const Tensor& like, ScalarType dtype, at::IntArrayRef shape) {
+    if (o == Py_None) return s.make(like, dtype, shape);
+    const Tensor& t = tensor(name, o);
+    need(name, t, s.dev, dtype, shape);
+    return t;
 }
 
 // Calls a C entry with `dev` current (the library looks up the SM count and the
@@ -183,15 +200,15 @@ PyObject* build_block_tables(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
         const int dev = device_of("ctx_len", ctx);
         void *ctx_p = need("ctx_len", ctx, dev, kI32, {n}), *add_p = need("new_len", add, dev, kI32, {n}),
              *free_p = need("free_pages", free, dev, kI32, {n_free}), *table_p = need("block_table", table, dev, kI32, {n, blocks});
-        Tensor cu = out("cu_seqlens", a[6], ctx, dev, kI32, {n + 1}), seq = out("seq_len", a[7], ctx, dev, kI32, {n}),
-               slot = out("slot_map", a[8], ctx, dev, kI64, {n_tokens}), pos = out("positions", a[9], ctx, dev, kI32, {n_tokens}),
-               taken = out("n_taken", a[10], ctx, dev, kI32, {1});
-        const cudaStream_t s = stream_of(a[11], dev);
+        const Stream s = stream_of(a[11], dev);
+        Tensor cu = out("cu_seqlens", a[6], s, ctx, kI32, {n + 1}), seq = out("seq_len", a[7], s, ctx, kI32, {n}),
+               slot = out("slot_map", a[8], s, ctx, kI64, {n_tokens}), pos = out("positions", a[9], s, ctx, kI32, {n_tokens}),
+               taken = out("n_taken", a[10], s, ctx, kI32, {1});
         call("kda_build_block_tables", dev, [&] {
             return g_kda.tables((const int32_t*)ctx_p, (const int32_t*)add_p, (const int32_t*)free_p, (int)n_free, (int)n,
                                 (int)blocks, (int)page, (int)n_tokens, (int32_t*)table_p, (int32_t*)cu.data_ptr(),
                                 (int32_t*)seq.data_ptr(), (int64_t*)slot.data_ptr(), (int32_t*)pos.data_ptr(),
-                                (int32_t*)taken.data_ptr(), s);
+                                (int32_t*)taken.data_ptr(), s.handle);
         });
         return tuple({cu, seq, slot, pos, taken});
     });
@@ -219,10 +236,10 @@ PyObject* cache_append(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
         const void *kp = rows("k", k, dev, dt, shape, ks), *vp = rows("v", v, dev, dt, shape, vs);
         void *kcp = need("k_cache", kc, dev, dt, kc.sizes()), *vcp = need("v_cache", vc, dev, dt, kc.sizes()),
              *sp = need("slot_map", slot, dev, kI64, {shape[0]});
-        const cudaStream_t s = stream_of(a[5], dev);
+        const Stream s = stream_of(a[5], dev);
         call("kda_cache_append", dev, [&] {
             return g_kda.append(kp, vp, (const int64_t*)sp, ks, vs, (int)shape[0], (int)shape[1], (int)shape[2],
-                                (int)kc.size(2), (int)kc.size(0), code, kcp, vcp, s);
+                                (int)kc.size(2), (int)kc.size(0), code, kcp, vcp, s.handle);
         });
         Py_RETURN_NONE;
     });
@@ -260,26 +277,26 @@ PyObject* paged_attention(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
         void *kcp = need("k_cache", kc, dev, dt, kc.sizes()), *vcp = need("v_cache", vc, dev, dt, kc.sizes()),
              *tp = need("block_table", table, dev, kI32, table.sizes()), *cup = need("cu_seqlens", cu, dev, kI32, {n + 1}),
              *sp = need("seq_len", seq, dev, kI32, {n});
-        Tensor o = out("o", a[8], q, dev, dt, q.sizes()), lse;
+        const Stream s = stream_of(a[12], dev);
+        Tensor o = out("o", a[8], s, q, dt, q.sizes()), lse;
         const int want_lse = a[9] != Py_None || PyObject_IsTrue(a[10]);
-        if (want_lse) lse = out("lse", a[9], q, dev, kF32, {T, heads});
+        if (want_lse) lse = out("lse", a[9], s, q, kF32, {T, heads});
         Tensor ws;
         size_t bytes;
         if (a[11] == Py_None) {
             bytes = g_kda.attention_size((int)T, (int)heads, (int)kv_heads, (int)d, code);
-            ws = at::empty({(int64_t)bytes}, q.options().dtype(ScalarType::Byte).requires_grad(false));
+            ws = s.make(q, ScalarType::Byte, {(int64_t)bytes});
         } else {
             ws = tensor("workspace", a[11]);
             if (!ws.is_cuda() || ws.get_device() != dev || !ws.is_contiguous())
                 value_error("workspace must be contiguous and on cuda:" + std::to_string(dev));
             bytes = (size_t)ws.numel() * ws.element_size();
         }
-        const cudaStream_t s = stream_of(a[12], dev);
         call("kda_paged_attention", dev, [&] {
             return g_kda.attention(qp, kcp, vcp, (const int32_t*)tp, (const int32_t*)cup, (const int32_t*)sp, qs, (int)n,
                                    (int)T, (int)heads, (int)kv_heads, (int)d, (int)kc.size(2), (int)blocks, (int)kc.size(0),
                                    (float)scale, (int)window, code, o.data_ptr(),
-                                   want_lse ? (float*)lse.data_ptr() : nullptr, ws.data_ptr(), bytes, s);
+                                   want_lse ? (float*)lse.data_ptr() : nullptr, ws.data_ptr(), bytes, s.handle);
         });
         if (want_lse) return tuple({o, lse});
         return THPVariable_Wrap(o);
@@ -304,11 +321,11 @@ PyObject* verify_draft(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
         void *pp = need("target", p, dev, dt, p_shape), *qp = has_draft ? need("draft", tensor("draft", a[1]), dev, dt, q_shape) : nullptr,
              *tp = need("draft_tokens", t, dev, kI32, {n, k}), *up = need("uniforms", u, dev, kF32, {n, k + 1}),
              *lp = has_len ? need("draft_len", tensor("draft_len", a[4]), dev, kI32, {n}) : nullptr;
-        Tensor tokens = out("tokens", a[5], p, dev, kI32, {n, k + 1}), commit = out("commit_len", a[6], p, dev, kI32, {n});
-        const cudaStream_t s = stream_of(a[7], dev);
+        const Stream s = stream_of(a[7], dev);
+        Tensor tokens = out("tokens", a[5], s, p, kI32, {n, k + 1}), commit = out("commit_len", a[6], s, p, kI32, {n});
         call("kda_verify_draft", dev, [&] {
             return g_kda.verify(pp, qp, (const int32_t*)tp, (const float*)up, (const int32_t*)lp, (int)n, (int)k, (int)vocab,
-                                code, (int32_t*)tokens.data_ptr(), (int32_t*)commit.data_ptr(), s);
+                                code, (int32_t*)tokens.data_ptr(), (int32_t*)commit.data_ptr(), s.handle);
         });
         return tuple({tokens, commit});
     });

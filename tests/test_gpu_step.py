@@ -400,6 +400,33 @@ def test_attention_other_stream_and_graph(dtype, d):
     assert torch.equal(o, kda.kda_paged_attention(*args))
 
 
+@pytest.mark.parametrize("dtype,d", [(BF, 128), (F32, 64)])
+def test_attention_memory_made_for_another_stream(dtype, d):
+    """The workspace that a call on another stream makes is not handed out again before
+    that stream has used it."""
+    dev = need_gpu()
+    c = make([(3000, 2), (2000, 30)], 8, 2, d, 32, dtype, dev)
+    args = on(c, dev)
+    want = kda.kda_paged_attention(*args)
+    size = kda.kda_paged_attention_workspace_size(*args[0].shape[:2], 2, d, dtype)
+    side = torch.cuda.Stream()
+    o = torch.empty_like(want)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(20_000_000)                       # ~10 ms before the call's kernels
+    kda.kda_paged_attention(*args, o=o, stream=side)
+    junk = [torch.full((size,), 255, dtype=torch.uint8, device=dev) for _ in range(3)]
+    side.synchronize()
+    torch.cuda.synchronize()
+    assert torch.equal(o, want) and len(junk) == 3
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(20_000_000)
+    got = kda.kda_verify_draft(torch.full((4, 2, 9), 1 / 9, device=dev), None, torch.zeros(4, 1, dtype=torch.int32, device=dev),
+                               torch.zeros(4, 2, device=dev), stream=side)
+    side.synchronize()
+    assert got[1].tolist() == [2] * 4
+
+
 def test_attention_many_requests():
     """As many requests as a step may have, most of them idle."""
     dev = need_gpu()
