@@ -277,28 +277,20 @@ kda_paged_attention_simt_kernel(const T* __restrict__ q, const T* __restrict__ k
 // Joins the parts of each cut unit: with M = max of the parts' references,
 //     o = sum_i 2^(m_i - M) o_i / sum_i 2^(m_i - M) l_i.
 // blockIdx.x names the CTA in which the unit begins.  D / 4 threads take the
-// columns of a row.  A unit cut once or twice gives each such group rows of its
-// own, two at a time; the parts of one cut more often are shared out among up
-// to eight groups, so that it costs a few load latencies too.  Reads each
-// partial row once.
+// columns of a row and four parts at once; where a unit has more, up to eight
+// such groups share out a row's parts.  Reads each partial row once.  Bound:
+// latency (description, parts, the first fetch of its instructions, so it is kept
+// short): 3 us for a few cut units, 4 to 6 us for a cut in each of 152 CTAs of 64 to 256 rows.
 constexpr int kMergeThreads = 256;
-struct Merged {
-    float top = -INFINITY, l = 0.f;
-    float4 acc = {0.f, 0.f, 0.f, 0.f};
-    __device__ __forceinline__ void add(const float2& st, const float4& v) {
-        if (st.y == 0.f) return;                       // the part saw no key of this row
-        const float m = fmaxf(top, st.x), ref = m == -INFINITY ? 0.f : m;
-        const float fo = exp2f(top - ref), fn = st.x == -INFINITY ? 1.f : exp2f(st.x - ref);
-        top = m;
-        l = fmaf(l, fo, fn * st.y);
-        acc.x = fmaf(acc.x, fo, fn * v.x); acc.y = fmaf(acc.y, fo, fn * v.y);
-        acc.z = fmaf(acc.z, fo, fn * v.z); acc.w = fmaf(acc.w, fo, fn * v.w);
-    }
-};
+__device__ __forceinline__ float merge_ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
 template <int D, typename T>
-__global__ void __launch_bounds__(kMergeThreads, 4)
+__global__ void __launch_bounds__(kMergeThreads, 5)
 kda_paged_merge_kernel(Partials parts, int Gv, int Hq, T* __restrict__ o, float* __restrict__ lse) {
-    constexpr int TPR = D / 4, GROUPS = kMergeThreads / TPR;
+    constexpr int TPR = D / 4, GROUPS = kMergeThreads / TPR, kU = 4;
     __shared__ float4 s_acc[kMergeThreads];
     __shared__ float2 s_st[GROUPS];
     kda_paged::wait_for_stream();
@@ -307,71 +299,78 @@ kda_paged_merge_kernel(Partials parts, int Gv, int Hq, T* __restrict__ o, float*
     if (me.w == 0) return;
     const int rows = me.z * Gv, n = me.w;
     const int x = threadIdx.x % TPR, grp = threadIdx.x / TPR;
-    auto part = [&](int i, int r, float2& st, float4& v) {
-        st = parts.stats(c0 + i, i == 0 ? 1 : 0)[r];
-        v = reinterpret_cast<const float4*>(parts.sums(c0 + i, i == 0 ? 1 : 0) + (size_t)r * D)[x];
-    };
-    auto put = [&](const Merged& m, int r) {
-        const float inv = m.l == 0.f ? 0.f : 1.f / m.l;
+    int share = 1;                                     // groups that share a row
+    while (share * kU < n && share < 8 && share < GROUPS) share <<= 1;
+    const int y = grp % share, per_pass = GROUPS / share;
+#pragma unroll 1
+    for (int r0 = blockIdx.y * per_pass; r0 < rows; r0 += gridDim.y * per_pass) {
+        const int r = min(r0 + grp / share, rows - 1);
+        float top = -INFINITY, l = 0.f;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        // kU more weighted sums into (top, l, acc); st.y = 0 marks a part that saw no key
+        auto add = [&](const float2* st, const float4* v) {
+            float m = top;
+#pragma unroll
+            for (int e = 0; e < kU; ++e) m = fmaxf(m, st[e].x);
+            const float ref = m == -INFINITY ? 0.f : m, f = merge_ex2(top - ref);
+            top = m;
+            l *= f;
+            acc.x *= f; acc.y *= f; acc.z *= f; acc.w *= f;
+#pragma unroll
+            for (int e = 0; e < kU; ++e) {
+                const float g = st[e].y == 0.f ? 0.f : merge_ex2(st[e].x - ref);
+                l = fmaf(g, st[e].y, l);
+                acc.x = fmaf(g, v[e].x, acc.x); acc.y = fmaf(g, v[e].y, acc.y);
+                acc.z = fmaf(g, v[e].z, acc.z); acc.w = fmaf(g, v[e].w, acc.w);
+            }
+        };
+        float2 st[kU];
+        float4 v[kU];
+#pragma unroll 1
+        for (int i0 = y; i0 < n; i0 += kU * share) {
+#pragma unroll
+            for (int e = 0; e < kU; ++e) {
+                const int i = i0 + e * share;
+                st[e] = make_float2(-INFINITY, 0.f);
+                v[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (i < n) {
+                    st[e] = parts.stats(c0 + i, i == 0 ? 1 : 0)[r];
+                    v[e] = reinterpret_cast<const float4*>(parts.sums(c0 + i, i == 0 ? 1 : 0) + (size_t)r * D)[x];
+                }
+            }
+            add(st, v);
+        }
+        if (share > 1) {
+            __syncthreads();                           // the pass before has been read
+            s_acc[threadIdx.x] = acc;
+            if (x == 0) s_st[grp] = make_float2(top, l);
+            __syncthreads();
+            if (y != 0) continue;
+            top = -INFINITY;
+            l = 0.f;
+            acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+            for (int g = 0; g < share; g += kU) {      // share is 2, 4 or 8
+#pragma unroll
+                for (int e = 0; e < kU; ++e) {
+                    const bool in = g + e < share;
+                    st[e] = in ? s_st[grp + g + e] : make_float2(-INFINITY, 0.f);
+                    v[e] = in ? s_acc[threadIdx.x + (g + e) * TPR] : make_float4(0.f, 0.f, 0.f, 0.f);
+                }
+                add(st, v);
+            }
+        }
+        if (r0 + grp / share >= rows) continue;
+        const float inv = l == 0.f ? 0.f : 1.f / l;
         const size_t at = (size_t)(me.x + r / Gv) * Hq + me.y + r % Gv;
         T* dst = o + at * D + 4 * x;
         if constexpr (sizeof(T) == 2) {
             *reinterpret_cast<uint2*>(dst) =
-                make_uint2(kda::pack_bf16x2(m.acc.x * inv, m.acc.y * inv), kda::pack_bf16x2(m.acc.z * inv, m.acc.w * inv));
+                make_uint2(kda::pack_bf16x2(acc.x * inv, acc.y * inv), kda::pack_bf16x2(acc.z * inv, acc.w * inv));
         } else {
-            *reinterpret_cast<float4*>(dst) = make_float4(m.acc.x * inv, m.acc.y * inv, m.acc.z * inv, m.acc.w * inv);
+            *reinterpret_cast<float4*>(dst) = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
         }
-        if (lse && x == 0) lse[at] = m.l == 0.f ? -INFINITY : (m.top + log2f(m.l)) * kLn2;
-    };
-    if (n <= 3) {
-        constexpr int kR = 2;                          // rows a group has in flight
-        const int step = gridDim.y * GROUPS;
-        for (int r0 = blockIdx.y * GROUPS + grp; r0 < rows; r0 += kR * step) {
-            float2 st[kR][3];
-            float4 v[kR][3];
-#pragma unroll
-            for (int e = 0; e < kR; ++e)
-#pragma unroll
-                for (int i = 0; i < 3; ++i) part(min(i, n - 1), min(r0 + e * step, rows - 1), st[e][i], v[e][i]);
-#pragma unroll
-            for (int e = 0; e < kR; ++e) {
-                Merged m;
-#pragma unroll
-                for (int i = 0; i < 3; ++i)
-                    if (i < n) m.add(st[e][i], v[e][i]);
-                if (r0 + e * step < rows) put(m, r0 + e * step);
-            }
-        }
-        return;
-    }
-    constexpr int kU = 2;                              // parts a group has in flight
-    int share = 2;                                     // groups that share a row
-    while (share * kU < n && share < 8 && share < GROUPS) share <<= 1;
-    const int y = grp % share, per_pass = GROUPS / share;
-    for (int r0 = blockIdx.y * per_pass; r0 < rows; r0 += gridDim.y * per_pass) {
-        const int r = r0 + grp / share;
-        Merged m;
-        if (r < rows) {
-            for (int i0 = y; i0 < n; i0 += kU * share) {
-                float2 st[kU];
-                float4 v[kU];
-#pragma unroll
-                for (int e = 0; e < kU; ++e) {
-                    st[e] = make_float2(-INFINITY, 0.f);
-                    v[e] = make_float4(0.f, 0.f, 0.f, 0.f);
-                    if (i0 + e * share < n) part(i0 + e * share, r, st[e], v[e]);
-                }
-#pragma unroll
-                for (int e = 0; e < kU; ++e) m.add(st[e], v[e]);
-            }
-        }
-        __syncthreads();                               // the pass before has been read
-        s_acc[threadIdx.x] = m.acc;
-        if (x == 0) s_st[grp] = make_float2(m.top, m.l);
-        __syncthreads();
-        if (y != 0) continue;
-        for (int g = 1; g < share; ++g) m.add(s_st[grp + g], s_acc[threadIdx.x + g * TPR]);
-        if (r < rows) put(m, r);
+        if (lse && x == 0) lse[at] = l == 0.f ? -INFINITY : (top + log2f(l)) * kLn2;
     }
 }
 
@@ -385,7 +384,7 @@ cudaError_t launch_merge(const kda_host::PagedArgs& a, const kda_host::PagedPlan
                                     cudaSharedmemCarveoutMaxShared);
     });
     if (e != cudaSuccess) return e;
-    return kda_host::launch_overlapped(kda_paged_merge_kernel<D, T>, dim3(ctas, std::min(4, p.rows)), kMergeThreads, 0,
+    return kda_host::launch_overlapped(kda_paged_merge_kernel<D, T>, dim3(ctas, std::min(10, p.rows)), kMergeThreads, 0,
                                        a.stream, 1, kda_host::paged_partials(a, p), p.Gv, a.Hq, static_cast<T*>(a.o),
                                        a.lse);
 }
