@@ -376,9 +376,9 @@ KDA_API size_t kda_paged_attention_workspace_size(int T, int H_q, int H_kv, int 
  * o           [T, H_q, d] dtype;  lse [T, H_q] float or NULL
  * workspace   kda_paged_attention_workspace_size bytes, 256-byte aligned
  * d is 32, 64 or 128; H_q a multiple of H_kv.  The scores, their statistics and
- * the sums are fp32; on the tensor-core path (bf16, d = 64 or 128, q 16-byte
- * aligned with a stride that is a multiple of 8) the weights enter the second
- * product as bf16.  Every other combination runs in fp32 on CUDA cores.
+ * the sums are fp32; on the tensor-core path (bf16, q 16-byte aligned with a
+ * stride that is a multiple of 8) the weights enter the second product as bf16.
+ * fp32 tensors, and bf16 with other rows of q, run in fp32 on CUDA cores.
  */
 KDA_API kda_status kda_paged_attention(const void* q, const void* k_cache, const void* v_cache,
                                const int32_t* block_table, const int32_t* cu_seqlens,

@@ -7,7 +7,7 @@
 // and o / l at the end; lse = (m + log2 l) ln 2.
 //
 // This path is for fp32 (whose accuracy the tensor cores' 16-bit operands do
-// not reach), head dimension 32, and rows of q that TMA cannot fetch.  A unit
+// not reach) and for rows of q that TMA cannot fetch.  A unit
 // has up to 32 rows; a tile of 64 keys and values is brought to shared memory
 // as fp32 and each of 256 threads forms 2 x 4 scores, then 4 rows x d / 32
 // columns of the weighted sum.  Bound: fp32 issue (one shared-memory load per

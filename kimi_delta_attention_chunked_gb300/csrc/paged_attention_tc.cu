@@ -1,5 +1,5 @@
 // paged_attention_tc.cu -- attention over a paged cache on the tensor cores
-// (bf16, head dimension 64 or 128).
+// (bf16).
 //
 // A unit (paged.cuh) is up to 2 x 128 rows: tile i of its rows holds BT = 128 /
 // Gv tokens with the Gv query heads that share a cache head, row = token * Gv +
@@ -65,7 +65,7 @@ constexpr int kTailBytes = 3072;
 
 template <int D>
 struct Cfg {
-    static constexpr int PANELS = D / 64;
+    static constexpr int PANELS = D < 64 ? 1 : D / 64;  // d = 32: a panel whose upper half TMA fills with zeros
     static constexpr int TILE = PANELS * kPanel;       // bytes of a tile of q, keys or values
     static constexpr int STAGES = D == 128 ? 5 : 10;
     static constexpr int KV0 = 2 * TILE;
@@ -405,7 +405,7 @@ kda_paged_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __
         older.flags = newer.flags = 0;
 
         // takes the elements that are not finite out of rows [a, b) of a value tile; all lanes
-        constexpr int CH = D / 8, RPI = 32 / CH;       // 16-byte chunks of a row, rows a warp handles at once
+        constexpr int CH = C::PANELS * 8, RPI = 32 / CH;   // 16-byte chunks of a row, rows a warp handles at once
         const int my_row = lane / CH, my_off = ((lane % CH) >> 3) * kPanel + (lane & 7) * 16;
         auto zero_rows = [&](unsigned char* v, int a, int b) {
             for (int r = a + my_row; r < b; r += RPI)
@@ -745,6 +745,7 @@ kda_paged_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __
                 }
                 if (!ok) break;
                 kda::tc_fence_after();
+                constexpr int kShare = D / 2 < 32 ? 32 : D / 2;      // columns that a half writes
                 if (busy) {
                     const float2 st = tl.stats[h ^ 1][row];
                     const float top = fmaxf(ref, st.x), base = top == -INFINITY ? 0.f : top;
@@ -752,7 +753,7 @@ kda_paged_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __
                     const float f0 = h == 0 ? fm : fo, f1 = h == 0 ? fo : fm;
                     const float sum_l = fmaf(fm, l, fo * st.y);
 #pragma unroll 1
-                    for (int c = h * (D / 2); c < (h + 1) * (D / 2); c += 32) {
+                    for (int c = h * kShare; c < min((h + 1) * kShare, D); c += 32) {
                         float y[32];
 #pragma unroll
                         for (int e = 0; e < 32; ++e) y[e] = 0.f;
@@ -860,7 +861,7 @@ cudaError_t launch_tc(const kda_host::PagedArgs& a) {
 
 namespace kda_host {
 
-bool paged_tc_supported(int d, kda_dtype dt) { return dt == KDA_BF16 && (d == 64 || d == 128); }
+bool paged_tc_supported(int d, kda_dtype dt) { return dt == KDA_BF16 && (d == 32 || d == 64 || d == 128); }
 
 PagedPlan paged_plan_tc(int T, int Hq, int Hkv) {
     PagedPlan p;
@@ -873,7 +874,7 @@ PagedPlan paged_plan_tc(int T, int Hq, int Hkv) {
 }
 
 cudaError_t launch_paged_attention_tc(const PagedArgs& a) {
-    return a.d == 128 ? launch_tc<128>(a) : launch_tc<64>(a);
+    return a.d == 128 ? launch_tc<128>(a) : a.d == 64 ? launch_tc<64>(a) : launch_tc<32>(a);
 }
 
 }  // namespace kda_host
