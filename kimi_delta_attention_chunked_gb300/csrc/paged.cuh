@@ -191,6 +191,9 @@ __device__ __forceinline__ Piece find_piece(const Shape& s, const int32_t* __res
     return *shared;
 }
 
+// A cut unit of more rows than this is joined by the blocks of all its CTAs (if they are many).
+constexpr int kSpreadRows = 64;
+
 // One unit, or the part of it that a CTA's piece holds.
 struct Unit {
     int n, kvh, qh0;                               // request, cache head, first query head
@@ -198,7 +201,7 @@ struct Unit {
     int pos, kend;                                 // position of token tok0; keys below kend exist
     int tb, te;                                    // tiles of this part
     int first, last;                               // the part holds the unit's first / last tile
-    int parts;                                     // CTAs that share the unit, from this one on (first && !last)
+    int start, parts;                              // CTA in which the unit begins (-1: not asked for), CTAs that share it
 };
 
 // Walks the units of a CTA's piece.  Used by all lanes of one warp together.  I:
@@ -350,8 +353,17 @@ struct Walker {
             u.last = u.te == te;
             // CTA c begins at total * c / ctas, so the last one that has a place below `fin` is
             // ceil(fin * ctas / total) - 1
+            u.start = c;
             u.parts = 1;
-            if (!u.last) u.parts = (int)((fin * (unsigned)ctas + total - 1) / total) - c;
+            if (!u.first) {
+                u.start = -1;
+                if (u.ntok * s.Gv > kSpreadRows) {
+                    const I tile0 = at - (unsigned)in + (unsigned)extra;
+                    u.start = (int)(((tile0 + 1) * (unsigned)ctas + total - 1) / total) - 1;
+                }
+            }
+            if (!u.last && u.start >= 0) u.parts = (int)((fin * (unsigned)ctas + total - 1) / total) - u.start;
+            else if (u.start >= 0) u.parts = c + 1 - u.start;
             at += (unsigned)take;
             in = 0;
             ++i;
@@ -364,13 +376,22 @@ struct Walker {
 // Partial rows of cut units in the workspace: CTA c's slot 0 holds a part that
 // goes on from CTA c - 1, slot 1 one that begins in CTA c and goes on in c + 1.
 // A slot is rows x d unnormalised sums, then rows x (reference, sum of weights),
-// the reference in units of log2.  `meta[c]` describes slot 1: (first token,
-// first query head, tokens, parts), parts = 0 where nothing begins and goes on.
+// the reference in units of log2.  meta[2 c + 1] describes slot 1: (first token,
+// first query head, tokens, parts), parts = 0 where nothing begins and goes on;
+// meta[2 c] is (CTA in which slot 0's unit begins, parts), or -1 where there is none.
 struct Partials {
     int4* meta;
     float* rows;
     int cap;                                       // rows of a slot
     int d;
+    __device__ __forceinline__ void clear(int c) const {
+        meta[2 * c] = make_int4(-1, 0, 0, 0);
+        meta[2 * c + 1] = make_int4(0, 0, 0, 0);
+    }
+    __device__ __forceinline__ void describe(int c, const Unit& u) const {
+        if (!u.first) meta[2 * c] = make_int4(u.start, u.parts, 0, 0);
+        else if (!u.last) meta[2 * c + 1] = make_int4(u.tok0, u.qh0, u.ntok, u.parts);
+    }
     __device__ __forceinline__ size_t slot(int c, int which) const {
         return ((size_t)c * 2 + which) * (size_t)cap * (d + 2);
     }

@@ -66,7 +66,7 @@ kda_paged_attention_simt_kernel(const T* __restrict__ q, const T* __restrict__ k
                                                             &s_piece);
         if (w == 0) walk.start(s, cu, seq_len, piece, blockIdx.x);
     }
-    if (tid == 0) parts.meta[blockIdx.x] = make_int4(0, 0, 0, 0);
+    if (tid == 0) parts.clear(blockIdx.x);
 
     constexpr int VC = D / 32;                         // value columns per thread
     for (;;) {
@@ -270,18 +270,19 @@ kda_paged_attention_simt_kernel(const T* __restrict__ q, const T* __restrict__ k
                 if (lane == 0) parts.stats(blockIdx.x, which)[r] = make_float2(rm, rl);
             }
         }
-        if (!whole && u.first && tid == 0) parts.meta[blockIdx.x] = make_int4(u.tok0, u.qh0, u.ntok, u.parts);
+        if (tid == 0) parts.describe(blockIdx.x, u);
     }
 }
 
 // Joins the parts of each cut unit: with M = max of the parts' references,
 //     o = sum_i 2^(m_i - M) o_i / sum_i 2^(m_i - M) l_i.
-// blockIdx.x names the CTA in which the unit begins.  D / 4 threads take the
-// columns of a row and four parts at once; where a unit has more, up to eight
+// The blocks of the CTA in which a unit begins take its rows; of one of kSpread parts
+// and more than kSpreadRows rows the blocks of all its CTAs do (few units, cut many times:
+// 8 units of 252 rows in 19 parts took 45 us without).  D / 4 threads take the columns of a row and four parts at once; where a unit has more, up to eight
 // such groups share out a row's parts.  Reads each partial row once.  Bound:
 // latency (description, parts, the first fetch of its instructions, so it is kept
 // short): 3 us for a few cut units, 4 to 6 us for a cut in each of 152 CTAs of 64 to 256 rows.
-constexpr int kMergeThreads = 256;
+constexpr int kMergeThreads = 256, kSpread = 6;
 __device__ __forceinline__ float merge_ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -294,16 +295,21 @@ kda_paged_merge_kernel(Partials parts, int Gv, int Hq, T* __restrict__ o, float*
     __shared__ float4 s_acc[kMergeThreads];
     __shared__ float2 s_st[GROUPS];
     kda_paged::wait_for_stream();
-    const int c0 = blockIdx.x;
-    const int4 me = parts.meta[c0];
+    const int c = blockIdx.x;
+    const int4 mine = parts.meta[2 * c + 1 - blockIdx.z];     // z = 0: the unit that begins here, 1: the one that goes on here
+    const int c0 = blockIdx.z == 0 ? c : mine.x;
+    if (blockIdx.z == 1 && (c0 < 0 || c0 >= c || mine.y < kSpread)) return;
+    const int4 me = blockIdx.z == 0 ? mine : parts.meta[2 * c0 + 1];
     if (me.w == 0) return;
-    const int rows = me.z * Gv, n = me.w;
     const int x = threadIdx.x % TPR, grp = threadIdx.x / TPR;
+    const int rows = me.z * Gv, n = me.w;
     int share = 1;                                     // groups that share a row
     while (share * kU < n && share < 8 && share < GROUPS) share <<= 1;
     const int y = grp % share, per_pass = GROUPS / share;
+    const bool spread = n >= kSpread && rows > kda_paged::kSpreadRows;
+    const int step = (spread ? n : 1) * gridDim.y * per_pass;
 #pragma unroll 1
-    for (int r0 = blockIdx.y * per_pass; r0 < rows; r0 += gridDim.y * per_pass) {
+    for (int r0 = ((c - c0) * gridDim.y + blockIdx.y) * per_pass; r0 < rows; r0 += step) {
         const int r = min(r0 + grp / share, rows - 1);
         float top = -INFINITY, l = 0.f;
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -384,7 +390,7 @@ cudaError_t launch_merge(const kda_host::PagedArgs& a, const kda_host::PagedPlan
                                     cudaSharedmemCarveoutMaxShared);
     });
     if (e != cudaSuccess) return e;
-    return kda_host::launch_overlapped(kda_paged_merge_kernel<D, T>, dim3(ctas, std::min(10, p.rows)), kMergeThreads, 0,
+    return kda_host::launch_overlapped(kda_paged_merge_kernel<D, T>, dim3(ctas, std::min(10, p.rows), p.rows > kda_paged::kSpreadRows ? 2 : 1), kMergeThreads, 0,
                                        a.stream, 1, kda_host::paged_partials(a, p), p.Gv, a.Hq, static_cast<T*>(a.o),
                                        a.lse);
 }
@@ -450,7 +456,7 @@ PagedPlan paged_plan_simt(int T, int Hq, int Hkv, int d) {
 int paged_slot_rows(int U, int T, int Gv) { return (std::min(U, std::max(T, 1)) * Gv + 3) & ~3; }
 
 size_t paged_plan_bytes(const PagedPlan& p, int d) {
-    return up256((size_t)p.max_ctas * sizeof(int4)) + up256((size_t)p.max_ctas * 2 * p.rows * (d + 2) * sizeof(float));
+    return up256((size_t)p.max_ctas * 2 * sizeof(int4)) + up256((size_t)p.max_ctas * 2 * p.rows * (d + 2) * sizeof(float));
 }
 
 kda_paged::Shape paged_shape(const PagedArgs& a, const PagedPlan& p) {
@@ -480,7 +486,7 @@ kda_paged::Shape paged_shape(const PagedArgs& a, const PagedPlan& p) {
 kda_paged::Partials paged_partials(const PagedArgs& a, const PagedPlan& p) {
     Partials x;
     x.meta = static_cast<int4*>(a.workspace);
-    x.rows = reinterpret_cast<float*>(static_cast<char*>(a.workspace) + up256((size_t)p.max_ctas * sizeof(int4)));
+    x.rows = reinterpret_cast<float*>(static_cast<char*>(a.workspace) + up256((size_t)p.max_ctas * 2 * sizeof(int4)));
     x.cap = p.rows;
     x.d = a.d;
     return x;

@@ -293,7 +293,7 @@ kda_paged_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __
 
     if (w == kWalkWarp) {
         // ---------------- unit descriptions
-        int4 meta = make_int4(0, 0, 0, 0);
+        if (lane == 0) parts.clear(blockIdx.x);
         auto publish = [&](auto& walk) {
             for (int k = 0;; ++k) {
                 Unit u;
@@ -306,7 +306,7 @@ kda_paged_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __
                     kda::mbar_arrive(&tl.u_full[k % kUnits]);
                 }
                 if (!more) break;
-                if (u.first && !u.last) meta = make_int4(u.tok0, u.qh0, u.ntok, u.parts);
+                if (lane == 0) parts.describe(blockIdx.x, u);
             }
         };
         if (s.narrow) {
@@ -318,7 +318,6 @@ kda_paged_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __
             walk.start(s, cu, seq_len, piece, blockIdx.x);
             publish(walk);
         }
-        if (lane == 0) parts.meta[blockIdx.x] = meta;
     } else if (w == kCopyWarp) {
         // ---------------- copies: the keys, then the values of each tile.  (With the values two
         // steps behind, in the order of the products, a unit's last ones came behind the next unit's
