@@ -7,8 +7,10 @@
 // unit, tile, are one line, and CTA c of C takes the c-th of C equal pieces of
 // it: every CTA has the same work whatever the lengths are.  Before a unit's
 // tiles the line has `extra` places that stand for its fixed cost (the pipeline
-// drains and the output is written, 2 to 4 us, the time of one to two tiles); without
-// them the CTAs of a decode batch's short requests finished 20 % behind the others.
+// drains and the output is written, 2 to 5 us).  On the tensor cores, with 0, 1, 2,
+// 3, 4 and 6 of them: 64 decode requests 252, 243, 237, 235, 236 and 238 us (the CTAs of
+// the short requests, with the most units, finished last), 32 x 8 tokens 57, 54, 53,
+// 52, 52 and 52 us.  On the CUDA cores, whose tiles take longer, 0 is best.
 // A unit that a border cuts is finished by each of its CTAs into fp32 partial
 // rows, which the merge kernel joins.  A CTA finds its piece itself, from the lengths
 // on the device: no plan is made on the host, and no extra launch is needed.
@@ -36,7 +38,7 @@ struct Shape {
     int Hq, Hkv, Hv, Gv, sub;                      // Hv = Hkv * sub groups of Gv query heads
     int blocks, page_log2, n_pages, window;
     int U, tile_log2;                              // tokens per unit, keys per tile
-    int narrow;                                    // few requests and tiles: see Walker::start_narrow
+    int extra;                                     // places on the line before a unit's tiles
 };
 
 // One request's lengths, inside the buffers whatever the device arrays hold.
@@ -59,13 +61,6 @@ __device__ __forceinline__ Req load_req(const Shape& s, const int32_t* __restric
     return r;
 }
 
-// Places before a unit's tiles, for so many tiles and CTAs: none in a short call, where a
-// CTA without tiles would leave another with two.
-template <typename I>
-__device__ __forceinline__ int unit_extra(I tiles, int C) {
-    return tiles >= (I)(8 * C) ? 2 : tiles >= (I)(2 * C) ? 1 : 0;
-}
-
 __device__ __forceinline__ int n_units(const Shape& s, const Req& r) { return (r.len + s.U - 1) / s.U; }
 
 // Tiles [tb, te) of unit i: those that hold a key some row sees, and one tile
@@ -80,18 +75,17 @@ __device__ __forceinline__ void unit_span(const Shape& s, const Req& r, int i, i
     if (te <= tb) te = tb + 1;
 }
 
-// Tiles of all units of a request, for one head.  A thread counts a request of
+// Length of all units of a request, for one head.  A thread counts a request of
 // few units by itself; the lanes of a warp share out one of many.
-template <typename I>
-__device__ __forceinline__ I request_tiles(const Shape& s, const Req& r) {
+__device__ __forceinline__ unsigned long long request_places(const Shape& s, const Req& r) {
     constexpr int kAlone = 8;
     const int units = n_units(s, r);
-    I cost = 0;
+    unsigned long long cost = 0;
     if (units <= kAlone) {
         for (int i = 0; i < units; ++i) {
             int tb, te;
             unit_span(s, r, i, tb, te);
-            cost += te - tb;
+            cost += te - tb + s.extra;
         }
     }
     unsigned many = __ballot_sync(0xffffffffu, units > kAlone);
@@ -104,11 +98,11 @@ __device__ __forceinline__ I request_tiles(const Shape& s, const Req& r) {
         q.pos0 = __shfl_sync(0xffffffffu, r.pos0, src);
         q.kend = __shfl_sync(0xffffffffu, r.kend, src);
         const int total = n_units(s, q);
-        I part = 0;
+        unsigned long long part = 0;
         for (int i = threadIdx.x & 31; i < total; i += 32) {
             int tb, te;
             unit_span(s, q, i, tb, te);
-            part += te - tb;
+            part += te - tb + s.extra;
         }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) part += __shfl_xor_sync(0xffffffffu, part, o);
@@ -119,11 +113,10 @@ __device__ __forceinline__ I request_tiles(const Shape& s, const Req& r) {
 
 // Where a CTA's piece begins and ends on the line of tiles.
 struct Piece {
-    unsigned long long begin, end, total;          // tiles [begin, end) of `total`
-    unsigned long long off;                        // begin - first tile of request n
-    unsigned long long tiles;                      // length of request n for one head
+    unsigned long long begin, end, total;          // places [begin, end) of `total`
+    unsigned long long off;                        // begin - first place of request n
+    unsigned long long len;                        // length of request n for one head
     int n, ctas;                                   // first request; CTAs that have a piece
-    int extra;                                     // places before a unit's tiles
 };
 
 // Finds the piece of CTA `c` of `C`.  Every thread of the block (NT of them)
@@ -133,16 +126,16 @@ __device__ __forceinline__ Piece find_piece(const Shape& s, const int32_t* __res
                                             const int32_t* __restrict__ seq_len, int c, int C,
                                             unsigned long long* cost,
                                             unsigned long long* red, Piece* shared) {
-    constexpr int NW = NT / 32, kExtra = 2;            // a large step
+    constexpr int NW = NT / 32;
     const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
     for (int base = 0; base < s.n_req; base += NT) {
         const int n = base + tid;
         Req r{0, 0, 0, 0};
         if (n < s.n_req) r = load_req(s, cu, seq_len, n);
-        const unsigned long long x = request_tiles<unsigned long long>(s, r) + (unsigned)(kExtra * n_units(s, r));
+        const unsigned long long x = request_places(s, r);
         if (n < s.n_req) cost[n] = x;
     }
-    if (tid == 0) *shared = Piece{0, 0, 0, 0, 0, 0, 0, 0};
+    if (tid == 0) *shared = Piece{0, 0, 0, 0, 0, 0, 0};
     __syncthreads();
     // each thread takes `per` consecutive requests of the running sum
     const int per = (s.n_req + NT - 1) / NT, n0 = min(tid * per, s.n_req), n1 = min(n0 + per, s.n_req);
@@ -181,10 +174,9 @@ __device__ __forceinline__ Piece find_piece(const Shape& s, const int32_t* __res
             shared->end = total * (unsigned)(c + 1) / (unsigned)ctas;
             shared->total = total;
             shared->off = begin - at;
-            shared->tiles = cost[n];
+            shared->len = cost[n];
             shared->n = n;
             shared->ctas = ctas;
-            shared->extra = kExtra;
         }
     }
     __syncthreads();
@@ -204,95 +196,32 @@ struct Unit {
     int start, parts;                              // CTA in which the unit begins (-1: not asked for), CTAs that share it
 };
 
-// Walks the units of a CTA's piece.  Used by all lanes of one warp together.  I:
-// 64 bits, or 32 where the products below stay under 2^32 (Shape::narrow).
-constexpr int kNarrowRequests = 256;
-constexpr long long kNarrowTiles = 1 << 22;            // times kMaxCtas: 2^31
-template <typename I>
+// Walks the units of a CTA's piece.  Used by all lanes of one warp together.
 struct Walker {
-    I at, end, total;
-    int ctas, c, extra;
+    unsigned long long at, end, total;
+    int ctas, c;
     int n, h, i, in;                               // next unit; places of it that lie before the piece
     Req r;
     int units;
 
-    // From the piece that the whole block found.
     __device__ __forceinline__ void start(const Shape& s, const int32_t* cu, const int32_t* seq_len, const Piece& p,
                                           int cta) {
         c = cta;
-        extra = p.extra;
-        at = (I)p.begin;
-        end = (I)p.end;
-        total = (I)p.total;
+        at = p.begin;
+        end = p.end;
+        total = p.total;
         ctas = p.ctas;
         n = p.n;
         if (at >= end) return;
         r = load_req(s, cu, seq_len, n);
-        first_unit(s, (I)p.off, (I)p.tiles);
-    }
-
-    // A step of few requests and tiles: this warp finds the piece of CTA `c` of `C` by
-    // itself, 32 requests at a time, in 32 bits, while the rest of the block sets
-    // up.  Kept short: a small call spends more on fetching instructions than on
-    // running them.
-    __device__ __forceinline__ void start_narrow(const Shape& s, const int32_t* cu, const int32_t* seq_len, int cta, int C) {
-        const int lane = threadIdx.x & 31;
-        c = cta;
-        Req q{0, 0, 0, 0};
-        unsigned x = 0, sum = 0, units_sum = 0;
-#pragma unroll 1
-        for (int base = 0; base < s.n_req; base += 32) {
-            q = Req{0, 0, 0, 0};
-            if (base + lane < s.n_req) q = load_req(s, cu, seq_len, base + lane);
-            x = request_tiles<unsigned>(s, q);
-            sum += x;
-            units_sum += n_units(s, q);
-        }
-        total = __reduce_add_sync(0xffffffffu, sum) * (unsigned)s.Hv;
-        extra = unit_extra(total, C);
-        total += (I)extra * __reduce_add_sync(0xffffffffu, units_sum) * (unsigned)s.Hv;
-        ctas = (int)min((unsigned)C, (unsigned)total);
-        at = end = 0;
-        if (c >= ctas) return;
-        at = total * (unsigned)c / (unsigned)ctas;
-        end = total * (unsigned)(c + 1) / (unsigned)ctas;
-        unsigned before = 0;
-#pragma unroll 1
-        for (int base = 0; base < s.n_req; base += 32) {
-            if (s.n_req > 32) {
-                q = Req{0, 0, 0, 0};
-                if (base + lane < s.n_req) q = load_req(s, cu, seq_len, base + lane);
-                x = request_tiles<unsigned>(s, q);
-            }
-            x += extra * n_units(s, q);
-            unsigned incl = x * (unsigned)s.Hv;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const unsigned t = __shfl_up_sync(0xffffffffu, incl, o);
-                if (lane >= o) incl += t;
-            }
-            const unsigned hit = __ballot_sync(0xffffffffu, (unsigned)at < before + incl);
-            if (hit) {
-                const int src = __ffs((int)hit) - 1;
-                n = base + src;
-                r.tok0 = __shfl_sync(0xffffffffu, q.tok0, src);
-                r.len = __shfl_sync(0xffffffffu, q.len, src);
-                r.pos0 = __shfl_sync(0xffffffffu, q.pos0, src);
-                r.kend = __shfl_sync(0xffffffffu, q.kend, src);
-                const unsigned tiles = __shfl_sync(0xffffffffu, x, src);
-                const unsigned to_n = before + __shfl_sync(0xffffffffu, incl, src) - tiles * (unsigned)s.Hv;
-                first_unit(s, (I)at - to_n, tiles);
-                return;
-            }
-            before += __shfl_sync(0xffffffffu, incl, 31);
-        }
+        first_unit(s, p.off, p.len);
     }
 
     // Head, unit and place that lie `off` places behind the start of request n, whose heads have `len` each.
-    __device__ __forceinline__ void first_unit(const Shape& s, I off, I len) {
+    __device__ __forceinline__ void first_unit(const Shape& s, unsigned long long off, unsigned long long len) {
         units = n_units(s, r);
         h = (int)(off / len);
-        I left = off - (I)h * len;
+        unsigned long long left = off - (unsigned long long)h * len;
         i = 0;
         in = (int)left;
         if (units <= 1) return;
@@ -303,7 +232,7 @@ struct Walker {
             if (base + lane < units) {
                 int tb, te;
                 unit_span(s, r, base + lane, tb, te);
-                x = te - tb + extra;
+                x = te - tb + s.extra;
             }
             unsigned incl = x;
 #pragma unroll
@@ -336,10 +265,10 @@ struct Walker {
             }
             int tb, te;
             unit_span(s, r, i, tb, te);
-            const int len = extra + te - tb;
-            const int take = (int)min((I)(len - in), (I)(end - at));
-            const int t0 = max(in - extra, 0), t1 = max(in + take - extra, 0);     // tiles of this part
-            const I fin = at - (unsigned)in + (unsigned)len;                       // the unit's end
+            const int len = s.extra + te - tb;
+            const int take = (int)min((unsigned long long)(len - in), end - at);
+            const int t0 = max(in - s.extra, 0), t1 = max(in + take - s.extra, 0);    // tiles of this part
+            const unsigned long long fin = at - (unsigned)in + (unsigned)len;         // the unit's end
             u.n = n;
             u.kvh = h / s.sub;
             u.qh0 = h * s.Gv;
@@ -358,7 +287,7 @@ struct Walker {
             if (!u.first) {
                 u.start = -1;
                 if (u.ntok * s.Gv > kSpreadRows) {
-                    const I tile0 = at - (unsigned)in + (unsigned)extra;
+                    const unsigned long long tile0 = at - (unsigned)in + (unsigned)s.extra;
                     u.start = (int)(((tile0 + 1) * (unsigned)ctas + total - 1) / total) - 1;
                 }
             }
@@ -513,7 +442,7 @@ inline int heads_per_unit(int group, int most) {
 
 // Partial-row geometry of an attention call: rows of a slot, most CTAs.
 struct PagedPlan {
-    int Gv, U, rows, tile_log2, max_ctas;
+    int Gv, U, rows, tile_log2, max_ctas, extra;
 };
 bool paged_tc_supported(int d, kda_dtype dt);
 PagedPlan paged_plan_tc(int T, int Hq, int Hkv);

@@ -34,8 +34,18 @@
 // out the elements that are not finite.  It notes if it found one; the output
 // warps then add such elements themselves to the rows that see them.
 //
-// Bound.  Few rows: HBM (the cache is read once); long chunks: the tensor cores
-// and the softmax warps beside them.
+// Bound, and what it measured (GPU time with the merge; HBM 6694 GB/s, 1885 TFLOP/s).
+// Decode: HBM, the cache is read once: 64 requests of 1 K to 16 K keys, 32/8 heads
+// of 128, 235 us, 0.93 of the copy rate.  32 requests x 8 tokens, 32/4 heads: 52 us,
+// floor 31: HBM while it streams, then the last unit's latency and the merge.
+// Long chunks: 2 x 4096 tokens over 12,000 and 27,001, 32/4 heads: 1.83 to 1.93 ms,
+// 1.50 to 1.58 PFLOP/s (the card is at its power limit): tensor pipe 69 % active.
+// What it took, in the order of its worth there: one elected lane issues (its
+// operands stay in uniform registers: 2.99 -> 2.21 ms); that warp's loop over the
+// key tiles in uniform control flow, with no more than waits and products (-> 1.91 ms).
+// Sixteen softmax warps took issue slots from it (2.50 -> 2.39 ms against 1.91).
+// Rounding: P enters its product as bf16, the type of V (both operands have one
+// type); the output's error against 64 bits is 2.3e-3, 1.7e-3 of it the bf16 output.
 #include <algorithm>
 #include <cuda.h>
 #include <cudaTypedefs.h>
@@ -259,15 +269,12 @@ kda_paged_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __
         const CUtensorMap* m = lane == 0 ? &qmap : lane == 1 ? &kmap : &vmap;
         asm volatile("prefetch.tensormap [%0];" ::"l"(m) : "memory");
     }
-    // this CTA's piece of the work: by the walking warp alone where it can
-    Piece piece{0, 0, 0, 0, 0, 0, 0, 0};
-    if (!s.narrow) {
-        auto* cost = reinterpret_cast<unsigned long long*>(sm + C::KV0);
-        auto* red = cost + kda_paged::kMaxRequests;
-        auto* shared_piece = reinterpret_cast<Piece*>(red + kThreads / 32);
-        piece = kda_paged::find_piece<kThreads>(s, cu, seq_len, blockIdx.x, gridDim.x, cost, red, shared_piece);
-        kda::fence_proxy_async_smem();                 // the scratch becomes the target of copies
-    }
+    // this CTA's piece of the work
+    auto* cost = reinterpret_cast<unsigned long long*>(sm + C::KV0);
+    auto* red = cost + kda_paged::kMaxRequests;
+    const Piece piece = kda_paged::find_piece<kThreads>(s, cu, seq_len, blockIdx.x, gridDim.x, cost, red,
+                                                        reinterpret_cast<Piece*>(red + kThreads / 32));
+    kda::fence_proxy_async_smem();                     // the scratch becomes the target of copies
     kda::tc_fence_before();
     __syncthreads();
     kda::tc_fence_after();
@@ -294,29 +301,20 @@ kda_paged_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __
     if (w == kWalkWarp) {
         // ---------------- unit descriptions
         if (lane == 0) parts.clear(blockIdx.x);
-        auto publish = [&](auto& walk) {
-            for (int k = 0;; ++k) {
-                Unit u;
-                const bool more = walk.next(s, cu, seq_len, u);
-                if (k >= kUnits && !wait(&tl.u_empty[k % kUnits], (k / kUnits - 1) & 1)) break;
-                __syncwarp();
-                if (lane == 0) {
-                    if (more) tl.units[k % kUnits].u = u;
-                    tl.units[k % kUnits].more = more;
-                    kda::mbar_arrive(&tl.u_full[k % kUnits]);
-                }
-                if (!more) break;
-                if (lane == 0) parts.describe(blockIdx.x, u);
+        Walker walk;
+        walk.start(s, cu, seq_len, piece, blockIdx.x);
+        for (int k = 0;; ++k) {
+            Unit u;
+            const bool more = walk.next(s, cu, seq_len, u);
+            if (k >= kUnits && !wait(&tl.u_empty[k % kUnits], (k / kUnits - 1) & 1)) break;
+            __syncwarp();
+            if (lane == 0) {
+                if (more) tl.units[k % kUnits].u = u;
+                tl.units[k % kUnits].more = more;
+                kda::mbar_arrive(&tl.u_full[k % kUnits]);
             }
-        };
-        if (s.narrow) {
-            Walker<unsigned> walk;
-            walk.start_narrow(s, cu, seq_len, blockIdx.x, gridDim.x);
-            publish(walk);
-        } else {
-            Walker<unsigned long long> walk;
-            walk.start(s, cu, seq_len, piece, blockIdx.x);
-            publish(walk);
+            if (!more) break;
+            if (lane == 0) parts.describe(blockIdx.x, u);
         }
     } else if (w == kCopyWarp) {
         // ---------------- copies: the keys, then the values of each tile.  (With the values two
@@ -869,6 +867,7 @@ PagedPlan paged_plan_tc(int T, int Hq, int Hkv) {
     p.rows = paged_slot_rows(p.U, T, p.Gv);
     p.tile_log2 = kKeysLog2;
     p.max_ctas = 160;
+    p.extra = 3;
     return p;
 }
 
