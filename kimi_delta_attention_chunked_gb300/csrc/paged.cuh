@@ -23,7 +23,6 @@
 namespace kda_paged {
 
 constexpr int kMaxRequests = KDA_MAX_STEP_REQUESTS;
-constexpr int kMaxCtas = 512;                      // most CTAs an attention launch uses
 
 // The kernels before this one on the stream are complete and their writes seen;
 // the kernel behind it may be set up from here on.
