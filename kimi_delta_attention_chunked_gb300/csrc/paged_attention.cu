@@ -276,7 +276,8 @@ kda_paged_attention_simt_kernel(const T* __restrict__ q, const T* __restrict__ k
 //     o = sum_i 2^(m_i - M) o_i / sum_i 2^(m_i - M) l_i.
 // The blocks of the CTA in which a unit begins take its rows; of one of kSpread parts
 // and more than kSpreadRows rows the blocks of all its CTAs do (few units, cut many times:
-// 8 units of 252 rows in 19 parts took 45 us without).  D / 4 threads take the columns of a row and four parts at once; where a unit has more, up to eight
+// 8 units of 252 rows in 19 parts: the whole call 74 us without, 42 with).  D / 4 threads
+// take the columns of a row and four parts at once; where a unit has more, up to eight
 // such groups share out a row's parts.  Reads each partial row once.  Bound:
 // latency (description, parts, the first fetch of its instructions, so it is kept
 // short): 3 us for a few cut units, 4 to 6 us for a cut in each of 152 CTAs of 64 to 256 rows.

@@ -14,10 +14,10 @@
 //   quick  p -> round(p 2^46), from the bits of two fp32 sums: with x = fl(p + 1),
 //          bits(x) - bits(1) = round(p 2^23), and with l = p - (x - 1) (exact),
 //          bits(l 2^23 + 1.5) - bits(1.5) = round(l 2^46): 5 fp32 instructions.
-// A quick sum of V terms is off by at most V.  Where that could decide the index
-// (the threshold within 2 V + 2 of a border of the element found, or so small a
-// sum; about once in a thousand draws at V = 160,000) one CTA does the row again
-// in the exact form.
+// A quick sum is off by at most one unit a term.  Where that could decide the index
+// (the threshold that near a border of the element found, or next to no sum; about once
+// in 3000 draws at V = 160,000) one CTA does the row again in the exact form, which adds
+// 42 us there: 240 us with one read in flight a thread in place of 16.
 //
 // A cluster of CTAs takes one request: each sums its part of the row, the parts
 // are exchanged through distributed shared memory, and the CTA that holds the
@@ -26,7 +26,8 @@
 // 128 requests, V = 160,001, fp32 (164 MB, floor 24.5 us), GPU time: 47 us with
 // the exact form throughout (issue bound), 37 us with the quick one.  Then three
 // CTAs of 512 threads an SM, 8 numbers of each row in flight a thread: 43 us with six of 256 (more,
-// smaller clusters wait longer for each other), 39 us with 4 numbers, 47 us with two of 1024.
+// smaller clusters wait longer for each other), 39 us with 4 numbers, 47 us with two of 1024,
+// 49 us with clusters of four, 39 to 44 us with the row's start fetched into L2 ahead.
 // What is left of it: the chain before the row (length, token, two probabilities: three
 // dependent reads) and behind it (cluster barrier, second scan), in which nothing streams.
 #include <algorithm>
@@ -134,11 +135,16 @@ __device__ __forceinline__ long long quick_sum(const Row<T>& row, int lo, int hi
 }
 
 // floor(u total), inside [0, total - 1]: u at or above 1 takes the last positive
-// element, u below 0 or NaN the first
+// element, u below 0 or NaN the first.  In whole numbers: u is m 2^-shift, the product
+// has up to 87 bits, and fp64 would round it.
 __device__ __forceinline__ long long threshold(float u, long long total) {
-    const double want = (double)u * (double)total;
-    const long long thr = want > 0.0 ? (want < 9.0e18 ? (long long)want : total) : 0;
-    return min(thr, total - 1);
+    if (!(u > 0.f)) return 0;
+    if (u >= 1.f) return total - 1;
+    const int b = __float_as_int(u), ex = max(b >> 23, 1), shift = 150 - ex;   // 24 ... 149
+    const unsigned long long m = (b & 0x7fffff) | (b >> 23 ? 0x800000 : 0);
+    const unsigned long long lo = m * (unsigned long long)total, hi = __umul64hi(m, total);
+    if (shift < 64) return (long long)(hi << (64 - shift) | lo >> shift);
+    return shift < 128 ? (long long)(hi >> (shift - 64)) : 0;
 }
 
 // The element of [c0, c1) at which the running sum passes `thr`, given its warps'
@@ -176,6 +182,30 @@ __device__ __forceinline__ int locate(const Row<T>& row, F part_lo, long long th
     return -1;
 }
 
+// Exact sum over [lo, hi), a warp's part, lanes side by side.
+template <typename T>
+__device__ __forceinline__ long long exact_sum(const Row<T>& row, int lo, int hi) {
+    const int lane = threadIdx.x & 31;
+    constexpr int kU = 8;
+    long long s = 0;
+    int v = lo + lane;
+    for (; v + 32 * (kU - 1) < hi; v += 32 * kU) {         // all reads ahead of the first use
+        float a[kU], b[kU];
+#pragma unroll
+        for (int e = 0; e < kU; ++e) a[e] = kda::io<T>::ld(row.p + v + 32 * e);
+#pragma unroll
+        for (int e = 0; e < kU; ++e) b[e] = row.q ? kda::io<T>::ld(row.q + v + 32 * e) : v + 32 * e == row.masked ? 1.f : 0.f;
+#pragma unroll
+        for (int e = 0; e < kU; ++e) {
+            const float x = clean(a[e]), y = clean(b[e]);
+            if (x > y) s += (long long)(fixed60(x) - fixed60(y));
+        }
+    }
+#pragma unroll 4
+    for (; v < hi; v += 32) s += row.template at<true>(v);
+    return warp_sum(s);
+}
+
 // The whole draw in the exact form, by one CTA.
 template <typename T>
 __device__ __noinline__ void draw_exact(Row<T> row, int V, float u, int32_t* out, long long* s_warp, long long* s_scan) {
@@ -183,10 +213,7 @@ __device__ __noinline__ void draw_exact(Row<T> row, int V, float u, int32_t* out
     auto part_lo = [&](int i) { return (int)((long long)V * i / kWarps); };
     long long total = 0;
     for (int attempt = 0; attempt < 2; ++attempt) {
-        long long s = 0;
-#pragma unroll 4
-        for (int v = part_lo(w) + lane; v < part_lo(w + 1); v += 32) s += row.template at<true>(v);
-        s = warp_sum(s);
+        const long long s = exact_sum(row, part_lo(w), part_lo(w + 1));
         __syncthreads();
         if (lane == 0) s_warp[w] = s;
         __syncthreads();
@@ -275,8 +302,7 @@ kda_verify_draft_kernel(const T* __restrict__ target, const T* __restrict__ draf
         if (tid == 0) commit_len[n] = a + 1;
     }
     const float u = uniforms[(size_t)n * (K + 1) + K];
-    const long long margin = 2ll * V + 2;
-    if (total <= margin) {                                 // next to nothing is left of the row
+    if (total <= 2ll * V + 2) {                            // next to nothing is left of the row
         if (rank == 0) draw_exact(row, V, u, out + a, s_warp, s_scan);
         return;
     }
@@ -285,6 +311,11 @@ kda_verify_draft_kernel(const T* __restrict__ target, const T* __restrict__ draf
     long long sum, value;
     const int v = locate<false>(row, part_lo, thr, s_warp, s_scan, sum, value);
     if (v >= 0) {
+        // by how much sum - u total can be off here: (1 - u) times the v elements before, u times
+        // those behind, a unit each (half of one without a draft row); 2^-10 more for the exact
+        // form's own floor (2^-14) and for the fp32 of this line
+        const float f = __saturatef(u), unit = row.q ? 1.f + 0x1p-10f : 0.5f + 0x1p-10f;
+        const long long margin = (long long)(unit * ((1.f - f) * v + f * (V - v))) + 4;
         if (thr - sum >= margin && sum + value - thr > margin) out[a] = v;
         else s_unsure = 1;
     }

@@ -506,6 +506,53 @@ def test_verify_tiny_probabilities():
     assert got[1].tolist() == [1, 1, 1, 2]
 
 
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("V", [10, 700, 20002])
+@pytest.mark.parametrize("with_draft", [False, True])
+def test_verify_threshold_on_a_border(dtype, V, with_draft):
+    """The running sum meets u times the whole sum exactly, or misses it by 2^-60: the
+    sums of a row's halves are equal, but for one small element of one of them."""
+    dev = need_gpu()
+    gen = torch.Generator().manual_seed(V)
+    half = V // 2
+    target = torch.zeros(6, 1 + with_draft, V, dtype=dtype)
+    for i in range(6):
+        h = ((torch.rand(half, generator=gen) + 0.01) / V).to(dtype)
+        h[half // 3] = 2.0 ** -53
+        row = torch.cat([h, h[torch.randperm(half, generator=gen)]])
+        more = 2.0 ** -53 * (1 + 2.0 ** -7) if not with_draft else 2.0 ** -52 * (1 + 2.0 ** -7)
+        if with_draft:
+            row[row == 2.0 ** -53] = 2.0 ** -52
+        small = (row == (2.0 ** -52 if with_draft else 2.0 ** -53)).nonzero()[:, 0]
+        assert small.numel() == 2
+        if i % 3:
+            row[small[i % 3 - 1]] = more
+        target[i, 0] = row
+    u = torch.full((6, 1 + with_draft), 0.5)
+    tokens = torch.full((6, int(with_draft)), -1, dtype=torch.int32)
+    got = run_verify(target, target[:, :1] / 2 if with_draft else None, tokens, u, None, dev)
+    assert got[0][:, 0].tolist() == [half, half - 1, half] * 2
+    u[:, -1] = 2.0 ** -140
+    run_verify(target, None, tokens, u, None, dev)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+def test_verify_threshold_is_not_rounded(dtype):
+    """3/4 of the whole sum lies 20 x 2^-60 below the sum of three quarters of the row;
+    rounded to 53 bits it would lie above."""
+    dev = need_gpu()
+    V = 4000
+    gen = torch.Generator().manual_seed(V)
+    h = ((torch.rand(V // 4, generator=gen) + 0.3) / V).to(dtype)
+    h[5] = 2.0 ** -50
+    row = torch.cat([h[torch.randperm(V // 4, generator=gen)] for _ in range(4)])
+    row[int((row == 2.0 ** -50).nonzero()[1])] = 2.0 ** -50 * (1 + 5 / 64)     # 80 x 2^-60 more
+    assert 0.5 < float(row.double().sum()) < 1 and V // 4 <= int((row == 2.0 ** -50 * (1 + 5 / 64)).nonzero()[0]) < V // 2
+    got = run_verify(row.expand(3, 1, V).contiguous(), None, torch.zeros(3, 0, dtype=torch.int32),
+                     torch.tensor([[0.75], [0.5], [0.25]]), None, dev)
+    assert got[0][0, 0].item() == 3 * V // 4 - 1
+
+
 def test_verify_feeds_commit_len():
     """commit_len goes to kda_decode_multi as it is: the state equals that after the committed tokens alone."""
     dev = need_gpu()
