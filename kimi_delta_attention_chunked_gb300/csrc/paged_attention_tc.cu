@@ -71,7 +71,7 @@ constexpr int kUnits = 4;                              // unit descriptions in f
 constexpr float kGrow = 8.f;                           // octaves that a score may exceed the reference
 constexpr float kLn2 = 0.69314718055994531f;
 constexpr float kLog2e = 1.44269504088896341f;
-constexpr int kTailBytes = 3072;
+constexpr int kTailBytes = 3 * 1024;
 
 template <int D>
 struct Cfg {
