@@ -60,6 +60,13 @@ __device__ __forceinline__ Req load_req(const Shape& s, const int32_t* __restric
     return r;
 }
 
+// First key that a row at `pos` (negative: before the sequence) sees.  No difference is formed
+// that could pass 32 bits: any window from 0 to 2^31 - 1 may meet any position, and a first key
+// that wraps below 0 would name a place before the block table.
+__host__ __device__ __forceinline__ int first_key(int pos, int window) {
+    return window > 0 && pos >= window ? pos - window + 1 : 0;
+}
+
 __device__ __forceinline__ int n_units(const Shape& s, const Req& r) { return (r.len + s.U - 1) / s.U; }
 
 // Tiles [tb, te) of unit i: those that hold a key some row sees, and one tile
@@ -67,8 +74,7 @@ __device__ __forceinline__ int n_units(const Shape& s, const Req& r) { return (r
 __device__ __forceinline__ void unit_span(const Shape& s, const Req& r, int i, int& tb, int& te) {
     const int first = i * s.U, last = min(r.len, first + s.U);
     const int hi = min(max(r.pos0 + last, 0), r.kend);
-    int lo = s.window > 0 ? max(0, r.pos0 + first - s.window + 1) : 0;
-    lo = min(lo, hi);
+    const int lo = min(first_key(r.pos0 + first, s.window), hi);
     tb = lo >> s.tile_log2;
     te = (hi + (1 << s.tile_log2) - 1) >> s.tile_log2;
     if (te <= tb) te = tb + 1;

@@ -92,7 +92,7 @@ kda_paged_attention_simt_kernel(const T* __restrict__ q, const T* __restrict__ k
         const int sr = tid >> 3, sx = tid & 7;
         const int my_pos = u.pos + sr / s.Gv;
         const int my_hi = sr < rows ? min(my_pos + 1, u.kend) : 0;
-        const int my_lo = s.window > 0 ? max(0, my_pos - s.window + 1) : 0;
+        const int my_lo = kda_paged::first_key(my_pos, s.window);
         float m = -INFINITY, l = 0.f;
         float acc[4][VC];
 #pragma unroll

@@ -187,8 +187,8 @@ __device__ __forceinline__ Sight sight(const Unit& u, int window, int first, int
     const int p0 = u.pos + first, p1 = u.pos + last;
     s.hi = min(max(p1 + 1, 0), u.kend);
     s.all_hi = min(max(p0 + 1, 0), u.kend);
-    s.lo = window > 0 ? max(0, p0 - window + 1) : 0;
-    s.all_lo = window > 0 ? max(0, p1 - window + 1) : 0;
+    s.lo = kda_paged::first_key(p0, window);
+    s.all_lo = kda_paged::first_key(p1, window);
     return s;
 }
 
@@ -584,7 +584,7 @@ kda_paged_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __
             const bool valid = row < rows_tile && tok < u.ntok;
             const int pos = u.pos + tok;
             const int hi = valid ? min(max(pos + 1, 0), u.kend) : 0;
-            const int lo = valid && s.window > 0 ? max(0, pos - s.window + 1) : 0;
+            const int lo = valid ? kda_paged::first_key(pos, s.window) : 0;
             const bool busy = __any_sync(0xffffffffu, valid);
             const Sight mine = sight(u, s.window, qi * BT, min(u.ntok, qi * BT + BT) - 1);
             auto page_of = [&](int tile) {             // lane's page of the tile: 0 where there is nothing to judge
