@@ -302,6 +302,9 @@ KDA_API kda_status kda_decode_multi(const void* q, const void* k, const void* v,
  * serves any lengths that its buffers hold.
  */
 #define KDA_MAX_STEP_REQUESTS 8192
+/* Most tokens that a request's row of the block table may cover in kda_paged_attention
+ * (max_blocks * page_size): positions and the ends of key tiles are 32-bit numbers. */
+#define KDA_MAX_STEP_POSITIONS (INT32_MAX - 511)
 
 /*
  * Block tables and slot map of one step.  Request n holds ctx_len[n] cached
@@ -326,7 +329,7 @@ KDA_API kda_status kda_decode_multi(const void* q, const void* k, const void* v,
  *                  -1, and the calls below leave their tokens out.
  * n_tokens is the size of slot_map; new tokens past it get no slot.  Tokens
  * past max_blocks * page_size get no page.  The new tokens of all requests
- * together must stay below 2^31.
+ * together must stay below 2^31, and so must the tokens (ctx + new) of each.
  */
 KDA_API kda_status kda_build_block_tables(const int32_t* ctx_len, const int32_t* new_len,
                                   const int32_t* free_pages, int n_free, int N, int max_blocks,
@@ -373,6 +376,7 @@ KDA_API size_t kda_paged_attention_workspace_size(int T, int H_q, int H_kv, int 
  * seq_len     [N] int32 device array
  * scale       finite and > 0
  * window      0: no window
+ * max_blocks  at most KDA_MAX_STEP_POSITIONS / page_size
  * o           [T, H_q, d] dtype;  lse [T, H_q] float or NULL
  * workspace   kda_paged_attention_workspace_size bytes, 256-byte aligned
  * d is 32, 64 or 128; H_q a multiple of H_kv.  The scores, their statistics and

@@ -44,7 +44,8 @@ struct Shape {
 struct Req {
     int tok0, len;                                 // first row of q, new tokens
     int pos0;                                      // position of the first new token (may be negative)
-    int kend;                                      // keys below it exist
+    int kend;                                      // keys below it exist; at most KDA_MAX_STEP_POSITIONS, so
+                                                   // that the end of its tile is still a 32-bit number
 };
 
 __device__ __forceinline__ Req load_req(const Shape& s, const int32_t* __restrict__ cu,

@@ -78,6 +78,7 @@ kda_status kda_paged_attention(const void* q, const void* k_cache, const void* v
     if (max_blocks < 0 || n_pages < 0 || window < 0 || !dtype_ok(dtype)) return KDA_ERR_INVALID_ARG;
     if (!dim_ok(d) || !page_ok(page_size)) return KDA_ERR_UNSUPPORTED;
     if (N > KDA_MAX_STEP_REQUESTS || H_q > (1 << 16)) return KDA_ERR_UNSUPPORTED;
+    if ((int64_t)max_blocks * page_size > KDA_MAX_STEP_POSITIONS) return KDA_ERR_UNSUPPORTED;
     if (!std::isfinite(scale) || !(scale > 0.f)) return KDA_ERR_INVALID_ARG;
     if (q_stride < (int64_t)H_q * d) return KDA_ERR_INVALID_ARG;
     if (T == 0 || N == 0) return KDA_OK;
