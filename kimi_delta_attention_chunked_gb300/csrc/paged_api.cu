@@ -105,6 +105,7 @@ kda_status kda_verify_draft(const void* target, const void* draft, const int32_t
                             int32_t* tokens, int32_t* commit_len, cudaStream_t stream) {
     if (N < 0 || K < 0 || V <= 0 || !dtype_ok(dtype)) return KDA_ERR_INVALID_ARG;
     if (K > 16 || N > (1 << 20)) return KDA_ERR_UNSUPPORTED;
+    if (V > (1 << 30)) return KDA_ERR_UNSUPPORTED;         // the places of a row and a thread's steps past its end are 32-bit
     if (N == 0) return KDA_OK;
     if (!target || !uniforms || !tokens || !commit_len || (K > 0 && !draft_tokens)) return KDA_ERR_INVALID_ARG;
     if (tokens == draft_tokens) return KDA_ERR_INVALID_ARG;

@@ -3,7 +3,7 @@ their kernels inside 32 bits and its buffer; nothing here reaches a GPU."""
 import pytest
 
 from kimi_delta_attention_chunked_gb300 import _lib as E
-from test_step_cpu import P, attention, lib  # noqa: F401
+from test_step_cpu import attention, lib, verify  # noqa: F401
 
 
 @pytest.mark.parametrize("page", [16, 256])
@@ -13,3 +13,10 @@ def test_attention_positions_fit_32_bits(lib, page):  # noqa: F811
     assert attention(lib, page=page, blocks=most + 1, bytes=0) == E.KDA_ERR_UNSUPPORTED
     assert attention(lib, page=page, blocks=2 ** 31 - 1, bytes=0) == E.KDA_ERR_UNSUPPORTED
     assert attention(lib, page=page, blocks=most, bytes=0) == E.KDA_ERR_WORKSPACE    # accepted up to the next check
+
+
+def test_verify_vocabulary_fits_32_bits(lib):  # noqa: F811
+    """Steps past the end of a row of almost 2^31 numbers would wrap, and read before it."""
+    assert verify(lib, V=2 ** 31 - 1, p=None) == E.KDA_ERR_UNSUPPORTED
+    assert verify(lib, V=2 ** 30 + 1, p=None) == E.KDA_ERR_UNSUPPORTED
+    assert verify(lib, V=2 ** 30, p=None) == E.KDA_ERR_INVALID_ARG      # accepted up to the next check
