@@ -109,6 +109,8 @@ kda_status kda_verify_draft(const void* target, const void* draft, const int32_t
     if (N == 0) return KDA_OK;
     if (!target || !uniforms || !tokens || !commit_len || (K > 0 && !draft_tokens)) return KDA_ERR_INVALID_ARG;
     if (tokens == draft_tokens) return KDA_ERR_INVALID_ARG;
+    const size_t esize = dtype == KDA_BF16 ? 2 : 4;
+    if (!aligned(target, esize) || !aligned(draft, esize)) return KDA_ERR_INVALID_ARG;
     const kda_host::VerifyArgs a{target, draft, draft_tokens, uniforms, draft_len, N, K, V, dtype, tokens,
                                  commit_len, stream};
     return from_cuda(kda_host::launch_verify_draft(a));

@@ -3,7 +3,7 @@ their kernels inside 32 bits and its buffer; nothing here reaches a GPU."""
 import pytest
 
 from kimi_delta_attention_chunked_gb300 import _lib as E
-from test_step_cpu import attention, lib, verify  # noqa: F401
+from test_step_cpu import P, attention, lib, verify  # noqa: F401
 
 
 @pytest.mark.parametrize("page", [16, 256])
@@ -20,3 +20,10 @@ def test_verify_vocabulary_fits_32_bits(lib):  # noqa: F811
     assert verify(lib, V=2 ** 31 - 1, p=None) == E.KDA_ERR_UNSUPPORTED
     assert verify(lib, V=2 ** 30 + 1, p=None) == E.KDA_ERR_UNSUPPORTED
     assert verify(lib, V=2 ** 30, p=None) == E.KDA_ERR_INVALID_ARG      # accepted up to the next check
+
+
+@pytest.mark.parametrize("kw", [dict(p=P(0x1002)), dict(q=P(0x2001)), dict(dt=E.KDA_BF16, p=P(0x1001)),
+                                dict(dt=E.KDA_BF16, q=P(0x2001))])
+def test_verify_rows_off_their_elements(lib, kw):  # noqa: F811
+    """The rows come as untyped pointers; an element off its own boundary cannot be read."""
+    assert verify(lib, **kw) == E.KDA_ERR_INVALID_ARG
