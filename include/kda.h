@@ -327,6 +327,7 @@ KDA_API kda_status kda_decode_multi(const void* q, const void* k, const void* v,
  * n_taken          [1] int32, written: pages needed.  More than n_free means
  *                  that the free list ran out: the entries without a page are
  *                  -1, and the calls below leave their tokens out.
+ * No output may lie over ctx_len, new_len or free_pages.
  * n_tokens is the size of slot_map; new tokens past it get no slot.  Tokens
  * past max_blocks * page_size get no page.  The new tokens of all requests
  * together must stay below 2^31, and so must the tokens (ctx + new) of each.

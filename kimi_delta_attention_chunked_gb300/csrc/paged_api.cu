@@ -40,6 +40,11 @@ kda_status kda_build_block_tables(const int32_t* ctx_len, const int32_t* new_len
     if (N > 0 && max_blocks > 0 && !block_table) return KDA_ERR_INVALID_ARG;
     if ((n_free > 0 && !free_pages) || (n_tokens > 0 && !slot_map)) return KDA_ERR_INVALID_ARG;
     if (!aligned(slot_map, 8)) return KDA_ERR_INVALID_ARG;
+    // every CTA reads the lengths and the free list for itself, so none may write over them
+    for (const void* in : {(const void*)ctx_len, (const void*)new_len, (const void*)free_pages})
+        for (const void* out : {(const void*)block_table, (const void*)cu_seqlens, (const void*)seq_len,
+                                (const void*)slot_map, (const void*)positions, (const void*)n_taken})
+            if (in && in == out) return KDA_ERR_INVALID_ARG;
     const kda_host::TablesArgs a{ctx_len, new_len, free_pages, n_free, N, max_blocks, page_size, n_tokens,
                                  block_table, cu_seqlens, seq_len, slot_map, positions, n_taken, stream};
     return from_cuda(kda_host::launch_build_tables(a));

@@ -3,7 +3,7 @@ their kernels inside 32 bits and its buffer; nothing here reaches a GPU."""
 import pytest
 
 from kimi_delta_attention_chunked_gb300 import _lib as E
-from test_step_cpu import P, attention, lib, verify  # noqa: F401
+from test_step_cpu import P, attention, lib, tables, verify  # noqa: F401
 
 
 @pytest.mark.parametrize("page", [16, 256])
@@ -27,3 +27,10 @@ def test_verify_vocabulary_fits_32_bits(lib):  # noqa: F811
 def test_verify_rows_off_their_elements(lib, kw):  # noqa: F811
     """The rows come as untyped pointers; an element off its own boundary cannot be read."""
     assert verify(lib, **kw) == E.KDA_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("kw", [dict(seq=P(0x1000)), dict(seq=P(0x2000)), dict(cu=P(0x1000)), dict(pos=P(0x2000)),
+                                dict(table=P(0x3000)), dict(taken=P(0x3000)), dict(slot=P(0x1000))])
+def test_tables_outputs_over_inputs(lib, kw):  # noqa: F811
+    """Lengths updated in place: the CTAs of a step of many tokens would read each other's results."""
+    assert tables(lib, **kw) == E.KDA_ERR_INVALID_ARG
