@@ -414,7 +414,8 @@ KDA_API kda_status kda_paged_attention(const void* q, const void* k_cache, const
  *               the request's last token and its drafts were run through
  *               kda_decode_multi as K + 1 tokens
  * Sums are exact to 2^-60 of a probability, in integers: no order of summation
- * enters the result.  Negative and NaN probabilities count as 0.  A target row
+ * enters the result.  Negative and NaN probabilities count as 0, except that a
+ * token whose own p or q is NaN does not stand.  A target row
  * without a positive entry draws V - 1.  K is at most 16, V at most 2^30.
  */
 KDA_API kda_status kda_verify_draft(const void* target, const void* draft, const int32_t* draft_tokens,

@@ -258,7 +258,8 @@ kda_verify_draft_kernel(const T* __restrict__ target, const T* __restrict__ draf
             const int x = draft_tokens[(size_t)n * K + lane];
             if (x >= 0 && x < V) {
                 const float p = kda::io<T>::ld(target + ((size_t)n * (K + 1) + lane) * V + x);
-                const float q = draft ? kda::io<T>::ld(draft + ((size_t)n * K + lane) * V + x) : 1.f;
+                float q = draft ? kda::io<T>::ld(draft + ((size_t)n * K + lane) * V + x) : 1.f;
+                if (q < 0.f) q = 0.f;                      // or a token with p = 0 would stand; a NaN fails the test below
                 const float u = uniforms[(size_t)n * (K + 1) + lane];
                 stands = lane < len && (double)u * (double)q < (double)p;
             }
