@@ -7,6 +7,12 @@ before it: shapes (ValueError), dtypes (TypeError), device and layout
 itself is compiled (csrc/step_binding.cpp), because a serving step makes these
 calls for every layer; like the library it is built by ``build.build()`` and
 there is no other path.
+
+``stream`` (a torch stream or a raw handle) names the stream of a call; without it
+the call goes to the current one.  Tensors passed in must be ready there.
+Tensors made for a call on another stream are memory of that stream, kept until
+the current stream is done with them too; before they are used elsewhere, that
+stream has to be waited for.
 """
 from __future__ import annotations
 

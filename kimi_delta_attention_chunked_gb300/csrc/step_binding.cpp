@@ -12,6 +12,7 @@
 #include <ATen/ops/empty.h>
 #include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAFunctions.h>
+#include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -109,37 +110,39 @@ const void* rows(const char* name, const Tensor& t, int dev, ScalarType dtype, a
     stride = std::max(t.stride(0), row);
     return t.data_ptr();
 }
-// The stream of a call.  Tensors made here belong to the current stream; used on another
-// one, the allocator must not hand their memory out again before that stream is done.
+// The stream of a call.  Tensors made here are that stream's own memory: the current
+// stream's could still be read or written by work queued there before they were freed, and
+// torch may fill new memory, which must come before the call's kernels.  What the caller gets is
+// most likely used on the current stream next, so its memory is not handed out again
+// before that stream is done with it either.
 struct Stream {
     cudaStream_t handle;
-    int dev;
-    bool other;
+    c10::cuda::CUDAStream current;
     Tensor make(const Tensor& like, ScalarType dtype, at::IntArrayRef shape) const {
-        Tensor t = at::empty(shape, like.options().dtype(dtype).requires_grad(false));
-        if (other && t.numel() > 0) {
-            const auto s = c10::cuda::getStreamFromExternal(handle, (c10::DeviceIndex)dev);
-            c10::cuda::CUDACachingAllocator::recordStream(t.storage().data_ptr(), s);
-        }
+        const auto options = like.options().dtype(dtype).requires_grad(false);
+        if (handle == current.stream()) return at::empty(shape, options);
+        const c10::cuda::CUDAStreamGuard guard(c10::cuda::getStreamFromExternal(handle, current.device_index()));
+        Tensor t = at::empty(shape, options);
+        if (t.numel() > 0) c10::cuda::CUDACachingAllocator::recordStream(t.storage().data_ptr(), current);
         return t;
     }
 };
 Stream stream_of(PyObject* o, int dev) {
-    const cudaStream_t current = c10::cuda::getCurrentCUDAStream(dev).stream();
-    if (o == Py_None) return {current, dev, false};
+    const c10::cuda::CUDAStream current = c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)dev);
+    if (o == Py_None) return {current.stream(), current};
     PyObject* handle = PyObject_HasAttrString(o, "cuda_stream") ? PyObject_GetAttrString(o, "cuda_stream") : PyNumber_Long(o);
     if (!handle) throw Refused{};
     void* p = PyLong_AsVoidPtr(handle);
     Py_DECREF(handle);
     if (!p && PyErr_Occurred()) throw Refused{};
-    return {static_cast<cudaStream_t>(p), dev, p != current};
+    return {static_cast<cudaStream_t>(p), current};
 }
 
 // the caller's output tensor, checked, or a new one (None)
 Tensor out(const char* name, PyObject* o, const Stream& s, const Tensor& like, ScalarType dtype, at::IntArrayRef shape) {
     if (o == Py_None) return s.make(like, dtype, shape);
     const Tensor& t = tensor(name, o);
-    need(name, t, s.dev, dtype, shape);
+    need(name, t, s.current.device_index(), dtype, shape);
     return t;
 }
 

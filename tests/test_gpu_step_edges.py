@@ -10,6 +10,7 @@ from test_gpu_step import BF, F32, check, make, on
 import kimi_delta_attention_chunked_gb300 as kda
 
 pytestmark = pytest.mark.gpu
+SLEEP = 20_000_000                                          # cycles, about 10 ms
 
 
 @pytest.mark.parametrize("dtype,d", [(BF, 128), (BF, 64), (BF, 32), (F32, 64)])
@@ -38,3 +39,105 @@ def test_verify_negative_draft_probability_counts_as_zero():
         # rows 0, 1: p = q = 0, the rest max(p - q, 0) is all on token 2; row 2: stands; row 3: 0.5 < 0.25 fails
         assert got[1].tolist() == [1, 1, 2, 1]
         assert got[0].tolist() == [[2, -1], [2, -1], [2, 1], [2, -1]]
+
+
+def small_verify(dev, n=64):
+    return (torch.full((n, 2, 9), 1 / 9, device=dev), None, torch.zeros(n, 1, dtype=torch.int32, device=dev),
+            torch.zeros(n, 2, device=dev))
+
+
+def workspace(args, dtype):
+    T, heads, d = args[0].shape
+    size = kda.kda_paged_attention_workspace_size(T, heads, args[1].shape[1], d, dtype)
+    return torch.empty(size, dtype=torch.uint8, device=args[0].device)
+
+
+@pytest.mark.parametrize("dtype,d", [(BF, 128), (F32, 64)])
+def test_outputs_of_another_stream_are_not_memory_that_the_current_stream_still_writes(dtype, d):
+    """A tensor freed with work of the current stream behind it is not the output of a call
+    that another stream runs at once."""
+    dev = need_gpu()
+    c = make([(300, 2), (90, 30), (5, 1)], 8, 2, d, 32, dtype, dev)
+    args = on(c, dev)
+    want, want_lse = kda.kda_paged_attention(*args, want_lse=True)
+    votes = small_verify(dev)
+    want_tokens, want_commit = kda.kda_verify_draft(*votes)
+    shapes = [(t.shape, t.dtype) for t in (want, want_lse, want_tokens, want_commit)]
+    side = torch.cuda.Stream()
+    ws = workspace(args, dtype)
+    kda.kda_paged_attention(*args, want_lse=True, workspace=ws, stream=side)         # kernels loaded, pools in use
+    kda.kda_verify_draft(*votes, stream=side)
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    stale = [torch.empty(s, dtype=t, device=dev) for s, t in shapes for _ in range(3)]
+    torch.cuda._sleep(SLEEP)
+    for t in stale:
+        t.fill_(7)                                          # runs after the sleep
+    del stale, t
+    got = [*kda.kda_paged_attention(*args, want_lse=True, workspace=ws, stream=side),
+           *kda.kda_verify_draft(*votes, stream=side)]
+    torch.cuda.synchronize()
+    for a, b in zip(got, (want, want_lse, want_tokens, want_commit)):
+        assert torch.equal(a, b)
+
+
+def test_outputs_of_another_stream_when_new_memory_is_filled():
+    """torch fills new memory where deterministic algorithms are asked for: before the call's
+    kernels, not after them."""
+    dev = need_gpu()
+    c = make([(300, 2), (90, 30)], 8, 2, 128, 32, BF, dev)
+    args = on(c, dev)
+    want = kda.kda_paged_attention(*args)
+    side = torch.cuda.Stream()
+    ws = workspace(args, BF)
+    torch.cuda.synchronize()
+    try:
+        torch.use_deterministic_algorithms(True)
+        torch.cuda._sleep(SLEEP)
+        got = kda.kda_paged_attention(*args, workspace=ws, stream=side)
+    finally:
+        torch.use_deterministic_algorithms(False)
+    torch.cuda.synchronize()
+    assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("dtype,d", [(BF, 128), (F32, 64)])
+def test_memory_of_a_call_on_another_stream_is_kept_until_that_stream_is_done(dtype, d):
+    """What a pending call on another stream writes (its workspace, outputs that nobody
+    holds any more) is not handed out to the current stream before it has run."""
+    dev = need_gpu()
+    c = make([(3000, 2), (2000, 30)], 8, 2, d, 32, dtype, dev)
+    args = on(c, dev)
+    votes = small_verify(dev)
+    kda.kda_paged_attention(*args)
+    shapes = [(t.shape, t.dtype) for t in (*kda.kda_verify_draft(*votes), args[0], workspace(args, dtype))]
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(SLEEP)
+    kda.kda_paged_attention(*args, stream=side)
+    kda.kda_verify_draft(*votes, stream=side)
+    junk = [torch.full(s, 77, dtype=t, device=dev) for s, t in shapes for _ in range(4)]
+    torch.cuda.synchronize()
+    for t in junk:
+        assert bool((t == 77).all())
+
+
+def test_outputs_read_on_the_current_stream_are_kept_until_it_is_done():
+    """An output freed with work of the current stream behind it is not handed out to the
+    other stream's next call before that work has run."""
+    dev = need_gpu()
+    c = make([(300, 2), (90, 30), (5, 1)], 8, 2, 128, 32, BF, dev)
+    args = on(c, dev)
+    other = [torch.zeros_like(args[0]), *args[1:]]
+    want = kda.kda_paged_attention(*args)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    got = kda.kda_paged_attention(*args, stream=side)
+    side.synchronize()
+    torch.cuda._sleep(SLEEP)
+    read = got.clone()
+    del got
+    later = [kda.kda_paged_attention(*other, stream=side) for _ in range(3)]
+    torch.cuda.synchronize()
+    assert torch.equal(read, want) and len(later) == 3
