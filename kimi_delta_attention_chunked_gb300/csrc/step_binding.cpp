@@ -146,17 +146,23 @@ Tensor out(const char* name, PyObject* o, const Stream& s, const Tensor& like, S
     return t;
 }
 
+// Gives up the interpreter lock; an exception that passes through gets it back first.
+struct Unlocked {
+    PyThreadState* const state = PyEval_SaveThread();
+    ~Unlocked() { PyEval_RestoreThread(state); }
+};
+
 // Calls a C entry with `dev` current (the library looks up the SM count and the
 // status word of the current device); raises on an error code.
 template <typename F>
 void call(const char* entry, int dev, F f) {
-    const int before = c10::cuda::current_device();
-    if (before != dev) c10::cuda::set_device(dev);
     kda_status st;
-    Py_BEGIN_ALLOW_THREADS
-    st = f();
-    Py_END_ALLOW_THREADS
-    if (before != dev) c10::cuda::set_device(before);
+    {
+        c10::cuda::OptionalCUDAGuard guard;
+        if (c10::cuda::current_device() != dev) guard.set_index((c10::DeviceIndex)dev);
+        const Unlocked unlocked;
+        st = f();
+    }
     if (st == KDA_OK) return;
     PyObject* e = PyObject_CallFunction(g_error, "is", (int)st, entry);
     if (e) {
@@ -176,6 +182,9 @@ PyObject* guarded(const char* name, Py_ssize_t got, Py_ssize_t want, F f) {
         return nullptr;
     } catch (const std::exception& e) {
         PyErr_SetString(PyExc_RuntimeError, e.what());
+        return nullptr;
+    } catch (...) {
+        PyErr_SetString(PyExc_RuntimeError, "unknown C++ exception");
         return nullptr;
     }
 }

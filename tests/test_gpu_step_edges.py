@@ -141,3 +141,17 @@ def test_outputs_read_on_the_current_stream_are_kept_until_it_is_done():
     later = [kda.kda_paged_attention(*other, stream=side) for _ in range(3)]
     torch.cuda.synchronize()
     assert torch.equal(read, want) and len(later) == 3
+
+
+def test_exception_behind_the_interpreter_lock():
+    """A tensor without memory raises, also where its pointer is asked for after the lock was given up."""
+    dev = need_gpu()
+    args = on(make([(90, 3)], 8, 2, 128, 32, BF, dev), dev)
+    want = kda.kda_paged_attention(*args)
+    from torch._subclasses.fake_tensor import FakeTensorMode
+    with FakeTensorMode():
+        fake = torch.empty(1 << 28, dtype=torch.uint8, device=dev)
+    for _ in range(3):
+        with pytest.raises(RuntimeError):
+            kda.kda_paged_attention(*args, workspace=fake)
+    assert torch.equal(kda.kda_paged_attention(*args), want)
