@@ -73,6 +73,13 @@ int64_t integer(const char* name, PyObject* o) {
     return v;
 }
 
+// a Python value's truth; asking may raise
+bool truth(PyObject* o) {
+    const int t = PyObject_IsTrue(o);
+    if (t < 0) throw Refused{};
+    return t != 0;
+}
+
 void check_shape(const char* name, const Tensor& t, at::IntArrayRef shape) {
     if (t.sizes() != shape) value_error(std::string(name) + " must have shape " + str(shape) + ", got " + str(t.sizes()));
 }
@@ -281,6 +288,7 @@ PyObject* paged_attention(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
             if (scale == -1.0 && PyErr_Occurred()) throw Refused{};
         }
         const int64_t window = integer("window", a[7]);
+        const bool want_lse = a[9] != Py_None || truth(a[10]);
         if (a[8] != Py_None) check_shape("o", tensor("o", a[8]), q.sizes());
         if (a[9] != Py_None) check_shape("lse", tensor("lse", a[9]), {T, heads});
         const int dev = device_of("q", q);
@@ -291,7 +299,6 @@ PyObject* paged_attention(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
              *sp = need("seq_len", seq, dev, kI32, {n});
         const Stream s = stream_of(a[12], dev);
         Tensor o = out("o", a[8], s, q, dt, q.sizes()), lse;
-        const int want_lse = a[9] != Py_None || PyObject_IsTrue(a[10]);
         if (want_lse) lse = out("lse", a[9], s, q, kF32, {T, heads});
         Tensor ws;
         size_t bytes;

@@ -1,9 +1,11 @@
 """Limits and refusals of the serving-step operators that keep every index of
 their kernels inside 32 bits and its buffer; nothing here reaches a GPU."""
 import pytest
+import torch
 
+import kimi_delta_attention_chunked_gb300 as kda
 from kimi_delta_attention_chunked_gb300 import _lib as E
-from test_step_cpu import P, attention, lib, tables, verify  # noqa: F401
+from test_step_cpu import P, attention, i32, lib, tables, verify, z  # noqa: F401
 
 
 @pytest.mark.parametrize("page", [16, 256])
@@ -34,3 +36,9 @@ def test_verify_rows_off_their_elements(lib, kw):  # noqa: F811
 def test_tables_outputs_over_inputs(lib, kw):  # noqa: F811
     """Lengths updated in place: the CTAs of a step of many tokens would read each other's results."""
     assert tables(lib, **kw) == E.KDA_ERR_INVALID_ARG
+
+
+def test_binding_want_lse_without_a_truth_value():
+    """What its truth value raises is raised, before anything is launched."""
+    with pytest.raises(RuntimeError, match="ambiguous"):
+        kda.kda_paged_attention(z(5, 4, 32), z(3, 2, 16, 32), z(3, 2, 16, 32), i32(2, 4), i32(3), i32(2), want_lse=z(2))
