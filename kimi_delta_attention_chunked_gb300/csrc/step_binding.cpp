@@ -83,6 +83,11 @@ bool truth(PyObject* o) {
 void check_shape(const char* name, const Tensor& t, at::IntArrayRef shape) {
     if (t.sizes() != shape) value_error(std::string(name) + " must have shape " + str(shape) + ", got " + str(t.sizes()));
 }
+// the C entries take sizes as int; a larger one must not be cut off
+void check_size(const char* name, const Tensor& t) {
+    for (const int64_t n : t.sizes())
+        if (n > INT32_MAX) value_error(std::string(name) + " " + str(t.sizes()) + " has a dim past 2^31 - 1");
+}
 void check_kind(const char* name, const Tensor& t, int dev, ScalarType dtype) {
     if (t.scalar_type() != dtype) refuse(PyExc_TypeError, std::string(name) + " must be " + str(dtype) + ", got " + str(t.scalar_type()));
     if (!t.is_cuda() || t.get_device() != dev) value_error(std::string(name) + " must be on cuda:" + std::to_string(dev));
@@ -212,6 +217,9 @@ PyObject* build_block_tables(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
                      &table = tensor("block_table", a[3]);
         if (ctx.dim() != 1 || table.dim() != 2 || free.dim() != 1)
             value_error("ctx_len and free_pages must have 1 dim, block_table 2");
+        check_size("ctx_len", ctx);
+        check_size("free_pages", free);
+        check_size("block_table", table);
         const int64_t n = ctx.size(0), blocks = table.size(1), n_free = free.size(0);
         check_shape("new_len", add, {n});
         const int64_t page = integer("page_size", a[4]), n_tokens = integer("n_tokens", a[5]);
@@ -237,6 +245,7 @@ void check_caches(const char* entry, const Tensor& k, const Tensor& v) {
     if (k.dim() != 4 || v.sizes() != k.sizes())
         value_error(std::string(entry) + ": k_cache and v_cache must have one shape [n_pages, H_kv, page_size, d], got " +
                     str(k.sizes()) + " and " + str(v.sizes()));
+    check_size("k_cache", k);
 }
 
 PyObject* cache_append(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
@@ -245,6 +254,7 @@ PyObject* cache_append(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
                      &vc = tensor("v_cache", a[3]), &slot = tensor("slot_map", a[4]);
         check_caches("kda_cache_append", kc, vc);
         if (k.dim() != 3) value_error("k must have 3 dims, got " + std::to_string(k.dim()));
+        check_size("k", k);
         const int64_t shape[3] = {k.size(0), kc.size(1), kc.size(3)};
         const kda_dtype code = code_of(kc);
         const ScalarType dt = kc.scalar_type();
@@ -271,6 +281,8 @@ PyObject* paged_attention(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
         check_caches("kda_paged_attention", kc, vc);
         if (q.dim() != 3 || table.dim() != 2)
             value_error("q must have 3 dims and block_table 2, got " + std::to_string(q.dim()) + " and " + std::to_string(table.dim()));
+        check_size("q", q);
+        check_size("block_table", table);
         const int64_t T = q.size(0), heads = q.size(1), d = kc.size(3), kv_heads = kc.size(1), n = table.size(0),
                       blocks = table.size(1);
         if (q.size(2) != d || kv_heads == 0 || heads % kv_heads != 0)
@@ -328,6 +340,8 @@ PyObject* verify_draft(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
         const bool has_draft = a[1] != Py_None, has_len = a[4] != Py_None;
         if (p.dim() != 3 || t.dim() != 2)
             value_error("target must have 3 dims and draft_tokens 2, got " + std::to_string(p.dim()) + " and " + std::to_string(t.dim()));
+        check_size("target", p);
+        check_size("draft_tokens", t);
         const int64_t n = t.size(0), k = t.size(1), vocab = p.size(2);
         const int64_t p_shape[3] = {n, k + 1, vocab}, q_shape[3] = {n, k, vocab};
         if (p.sizes() != at::IntArrayRef(p_shape) || (has_draft && tensor("draft", a[1]).sizes() != at::IntArrayRef(q_shape)))

@@ -42,3 +42,29 @@ def test_binding_want_lse_without_a_truth_value():
     """What its truth value raises is raised, before anything is launched."""
     with pytest.raises(RuntimeError, match="ambiguous"):
         kda.kda_paged_attention(z(5, 4, 32), z(3, 2, 16, 32), z(3, 2, 16, 32), i32(2, 4), i32(3), i32(2), want_lse=z(2))
+
+
+BIG = 2 ** 32 + 7                                           # 7 when cut to 32 bits
+
+
+def big(dt, *shape):
+    """A tensor of that shape over a single number."""
+    return torch.zeros((1,) * len(shape), dtype=dt).expand(*shape)
+
+
+@pytest.mark.parametrize("call", [
+    lambda: kda.kda_build_block_tables(i32(3), i32(3), big(torch.int32, BIG), i32(3, 4), 16, 8),
+    lambda: kda.kda_build_block_tables(i32(3), i32(3), i32(4), big(torch.int32, 3, BIG), 16, 8),
+    lambda: kda.kda_build_block_tables(big(torch.int32, BIG), big(torch.int32, BIG), i32(4), big(torch.int32, BIG, 4), 16, 8),
+    lambda: kda.kda_cache_append(big(torch.float32, BIG, 2, 32), big(torch.float32, BIG, 2, 32), z(3, 2, 16, 32), z(3, 2, 16, 32),
+                                 big(torch.int64, BIG)),
+    lambda: kda.kda_cache_append(z(5, 2, 32), z(5, 2, 32), big(torch.float32, BIG, 2, 16, 32), big(torch.float32, BIG, 2, 16, 32),
+                                 z(5, dt=torch.int64)),
+    lambda: kda.kda_paged_attention(big(torch.float32, BIG, 4, 32), z(3, 2, 16, 32), z(3, 2, 16, 32), i32(2, 4), i32(3), i32(2)),
+    lambda: kda.kda_paged_attention(z(5, 4, 32), z(3, 2, 16, 32), z(3, 2, 16, 32), big(torch.int32, 2, BIG), i32(3), i32(2)),
+    lambda: kda.kda_verify_draft(big(torch.float32, 2, 4, BIG), None, i32(2, 3), z(2, 4)),
+    lambda: kda.kda_verify_draft(big(torch.float32, BIG, 1, 9), None, big(torch.int32, BIG, 0), big(torch.float32, BIG, 1)),
+])
+def test_binding_sizes_are_not_cut_off(call):
+    with pytest.raises(ValueError, match="past 2"):
+        call()
