@@ -142,6 +142,14 @@ struct Stream {
 Stream stream_of(PyObject* o, int dev) {
     const c10::cuda::CUDAStream current = c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)dev);
     if (o == Py_None) return {current.stream(), current};
+    if (PyObject_HasAttrString(o, "device_index")) {       // a torch stream; a raw handle does not tell
+        PyObject* index = PyObject_GetAttrString(o, "device_index");
+        if (!index) throw Refused{};
+        const long of = PyLong_AsLong(index);
+        Py_DECREF(index);
+        if (of == -1 && PyErr_Occurred()) throw Refused{};
+        if (of != dev) value_error("stream must be on cuda:" + std::to_string(dev) + ", not cuda:" + std::to_string(of));
+    }
     PyObject* handle = PyObject_HasAttrString(o, "cuda_stream") ? PyObject_GetAttrString(o, "cuda_stream") : PyNumber_Long(o);
     if (!handle) throw Refused{};
     void* p = PyLong_AsVoidPtr(handle);

@@ -155,3 +155,23 @@ def test_exception_behind_the_interpreter_lock():
         with pytest.raises(RuntimeError):
             kda.kda_paged_attention(*args, workspace=fake)
     assert torch.equal(kda.kda_paged_attention(*args), want)
+
+
+def test_stream_of_another_device_is_refused():
+    """A torch stream names its device; the call's tensors have to be there."""
+    dev = need_gpu()
+
+    class Elsewhere:
+        cuda_stream, device_index = 0, 1
+
+    args = on(make([(20, 3)], 4, 2, 32, 16, F32, dev), dev)
+    with pytest.raises(ValueError, match="stream must be on cuda:0, not cuda:1"):
+        kda.kda_paged_attention(*args, stream=Elsewhere())
+    with pytest.raises(ValueError, match="stream must be on cuda:0"):
+        kda.kda_verify_draft(*small_verify(dev), stream=Elsewhere())
+    want = kda.kda_paged_attention(*args)
+    torch.cuda.synchronize()
+    for stream in (torch.cuda.default_stream(), torch.cuda.Stream(), 0, torch.cuda.ExternalStream(torch.cuda.Stream().cuda_stream)):
+        got = kda.kda_paged_attention(*args, stream=stream)
+        torch.cuda.synchronize()
+        assert torch.equal(got, want)
