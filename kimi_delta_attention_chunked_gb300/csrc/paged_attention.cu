@@ -422,21 +422,21 @@ namespace kda_host {
 
 int sm_count() {
     constexpr int kMaxDevices = 64;
-    static int counts[kMaxDevices] = {};               // 0: not asked yet; every writer stores the same value
+    static std::atomic<int> counts[kMaxDevices] = {};  // 0: not asked yet; threads that ask at once store the same value
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) {
         (void)cudaGetLastError();
         return 148;
     }
-    if (counts[dev] == 0) {
-        int n = 0;
+    int n = counts[dev].load(std::memory_order_relaxed);
+    if (n == 0) {
         if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) {
             (void)cudaGetLastError();
             return 148;
         }
-        counts[dev] = n;
+        counts[dev].store(n, std::memory_order_relaxed);
     }
-    return counts[dev];
+    return n;
 }
 
 PagedPlan paged_plan_simt(int T, int Hq, int Hkv, int d) {

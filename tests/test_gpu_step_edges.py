@@ -1,5 +1,6 @@
 """Edges of the serving-step operators on the GPU."""
 import math
+import threading
 
 import pytest
 import torch
@@ -141,6 +142,58 @@ def test_outputs_read_on_the_current_stream_are_kept_until_it_is_done():
     later = [kda.kda_paged_attention(*other, stream=side) for _ in range(3)]
     torch.cuda.synchronize()
     assert torch.equal(read, want) and len(later) == 3
+
+
+def test_calls_at_once_on_two_streams():
+    """Attention on the tensor cores and on the CUDA cores, and verification, in two streams at once."""
+    dev = need_gpu()
+    sets = [make([(900, 2), (90, 30)], 8, 2, 128, 32, BF, dev, seed=1), make([(2000, 1), (40, 9)], 8, 2, 64, 16, BF, dev, seed=2),
+            make([(300, 3)], 4, 2, 64, 16, F32, dev, seed=3)]
+    args = [on(c, dev) for c in sets]
+    votes = small_verify(dev)
+    want = [kda.kda_paged_attention(*a) for a in args]
+    tokens, _ = kda.kda_verify_draft(*votes)
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    got = []
+    for i in range(30):
+        for k, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                j = (i + k) % 3
+                got.append((kda.kda_paged_attention(*args[j]), want[j]))
+                got.append((kda.kda_verify_draft(*votes)[0], tokens))
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in got)
+    assert kda.kda_get_last_device_status() == 0
+
+
+def test_calls_at_once_from_two_threads():
+    """The binding gives up the interpreter lock around each call."""
+    dev = need_gpu()
+    args = on(make([(900, 2), (90, 30)], 8, 2, 128, 32, BF, dev, seed=1), dev)
+    votes = small_verify(dev)
+    want, tokens = kda.kda_paged_attention(*args), kda.kda_verify_draft(*votes)[0]
+    torch.cuda.synchronize()
+    bad = []
+
+    def work():
+        stream = torch.cuda.Stream()
+        with torch.cuda.stream(stream):
+            for _ in range(100):
+                o = kda.kda_paged_attention(*args)
+                t = kda.kda_verify_draft(*votes)[0]
+                with pytest.raises(ValueError):
+                    kda.kda_paged_attention(*args[:5], args[5][:1])
+            stream.synchronize()
+        if not (torch.equal(o, want) and torch.equal(t, tokens)):
+            bad.append(threading.get_ident())
+
+    threads = [threading.Thread(target=work) for _ in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not bad and kda.kda_get_last_device_status() == 0
 
 
 def test_exception_behind_the_interpreter_lock():
