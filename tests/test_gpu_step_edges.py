@@ -6,7 +6,7 @@ import pytest
 import torch
 
 from _gpu import need_gpu
-from test_gpu_step import BF, F32, check, make, on
+from test_gpu_step import BF, F32, check, dists, make, on, run_verify
 
 import kimi_delta_attention_chunked_gb300 as kda
 
@@ -142,6 +142,34 @@ def test_outputs_read_on_the_current_stream_are_kept_until_it_is_done():
     later = [kda.kda_paged_attention(*other, stream=side) for _ in range(3)]
     torch.cuda.synchronize()
     assert torch.equal(read, want) and len(later) == 3
+
+
+@pytest.mark.parametrize("d", [32, 64, 128])
+@pytest.mark.parametrize("lens,Hq,Hkv", [
+    ([(6000, 32)], 8, 1),                                   # 256 rows, a part in each of 47 CTAs
+    ([(3000, 63)], 8, 1),                                   # a full unit and a short one
+    ([(1500, 63)], 4, 1),                                   # one unit of 252 rows
+    ([(2500, 12), (1, 1), (1300, 20)], 16, 2),
+    ([(2300, 9)], 24, 1),                                   # 216 rows, groups that do not fill a tile
+])
+def test_attention_units_joined_by_all_their_ctas(d, lens, Hq, Hkv):
+    """Units of more than 64 rows in many parts."""
+    dev = need_gpu()
+    c = make(lens, Hq, Hkv, d, 64, BF, dev, seed=d + Hq)
+    o, _ = check(c, dev)
+    again = kda.kda_paged_attention(*on(c, dev)).double().cpu()
+    assert torch.equal(o, again)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("ctas", range(1, 9))
+def test_verify_every_cluster_size(dtype, ctas):
+    """A row is shared by V / 4096 CTAs, up to eight."""
+    dev = need_gpu()
+    V = 4096 * ctas + 17 * ctas + 3
+    target, draft, tokens, u = dists(2, 2, V, dtype, ctas)
+    run_verify(target, draft, tokens, u, [2, 1], dev)
+    run_verify(target, None, tokens, u, [1, 2], dev)
 
 
 def test_calls_at_once_on_two_streams():
