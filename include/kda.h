@@ -286,7 +286,9 @@ KDA_API kda_status kda_decode_multi(const void* q, const void* k, const void* v,
 
 /*
  * ---------------------------------------------------------------------------
- * Serving step of a model that mixes KDA layers with softmax-attention layers.
+ * Serving step of a model that mixes KDA layers with softmax-attention layers
+ * of grouped query heads (keys and values of one head size, 32, 64 or 128; latent
+ * attention, whose keys and values have other sizes, is not among them).
  * The attention layers keep keys and values in a paged cache:
  *
  *   k_cache, v_cache  [n_pages, H_kv, page_size, d] dtype, 16-byte aligned
@@ -345,7 +347,8 @@ KDA_API kda_status kda_build_block_tables(const int32_t* ctx_len, const int32_t*
  * k, v      [T, H_kv, d] dtype; consecutive tokens are k_stride and v_stride
  *           elements apart (at least H_kv * d, so that both may be slices of a
  *           fused projection); any alignment of the elements
- * slot_map  [T] int64.  Two tokens with one slot leave either's row there.
+ * slot_map  [T] int64.  What a slot named by two tokens holds is unspecified: each
+ *           piece of its row is either one's.
  */
 KDA_API kda_status kda_cache_append(const void* k, const void* v, const int64_t* slot_map,
                             int64_t k_stride, int64_t v_stride, int T, int H_kv, int d, int page_size,
@@ -471,10 +474,12 @@ KDA_API kda_status kda_set_trace_events(void* const* events, int n_events);
  *     in plain words", inside which the chunked form's staged decay factors
  *     stay finite and the accuracy target is stated; the call still computes.
  *     (The *_fused calls clamp the log-decay themselves and are not checked.)
- *   - Device checks: the tensor-core kernels check the workspace slots and
- *     segment indices they derive from the call's lengths against the sizes
+ *   - Device checks: the tensor-core prefill kernels check the workspace slots
+ *     and segment indices they derive from the call's lengths against the sizes
  *     they were given; an index outside records KDA_ERR_DEVICE_CHECK and the
  *     access is skipped.  Nothing traps.
+ * The serving-step operators are the same in both libraries: they bring lengths,
+ * slots and pages from the device into their buffers' range always.
  * kda_get_last_device_status of the same library reports either code.
  * Returns 1 in the debug library, 0 in the release library.
  */

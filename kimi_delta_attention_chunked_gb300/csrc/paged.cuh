@@ -5,7 +5,11 @@
 // Gv query heads that share a cache head, against the 128- or 64-key tiles that
 // any of their rows sees.  The tiles of all units, in the order request, head,
 // unit, tile, are one line, and CTA c of C takes the c-th of C equal pieces of
-// it: every CTA has the same work whatever the lengths are.  Before a unit's
+// it: every CTA has the same number of places whatever the lengths are.  A place is a key
+// tile, though, and on the tensor cores a unit of two row tiles takes two steps for it, one of
+// a single row tile one: in batches that mix the two the pieces differ in work (16 requests
+// of 1 to 513 tokens under a window of 1024: 20 steps in the busiest CTA, 9.2 on average,
+// 12 with no places for the fixed cost).  Before a unit's
 // tiles the line has `extra` places that stand for its fixed cost (the pipeline
 // drains and the output is written, 2 to 5 us).  On the tensor cores, with 0, 1, 2,
 // 3, 4 and 6 of them: 64 decode requests 252, 243, 237, 235, 236 and 238 us (the CTAs of

@@ -38,8 +38,10 @@
 // Decode: HBM, the cache is read once: 64 requests of 1 K to 16 K keys, 32/8 heads
 // of 128, 235 us, 0.93 of the copy rate.  32 requests x 8 tokens, 32/4 heads: 52 us,
 // floor 31: HBM while it streams, then the last unit's latency and the merge.
-// Long chunks: 2 x 4096 tokens over 12,000 and 27,001, 32/4 heads: 1.83 to 1.93 ms,
-// 1.50 to 1.58 PFLOP/s (the card is at its power limit): tensor pipe 69 % active.
+// Long chunks: 2 x 4096 tokens over 12,000 and 27,001, 32/4 heads: 1.79 to 1.96 ms from run
+// to run, 1.48 to 1.61 PFLOP/s (the card is at its power limit): tensor pipe 69 % active.
+// With heads of 64 and 32 the same chunk takes 1.61 and 1.56 ms: the softmax warps, 3.5 to
+// 3.6e12 weights a second.  Mixed lengths: uneven pieces (paged.cuh).
 // What it took, in the order of its worth there: one elected lane issues (its
 // operands stay in uniform registers: 2.99 -> 2.21 ms); that warp's loop over the
 // key tiles in uniform control flow, with no more than waits and products (-> 1.91 ms).
@@ -372,7 +374,9 @@ kda_paged_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __
             }
         }
     } else if (w == kIssueWarp) {
-        // ---------------- products.  All lanes wait, lane 0 issues
+        // ---------------- products.  All lanes wait, an elected one issues.  P_h lies over S_h: the
+        // scores of a half's next step are issued behind its product P_h V, which waited for P_h, and
+        // the tensor cores take products in the order of issue, so neither is overwritten in use
         const uint32_t id_s = kda::idesc_bf16(128, 128, 0, 0), id_o = kda::idesc_bf16(128, D, 0, 1);
         const uint64_t q_desc = kda::sw128_desc(kda::smem_u32(sm), 16, 1024);
         const uint64_t k_desc = kda::sw128_desc(kda::smem_u32(sm + C::KV0), 16, 1024);
@@ -570,9 +574,6 @@ kda_paged_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __
         int n_s = 0, n_j = 0, g = 0;
         uint32_t o_phase = 0;                          // bit h: parity of the next O_h
         bool ok = true;
-        // Round -1 takes one step over whatever TMEM holds, for the sake of its instructions:
-        // fetching them for the first time takes thousands of cycles, and these warps wait that
-        // long for the first keys anyway.  Its arrival tells the issuing warp that S is free
         for (int k = 0; ok; ++k) {
             Unit u;
             if (!read_unit(k, u)) break;

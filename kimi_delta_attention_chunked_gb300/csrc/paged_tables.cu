@@ -16,7 +16,8 @@
 // Bound: 12 bytes a token are written; below ~100,000 tokens the launch and the
 // chain of dependent reads (lengths, running sum, free list) set the time: 24
 // requests of one token 3.4 us, 320 prompts of 860,000 tokens 7.3 us (10.3 MB,
-// floor 1.5 us; GPU time).  Three CTAs of 256 threads an SM, four tokens a thread:
+// floor 1.5 us; GPU time): the same chain, then a search a thread and a look-up a token that
+// wait for each other (issue slots 32 % busy, DRAM next to idle).  Three CTAs of 256 threads an SM, four tokens a thread:
 // one or two take 12.7 and 8.5 us, four of 512 threads 9.5 us (each forms the
 // sums again), eight tokens a thread 8.6 us (more code to fetch than it saves).
 //

@@ -28,6 +28,8 @@
 // CTAs of 512 threads an SM, 8 numbers of each row in flight a thread: 43 us with six of 256 (more,
 // smaller clusters wait longer for each other), 39 us with 4 numbers, 47 us with two of 1024,
 // 49 us with clusters of four, 39 to 44 us with the row's start fetched into L2 ahead.
+// bf16 rows 32 us (floor 12.2: half the bytes, the same sums, 2-byte loads); without draft rows
+// 22 us in fp32 and 21 us in bf16.
 // What is left of it: the chain before the row (length, token, two probabilities: three
 // dependent reads) and behind it (cluster barrier, second scan), in which nothing streams.
 #include <algorithm>
