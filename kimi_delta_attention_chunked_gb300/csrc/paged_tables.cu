@@ -114,7 +114,7 @@ kda_build_tables_kernel(const int32_t* __restrict__ ctx_len, const int32_t* __re
     for (int m = first; m < taken; m += stride) {
         const int n = find(s_page, m);
         const int b = pages_of(s_ctx[n]) + (m - s_page[n]);
-        if (b < blocks) block_table[(size_t)n * blocks + b] = m < n_free ? free_pages[m] : -1;
+        if ((unsigned)b < (unsigned)blocks) block_table[(size_t)n * blocks + b] = m < n_free ? free_pages[m] : -1;
     }
     // four consecutive tokens a thread: one search, 16-byte stores
     for (long long t0 = (long long)first * kTokensPerThread; t0 < n_tokens; t0 += (long long)stride * kTokensPerThread) {
@@ -138,7 +138,7 @@ kda_build_tables_kernel(const int32_t* __restrict__ ctx_len, const int32_t* __re
                 id = block_table[(size_t)n * blocks + b];
             } else {
                 const int m = s_page[n] + b - have;
-                id = m < n_free ? free_pages[m] : -1;
+                id = (unsigned)m < (unsigned)n_free ? free_pages[m] : -1;   // sums that wrapped stay inside, too
             }
             if (id >= 0) slot[e] = ((long long)id << page_log2) + (pos & (long long)(page - 1));
         }

@@ -6,7 +6,7 @@ import pytest
 import torch
 
 from _gpu import need_gpu
-from test_gpu_step import BF, F32, check, dists, make, on, run_verify
+from test_gpu_step import BF, F32, check, dists, i32, make, on, run_verify
 
 import kimi_delta_attention_chunked_gb300 as kda
 
@@ -256,3 +256,20 @@ def test_stream_of_another_device_is_refused():
         got = kda.kda_paged_attention(*args, stream=stream)
         torch.cuda.synchronize()
         assert torch.equal(got, want)
+
+
+def test_tables_lengths_whose_sums_wrap():
+    """Lengths past 2^31 together are outside the contract; the results mean nothing, and
+    nothing outside the buffers is written."""
+    dev = need_gpu()
+    big = 2 ** 31 - 1
+    for ctx, new in (([0, 0, 5], [big, big, 7]), ([big, 3, big], [big, big, big]), ([big - 3, 40, 0], [9, big, 40])):
+        whole = torch.full((7, 4), 9, dtype=torch.int32, device=dev)
+        outs = [torch.full((n + 8,), 9, dtype=t, device=dev) for n, t in
+                ((4, torch.int32), (3, torch.int32), (500, torch.int64), (500, torch.int32), (1, torch.int32))]
+        kda.kda_build_block_tables(i32(ctx, dev), i32(new, dev), i32([1, 2, 3, 4, 5], dev), whole[2:5], 16, 500,
+                                   **dict(zip(("cu_seqlens", "seq_len", "slot_map", "positions", "n_taken"), (o[4:-4] for o in outs))))
+        assert bool((whole[:2] == 9).all()) and bool((whole[5:] == 9).all())
+        assert all(bool((o[:4] == 9).all()) and bool((o[-4:] == 9).all()) for o in outs)
+        slots = outs[2][4:-4]
+        assert bool(((slots >= -1) & (slots < 10 * 16)).all())
