@@ -378,7 +378,7 @@ KDA_API size_t kda_paged_attention_workspace_size(int T, int H_q, int H_kv, int 
  * cu_seqlens  [N + 1] int32 device array, 0 = cu[0] <= ... <= cu[N] <= T;
  *             rows of q at and past cu[N] are padding, their o is not written
  * seq_len     [N] int32 device array
- * scale       finite and > 0
+ * scale       > 0 and at most 2^127
  * window      0: no window
  * max_blocks  at most KDA_MAX_STEP_POSITIONS / page_size
  * o           [T, H_q, d] dtype;  lse [T, H_q] float or NULL

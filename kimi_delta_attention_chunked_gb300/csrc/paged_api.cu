@@ -1,7 +1,6 @@
 // paged_api.cu -- C entry points of the serving-step operators: argument
 // checks, path selection, launches.  See include/kda.h for their contracts.
 #include <algorithm>
-#include <cmath>
 
 #include "paged.cuh"
 
@@ -84,7 +83,8 @@ kda_status kda_paged_attention(const void* q, const void* k_cache, const void* v
     if (!dim_ok(d) || !page_ok(page_size)) return KDA_ERR_UNSUPPORTED;
     if (N > KDA_MAX_STEP_REQUESTS || H_q > (1 << 16)) return KDA_ERR_UNSUPPORTED;
     if ((int64_t)max_blocks * page_size > KDA_MAX_STEP_POSITIONS) return KDA_ERR_UNSUPPORTED;
-    if (!std::isfinite(scale) || !(scale > 0.f)) return KDA_ERR_INVALID_ARG;
+    // at most 2^127: the kernels work with scale log2(e), which has to be finite too
+    if (!(scale > 0.f) || !(scale <= 0x1p127f)) return KDA_ERR_INVALID_ARG;
     if (q_stride < (int64_t)H_q * d) return KDA_ERR_INVALID_ARG;
     if (T == 0 || N == 0) return KDA_OK;
     if (!q || !cu_seqlens || !seq_len || !o) return KDA_ERR_INVALID_ARG;

@@ -68,3 +68,10 @@ def big(dt, *shape):
 def test_binding_sizes_are_not_cut_off(call):
     with pytest.raises(ValueError, match="past 2"):
         call()
+
+
+def test_attention_scale_stays_finite_in_octaves(lib):  # noqa: F811
+    """scale log2(e) past the largest float would make NaN of a score of 0."""
+    assert attention(lib, scale=2.5e38, bytes=0) == E.KDA_ERR_INVALID_ARG
+    assert attention(lib, scale=2.0 ** 127, bytes=0) == E.KDA_ERR_WORKSPACE      # accepted up to the next check
+    assert attention(lib, scale=1e-45, bytes=0) == E.KDA_ERR_WORKSPACE
