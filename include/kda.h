@@ -288,8 +288,7 @@ KDA_API kda_status kda_decode_multi(const void* q, const void* k, const void* v,
  * ---------------------------------------------------------------------------
  * Serving step of a model that mixes KDA layers with softmax-attention layers
  * of grouped query heads (keys and values of one head size, 32, 64 or 128; latent
- * attention, whose keys and values have other sizes, is not among them).
- * The attention layers keep keys and values in a paged cache:
+ * attention has its own calls below).  The attention layers keep keys and values in a paged cache:
  *
  *   k_cache, v_cache  [n_pages, H_kv, page_size, d] dtype, 16-byte aligned
  *   slot              page * page_size + (place inside the page)
@@ -394,6 +393,130 @@ KDA_API kda_status kda_paged_attention(const void* q, const void* k_cache, const
                                int H_kv, int d, int page_size, int max_blocks, int n_pages,
                                float scale, int window, kda_dtype dtype, void* o, float* lse,
                                void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/*
+ * ---------------------------------------------------------------------------
+ * Latent attention.  A layer may keep, of each token, one latent vector of 512
+ * channels that all heads share and a rotated key part of 64 channels beside it:
+ *
+ *   cache  [n_pages, page_size, 576] dtype, 16-byte aligned: the latent, then the
+ *          key part; slots and block tables as above
+ *
+ * and has two forms.  Absorbed (kda_latent_attention): the query holds the key
+ * projection already, 512 + 64 channels a head against a cache row, and the latents
+ * are the values, 512 channels a head of output.  Expanded (kda_expanded_attention): keys
+ * and values were projected from the latents again, 128 + 64 channels of a key (the 64
+ * shared by the heads) and 128 of a value.  Single tokens and a few of them take the
+ * first, prompts the second.  kda_rotary turns queries, and the key parts that go into the
+ * expanded form; kda_latent_append turns the cache's on their way.
+ */
+
+/*
+ * Rotary positions.  Of each head's d channels the first `rot` are turned in
+ * rot / 2 pairs: pair i of a token at position p, with angle w = p * inv_freq[i],
+ *     (a, b) -> factor (a cos w - b sin w, b cos w + a sin w)
+ * is channels (2 i, 2 i + 1) when `interleaved`, else (i, i + rot / 2).  The other
+ * channels are copied.  The angle is formed to 2^-32 turns for every int32 position and
+ * frequency below 1 (radians a position); sine, cosine and products are fp32.
+ *
+ * x, out     [T, H, d] dtype, strides in elements, the channels contiguous.  out may be
+ *            x itself with the same strides (the other channels then stay as they
+ *            are), else the two may share no element; the rows of out may not overlap
+ * positions  [T] int32;  inv_freq [rot / 2] float, both device arrays
+ * factor     finite; multiplies what is turned
+ * rot is even; d is at most 256 (more: KDA_ERR_UNSUPPORTED).
+ */
+KDA_API kda_status kda_rotary(const void* x, const int32_t* positions, const float* inv_freq, int64_t x_token_stride,
+                      int64_t x_head_stride, int64_t out_token_stride, int64_t out_head_stride, int T, int H, int d,
+                      int rot, int interleaved, float factor, kda_dtype dtype, void* out, cudaStream_t stream);
+
+/*
+ * Writes the latents and key parts of T new tokens into the paged latent cache, the
+ * key part turned by its token's position on the way (as kda_rotary does with 64 of 64
+ * channels).  Row t goes to slot_map[t]; slots below 0 or at and past
+ * n_pages * page_size are skipped.
+ *
+ * c          [T, 512] dtype, k_rope [T, 64] dtype: consecutive tokens are c_stride
+ *            and k_rope_stride elements apart (both may be slices of one projection)
+ * slot_map   [T] int64.  What a slot named by two tokens holds is unspecified: each
+ *            piece of its row is either one's.
+ * positions  [T] int32, inv_freq [32] float; both NULL: the key part is copied
+ */
+KDA_API kda_status kda_latent_append(const void* c, const void* k_rope, const int64_t* slot_map, const int32_t* positions,
+                             const float* inv_freq, int64_t c_stride, int64_t k_rope_stride, int T, int page_size,
+                             int n_pages, int interleaved, float factor, kda_dtype dtype, void* cache,
+                             cudaStream_t stream);
+
+/* Bytes of device workspace kda_latent_attention needs for T new tokens. */
+KDA_API size_t kda_latent_attention_workspace_size(int T, int H, kda_dtype dtype);
+
+/*
+ * Absorbed attention of new tokens over a paged latent cache that holds their own
+ * rows already.  Token i of the m = cu_seqlens[n + 1] - cu_seqlens[n] new tokens of
+ * request n stands at position p = seq_len[n] - m + i and sees the cache rows c_j,
+ * j <= p, of its request.  Per head h:
+ *
+ *     o = sum_j exp(scale q.c_j - lse) c_j[0 .. 511],   lse = ln sum_j exp(scale q.c_j)
+ *
+ * One call serves any mix of single tokens (decode), a few tokens (verify) and chunks.
+ * A row that sees no key gives o = 0, lse = -inf.  Keys whose block_table entry names
+ * no page of the cache are left out, as are keys past max_blocks * page_size.  What
+ * stands in the cache at places that a row does not see, NaN among it, does not reach
+ * that row.
+ *
+ * q           [T, H, 576] dtype, consecutive tokens q_stride elements apart
+ * cu_seqlens  [N + 1] int32 device array, 0 = cu[0] <= ... <= cu[N] <= T;
+ *             rows of q at and past cu[N] are padding, their o is not written
+ * seq_len     [N] int32 device array
+ * scale       > 0 and at most 2^127 (of the expanded head: usually 192^-1/2)
+ * max_blocks  at most KDA_MAX_STEP_POSITIONS / page_size
+ * o           [T, H, 512] dtype, 16-byte aligned;  lse [T, H] float or NULL
+ * workspace   kda_latent_attention_workspace_size bytes, 256-byte aligned; a call has it to
+ *             itself until it is complete
+ * The scores, their statistics and the sums are fp32.
+ */
+KDA_API kda_status kda_latent_attention(const void* q, const void* cache, const int32_t* block_table,
+                                const int32_t* cu_seqlens, const int32_t* seq_len, int64_t q_stride, int N, int T, int H,
+                                int page_size, int max_blocks, int n_pages, float scale, kda_dtype dtype, void* o,
+                                float* lse, void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/* Bytes of device workspace kda_expanded_attention needs for T new tokens. */
+KDA_API size_t kda_expanded_attention_workspace_size(int T, int H, kda_dtype dtype);
+
+/*
+ * Expanded attention over packed keys and values.  Request n has the rows
+ * cu_seqlens[n] .. cu_seqlens[n + 1] - 1 of q (m of them) and the rows
+ * cu_seqlens_k[n] .. of the keys and values (s of them).  When `causal`, token i stands
+ * at position s - m + i and sees the keys j up to its own; else every token sees all
+ * keys of its request (an earlier part of the context, whose result is joined to the
+ * rest by the lse).  Per head h:
+ *
+ *     z_j = scale (q[0 .. 127].k_nope[j, h] + q[128 .. 191].k_rope[j])
+ *     o = sum_j exp(z_j - lse) v[j, h],   lse = ln sum_j exp(z_j)
+ *
+ * A row that sees no key gives o = 0, lse = -inf.  What stands in the keys and values at
+ * places that a row does not see, NaN among it, does not reach that row.
+ *
+ * q             [T, H, 192] dtype, consecutive tokens q_stride elements apart
+ * k_nope, v     [S, H, 128] dtype, token and head strides in elements (both may be slices of
+ *               one projection; tokens and heads may lie in either order);
+ *               k_rope [S, 64] dtype, tokens k_rope_stride elements apart
+ * cu_seqlens, cu_seqlens_k  [N + 1] int32 device arrays, rising from 0, at most T and S
+ *               at the end; rows of q at and past cu_seqlens[N] are padding, their o is
+ *               not written
+ * S + T         at most KDA_MAX_STEP_POSITIONS
+ * scale         > 0 and at most 2^127
+ * o             [T, H, 128] dtype, 16-byte aligned;  lse [T, H] float or NULL
+ * workspace     kda_expanded_attention_workspace_size bytes, 256-byte aligned; a call has it
+ *               to itself until it is complete
+ * The scores, their statistics and the sums are fp32.
+ */
+KDA_API kda_status kda_expanded_attention(const void* q, const void* k_nope, const void* k_rope, const void* v,
+                                  const int32_t* cu_seqlens, const int32_t* cu_seqlens_k, int64_t q_stride,
+                                  int64_t k_token_stride, int64_t k_head_stride, int64_t k_rope_stride,
+                                  int64_t v_token_stride, int64_t v_head_stride, int N, int T, int S, int H, float scale,
+                                  int causal, kda_dtype dtype, void* o, float* lse, void* workspace,
+                                  size_t workspace_bytes, cudaStream_t stream);
 
 /*
  * Verification of drafted tokens against the target's probabilities.  Request

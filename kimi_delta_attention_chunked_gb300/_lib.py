@@ -24,7 +24,9 @@ SYMBOLS = ("kda_prefill_workspace_size", "kda_prefill", "kda_prefill_ckpt", "kda
            "kda_prefill_noalloc", "kda_decode", "kda_decode_fused", "kda_decode_multi",
            "kda_get_last_device_status", "kda_check_wait_timeout", "kda_set_trace_events", "kda_debug_build",
            "kda_status_string", "kda_build_block_tables", "kda_cache_append", "kda_paged_attention_workspace_size",
-           "kda_paged_attention", "kda_verify_draft")
+           "kda_paged_attention", "kda_verify_draft", "kda_rotary", "kda_latent_append",
+           "kda_latent_attention_workspace_size", "kda_latent_attention", "kda_expanded_attention_workspace_size",
+           "kda_expanded_attention")
 NOALLOC_SCRATCH_BYTES = 64 << 20
 
 _lock = threading.Lock()
@@ -92,6 +94,18 @@ def _open(path):
     lib.kda_paged_attention.restype = I
     lib.kda_verify_draft.argtypes = [P, P, P, P, P, I, I, I, I, P, P, P]
     lib.kda_verify_draft.restype = I
+    lib.kda_rotary.argtypes = [P, P, P, L, L, L, L, I, I, I, I, I, F, I, P, P]
+    lib.kda_rotary.restype = I
+    lib.kda_latent_append.argtypes = [P, P, P, P, P, L, L, I, I, I, I, F, I, P, P]
+    lib.kda_latent_append.restype = I
+    lib.kda_latent_attention_workspace_size.argtypes = [I, I, I]
+    lib.kda_latent_attention_workspace_size.restype = Z
+    lib.kda_latent_attention.argtypes = [P, P, P, P, P, L, I, I, I, I, I, I, F, I, P, P, P, Z, P]
+    lib.kda_latent_attention.restype = I
+    lib.kda_expanded_attention_workspace_size.argtypes = [I, I, I]
+    lib.kda_expanded_attention_workspace_size.restype = Z
+    lib.kda_expanded_attention.argtypes = [P, P, P, P, P, P, L, L, L, L, L, L, I, I, I, I, F, I, I, P, P, P, Z, P]
+    lib.kda_expanded_attention.restype = I
     lib.kda_get_last_device_status.argtypes = [P]
     lib.kda_get_last_device_status.restype = I
     lib.kda_check_wait_timeout.argtypes = [ctypes.c_longlong, P]

@@ -42,7 +42,9 @@ def _load():
             entry = lambda name: ctypes.cast(getattr(lib, name), ctypes.c_void_p).value  # noqa: E731
             mod.set_entries(_lib.KDAError, entry("kda_build_block_tables"), entry("kda_cache_append"),
                             entry("kda_paged_attention_workspace_size"), entry("kda_paged_attention"),
-                            entry("kda_verify_draft"))
+                            entry("kda_verify_draft"), entry("kda_rotary"), entry("kda_latent_append"),
+                            entry("kda_latent_attention_workspace_size"), entry("kda_latent_attention"),
+                            entry("kda_expanded_attention_workspace_size"), entry("kda_expanded_attention"))
             _binding = mod
         return _binding
 

@@ -44,6 +44,14 @@ struct Shape {
     int extra;                                     // places on the line before a unit's tiles
 };
 
+// The same over packed keys: those of request n lie at rows cu_k[n] .. cu_k[n + 1] - 1 of [S, ...]
+// tensors, without pages.  Where the lengths of a paged call come as cu and seq_len, those of a
+// packed one come as cu and cu_k.
+struct PackedShape : Shape {
+    int S;                                         // rows of the keys
+    int causal;                                    // 0: every row sees all keys of its request
+};
+
 // One request's lengths, inside the buffers whatever the device arrays hold.
 struct Req {
     int tok0, len;                                 // first row of q, new tokens
@@ -62,6 +70,18 @@ __device__ __forceinline__ Req load_req(const Shape& s, const int32_t* __restric
     r.pos0 = seq - r.len;
     const long long cap = (long long)s.blocks << s.page_log2;
     r.kend = (int)min((long long)seq, cap);
+    return r;
+}
+
+__device__ __forceinline__ Req load_req(const PackedShape& s, const int32_t* __restrict__ cu,
+                                        const int32_t* __restrict__ cu_k, int n) {
+    Req r;
+    r.tok0 = min(max(cu[n], 0), s.T);
+    const int end = min(max(cu[n + 1], r.tok0), s.T);
+    r.len = end - r.tok0;
+    const int key0 = min(max(cu_k[n], 0), s.S);
+    r.kend = min(max(cu_k[n + 1], key0), s.S) - key0;
+    r.pos0 = s.causal ? r.kend - r.len : r.kend;   // at kend and behind it, a row sees every key
     return r;
 }
 
@@ -131,8 +151,8 @@ struct Piece {
 
 // Finds the piece of CTA `c` of `C`.  Every thread of the block (NT of them)
 // calls it; `cost` holds n_req words and `red` NT / 32, of 64 bits, and free again after the block's next barrier.
-template <int NT>
-__device__ __forceinline__ Piece find_piece(const Shape& s, const int32_t* __restrict__ cu,
+template <int NT, class Sh>
+__device__ __forceinline__ Piece find_piece(const Sh& s, const int32_t* __restrict__ cu,
                                             const int32_t* __restrict__ seq_len, int c, int C,
                                             unsigned long long* cost,
                                             unsigned long long* red, Piece* shared) {
@@ -214,7 +234,8 @@ struct Walker {
     Req r;
     int units;
 
-    __device__ __forceinline__ void start(const Shape& s, const int32_t* cu, const int32_t* seq_len, const Piece& p,
+    template <class Sh>
+    __device__ __forceinline__ void start(const Sh& s, const int32_t* cu, const int32_t* seq_len, const Piece& p,
                                           int cta) {
         c = cta;
         at = p.begin;
@@ -262,7 +283,8 @@ struct Walker {
     }
 
     // The next part, or false at the end of the piece.
-    __device__ __forceinline__ bool next(const Shape& s, const int32_t* cu, const int32_t* seq_len, Unit& u) {
+    template <class Sh>
+    __device__ __forceinline__ bool next(const Sh& s, const int32_t* cu, const int32_t* seq_len, Unit& u) {
         while (at < end) {
             while (i >= units) {
                 i = 0;

@@ -2,20 +2,17 @@
 // checks, path selection, launches.  See include/kda.h for their contracts.
 #include <algorithm>
 
+#include "api_checks.cuh"
 #include "paged.cuh"
 
 namespace {
 
-kda_status from_cuda(cudaError_t e) {
-    if (e == cudaSuccess) return KDA_OK;
-    if (e == cudaErrorNotSupported) return KDA_ERR_UNSUPPORTED;
-    return KDA_ERR_CUDA;
-}
+using kda_host::aligned;
+using kda_host::dtype_ok;
+using kda_host::from_cuda;
+using kda_host::page_ok;
 
-bool page_ok(int p) { return p == 16 || p == 32 || p == 64 || p == 128 || p == 256; }
 bool dim_ok(int d) { return d == 32 || d == 64 || d == 128; }
-bool dtype_ok(kda_dtype t) { return t == KDA_FP32 || t == KDA_BF16; }
-bool aligned(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
 
 // Enough for either path: which one runs also depends on the alignment of q.
 size_t attention_workspace(int T, int Hq, int Hkv, int d, kda_dtype dt) {

@@ -3,8 +3,8 @@
 //
 // A serving step calls these for every layer, and at small sizes a call costs
 // more on the host than on the GPU; the same checks written in Python and passed
-// through ctypes took 8 to 25 us a call.  _paged.py holds the signatures and
-// their documentation and passes every argument by position.  The C entries are
+// through ctypes took 8 to 25 us a call.  _paged.py and _latent.py hold the signatures and
+// their documentation and pass every argument by position.  The C entries are
 // handed over by _lib.py, which loads libkda.so.
 #include <Python.h>
 
@@ -34,6 +34,12 @@ struct Entries {
     decltype(&kda_paged_attention_workspace_size) attention_size;
     decltype(&kda_paged_attention) attention;
     decltype(&kda_verify_draft) verify;
+    decltype(&kda_rotary) rotary;
+    decltype(&kda_latent_append) latent_append;
+    decltype(&kda_latent_attention_workspace_size) latent_size;
+    decltype(&kda_latent_attention) latent;
+    decltype(&kda_expanded_attention_workspace_size) expanded_size;
+    decltype(&kda_expanded_attention) expanded;
 } g_kda{};
 PyObject* g_error = nullptr;                           // _lib.KDAError
 
@@ -121,6 +127,22 @@ const void* rows(const char* name, const Tensor& t, int dev, ScalarType dtype, a
     if (shape[0] > 1 && t.stride(0) < row) value_error(std::string(name) + ": tokens must not overlap");
     stride = std::max(t.stride(0), row);
     return t.data_ptr();
+}
+// a [tokens, heads, d] tensor whose tokens and heads may lie at any strides: pointer and
+// strides in elements (of a dim of one: as if it were packed).  Whether rows overlap is the C entry's to judge.
+const void* strided(const char* name, const Tensor& t, int dev, ScalarType dtype, at::IntArrayRef shape, int64_t& token,
+                    int64_t& head) {
+    check_shape(name, t, shape);
+    check_kind(name, t, dev, dtype);
+    if (t.stride(2) != 1 && shape[2] > 1) value_error(std::string(name) + ": the channels of a head must be contiguous");
+    head = shape[1] > 1 ? t.stride(1) : shape[2];
+    token = shape[0] > 1 ? t.stride(0) : std::max(t.stride(1), shape[2]) * shape[1];
+    return t.data_ptr();
+}
+double number(PyObject* o) {
+    const double x = PyFloat_AsDouble(o);
+    if (x == -1.0 && PyErr_Occurred()) throw Refused{};
+    return x;
 }
 // The stream of a call.  Tensors made here are that stream's own memory: the current
 // stream's could still be read or written by work queued there before they were freed, and
@@ -372,14 +394,178 @@ PyObject* verify_draft(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
     });
 }
 
-// set_entries(error class, five C function addresses): called once by _paged.py
+// the caller's workspace, checked, or a new one (None) of `bytes`; `bytes` becomes its size
+Tensor scratch(PyObject* o, const Stream& s, const Tensor& like, size_t& bytes) {
+    if (o == Py_None) return s.make(like, ScalarType::Byte, {(int64_t)bytes});
+    const Tensor& ws = tensor("workspace", o);
+    if (!ws.is_cuda() || ws.get_device() != s.current.device_index() || !ws.is_contiguous())
+        value_error("workspace must be contiguous and on cuda:" + std::to_string(s.current.device_index()));
+    bytes = (size_t)ws.numel() * ws.element_size();
+    return ws;
+}
+
+PyObject* rotary(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
+    return guarded("kda_rotary", n_args, 7, [&] {
+        const Tensor &x = tensor("x", a[0]), &pos = tensor("positions", a[1]), &freq = tensor("inv_freq", a[2]);
+        if (x.dim() != 3 || freq.dim() != 1)
+            value_error("x must have 3 dims and inv_freq 1, got " + std::to_string(x.dim()) + " and " + std::to_string(freq.dim()));
+        check_size("x", x);
+        const int64_t T = x.size(0), heads = x.size(1), d = x.size(2), rot = 2 * freq.size(0);
+        if (rot > d) value_error("inv_freq " + str(freq.sizes()) + " has more pairs than heads of " + std::to_string(d));
+        const double factor = number(a[3]);
+        const bool interleaved = truth(a[4]);
+        const kda_dtype code = code_of(x);
+        const ScalarType dt = x.scalar_type();
+        const int dev = device_of("x", x);
+        int64_t xt, xh, ot, oh;
+        const void *xp = strided("x", x, dev, dt, x.sizes(), xt, xh), *pp = need("positions", pos, dev, kI32, {T}),
+                   *fp = need("inv_freq", freq, dev, kF32, {freq.size(0)});
+        const Stream s = stream_of(a[6], dev);
+        const Tensor out = a[5] == Py_None ? s.make(x, dt, x.sizes()) : tensor("out", a[5]);
+        void* op = const_cast<void*>(strided("out", out, dev, dt, x.sizes(), ot, oh));
+        call("kda_rotary", dev, [&] {
+            return g_kda.rotary(xp, (const int32_t*)pp, (const float*)fp, xt, xh, ot, oh, (int)T, (int)heads, (int)d, (int)rot,
+                                interleaved, (float)factor, code, op, s.handle);
+        });
+        return THPVariable_Wrap(out);
+    });
+}
+
+constexpr int64_t kLatent = 512, kRope = 64, kNope = 128, kValue = 128;
+
+void check_latent_cache(const char* entry, const Tensor& cache) {
+    if (cache.dim() != 3 || cache.size(2) != kLatent + kRope)
+        value_error(std::string(entry) + ": cache must have shape [n_pages, page_size, 576], got " + str(cache.sizes()));
+    check_size("cache", cache);
+}
+
+// a [tokens, d] tensor whose tokens may lie further apart than d
+const void* lines(const char* name, const Tensor& t, int dev, ScalarType dtype, at::IntArrayRef shape, int64_t& stride) {
+    check_shape(name, t, shape);
+    check_kind(name, t, dev, dtype);
+    if (t.stride(1) != 1) value_error(std::string(name) + ": the channels of a token must be contiguous");
+    if (shape[0] > 1 && t.stride(0) < shape[1]) value_error(std::string(name) + ": tokens must not overlap");
+    stride = std::max(t.stride(0), shape[1]);
+    return t.data_ptr();
+}
+
+PyObject* latent_append(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
+    return guarded("kda_latent_append", n_args, 9, [&] {
+        const Tensor &c = tensor("c", a[0]), &r = tensor("k_rope", a[1]), &cache = tensor("cache", a[2]), &slot = tensor("slot_map", a[3]);
+        check_latent_cache("kda_latent_append", cache);
+        if (c.dim() != 2) value_error("c must have 2 dims, got " + std::to_string(c.dim()));
+        check_size("c", c);
+        const int64_t T = c.size(0);
+        check_shape("c", c, {T, kLatent});
+        check_shape("k_rope", r, {T, kRope});
+        const kda_dtype code = code_of(cache);
+        const ScalarType dt = cache.scalar_type();
+        const int dev = device_of("cache", cache);
+        const bool turned = a[4] != Py_None || a[5] != Py_None;
+        if (turned && (a[4] == Py_None || a[5] == Py_None)) value_error("positions and inv_freq come together");
+        const double factor = number(a[6]);
+        const bool interleaved = truth(a[7]);
+        int64_t cs, rs;
+        const void *cp = lines("c", c, dev, dt, {T, kLatent}, cs), *rp = lines("k_rope", r, dev, dt, {T, kRope}, rs);
+        void *kp = need("cache", cache, dev, dt, cache.sizes()), *sp = need("slot_map", slot, dev, kI64, {T}),
+             *pp = turned ? need("positions", tensor("positions", a[4]), dev, kI32, {T}) : nullptr,
+             *fp = turned ? need("inv_freq", tensor("inv_freq", a[5]), dev, kF32, {kRope / 2}) : nullptr;
+        const Stream s = stream_of(a[8], dev);
+        call("kda_latent_append", dev, [&] {
+            return g_kda.latent_append(cp, rp, (const int64_t*)sp, (const int32_t*)pp, (const float*)fp, cs, rs, (int)T,
+                                       (int)cache.size(1), (int)cache.size(0), interleaved, (float)factor, code, kp, s.handle);
+        });
+        Py_RETURN_NONE;
+    });
+}
+
+PyObject* latent_attention(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
+    return guarded("kda_latent_attention", n_args, 11, [&]() -> PyObject* {
+        const Tensor &q = tensor("q", a[0]), &cache = tensor("cache", a[1]), &table = tensor("block_table", a[2]),
+                     &cu = tensor("cu_seqlens", a[3]), &seq = tensor("seq_len", a[4]);
+        check_latent_cache("kda_latent_attention", cache);
+        if (q.dim() != 3 || table.dim() != 2)
+            value_error("q must have 3 dims and block_table 2, got " + std::to_string(q.dim()) + " and " + std::to_string(table.dim()));
+        check_size("q", q);
+        check_size("block_table", table);
+        const int64_t T = q.size(0), heads = q.size(1), n = table.size(0), blocks = table.size(1);
+        check_shape("q", q, {T, heads, kLatent + kRope});
+        check_shape("cu_seqlens", cu, {n + 1});
+        check_shape("seq_len", seq, {n});
+        const kda_dtype code = code_of(q);
+        const ScalarType dt = q.scalar_type();
+        const double scale = number(a[5]);
+        const bool want_lse = a[7] != Py_None || truth(a[8]);
+        const int dev = device_of("q", q);
+        int64_t qs;
+        const void* qp = rows("q", q, dev, dt, q.sizes(), qs);
+        void *kp = need("cache", cache, dev, dt, cache.sizes()), *tp = need("block_table", table, dev, kI32, table.sizes()),
+             *cup = need("cu_seqlens", cu, dev, kI32, {n + 1}), *sp = need("seq_len", seq, dev, kI32, {n});
+        const Stream s = stream_of(a[10], dev);
+        Tensor o = out("o", a[6], s, q, dt, {T, heads, kLatent}), lse;
+        if (want_lse) lse = out("lse", a[7], s, q, kF32, {T, heads});
+        size_t bytes = g_kda.latent_size((int)T, (int)heads, code);
+        const Tensor ws = scratch(a[9], s, q, bytes);
+        call("kda_latent_attention", dev, [&] {
+            return g_kda.latent(qp, kp, (const int32_t*)tp, (const int32_t*)cup, (const int32_t*)sp, qs, (int)n, (int)T, (int)heads,
+                                (int)cache.size(1), (int)blocks, (int)cache.size(0), (float)scale, code, o.data_ptr(),
+                                want_lse ? (float*)lse.data_ptr() : nullptr, ws.data_ptr(), bytes, s.handle);
+        });
+        if (want_lse) return tuple({o, lse});
+        return THPVariable_Wrap(o);
+    });
+}
+
+PyObject* expanded_attention(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
+    return guarded("kda_expanded_attention", n_args, 13, [&]() -> PyObject* {
+        const Tensor &q = tensor("q", a[0]), &kn = tensor("k_nope", a[1]), &kr = tensor("k_rope", a[2]), &v = tensor("v", a[3]),
+                     &cu = tensor("cu_seqlens", a[4]), &cuk = tensor("cu_seqlens_k", a[5]);
+        if (q.dim() != 3 || v.dim() != 3 || cu.dim() != 1)
+            value_error("q and v must have 3 dims and cu_seqlens 1, got " + std::to_string(q.dim()) + ", " + std::to_string(v.dim()) +
+                        " and " + std::to_string(cu.dim()));
+        check_size("q", q);
+        check_size("v", v);
+        check_size("cu_seqlens", cu);
+        const int64_t T = q.size(0), heads = q.size(1), S = v.size(0), n = cu.size(0) - 1;
+        if (n < 0) value_error("cu_seqlens must not be empty");
+        check_shape("q", q, {T, heads, kNope + kRope});
+        check_shape("k_nope", kn, {S, heads, kNope});
+        check_shape("k_rope", kr, {S, kRope});
+        check_shape("v", v, {S, heads, kValue});
+        check_shape("cu_seqlens_k", cuk, {n + 1});
+        const kda_dtype code = code_of(q);
+        const ScalarType dt = q.scalar_type();
+        const double scale = a[6] == Py_None ? 1.0 / std::sqrt((double)(kNope + kRope)) : number(a[6]);
+        const bool causal = truth(a[7]), want_lse = a[9] != Py_None || truth(a[10]);
+        const int dev = device_of("q", q);
+        int64_t qs, knt, knh, krs, vt, vh;
+        const void *qp = rows("q", q, dev, dt, q.sizes(), qs), *knp = strided("k_nope", kn, dev, dt, kn.sizes(), knt, knh),
+                   *krp = lines("k_rope", kr, dev, dt, kr.sizes(), krs), *vp = strided("v", v, dev, dt, v.sizes(), vt, vh);
+        void *cup = need("cu_seqlens", cu, dev, kI32, {n + 1}), *cukp = need("cu_seqlens_k", cuk, dev, kI32, {n + 1});
+        const Stream s = stream_of(a[12], dev);
+        Tensor o = out("o", a[8], s, q, dt, {T, heads, kValue}), lse;
+        if (want_lse) lse = out("lse", a[9], s, q, kF32, {T, heads});
+        size_t bytes = g_kda.expanded_size((int)T, (int)heads, code);
+        const Tensor ws = scratch(a[11], s, q, bytes);
+        call("kda_expanded_attention", dev, [&] {
+            return g_kda.expanded(qp, knp, krp, vp, (const int32_t*)cup, (const int32_t*)cukp, qs, knt, knh, krs, vt, vh, (int)n,
+                                  (int)T, (int)S, (int)heads, (float)scale, causal, code, o.data_ptr(),
+                                  want_lse ? (float*)lse.data_ptr() : nullptr, ws.data_ptr(), bytes, s.handle);
+        });
+        if (want_lse) return tuple({o, lse});
+        return THPVariable_Wrap(o);
+    });
+}
+
+// set_entries(error class, C function addresses in the order of Entries): called once by _paged.py
+constexpr int kEntries = 11;
 PyObject* set_entries(PyObject*, PyObject* const* a, Py_ssize_t n) {
-    if (n != 6) {
+    if (n != kEntries + 1) {
         PyErr_SetString(PyExc_TypeError, "set_entries: wrong number of arguments");
         return nullptr;
     }
-    void* p[5];
-    for (int i = 0; i < 5; ++i) {
+    void* p[kEntries];
+    for (int i = 0; i < kEntries; ++i) {
         p[i] = PyLong_AsVoidPtr(a[i + 1]);
         if (!p[i]) {
             if (!PyErr_Occurred()) PyErr_SetString(PyExc_ValueError, "set_entries: null entry");
@@ -391,6 +577,12 @@ PyObject* set_entries(PyObject*, PyObject* const* a, Py_ssize_t n) {
     g_kda.attention_size = reinterpret_cast<decltype(g_kda.attention_size)>(p[2]);
     g_kda.attention = reinterpret_cast<decltype(g_kda.attention)>(p[3]);
     g_kda.verify = reinterpret_cast<decltype(g_kda.verify)>(p[4]);
+    g_kda.rotary = reinterpret_cast<decltype(g_kda.rotary)>(p[5]);
+    g_kda.latent_append = reinterpret_cast<decltype(g_kda.latent_append)>(p[6]);
+    g_kda.latent_size = reinterpret_cast<decltype(g_kda.latent_size)>(p[7]);
+    g_kda.latent = reinterpret_cast<decltype(g_kda.latent)>(p[8]);
+    g_kda.expanded_size = reinterpret_cast<decltype(g_kda.expanded_size)>(p[9]);
+    g_kda.expanded = reinterpret_cast<decltype(g_kda.expanded)>(p[10]);
     Py_INCREF(a[0]);
     Py_XSETREF(g_error, a[0]);
     Py_RETURN_NONE;
@@ -398,7 +590,9 @@ PyObject* set_entries(PyObject*, PyObject* const* a, Py_ssize_t n) {
 
 #define STEP_METHOD(name) {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(name)), METH_FASTCALL, nullptr}
 PyMethodDef g_methods[] = {STEP_METHOD(set_entries),     STEP_METHOD(build_block_tables), STEP_METHOD(cache_append),
-                           STEP_METHOD(paged_attention), STEP_METHOD(verify_draft),       {nullptr, nullptr, 0, nullptr}};
+                           STEP_METHOD(paged_attention), STEP_METHOD(verify_draft),       STEP_METHOD(rotary),
+                           STEP_METHOD(latent_append),   STEP_METHOD(latent_attention),   STEP_METHOD(expanded_attention),
+                           {nullptr, nullptr, 0, nullptr}};
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_step_binding", nullptr, -1, g_methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace
