@@ -89,8 +89,10 @@ kda_paged::PackedShape expanded_shape(const ExpandedArgs& a, const PagedPlan& p)
 cudaError_t launch_rotary(const RotaryArgs& a);
 cudaError_t launch_latent_append(const LatentAppendArgs& a);
 PagedPlan latent_plan_simt(int T, int H);
+PagedPlan latent_plan_tc(int T, int H);
 PagedPlan expanded_plan_simt(int T);
 cudaError_t launch_latent_attention_simt(const LatentArgs& a);
+cudaError_t launch_latent_attention_tc(const LatentArgs& a);
 cudaError_t launch_expanded_attention_simt(const ExpandedArgs& a);
 
 }  // namespace kda_host

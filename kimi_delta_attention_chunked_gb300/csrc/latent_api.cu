@@ -1,5 +1,6 @@
 // latent_api.cu -- C entry points of the latent-attention operators: argument
 // checks, path selection, launches.  See include/kda.h for their contracts.
+#include <algorithm>
 #include <cmath>
 
 #include "api_checks.cuh"
@@ -22,8 +23,11 @@ using kda_latent::kValue;
 
 constexpr int kMaxHeads = 1 << 16;
 
-size_t latent_workspace(int T, int H) {
-    return kda_host::paged_plan_bytes(kda_host::latent_plan_simt(T, H), kLatent);
+// Enough for either path: which one runs also depends on alignment.
+size_t latent_workspace(int T, int H, kda_dtype dt) {
+    const size_t simt = kda_host::paged_plan_bytes(kda_host::latent_plan_simt(T, H), kLatent);
+    if (dt != KDA_BF16) return simt;
+    return std::max(simt, kda_host::paged_plan_bytes(kda_host::latent_plan_tc(T, H), kLatent));
 }
 size_t expanded_workspace(int T) { return kda_host::paged_plan_bytes(kda_host::expanded_plan_simt(T), kValue); }
 
@@ -70,7 +74,7 @@ kda_status kda_latent_append(const void* c, const void* k_rope, const int64_t* s
 
 size_t kda_latent_attention_workspace_size(int T, int H, kda_dtype dtype) {
     if (T < 0 || H <= 0 || H > kMaxHeads || !dtype_ok(dtype)) return 0;
-    return latent_workspace(T, H);
+    return latent_workspace(T, H, dtype);
 }
 
 kda_status kda_latent_attention(const void* q, const void* cache, const int32_t* block_table, const int32_t* cu_seqlens,
@@ -88,10 +92,13 @@ kda_status kda_latent_attention(const void* q, const void* cache, const int32_t*
     if ((n_pages > 0 && !cache) || (max_blocks > 0 && !block_table)) return KDA_ERR_INVALID_ARG;
     if (!aligned(cache, 16) || !aligned(o, 16) || !aligned(q, element_size(dtype))) return KDA_ERR_INVALID_ARG;
     if (o == q || o == cache) return KDA_ERR_INVALID_ARG;
-    if (!workspace || workspace_bytes < latent_workspace(T, H) || !aligned(workspace, 256)) return KDA_ERR_WORKSPACE;
+    if (!workspace || workspace_bytes < latent_workspace(T, H, dtype) || !aligned(workspace, 256)) return KDA_ERR_WORKSPACE;
     const kda_host::LatentArgs a{q, cache, block_table, cu_seqlens, seq_len, q_stride, N, T, H, page_size, max_blocks, n_pages,
                                  scale, dtype, o, lse, workspace, stream, kda_host::status_word()};
-    return from_cuda(kda_host::launch_latent_attention_simt(a));
+    // the tensor-core path fetches q by TMA, whose rows start on 16-byte boundaries, and
+    // describes the cache to it, which an empty one cannot be
+    const bool tc = dtype == KDA_BF16 && aligned(q, 16) && q_stride % 8 == 0 && n_pages > 0 && max_blocks > 0;
+    return from_cuda(tc ? kda_host::launch_latent_attention_tc(a) : kda_host::launch_latent_attention_simt(a));
 }
 
 size_t kda_expanded_attention_workspace_size(int T, int H, kda_dtype dtype) {

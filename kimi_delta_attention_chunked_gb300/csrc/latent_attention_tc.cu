@@ -1,0 +1,697 @@
+// latent_attention_tc.cu -- absorbed attention over the paged latent cache on the tensor
+// cores (bf16), by pairs of CTAs.
+//
+// A cache row of 576 channels is the key of every head and its first 512 channels the
+// value.  A unit (paged.cuh) is up to 128 rows (a token and a query head each), 64 in either
+// CTA of a cluster of two.  Per tile of KEYS keys, with cta_group::2 products of M = 128:
+//     S = Q K^T     (128 x KEYS over 576 channels, both operands in shared memory)
+//     P = 2^(scale log2(e) S - m)   (registers; bf16 to shared memory)
+//     O += P V      (128 x 512 over KEYS keys, two products of N = 256)
+//
+// Why a pair.  128 rows of 512 sums are the whole TMEM of an SM.  With M = 128 over two CTAs
+// each holds 64 rows, and those use all 128 lanes: lanes 0-63 the first half of a product's N
+// columns, lanes 64-127 the second.  So O takes 256 columns of TMEM and S KEYS / 2, S is double
+// buffered, and the tensor cores run at their full rate.  64 rows in a CTA alone would pay
+// twice the tensor time for the same rows: half of the lanes stay idle there.
+//
+// Where the operands lie.  Of B each CTA brings half of N.  For S that is half of the tile's
+// keys with all 576 channels, nine panels of 64 channels (panel 8 the rotated part).  For O it is half
+// of the value channels with all keys, and a product's descriptors name the same place in both CTAs.
+// So once S is complete, each CTA fetches over the four panels whose channels it does not need
+// the other half's keys in its own channels, as follows (lo and hi: the tile's first and second half
+// of the keys; CTA 0 loads lo, CTA 1 hi):
+//     place         0,1       2,3       4,5       6,7       8
+//     CTA 0, S     lo 0,1    lo 2,3    lo 4,5    lo 6,7    lo 8
+//     CTA 0, O     lo 0,1    hi 0,1    lo 4,5    hi 4,5
+//     CTA 1, S     hi 0,1    hi 2,3    hi 4,5    hi 6,7    hi 8
+//     CTA 1, O     lo 2,3    hi 2,3    lo 6,7    hi 6,7
+// Every cache row comes from HBM once; the four panels fetched again come from L2.
+//
+// Warps of each CTA: 0-3 softmax and output (a thread has one row and one half of the keys and
+// of the channels); 4 copies tiles and queries; 5 copies the four panels anew; 6 issues the
+// products (in CTA 0, for both); 7 walks the units.  Barriers of loads and of P are CTA 0's, where the
+// products are issued; a product's completion is told to both.
+//
+// Masked places.  A zero weight times a NaN or infinity in V is NaN.  So in a tile that not every
+// row sees whole, once S is complete, the softmax warps zero the rows of V that no row of the unit
+// sees, and in rows that some see and some do not take out the elements that are not finite.  They note
+// if they found one (in both CTAs); the output then adds such elements to the rows that see them.
+#include <algorithm>
+
+#include "attention_tc.cuh"
+#include "latent.cuh"
+
+namespace {
+
+using namespace kda_tc;
+using kda_latent::kLatent;
+using kda_latent::kRow;
+using kda_paged::Partials;
+using kda_paged::Piece;
+using kda_paged::Shape;
+using kda_paged::Walker;
+
+constexpr int kThreads = 256;
+constexpr int kCopyWarp = 4, kSwapWarp = 5, kIssueWarp = 6, kWalkWarp = 7;
+constexpr int kRows = 64;                              // rows of a CTA
+constexpr int kPanels = kRow / 64;                     // of a key
+constexpr int kQPanel = kRows * 128;                   // bytes of 64 rows x 64 channels
+constexpr int kUnits = 4;                              // unit descriptions in flight
+constexpr int kTailBytes = 3 * 1024;
+
+template <int KEYS>
+struct Cfg {
+    static constexpr int HALF = KEYS / 2;              // keys that a CTA loads of a tile
+    static constexpr int LOG2 = KEYS == 128 ? 7 : 6;
+    static constexpr int PANEL = HALF * 128;
+    static constexpr int TILE = kPanels * PANEL;
+    static constexpr int STAGES = 4;
+    static constexpr int KV0 = kPanels * kQPanel;
+    static constexpr int P0 = KV0 + STAGES * TILE;     // 64 rows x KEYS weights
+    static constexpr int TAIL = P0 + kRows * KEYS * 2;
+    static constexpr int SMEM = TAIL + kTailBytes;
+    static constexpr uint32_t TMEM_S = 256;            // columns: O from 0, the two S behind it
+    static_assert(SMEM <= 227 * 1024, "shared memory");
+    static_assert(STAGES * TILE >= kda_paged::kMaxRequests * 8 + 512, "scratch of find_piece");
+    static_assert(KEYS == 64, "the layout of P has one panel");
+};
+
+// How a unit's rows lie in the two CTAs.
+struct Tiling {
+    int heads;                                         // heads of a row tile
+    int tokens;                                        // tokens of a row tile
+    int by_heads;                                      // the CTAs share a token's heads; else they share the tokens
+};
+
+struct UnitSlot {
+    Unit u;
+    int more;                                          // 0: no further unit
+};
+
+struct Tail {
+    uint64_t kv_full[4], sw_full[4], q_full, p_full;   // CTA 0's are used
+    uint64_t kv_empty[4], s_full[2], q_empty, landed;  // each CTA's own
+    uint64_t join[2];                                  // of the two warps that share rows
+    uint64_t u_full[kUnits], u_empty[kUnits];
+    uint64_t drain;
+    uint32_t tmem;
+    int abort;
+    int odd_values[4];                                 // per unit, in turn: values that are not finite were taken out
+    UnitSlot units[kUnits];
+    float top[2][2][kRows];                            // per step, in turn: largest score of each half of the keys
+    float sum[2][kRows];                               // sum of the weights of each half
+};
+static_assert(sizeof(Tail) <= kTailBytes, "tail");
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+// A shared-memory address of CTA `rank` of the cluster, at the place that p has here.
+__device__ __forceinline__ uint32_t at_rank(const void* p, uint32_t rank) {
+    uint32_t r;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(kda::smem_u32(p)), "r"(rank));
+    return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
+__device__ __forceinline__ void arrive_remote(uint32_t bar) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ bool try_wait_cluster(uint64_t* bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(kda::smem_u32(bar)), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+// Tile load into this CTA's shared memory whose bytes are counted on CTA 0's barrier.
+__device__ __forceinline__ void load_pair(uint32_t dst, const void* tmap, int x, int y, int z, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%2, "
+        "%3, %4}], [%5];" ::"r"(dst),
+        "l"(tmap), "r"(x), "r"(y), "r"(z), "r"(bar)
+        : "memory");
+}
+__device__ __forceinline__ void mma_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+// Arrive once on the barrier at this place in both CTAs when the products issued so far are done.
+__device__ __forceinline__ void commit_pair(uint64_t* bar) {
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+            kda::smem_u32(bar)),
+        "h"((uint16_t)3)
+        : "memory");
+}
+
+// Adds to o[0..31] (channels c0 ..) the values that are not finite, of the keys that this row sees
+// among those that not all rows of the unit see.
+template <int LOG2>
+__device__ __forceinline__ void add_odd_values(float* o, int c0, const Unit& u, const Sight& un, int hi, const Shape& s,
+                                               const __nv_bfloat16* cache, const int32_t* table) {
+    const int b = min(min(un.hi, hi), u.te << LOG2);
+    for (int key = max(un.all_hi, u.tb << LOG2); key < b; ++key) {
+        const int page = table[(size_t)u.n * s.blocks + (key >> s.page_log2)];
+        if (page < 0 || page >= s.n_pages) continue;
+        const __nv_bfloat16* v =
+            cache + (((size_t)page << s.page_log2) + (key & ((1 << s.page_log2) - 1))) * kRow + c0;
+#pragma unroll
+        for (int c = 0; c < 32; ++c) {
+            const float x = __bfloat162float(v[c]);
+            if ((__float_as_uint(x) & 0x7f800000u) == 0x7f800000u) o[c] += x;
+        }
+    }
+}
+
+template <int KEYS>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+kda_latent_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
+                               const __nv_bfloat16* __restrict__ cache, const int32_t* __restrict__ table,
+                               const int32_t* __restrict__ cu, const int32_t* __restrict__ seq_len, Shape s, Tiling tiling,
+                               float scale_log2, __nv_bfloat16* __restrict__ o, float* __restrict__ lse, Partials parts,
+                               int* status) {
+    using C = Cfg<KEYS>;
+    extern __shared__ __align__(1024) unsigned char sm[];
+    Tail& tl = *reinterpret_cast<Tail*>(sm + C::TAIL);
+    const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
+    const int rank = (int)cluster_rank(), cluster = blockIdx.x >> 1;
+
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the merge may be set up; it waits for this grid
+    if (w == kIssueWarp) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(kda::smem_u32(&tl.tmem))
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    }
+    if (tid == 0) {
+        for (int i = 0; i < C::STAGES; ++i) {
+            kda::mbar_init(&tl.kv_full[i], 1);
+            kda::mbar_init(&tl.sw_full[i], 1);
+            kda::mbar_init(&tl.kv_empty[i], 1);
+        }
+        kda::mbar_init(&tl.q_full, 1);
+        kda::mbar_init(&tl.q_empty, 1);
+        kda::mbar_init(&tl.p_full, 8);
+        kda::mbar_init(&tl.landed, 1);
+        for (int i = 0; i < 2; ++i) {
+            kda::mbar_init(&tl.s_full[i], 1);
+            kda::mbar_init(&tl.join[i], 2);
+        }
+        for (int i = 0; i < kUnits; ++i) {
+            kda::mbar_init(&tl.u_full[i], 1);
+            kda::mbar_init(&tl.u_empty[i], rank == 0 ? 7 : 6);
+        }
+        kda::mbar_init(&tl.drain, 1);
+        kda::fence_barrier_init();
+        tl.abort = 0;
+        for (int i = 0; i < 4; ++i) tl.odd_values[i] = 0;
+    }
+    if (w == kCopyWarp && lane < 2) {
+        const CUtensorMap* m = lane == 0 ? &qmap : &kmap;
+        asm volatile("prefetch.tensormap [%0];" ::"l"(m) : "memory");
+    }
+    // this pair's piece of the work; both CTAs find the same
+    auto* cost = reinterpret_cast<unsigned long long*>(sm + C::KV0);
+    auto* red = cost + kda_paged::kMaxRequests;
+    const Piece piece = kda_paged::find_piece<kThreads>(s, cu, seq_len, cluster, gridDim.x >> 1, cost, red,
+                                                        reinterpret_cast<Piece*>(red + kThreads / 32));
+    kda::fence_proxy_async_smem();                     // the scratch becomes the target of copies
+    kda::tc_fence_before();
+    __syncthreads();
+    cluster_sync();                                    // both CTAs' barriers are there
+    kda::tc_fence_after();
+    const uint32_t tmem = (uint32_t)uniform((int)tl.tmem);
+    volatile int* abort_f = &tl.abort;
+    // true once the phase is complete; false when this CTA gives up.  Called by all
+    // lanes of a warp, with one answer for all of them, so that none leaves a loop alone
+    auto wait = [&](uint64_t* b, uint32_t parity) -> bool {
+        if (__all_sync(0xffffffffu, try_wait_cluster(b, parity))) return true;
+        return wait_longer(b, parity, &tl.abort, status) && __all_sync(0xffffffffu, try_wait_cluster(b, parity));
+    };
+    auto read_unit = [&](int k, Unit& u) -> bool {
+        if (!wait(&tl.u_full[k % kUnits], (k / kUnits) & 1)) return false;
+        const UnitSlot& sl = tl.units[k % kUnits];
+        u = sl.u;
+        const bool more = sl.more != 0;
+        __syncwarp();
+        if (lane == 0) kda::mbar_arrive(&tl.u_empty[k % kUnits]);
+        return more;
+    };
+    // pages of a half of a tile
+    const int pieces = (1 << s.page_log2) >= C::HALF ? 1 : C::HALF >> s.page_log2;
+    const int piece_log2 = min(s.page_log2, C::LOG2 - 1);
+    // lane's page of half `which` of the tile: lane's piece is lane % pieces; n_pages reads as zeros
+    auto page_of = [&](const Unit& u, int tile, int which) {
+        const int key = (tile << C::LOG2) + which * C::HALF + ((lane % pieces) << piece_log2);
+        int page = -1;
+        if (key < u.kend) page = table[(size_t)u.n * s.blocks + (key >> s.page_log2)];
+        return page < 0 || page >= s.n_pages ? s.n_pages : page;
+    };
+    // first place in its page of half `which` of a tile
+    auto place_of = [&](int tile, int which) {
+        return pieces > 1 ? 0 : ((tile << C::LOG2) + which * C::HALF) & ((1 << s.page_log2) - 1);
+    };
+    // the tile is not whole for every row of the unit
+    auto edge = [&](const Sight& si, int tile) { return ((tile + 1) << C::LOG2) > si.all_hi; };
+    int n_ld = 0, n_q = 0;                             // copies issued
+
+    if (w == kWalkWarp) {
+        // ---------------- unit descriptions
+        if (lane == 0 && rank == 0) parts.clear(cluster);
+        Walker walk;
+        walk.start(s, cu, seq_len, piece, cluster);
+        for (int k = 0;; ++k) {
+            Unit u;
+            const bool more = walk.next(s, cu, seq_len, u);
+            if (k >= kUnits && !wait(&tl.u_empty[k % kUnits], (k / kUnits - 1) & 1)) break;
+            __syncwarp();
+            if (lane == 0) {
+                if (more) tl.units[k % kUnits].u = u;
+                tl.units[k % kUnits].more = more;
+                kda::mbar_arrive(&tl.u_full[k % kUnits]);
+            }
+            if (!more) break;
+            if (lane == 0 && rank == 0) parts.describe(cluster, u);
+        }
+    } else if (w == kCopyWarp) {
+        // ---------------- this CTA's half of every tile, and its rows of the queries
+        bool ok = true;
+        const int q_bytes = kPanels * tiling.heads * tiling.tokens * 128;
+        const uint32_t q_bar = at_rank(&tl.q_full, 0);
+        for (int k = 0; ok; ++k) {
+            Unit u;
+            if (!read_unit(k, u)) break;
+            const bool both = tiling.by_heads || u.ntok > tiling.tokens;      // the second CTA has rows too
+            int next_page = page_of(u, u.tb, rank);
+            for (int tile = u.tb; tile < u.te; ++tile) {
+                const int page = next_page, st = n_ld % C::STAGES, y = place_of(tile, rank);
+                if (tile + 1 < u.te) next_page = page_of(u, tile + 1, rank);
+                if (n_ld >= C::STAGES && !wait(&tl.kv_empty[st], (n_ld / C::STAGES - 1) & 1)) { ok = false; break; }
+                __syncwarp();
+                if (lane == 0 && rank == 0) kda::mbar_arrive_expect_tx(&tl.kv_full[st], 2 * C::TILE);
+                __syncwarp();
+                const uint32_t dst = kda::smem_u32(sm + C::KV0 + st * C::TILE) + ((lane % pieces) << (piece_log2 + 7));
+                const uint32_t bar = at_rank(&tl.kv_full[st], 0);
+                for (int c = lane / pieces; c < kPanels; c += 32 / pieces)
+                    load_pair(dst + c * C::PANEL, &kmap, c * 64, y, page, bar);
+                ++n_ld;
+                if (tile == u.tb) {
+                    if (k > 0 && !wait(&tl.q_empty, (k - 1) & 1)) { ok = false; break; }
+                    __syncwarp();
+                    if (lane == 0 && rank == 0) kda::mbar_arrive_expect_tx(&tl.q_full, (both ? 2 : 1) * q_bytes);
+                    __syncwarp();
+                    if ((rank == 0 || both) && lane < kPanels)
+                        load_pair(kda::smem_u32(sm) + lane * kQPanel, &qmap, lane * 64,
+                                  u.qh0 + (tiling.by_heads ? rank * tiling.heads : 0),
+                                  u.tok0 + (tiling.by_heads ? 0 : rank * tiling.tokens), q_bar);
+                    ++n_q;
+                }
+            }
+        }
+    } else if (w == kSwapWarp) {
+        // ---------------- once S is complete, the other half's keys in this CTA's channels over
+        // the panels whose channels it does not need: CTA 0 at places 2, 3, 6, 7, CTA 1 at 0, 1, 4, 5
+        int g = 0;
+        bool ok = true;
+        for (int k = 0; ok; ++k) {
+            Unit u;
+            if (!read_unit(k, u)) break;
+            int next_page = page_of(u, u.tb, rank ^ 1);
+            for (int tile = u.tb; tile < u.te; ++tile, ++g) {
+                const int page = next_page, st = g % C::STAGES, y = place_of(tile, rank ^ 1);
+                if (tile + 1 < u.te) next_page = page_of(u, tile + 1, rank ^ 1);
+                if (!wait(&tl.s_full[g & 1], (g >> 1) & 1)) { ok = false; break; }
+                __syncwarp();
+                if (lane == 0 && rank == 0) kda::mbar_arrive_expect_tx(&tl.sw_full[st], 8 * C::PANEL);
+                __syncwarp();
+                const uint32_t dst = kda::smem_u32(sm + C::KV0 + st * C::TILE) + ((lane % pieces) << (piece_log2 + 7));
+                const uint32_t bar = at_rank(&tl.sw_full[st], 0);
+                for (int i = lane / pieces; i < 4; i += 32 / pieces) {
+                    const int c = 4 * (i >> 1) + (i & 1) + 2 * rank;          // channels, in panels; places: c ^ 2
+                    load_pair(dst + (c ^ 2) * C::PANEL, &kmap, c * 64, y, page, bar);
+                }
+            }
+        }
+        n_ld = g;
+    } else if (w == kIssueWarp) {
+        // ---------------- products: CTA 0 issues for both.  All lanes wait, an elected one issues
+        const uint32_t id_s = kda::idesc_bf16(128, KEYS, 0, 0), id_o = kda::idesc_bf16(128, 256, 0, 1);
+        const uint64_t q_desc = kda::sw128_desc(kda::smem_u32(sm), 16, 1024);
+        const uint64_t k_desc = kda::sw128_desc(kda::smem_u32(sm + C::KV0), 16, 1024);
+        const uint64_t v_desc = kda::sw128_desc(kda::smem_u32(sm + C::KV0), C::PANEL, 1024);
+        const uint64_t p_desc = kda::sw128_desc(kda::smem_u32(sm + C::P0), 16, 1024);
+        int g = 0;
+        bool issued = false, due = false, due_first = false, due_edge = false, ok = rank == 0;
+        // O (+)= P V of step g
+        auto values_step = [&](int step) -> bool {
+            const int st = step % C::STAGES;
+            if (!wait(&tl.sw_full[st], (step / C::STAGES) & 1)) return false;
+            if (due_edge && lane < 2) arrive_remote(at_rank(&tl.landed, lane));      // both CTAs may clean
+            __syncwarp();
+            if (!wait(&tl.p_full, step & 1)) return false;
+            kda::tc_fence_after();
+            if (elect_one()) {
+                const uint64_t b = v_desc + kda::desc_step(st * C::TILE);
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+#pragma unroll
+                    for (int i = 0; i < KEYS / 16; ++i) {
+                        const int hi = i >= C::HALF / 16;          // second half of the keys: two places on
+                        mma_pair(tmem + j * 128, p_desc + kda::desc_step(i * 32),
+                                 b + kda::desc_step((4 * j + 2 * hi) * C::PANEL + (i - hi * (C::HALF / 16)) * 2048), id_o,
+                                 (i > 0 || !due_first) ? 1u : 0u);
+                    }
+                commit_pair(&tl.kv_empty[st]);
+            }
+            __syncwarp();
+            return true;
+        };
+        for (int k = 0; ok; ++k) {
+            Unit u;
+            if (!read_unit(k, u)) break;
+            const Sight si = sight(u, 0, 0, u.ntok - 1);
+            const int tb = uniform(u.tb), te = uniform(u.te);
+            for (int tile = tb; tile < te; ++tile, ++g) {
+                const int st = g % C::STAGES;
+                ok = wait(&tl.kv_full[st], (g / C::STAGES) & 1);
+                if (ok && tile == tb) ok = wait(&tl.q_full, k & 1);
+                if (!ok) break;
+                kda::tc_fence_after();
+                if (elect_one()) {
+                    const uint64_t b = k_desc + kda::desc_step(st * C::TILE);
+                    const uint32_t d = tmem + C::TMEM_S + (g & 1) * C::HALF;
+#pragma unroll
+                    for (int i = 0; i < kRow / 16; ++i)
+                        mma_pair(d, q_desc + kda::desc_step((i >> 2) * kQPanel + (i & 3) * 32),
+                                 b + kda::desc_step((i >> 2) * C::PANEL + (i & 3) * 32), id_s, i > 0 ? 1u : 0u);
+                    commit_pair(&tl.s_full[g & 1]);
+                    if (tile == te - 1) commit_pair(&tl.q_empty);
+                }
+                __syncwarp();
+                issued = true;
+                if (due) ok = values_step(g - 1);
+                if (!ok) break;
+                due = true;
+                due_first = tile == tb;
+                due_edge = edge(si, tile);
+            }
+        }
+        if (ok && due) ok = values_step(g - 1);
+        if (issued) {                                  // no product in flight when TMEM is freed
+            if (elect_one()) commit_pair(&tl.drain);
+            __syncwarp();
+            (void)kda::mbar_wait(&tl.drain, 0, kda::kWaitCycles);
+        }
+    } else {
+        // ---------------- softmax and output: row, half of the keys and of each product's channels
+        const int row = tid & 63, half = tid >> 6;
+        const uint32_t lane_off = (uint32_t)(w * 32) << 16;
+        const int tok_in = tiling.by_heads ? 0 : rank * tiling.tokens + row / tiling.heads;
+        const int head_in = tiling.by_heads ? rank * tiling.heads + row : row % tiling.heads;
+        const bool in_tile = row < tiling.heads * tiling.tokens;
+        const uint32_t p_bar = at_rank(&tl.p_full, 0);
+        int g = 0, n_landed = 0, n_join = 0;
+        auto join = [&]() -> bool {                    // the two threads of a row meet: their warps do
+            __syncwarp();
+            if (lane == 0) kda::mbar_arrive(&tl.join[w & 1]);
+            return wait(&tl.join[w & 1], n_join++ & 1);
+        };
+        bool ok = true;
+        for (int k = 0; ok; ++k) {
+            Unit u;
+            if (!read_unit(k, u)) break;
+            const bool valid = in_tile && tok_in < u.ntok && u.qh0 + head_in < s.Hq;
+            const int hi = valid ? min(max(u.pos + tok_in + 1, 0), u.kend) : 0;
+            const bool busy = __any_sync(0xffffffffu, valid);
+            const Sight si = sight(u, 0, 0, u.ntok - 1);
+            // lane's page of this half of the tile: 0 where there is nothing to judge
+            auto judge = [&](int tile) {
+                const int key = (tile << C::LOG2) + half * C::HALF + (lane << piece_log2);
+                return lane < pieces && key < u.kend ? table[(size_t)u.n * s.blocks + (key >> s.page_log2)] : 0;
+            };
+            float m = -INFINITY, l = 0.f;
+            int page = busy ? judge(u.tb) : 0;
+            for (int tile = u.tb; tile < u.te; ++tile, ++g) {
+                const int k0 = (tile << C::LOG2) + half * C::HALF;
+                const unsigned missing = __ballot_sync(0xffffffffu, page < 0 || page >= s.n_pages);
+                if (busy && tile + 1 < u.te) page = judge(tile + 1);
+                const bool at_edge = edge(si, tile);
+                const int before = g - 1;              // its product must be complete before P and O are touched
+                auto wait_before = [&] {
+                    return before < 0 || wait(&tl.kv_empty[before % C::STAGES], (before / C::STAGES) & 1);
+                };
+                if (!wait(&tl.s_full[g & 1], (g >> 1) & 1)) { ok = false; break; }
+                kda::tc_fence_after();
+                uint32_t p[C::HALF / 2];
+                if (busy) {
+                    float x[C::HALF];
+#pragma unroll
+                    for (int c = 0; c < C::HALF; c += 32)
+                        kda::tmem_ld32(tmem + lane_off + C::TMEM_S + (g & 1) * C::HALF + c, x + c);
+                    kda::tmem_wait_ld();
+                    if (at_edge || missing) {
+#pragma unroll
+                        for (int c = 0; c < C::HALF; c += 16) {
+                            const bool none = (missing >> (c >> piece_log2)) & 1;
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) x[c + e] = none || k0 + c + e >= hi ? -INFINITY : x[c + e];
+                        }
+                    }
+                    float top[4] = {x[0], x[1], x[2], x[3]};
+#pragma unroll
+                    for (int c = 4; c < C::HALF; c += 4)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) top[e] = fmaxf(top[e], x[c + e]);
+                    float big = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+                    tl.top[g & 1][half][row] = big;
+                    if (!join()) { ok = false; break; }
+                    big = fmaxf(big, tl.top[g & 1][half ^ 1][row]);
+                    if (tile == u.tb) {
+                        m = big;
+                    } else {
+                        const bool grow = (big - m) * scale_log2 > kGrow;
+                        if (__any_sync(0xffffffffu, grow)) {
+                            if (!wait_before()) { ok = false; break; }
+                            kda::tc_fence_after();
+                            const float f = grow ? ex2((m - big) * scale_log2) : 1.f;
+#pragma unroll 1
+                            for (int c = 0; c < 256; c += 16) {
+                                float y[16];
+                                kda::tmem_ld16(tmem + lane_off + c, y);
+                                kda::tmem_wait_ld();
+#pragma unroll
+                                for (int e = 0; e < 16; ++e) y[e] *= f;
+                                kda::tmem_st16(tmem + lane_off + c, y);
+                            }
+                            kda::tmem_wait_st();
+                            l *= f;
+                            if (grow) m = big;
+                        }
+                    }
+                    const float ref = m == -INFINITY ? 0.f : m * scale_log2;
+                    const uint64_t sc2 = pack2(scale_log2, scale_log2), off2 = pack2(-ref, -ref);
+                    uint64_t sum[2] = {0, 0};
+#pragma unroll
+                    for (int c = 0; c < C::HALF; c += 2) {
+                        float a, b;
+                        unpack2(fma2(pack2(x[c], x[c + 1]), sc2, off2), a, b);
+                        a = ex2(a);
+                        b = ex2(b);
+                        sum[(c >> 1) & 1] = add2(sum[(c >> 1) & 1], pack2(a, b));
+                        p[c >> 1] = kda::pack_bf16x2(a, b);
+                    }
+                    float sa, sb;
+                    unpack2(add2(sum[0], sum[1]), sa, sb);
+                    l += sa + sb;
+                }
+                if (!wait_before()) { ok = false; break; }
+                if (busy) {
+                    unsigned char* dst = sm + C::P0 + row * 128;
+#pragma unroll
+                    for (int i = 0; i < C::HALF / 8; ++i)
+                        *reinterpret_cast<uint4*>(dst + (((half * (C::HALF / 8) + i) ^ (row & 7)) << 4)) =
+                            make_uint4(p[4 * i], p[4 * i + 1], p[4 * i + 2], p[4 * i + 3]);
+                }
+                if (at_edge) {
+                    // values that must not meet a zero weight (see the header)
+                    if (!wait(&tl.landed, n_landed & 1)) { ok = false; break; }
+                    ++n_landed;
+                    unsigned char* v = sm + C::KV0 + (g % C::STAGES) * C::TILE;
+                    const int t0 = tile << C::LOG2;
+                    int odd = 0;
+#pragma unroll 1
+                    for (int e = tid; e < 8 * C::HALF * 8; e += 128) {
+                        const int chunk = e & 7, r = (e >> 3) & (C::HALF - 1), place = (e >> 3) / C::HALF;
+                        const int key = t0 + ((place >> 1) & 1) * C::HALF + r;
+                        if (key < si.all_hi) continue;
+                        uint4* at = reinterpret_cast<uint4*>(v + place * C::PANEL + r * 128 + chunk * 16);
+                        uint4 x = make_uint4(0, 0, 0, 0);
+                        if (key < si.hi) {
+                            x = *at;
+                            uint32_t* y = reinterpret_cast<uint32_t*>(&x);
+                            int found = 0;
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                if ((y[i] & 0x7f80u) == 0x7f80u) { y[i] &= 0xffff0000u; found = 1; }
+                                if ((y[i] & 0x7f800000u) == 0x7f800000u) { y[i] &= 0x0000ffffu; found = 1; }
+                            }
+                            if (!found) continue;
+                            odd = 1;
+                        }
+                        *at = x;
+                    }
+                    if (odd) {
+                        for (uint32_t r = 0; r < 2; ++r)
+                            asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(at_rank(&tl.odd_values[k & 3], r)), "r"(1) : "memory");
+                    }
+                }
+                kda::fence_proxy_async_smem();
+                kda::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) arrive_remote(p_bar);
+            }
+            if (!ok) break;
+            // ---- output
+            const int last = g - 1;
+            if (busy) {
+                tl.sum[half][row] = l;
+                if (!join()) break;
+                l += tl.sum[half ^ 1][row];
+            }
+            if (!wait(&tl.kv_empty[last % C::STAGES], (last / C::STAGES) & 1)) break;
+            kda::tc_fence_after();
+            if (busy) {
+                const bool whole = u.first && u.last;
+                const int which = u.first ? 1 : 0;
+                const size_t at = (size_t)(u.tok0 + tok_in) * s.Hq + u.qh0 + head_in;
+                const int prow = rank * tiling.heads * tiling.tokens + row;          // row of a partial slot
+                const float inv = l == 0.f ? 0.f : 1.f / l;
+                const bool add = *(volatile int*)&tl.odd_values[k & 3] != 0 && valid;
+#pragma unroll 1
+                for (int c = 0; c < 256; c += 32) {
+                    float y[32];
+                    kda::tmem_ld32(tmem + lane_off + c, y);
+                    kda::tmem_wait_ld();
+                    const int c0 = (c & 128) * 2 + half * 128 + (c & 127);          // channel
+                    if (add) add_odd_values<C::LOG2>(y, c0, u, si, hi, s, cache, table);
+                    if (!valid) continue;
+                    if (whole) {
+                        uint4* dst = reinterpret_cast<uint4*>(o + at * kLatent + c0);
+#pragma unroll
+                        for (int e = 0; e < 32; e += 8)
+                            dst[e / 8] = make_uint4(kda::pack_bf16x2(y[e] * inv, y[e + 1] * inv),
+                                                    kda::pack_bf16x2(y[e + 2] * inv, y[e + 3] * inv),
+                                                    kda::pack_bf16x2(y[e + 4] * inv, y[e + 5] * inv),
+                                                    kda::pack_bf16x2(y[e + 6] * inv, y[e + 7] * inv));
+                    } else {
+                        float4* dst = reinterpret_cast<float4*>(parts.sums(cluster, which) + (size_t)prow * kLatent + c0);
+#pragma unroll
+                        for (int e = 0; e < 32; e += 4) dst[e / 4] = make_float4(y[e], y[e + 1], y[e + 2], y[e + 3]);
+                    }
+                }
+                if (valid && half == 0) {
+                    const float ref = m == -INFINITY ? -INFINITY : m * scale_log2;
+                    if (!whole) parts.stats(cluster, which)[prow] = make_float2(ref, l);
+                    else if (lse) lse[at] = l == 0.f ? -INFINITY : (ref + log2f(l)) * kLn2;
+                }
+            }
+            // no CTA is at the unit after the next before this one has arrived for the next
+            if (row == 0 && half == 0) tl.odd_values[(k + 2) & 3] = 0;
+            kda::tc_fence_before();
+        }
+    }
+    kda::tc_fence_before();
+    __syncthreads();
+    if (*abort_f && rank == 0) {                       // no copy in flight into shared memory that is given up
+        if (w == kCopyWarp) {
+            for (int i = max(0, n_ld - C::STAGES); i < n_ld; ++i)
+                (void)kda::mbar_wait(&tl.kv_full[i % C::STAGES], (i / C::STAGES) & 1, kda::kWaitCycles);
+            if (n_q > 0) (void)kda::mbar_wait(&tl.q_full, (n_q - 1) & 1, kda::kWaitCycles);
+        }
+        if (w == kSwapWarp)
+            for (int i = max(0, n_ld - C::STAGES); i < n_ld; ++i)
+                (void)kda::mbar_wait(&tl.sw_full[i % C::STAGES], (i / C::STAGES) & 1, kda::kWaitCycles);
+    }
+    __syncthreads();
+    cluster_sync();                                    // the other CTA is done with this one's memory and TMEM
+    if (w == kIssueWarp)
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+}
+
+// ---- host
+Tiling tiling_of(int H) {
+    const int groups = kda_host::latent_groups(H, kRows);
+    Tiling t;
+    t.heads = (H + groups - 1) / groups;
+    t.by_heads = groups > 1;
+    t.tokens = t.by_heads ? 1 : kRows / t.heads;
+    return t;
+}
+
+bool make_map(CUtensorMap* m, const void* base, cuuint64_t d1, cuuint64_t d2, cuuint64_t stride1, cuuint64_t stride2, int box1,
+              int box2) {
+    const cuuint64_t dims[3] = {(cuuint64_t)kRow, d1, d2};
+    const cuuint64_t strides[2] = {stride1, stride2};
+    const cuuint32_t box[3] = {64, (cuuint32_t)box1, (cuuint32_t)box2};
+    const cuuint32_t one[3] = {1, 1, 1};
+    return kda_host::tensor_map_encoder()(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box,
+                                          one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                                          CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+constexpr int kKeys = 64;
+
+}  // namespace
+
+namespace kda_host {
+
+PagedPlan latent_plan_tc(int T, int H) {
+    const Tiling t = tiling_of(H);
+    PagedPlan p;
+    p.Gv = t.by_heads ? 2 * t.heads : t.heads;         // heads of a unit
+    p.U = t.by_heads ? 1 : 2 * t.tokens;
+    p.rows = paged_slot_rows(p.U, T, p.Gv);
+    p.tile_log2 = Cfg<kKeys>::LOG2;
+    p.max_ctas = 80;                                   // pairs
+    p.extra = 4;
+    return p;
+}
+
+cudaError_t launch_latent_attention_tc(const LatentArgs& a) {
+    const PagedPlan p = latent_plan_tc(a.T, a.H);
+    const PagedArgs pa = latent_view(a);
+    const Tiling t = tiling_of(a.H);
+    if (!tensor_map_encoder()) return cudaErrorNotSupported;
+    CUtensorMap qm, km;
+    constexpr cuuint64_t row = kRow * 2;
+    if (!make_map(&qm, a.q, a.H, a.T, row, (cuuint64_t)a.q_stride * 2, t.heads, t.tokens) ||
+        !make_map(&km, a.cache, a.page_size, a.n_pages, row, row * a.page_size, std::min(a.page_size, Cfg<kKeys>::HALF), 1))
+        return cudaErrorInvalidValue;
+    auto kern = kda_latent_attention_tc_kernel<kKeys>;
+    static OncePerDevice once;
+    const cudaError_t e = once.run([&] {
+        return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<kKeys>::SMEM);
+    });
+    if (e != cudaSuccess) return e;
+    const int pairs = std::min(p.max_ctas, sm_count() / 2);
+    kern<<<2 * pairs, kThreads, Cfg<kKeys>::SMEM, a.stream>>>(
+        qm, km, static_cast<const __nv_bfloat16*>(a.cache), a.block_table, a.cu_seqlens, a.seq_len, latent_shape(a, p), t,
+        a.scale * kLog2e, static_cast<__nv_bfloat16*>(a.o), a.lse, paged_partials(pa, p), a.status);
+    const cudaError_t err = cudaGetLastError();
+    if (err != cudaSuccess) return err;
+    return launch_paged_merge(pa, p, pairs);
+}
+
+}  // namespace kda_host
