@@ -1,0 +1,657 @@
+// expanded_attention_tc.cu -- expanded latent attention over packed keys and values on the
+// tensor cores (bf16), by pairs of CTAs.
+//
+// A unit (paged.cuh) is up to 512 new tokens of one request and head: two row tiles of 2 x 128
+// rows, of which CTA r of a cluster of two has rows 128 r .. 128 r + 127.  Per tile of 128 keys,
+// with cta_group::2 products of M = 256:
+//     S = Q K^T     (256 x 128 over 192 channels: 128 of k_nope, 64 of k_rope; S in TMEM)
+//     P = 2^(scale log2(e) S - m)   (registers; written back over S as bf16)
+//     O += P V      (256 x 128 over 128 keys; P from TMEM, O in TMEM)
+// m is a reference per row that moves, with O and the sum of weights, only when a score exceeds
+// it by more than 8 octaves.
+//
+// Why a pair: each CTA brings half of B, 64 keys of 192 channels and 64 value channels of 128
+// keys, 40 KB of a tile instead of 80.  Three tiles fit beside the queries (96 KB), which one CTA
+// alone could not do with two, and a product reads 3/4 of the bytes from shared memory that
+// it takes the tensor cores to multiply, where one of a CTA alone reads as many and waits for them.
+//
+// Work goes in steps of one row tile and one key tile; step g uses half g & 1 of TMEM (S, O) and
+// of the softmax warps, so that the tensor cores run one half's products while the other half's
+// weights are formed.  A unit with two row tiles takes its key tiles in two steps each; one with
+// one (up to 256 tokens) sends its key tiles to the two halves in turn, which hold the sums over the
+// even and the odd ones and are joined at the end.
+//
+// Warps of each CTA: 0-3 and 4-7 softmax and output of half 0 and 1; 8 copies; 9 issues the
+// products (in CTA 0, for both); 10 walks the units.  Barriers of loads and of P are CTA 0's.
+//
+// Masked places.  A zero weight times a NaN or infinity in V is NaN.  So in a tile that not every row
+// of the unit sees whole, the softmax warps of its first step zero the rows of V that no row sees (the
+// next request's), and in the rows that some see and some do not take out the elements that are not
+// finite; the output adds such elements to the rows that see them.
+#include <algorithm>
+
+#include "attention_pair.cuh"
+#include "latent.cuh"
+
+namespace {
+
+using namespace kda_tc;
+using kda_latent::kKey;
+using kda_latent::kNope;
+using kda_latent::kValue;
+using kda_paged::PackedShape;
+using kda_paged::Partials;
+using kda_paged::Piece;
+using kda_paged::Walker;
+
+constexpr int kThreads = 384;
+constexpr int kCopyWarp = 8, kIssueWarp = 9, kWalkWarp = 10;
+constexpr int kKeys = 128, kKeysLog2 = 7;              // keys of a tile
+constexpr int kRows = 128;                             // rows of a CTA's part of a row tile
+constexpr int kTileTokens = 2 * kRows;                 // tokens of a row tile
+constexpr int kPanels = kKey / 64;
+constexpr int kQPanel = kRows * 128;                   // bytes of 128 rows x 64 channels
+constexpr int kQTile = kPanels * kQPanel;
+constexpr int kKPanel = kKeys / 2 * 128;               // of 64 keys x 64 channels
+constexpr int kKTile = kPanels * kKPanel;
+constexpr int kVTile = kKeys * 128;                    // of 128 keys x 64 channels
+constexpr int kStages = 3;
+constexpr int kK0 = 2 * kQTile, kV0 = kK0 + kStages * kKTile, kTail0 = kV0 + kStages * kVTile;
+constexpr int kUnits = 4;                              // unit descriptions in flight
+constexpr int kTailBytes = 4 * 1024;
+constexpr int kSmem = kTail0 + kTailBytes;
+constexpr uint32_t kTmemO = 256;                       // columns: S halves at 0 and 128, O halves from 256
+static_assert(kSmem <= 227 * 1024, "shared memory");
+static_assert(kStages * kKTile >= kda_paged::kMaxRequests * 8 + 512, "scratch of find_piece");
+
+struct UnitSlot {
+    Unit u;
+    int more;                                          // 0: no further unit
+};
+
+struct Tail {
+    uint64_t k_full[kStages], v_full[kStages], q_full, p_full[2];     // CTA 0's are used
+    uint64_t k_empty[kStages], v_empty[kStages], q_empty, s_full[2], o_full[2], landed[2];    // each CTA's own
+    uint64_t join_a, join_b;
+    uint64_t u_full[kUnits], u_empty[kUnits];
+    uint64_t drain;
+    uint32_t tmem;
+    int abort;
+    int odd_values[8];                                 // per unit, in turn: values that are not finite were taken out
+    UnitSlot units[kUnits];
+    float2 stats[2][kRows];                            // (reference in octaves, sum of weights) of each half's rows
+};
+static_assert(sizeof(Tail) <= kTailBytes, "tail");
+
+// Where the values lie in global memory.
+struct Values {
+    const __nv_bfloat16* v;
+    long long token, head;
+};
+
+// Adds to o[0..31] (channels c0 ..) the values that are not finite, of the keys that this row sees
+// among those that not all rows of the unit see.
+__device__ __forceinline__ void add_odd_values(float* o, int c0, const Unit& u, const Sight& un, int hi, int key0,
+                                               const Values& vs) {
+    const int b = min(min(un.hi, hi), u.te << kKeysLog2);
+    for (int key = max(un.all_hi, u.tb << kKeysLog2); key < b; ++key) {
+        const __nv_bfloat16* v = vs.v + (key0 + (long long)key) * vs.token + u.kvh * vs.head + c0;
+#pragma unroll
+        for (int c = 0; c < 32; ++c) {
+            const float x = __bfloat162float(v[c]);
+            if ((__float_as_uint(x) & 0x7f800000u) == 0x7f800000u) o[c] += x;
+        }
+    }
+}
+
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+kda_expanded_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap nmap,
+                                 const __grid_constant__ CUtensorMap rmap, const __grid_constant__ CUtensorMap vmap,
+                                 Values values, const int32_t* __restrict__ cu, const int32_t* __restrict__ cu_k,
+                                 PackedShape s, float scale_log2, __nv_bfloat16* __restrict__ o, float* __restrict__ lse,
+                                 Partials parts, int* status) {
+    extern __shared__ __align__(1024) unsigned char sm[];
+    Tail& tl = *reinterpret_cast<Tail*>(sm + kTail0);
+    const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
+    const int rank = (int)cluster_rank(), cluster = blockIdx.x >> 1;
+
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the merge may be set up; it waits for this grid
+    if (w == kIssueWarp) alloc_pair(&tl.tmem);
+    if (tid == 0) {
+        for (int i = 0; i < kStages; ++i) {
+            kda::mbar_init(&tl.k_full[i], 1);
+            kda::mbar_init(&tl.v_full[i], 1);
+            kda::mbar_init(&tl.k_empty[i], 1);
+            kda::mbar_init(&tl.v_empty[i], 1);
+        }
+        kda::mbar_init(&tl.q_full, 1);
+        kda::mbar_init(&tl.q_empty, 1);
+        for (int i = 0; i < 2; ++i) {
+            kda::mbar_init(&tl.s_full[i], 1);
+            kda::mbar_init(&tl.p_full[i], 8);
+            kda::mbar_init(&tl.o_full[i], 1);
+            kda::mbar_init(&tl.landed[i], 1);
+        }
+        kda::mbar_init(&tl.join_a, 8);
+        kda::mbar_init(&tl.join_b, 8);
+        for (int i = 0; i < kUnits; ++i) {
+            kda::mbar_init(&tl.u_full[i], 1);
+            kda::mbar_init(&tl.u_empty[i], rank == 0 ? 10 : 9);
+        }
+        kda::mbar_init(&tl.drain, 1);
+        kda::fence_barrier_init();
+        tl.abort = 0;
+        for (int i = 0; i < 8; ++i) tl.odd_values[i] = 0;
+    }
+    if (w == kCopyWarp && lane < 4) {
+        const CUtensorMap* m = lane == 0 ? &qmap : lane == 1 ? &nmap : lane == 2 ? &rmap : &vmap;
+        asm volatile("prefetch.tensormap [%0];" ::"l"(m) : "memory");
+    }
+    // this pair's piece of the work; both CTAs find the same
+    auto* cost = reinterpret_cast<unsigned long long*>(sm + kK0);
+    auto* red = cost + kda_paged::kMaxRequests;
+    const Piece piece = kda_paged::find_piece<kThreads>(s, cu, cu_k, cluster, gridDim.x >> 1, cost, red,
+                                                        reinterpret_cast<Piece*>(red + kThreads / 32));
+    kda::fence_proxy_async_smem();                     // the scratch becomes the target of copies
+    kda::tc_fence_before();
+    __syncthreads();
+    cluster_sync();                                    // both CTAs' barriers are there
+    kda::tc_fence_after();
+    const uint32_t tmem = (uint32_t)uniform((int)tl.tmem);
+    volatile int* abort_f = &tl.abort;
+    // true once the phase is complete; false when this CTA gives up.  Called by all
+    // lanes of a warp, with one answer for all of them, so that none leaves a loop alone
+    auto wait = [&](uint64_t* b, uint32_t parity) -> bool {
+        if (__all_sync(0xffffffffu, try_wait_cluster(b, parity))) return true;
+        return wait_longer(b, parity, &tl.abort, status) && __all_sync(0xffffffffu, try_wait_cluster(b, parity));
+    };
+    auto read_unit = [&](int k, Unit& u) -> bool {
+        if (!wait(&tl.u_full[k % kUnits], (k / kUnits) & 1)) return false;
+        const UnitSlot& sl = tl.units[k % kUnits];
+        u = sl.u;
+        const bool more = sl.more != 0;
+        __syncwarp();
+        if (lane == 0) kda::mbar_arrive(&tl.u_empty[k % kUnits]);
+        return more;
+    };
+    auto first_row = [&](const Unit& u) { return min(max(cu_k[u.n], 0), s.S); };      // of the request's keys
+    int n_ld = 0, n_q = 0;                             // tiles and queries whose copies were issued
+
+    if (w == kWalkWarp) {
+        // ---------------- unit descriptions
+        if (lane == 0 && rank == 0) parts.clear(cluster);
+        Walker walk;
+        walk.start(s, cu, cu_k, piece, cluster);
+        for (int k = 0;; ++k) {
+            Unit u;
+            const bool more = walk.next(s, cu, cu_k, u);
+            if (k >= kUnits && !wait(&tl.u_empty[k % kUnits], (k / kUnits - 1) & 1)) break;
+            __syncwarp();
+            if (lane == 0) {
+                if (more) tl.units[k % kUnits].u = u;
+                tl.units[k % kUnits].more = more;
+                kda::mbar_arrive(&tl.u_full[k % kUnits]);
+            }
+            if (!more) break;
+            if (lane == 0 && rank == 0) parts.describe(cluster, u);
+        }
+    } else if (w == kCopyWarp) {
+        // ---------------- copies: of each tile this CTA's keys, then its channels of the values
+        bool ok = true;
+        for (int k = 0; ok; ++k) {
+            Unit u;
+            if (!read_unit(k, u)) break;
+            const bool two = u.ntok > kTileTokens;
+            const int key0 = first_row(u);
+            for (int tile = u.tb; tile < u.te; ++tile) {
+                const int st = n_ld % kStages, at = key0 + (tile << kKeysLog2);
+                const uint32_t parity = (n_ld / kStages - 1) & 1;
+                if (n_ld >= kStages && !wait(&tl.k_empty[st], parity)) { ok = false; break; }
+                __syncwarp();
+                if (lane == 0) {
+                    if (rank == 0) kda::mbar_arrive_expect_tx(&tl.k_full[st], 2 * kKTile);
+                    const uint32_t dst = kda::smem_u32(sm + kK0 + st * kKTile), bar = at_rank(&tl.k_full[st], 0);
+                    const int y = at + rank * (kKeys / 2);
+                    load_pair(dst, &nmap, 0, u.kvh, y, bar);
+                    load_pair(dst + kKPanel, &nmap, 64, u.kvh, y, bar);
+                    load_pair(dst + 2 * kKPanel, &rmap, 0, 0, y, bar);
+                }
+                __syncwarp();
+                if (tile == u.tb) {
+                    if (k > 0 && !wait(&tl.q_empty, (k - 1) & 1)) { ok = false; break; }
+                    __syncwarp();
+                    if (lane == 0) {
+                        if (rank == 0) kda::mbar_arrive_expect_tx(&tl.q_full, (two ? 4 : 2) * kQTile);
+                        const uint32_t bar = at_rank(&tl.q_full, 0);
+                        for (int i = 0; i < (two ? 2 : 1); ++i)
+                            for (int c = 0; c < kPanels; ++c)
+                                load_pair(kda::smem_u32(sm) + i * kQTile + c * kQPanel, &qmap, c * 64, u.qh0,
+                                          u.tok0 + i * kTileTokens + rank * kRows, bar);
+                    }
+                    ++n_q;
+                    __syncwarp();
+                }
+                if (n_ld >= kStages && !wait(&tl.v_empty[st], parity)) { ok = false; break; }
+                __syncwarp();
+                if (lane == 0) {
+                    if (rank == 0) kda::mbar_arrive_expect_tx(&tl.v_full[st], 2 * kVTile);
+                    load_pair(kda::smem_u32(sm + kV0 + st * kVTile), &vmap, rank * 64, u.kvh, at, at_rank(&tl.v_full[st], 0));
+                }
+                __syncwarp();
+                ++n_ld;
+            }
+        }
+    } else if (w == kIssueWarp) {
+        // ---------------- products: CTA 0 issues for both.  All lanes wait, an elected one issues.
+        // P_h lies over S_h: the scores of a half's next step are issued behind its product P_h V, which
+        // waited for P_h, and the tensor cores take products in the order of issue
+        const uint32_t id_s = kda::idesc_bf16(256, kKeys, 0, 0), id_o = kda::idesc_bf16(256, kValue, 0, 1);
+        const uint64_t q_desc = kda::sw128_desc(kda::smem_u32(sm), 16, 1024);
+        const uint64_t k_desc = kda::sw128_desc(kda::smem_u32(sm + kK0), 16, 1024);
+        const uint64_t v_desc = kda::sw128_desc(kda::smem_u32(sm + kV0), kVTile, 1024);
+        int g = 0, n_k = 0;                            // steps; key tiles taken
+        uint32_t p_phase = 0;                          // bit h: parity of the next P_h
+        bool issued = false, ok = rank == 0;
+        // a step whose second product is due: flags, its tile's place in the ring
+        enum { kFirstUse = 1, kLastUse = 2, kAdd = 4, kFinal = 8, kDue = 16, kEdge = 32 };
+        struct Pending { int flags, at; };
+        Pending older{0, 0}, newer{0, 0};              // of steps g - 2 and g - 1
+        auto issue_scores = [&](int h, int tile, int at, int flags) {     // S_h = Q_tile K^T; one lane
+            const uint64_t a = q_desc + kda::desc_step(tile * kQTile), b = k_desc + kda::desc_step(at % kStages * kKTile);
+#pragma unroll
+            for (int i = 0; i < kKey / 16; ++i)
+                mma_pair(tmem + h * 128, a + kda::desc_step((i >> 2) * kQPanel + (i & 3) * 32),
+                         b + kda::desc_step((i >> 2) * kKPanel + (i & 3) * 32), id_s, i > 0 ? 1u : 0u);
+            commit_pair(&tl.s_full[h]);
+            if (flags & kLastUse) commit_pair(&tl.k_empty[at % kStages]);
+            if (flags & kFinal) commit_pair(&tl.q_empty);
+        };
+        auto issue_values = [&](int h, const Pending& pv) {               // O_h += P_h V; one lane
+            const uint64_t b = v_desc + kda::desc_step(pv.at % kStages * kVTile);
+#pragma unroll
+            for (int i = 0; i < kKeys / 16; ++i)
+                mma_pair_ta(tmem + kTmemO + h * 128, tmem + h * 128 + 8 * i, b + kda::desc_step(i * 2048), id_o,
+                            (i > 0 || (pv.flags & kAdd)) ? 1u : 0u);
+            if (pv.flags & kLastUse) commit_pair(&tl.v_empty[pv.at % kStages]);
+            if (pv.flags & kFinal) commit_pair(&tl.o_full[h]);
+        };
+        // values there, weights there (and what has to be cleaned is)
+        auto take_values = [&](int h, const Pending& pv) -> bool {
+            if (pv.flags & kFirstUse) {
+                if (!wait(&tl.v_full[pv.at % kStages], (pv.at / kStages) & 1)) return false;
+                if ((pv.flags & kEdge) && lane < 2) arrive_remote(at_rank(&tl.landed[h], lane));
+                __syncwarp();
+            }
+            if (!wait(&tl.p_full[h], (p_phase >> h) & 1)) return false;
+            p_phase ^= 1u << h;
+            kda::tc_fence_after();
+            return true;
+        };
+        auto values_step = [&](int h, const Pending& pv) -> bool {
+            if (!take_values(h, pv)) return false;
+            if (elect_one()) issue_values(h, pv);
+            __syncwarp();
+            return true;
+        };
+        auto take_keys = [&](int at) -> bool {
+            if (!wait(&tl.k_full[at % kStages], (at / kStages) & 1)) return false;
+            kda::tc_fence_after();
+            return true;
+        };
+        for (int k = 0; ok; ++k) {
+            Unit u;
+            if (!read_unit(k, u)) break;
+            const int two = uniform(u.ntok > kTileTokens), tiles = uniform(u.te - u.tb), steps = tiles << two;
+            const int tb = uniform(u.tb);
+            const int whole = uniform(sight(u, 0, 0, u.ntok - 1).all_hi >> kKeysLog2);    // tiles below it: all rows see all
+            auto due = [&](int t, int at) {            // the second product of step t
+                Pending pv;
+                pv.at = at;
+                pv.flags = kDue | (!two || !(t & 1) ? kFirstUse : 0) | (!two || (t & 1) ? kLastUse : 0) | (t >= 2 ? kAdd : 0) |
+                           (t >= steps - 2 ? kFinal : 0) | (tb + (t >> two) >= whole ? kEdge : 0);
+                return pv;
+            };
+            // a unit of two row tiles past its first key tile goes through the loop below this one
+            const int slow = two ? 2 : steps;
+            for (int t = 0; t < slow; ++t, ++g) {
+                const int h = g & 1, first = !two || t == 0;
+                if (older.flags & kDue) ok = values_step(h, older);
+                if (ok && first) ok = take_keys(n_k);
+                if (ok && t == 0) ok = wait(&tl.q_full, k & 1);
+                if (!ok) break;
+                kda::tc_fence_after();
+                if (elect_one())
+                    issue_scores(h, two & t, n_k, (!two || t == 1 ? kLastUse : 0) | (t == steps - 1 ? kFinal : 0));
+                __syncwarp();
+                issued = true;
+                older = newer;
+                newer = due(t, n_k);
+                if (!two || t == 1) ++n_k;
+            }
+            if (!ok || slow == steps) continue;
+            // the tensor cores' time is here: as few instructions between products as can be
+            const int h0 = g & 1, h1 = h0 ^ 1;
+            for (int j = 1; j < tiles; ++j, ++n_k) {
+                Pending pv{kDue | kFirstUse | (j > 1 ? kAdd : 0) | (tb + j - 1 >= whole ? kEdge : 0), n_k - 1};
+                ok = take_values(h0, pv);
+                if (!ok) break;
+                if (elect_one()) issue_values(h0, pv);
+                ok = take_keys(n_k);
+                if (!ok) break;
+                if (elect_one()) issue_scores(h0, 0, n_k, 0);
+                pv.flags = kDue | kLastUse | (j > 1 ? kAdd : 0);
+                ok = take_values(h1, pv);
+                if (!ok) break;
+                if (elect_one()) {
+                    issue_values(h1, pv);
+                    issue_scores(h1, 1, n_k, kLastUse | (j == tiles - 1 ? kFinal : 0));
+                }
+            }
+            __syncwarp();
+            g += steps - 2;
+            older = due(steps - 2, n_k - 1);
+            newer = due(steps - 1, n_k - 1);
+        }
+        if (ok && (older.flags & kDue)) ok = values_step(g & 1, older);
+        if (ok && (newer.flags & kDue)) ok = values_step((g + 1) & 1, newer);
+        if (issued) {                                  // no product in flight when TMEM is freed
+            if (elect_one()) commit_pair(&tl.drain);
+            __syncwarp();
+            (void)kda::mbar_wait(&tl.drain, 0, kda::kWaitCycles);
+        }
+    } else if (w < 8) {
+        // ---------------- softmax and output of half h
+        const int h = w >> 2, row = tid & 127;
+        const uint32_t lane_off = (uint32_t)((w & 3) * 32) << 16;
+        const uint32_t tS = tmem + lane_off + h * 128;
+        const uint32_t p_bar = at_rank(&tl.p_full[h], 0);
+        int n_s = 0, n_j = 0, g = 0, n_landed = 0, n_v = 0;               // n_v: key tiles of the units before
+        uint32_t o_phase = 0;                          // bit h: parity of the next O_h
+        bool ok = true;
+        for (int k = 0; ok; ++k) {
+            Unit u;
+            if (!read_unit(k, u)) break;
+            const bool two = u.ntok > kTileTokens;
+            const int tiles = u.te - u.tb, steps = tiles << (two ? 1 : 0);
+            const int t0 = (h ^ g) & 1;                // this half's first step
+            const int qi = two ? t0 : 0;               // its row tile
+            const int first = qi * kTileTokens + rank * kRows, tok = first + row;
+            const bool valid = tok < u.ntok;
+            const int pos = u.pos + tok;
+            const int hi = valid ? min(max(pos + 1, 0), u.kend) : 0;
+            const bool busy = __any_sync(0xffffffffu, valid);
+            const Sight un = sight(u, 0, 0, u.ntok - 1);
+            const int mine = min(max(u.pos + first + 1, 0), u.kend);      // keys that all of this CTA's rows see
+            float m = -INFINITY, l = 0.f;
+            for (int t = t0; t < steps; t += 2) {
+                const int j = two ? t >> 1 : t, k0 = (u.tb + j) << kKeysLog2;
+                if (!wait(&tl.s_full[h], n_s & 1)) { ok = false; break; }
+                ++n_s;
+                kda::tc_fence_after();
+                if (busy) {
+                    if (k0 + kKeys > mine) {
+                        // scores of keys this row does not see become -inf, in place.  Rolled: these
+                        // tiles are few, and a short call's time goes into fetching instructions
+#pragma unroll 1
+                        for (int c = 0; c < kKeys; c += 32) {
+                            const int b = hi - k0 - c;
+                            const uint32_t seen = b >= 32 ? 0xffffffffu : (1u << max(b, 0)) - 1u;
+                            float y[32];
+                            kda::tmem_ld32(tS + c, y);
+                            kda::tmem_wait_ld();
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) y[e] = (seen >> e) & 1 ? y[e] : -INFINITY;
+                            tmem_st32(tS + c, reinterpret_cast<const uint32_t*>(y));
+                        }
+                        kda::tmem_wait_st();
+                    }
+                    float x[128];
+#pragma unroll
+                    for (int c = 0; c < 128; c += 32) kda::tmem_ld32(tS + c, x + c);
+                    kda::tmem_wait_ld();
+                    float top[4] = {x[0], x[1], x[2], x[3]};
+#pragma unroll
+                    for (int c = 4; c < 128; c += 4)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) top[e] = fmaxf(top[e], x[c + e]);
+                    const float big = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+                    if (t < 2) {
+                        m = big;
+                    } else {
+                        // S complete means that this half's product before it is too, so O stands still
+                        const bool grow = (big - m) * scale_log2 > kGrow;
+                        if (__any_sync(0xffffffffu, grow)) {
+                            const float f = grow ? ex2((m - big) * scale_log2) : 1.f;
+                            const uint32_t tO = tmem + lane_off + kTmemO + h * 128;
+#pragma unroll 1
+                            for (int c = 0; c < kValue; c += 16) {
+                                float y[16];
+                                kda::tmem_ld16(tO + c, y);
+                                kda::tmem_wait_ld();
+#pragma unroll
+                                for (int e = 0; e < 16; ++e) y[e] *= f;
+                                kda::tmem_st16(tO + c, y);
+                            }
+                            l *= f;
+                            if (grow) m = big;
+                        }
+                    }
+                    const float ref = m == -INFINITY ? 0.f : m * scale_log2;
+                    const uint64_t sc2 = pack2(scale_log2, scale_log2), off2 = pack2(-ref, -ref);
+                    uint64_t sum[2] = {0, 0};
+#pragma unroll
+                    for (int c0 = 0; c0 < 128; c0 += 64) {
+                        uint32_t p[32];
+#pragma unroll
+                        for (int c = 0; c < 64; c += 2) {
+                            float a, b;
+                            unpack2(fma2(pack2(x[c0 + c], x[c0 + c + 1]), sc2, off2), a, b);
+                            a = ex2(a);
+                            b = ex2(b);
+                            sum[(c >> 1) & 1] = add2(sum[(c >> 1) & 1], pack2(a, b));
+                            p[c >> 1] = kda::pack_bf16x2(a, b);
+                        }
+                        tmem_st32(tS + c0 / 2, p);
+                    }
+                    float sa, sb;
+                    unpack2(add2(sum[0], sum[1]), sa, sb);
+                    l += sa + sb;
+                    kda::tmem_wait_st();
+                }
+                if ((!two || !(t & 1)) && k0 + kKeys > un.all_hi) {
+                    // values that must not meet a zero weight (see the header)
+                    if (!wait(&tl.landed[h], n_landed & 1)) { ok = false; break; }
+                    ++n_landed;
+                    unsigned char* v = sm + kV0 + (n_v + j) % kStages * kVTile;
+                    bool odd = false;
+#pragma unroll 1
+                    for (int e = row; e < kKeys * 8; e += 128) {
+                        const int key = k0 + (e >> 3);
+                        if (key < un.all_hi) continue;
+                        uint4* at = reinterpret_cast<uint4*>(v + e * 16);
+                        uint4 x = make_uint4(0, 0, 0, 0);
+                        if (key < un.hi) {
+                            x = *at;
+                            if (!take_odd(x)) continue;
+                            odd = true;
+                        }
+                        *at = x;
+                    }
+                    if (odd) flag_pair(&tl.odd_values[k & 7]);
+                    kda::fence_proxy_async_smem();
+                }
+                kda::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) arrive_remote(p_bar);
+            }
+            if (!ok) break;
+            // ---- output
+            const bool whole = u.first && u.last;
+            const int which = u.first ? 1 : 0;
+            const size_t at = (size_t)(u.tok0 + tok) * s.Hq + u.qh0;
+            const float ref = m == -INFINITY ? -INFINITY : m * scale_log2;
+            const int key0 = first_row(u);
+            // writes 32 columns of this row: o, or unnormalised sums
+            auto put = [&](float* y, int c0, float sum_l) {
+                if (*(volatile int*)&tl.odd_values[k & 7] && valid) add_odd_values(y, c0, u, un, hi, key0, values);
+                if (!valid) return;
+                if (whole) {
+                    const float inv = sum_l == 0.f ? 0.f : 1.f / sum_l;
+                    uint4* dst = reinterpret_cast<uint4*>(o + at * kValue + c0);
+#pragma unroll
+                    for (int e = 0; e < 32; e += 8)
+                        dst[e / 8] = make_uint4(kda::pack_bf16x2(y[e] * inv, y[e + 1] * inv),
+                                                kda::pack_bf16x2(y[e + 2] * inv, y[e + 3] * inv),
+                                                kda::pack_bf16x2(y[e + 4] * inv, y[e + 5] * inv),
+                                                kda::pack_bf16x2(y[e + 6] * inv, y[e + 7] * inv));
+                } else {
+                    float4* dst = reinterpret_cast<float4*>(parts.sums(cluster, which) + (size_t)tok * kValue + c0);
+#pragma unroll
+                    for (int e = 0; e < 32; e += 4) dst[e / 4] = make_float4(y[e], y[e + 1], y[e + 2], y[e + 3]);
+                }
+            };
+            auto put_stats = [&](float r, float sum_l) {
+                if (!valid) return;
+                if (whole) {
+                    if (lse) lse[at] = sum_l == 0.f ? -INFINITY : (r + log2f(sum_l)) * kLn2;
+                } else {
+                    parts.stats(cluster, which)[tok] = make_float2(r, sum_l);
+                }
+            };
+            if (two) {
+                ok = wait(&tl.o_full[h], (o_phase >> h) & 1);
+                o_phase ^= 3;
+                if (!ok) break;
+                kda::tc_fence_after();
+                if (busy) {
+#pragma unroll 1
+                    for (int c = 0; c < kValue; c += 32) {
+                        float y[32];
+                        kda::tmem_ld32(tmem + lane_off + kTmemO + h * 128 + c, y);
+                        kda::tmem_wait_ld();
+                        put(y, c, l);
+                    }
+                    put_stats(ref, l);
+                }
+            } else {
+                // the halves hold the sums over every second key tile: each joins half of the columns
+                const bool has[2] = {(g & 1) == 0 || steps > 1, (g & 1) == 1 || steps > 1};
+                tl.stats[h][row] = make_float2(ref, l);
+                __syncwarp();
+                if (lane == 0) kda::mbar_arrive(&tl.join_a);
+                ok = wait(&tl.join_a, n_j & 1);
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    if (!has[e]) continue;
+                    ok = ok && wait(&tl.o_full[e], (o_phase >> e) & 1);
+                    o_phase ^= 1u << e;
+                }
+                if (!ok) break;
+                kda::tc_fence_after();
+                if (busy) {
+                    const float2 st = tl.stats[h ^ 1][row];
+                    const float top = fmaxf(ref, st.x), base = top == -INFINITY ? 0.f : top;
+                    const float fm = l == 0.f ? 0.f : ex2(ref - base), fo = st.y == 0.f ? 0.f : ex2(st.x - base);
+                    const float f0 = h == 0 ? fm : fo, f1 = h == 0 ? fo : fm;
+                    const float sum_l = fmaf(fm, l, fo * st.y);
+#pragma unroll 1
+                    for (int c = h * 64; c < h * 64 + 64; c += 32) {
+                        float y[32];
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) y[e] = 0.f;
+#pragma unroll
+                        for (int b = 0; b < 2; ++b) {
+                            if (!has[b]) continue;
+                            float z[32];
+                            kda::tmem_ld32(tmem + lane_off + kTmemO + b * 128 + c, z);
+                            kda::tmem_wait_ld();
+                            const float f = b == 0 ? f0 : f1;
+                            if (f != 0.f) {
+#pragma unroll
+                                for (int e = 0; e < 32; ++e) y[e] = fmaf(f, z[e], y[e]);
+                            }
+                        }
+                        put(y, c, sum_l);
+                    }
+                    if (h == 0) put_stats(top, sum_l);
+                }
+                kda::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) kda::mbar_arrive(&tl.join_b);
+                ok = wait(&tl.join_b, n_j & 1);
+                ++n_j;
+                if (!ok) break;
+            }
+            // for the unit after the next three: no warp of either CTA is there yet, and none is still at
+            // the one four back (every unit takes all warps of one half, and the halves meet within two)
+            if (tid == 0) tl.odd_values[(k + 4) & 7] = 0;
+            g += steps;
+            n_v += tiles;
+        }
+    }
+    kda::tc_fence_before();
+    __syncthreads();
+    if (*abort_f && rank == 0 && w == kCopyWarp) {     // no copy in flight into shared memory that is given up
+        for (int i = max(0, n_ld - kStages); i <= n_ld; ++i) {
+            (void)kda::mbar_wait(&tl.k_full[i % kStages], (i / kStages) & 1, i < n_ld ? kda::kWaitCycles : 10000000);
+            (void)kda::mbar_wait(&tl.v_full[i % kStages], (i / kStages) & 1, i < n_ld ? kda::kWaitCycles : 10000000);
+        }
+        if (n_q > 0) (void)kda::mbar_wait(&tl.q_full, (n_q - 1) & 1, kda::kWaitCycles);
+    }
+    __syncthreads();
+    cluster_sync();                                    // the other CTA is done with this one's memory and TMEM
+    if (w == kIssueWarp) dealloc_pair(tmem);
+}
+
+// ---- host
+bool make_map(CUtensorMap* m, const void* base, int channels, cuuint64_t d1, cuuint64_t d2, cuuint64_t stride1,
+              cuuint64_t stride2, int box2) {
+    const cuuint64_t dims[3] = {(cuuint64_t)channels, d1, d2};
+    const cuuint64_t strides[2] = {stride1, stride2};
+    const cuuint32_t box[3] = {64, 1, (cuuint32_t)box2};
+    const cuuint32_t one[3] = {1, 1, 1};
+    return kda_host::tensor_map_encoder()(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box,
+                                          one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                                          CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+}  // namespace
+
+namespace kda_host {
+
+PagedPlan expanded_plan_tc(int T) {
+    PagedPlan p;
+    p.Gv = 1;
+    p.U = 2 * kTileTokens;
+    p.rows = paged_slot_rows(p.U, T, 1);
+    p.tile_log2 = kKeysLog2;
+    p.max_ctas = 80;                                   // pairs
+    p.extra = 3;
+    return p;
+}
+
+cudaError_t launch_expanded_attention_tc(const ExpandedArgs& a) {
+    const PagedPlan p = expanded_plan_tc(a.T);
+    const PagedArgs pa = expanded_view(a);
+    if (!tensor_map_encoder()) return cudaErrorNotSupported;
+    CUtensorMap qm, nm, rm, vm;
+    if (!make_map(&qm, a.q, kKey, a.H, a.T, kKey * 2, (cuuint64_t)a.q_stride * 2, kRows) ||
+        !make_map(&nm, a.k_nope, kNope, a.H, a.S, (cuuint64_t)a.kn_head * 2, (cuuint64_t)a.kn_token * 2, kKeys / 2) ||
+        !make_map(&rm, a.k_rope, 64, 1, a.S, 128, (cuuint64_t)a.kr_stride * 2, kKeys / 2) ||
+        !make_map(&vm, a.v, kValue, a.H, a.S, (cuuint64_t)a.v_head * 2, (cuuint64_t)a.v_token * 2, kKeys))
+        return cudaErrorInvalidValue;
+    auto kern = kda_expanded_attention_tc_kernel;
+    static OncePerDevice once;
+    const cudaError_t e = once.run([&] { return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem); });
+    if (e != cudaSuccess) return e;
+    const int pairs = std::min(p.max_ctas, sm_count() / 2);
+    kern<<<2 * pairs, kThreads, kSmem, a.stream>>>(
+        qm, nm, rm, vm, Values{static_cast<const __nv_bfloat16*>(a.v), a.v_token, a.v_head}, a.cu_seqlens, a.cu_seqlens_k,
+        expanded_shape(a, p), a.scale * kLog2e, static_cast<__nv_bfloat16*>(a.o), a.lse, paged_partials(pa, p), a.status);
+    const cudaError_t err = cudaGetLastError();
+    if (err != cudaSuccess) return err;
+    return launch_paged_merge(pa, p, pairs);
+}
+
+}  // namespace kda_host

@@ -91,8 +91,10 @@ cudaError_t launch_latent_append(const LatentAppendArgs& a);
 PagedPlan latent_plan_simt(int T, int H);
 PagedPlan latent_plan_tc(int T, int H);
 PagedPlan expanded_plan_simt(int T);
+PagedPlan expanded_plan_tc(int T);
 cudaError_t launch_latent_attention_simt(const LatentArgs& a);
 cudaError_t launch_latent_attention_tc(const LatentArgs& a);
 cudaError_t launch_expanded_attention_simt(const ExpandedArgs& a);
+cudaError_t launch_expanded_attention_tc(const ExpandedArgs& a);
 
 }  // namespace kda_host

@@ -29,7 +29,11 @@ size_t latent_workspace(int T, int H, kda_dtype dt) {
     if (dt != KDA_BF16) return simt;
     return std::max(simt, kda_host::paged_plan_bytes(kda_host::latent_plan_tc(T, H), kLatent));
 }
-size_t expanded_workspace(int T) { return kda_host::paged_plan_bytes(kda_host::expanded_plan_simt(T), kValue); }
+size_t expanded_workspace(int T, kda_dtype dt) {
+    const size_t simt = kda_host::paged_plan_bytes(kda_host::expanded_plan_simt(T), kValue);
+    if (dt != KDA_BF16) return simt;
+    return std::max(simt, kda_host::paged_plan_bytes(kda_host::expanded_plan_tc(T), kValue));
+}
 
 }  // namespace
 
@@ -103,7 +107,7 @@ kda_status kda_latent_attention(const void* q, const void* cache, const int32_t*
 
 size_t kda_expanded_attention_workspace_size(int T, int H, kda_dtype dtype) {
     if (T < 0 || H <= 0 || H > kMaxHeads || !dtype_ok(dtype)) return 0;
-    return expanded_workspace(T);
+    return expanded_workspace(T, dtype);
 }
 
 kda_status kda_expanded_attention(const void* q, const void* k_nope, const void* k_rope, const void* v,
@@ -130,11 +134,18 @@ kda_status kda_expanded_attention(const void* q, const void* k_nope, const void*
     if (!aligned(q, size) || !aligned(k_nope, size) || !aligned(k_rope, size) || !aligned(v, size) || !aligned(o, 16))
         return KDA_ERR_INVALID_ARG;
     if (o == q || o == k_nope || o == k_rope || o == v) return KDA_ERR_INVALID_ARG;
-    if (!workspace || workspace_bytes < expanded_workspace(T) || !aligned(workspace, 256)) return KDA_ERR_WORKSPACE;
+    if (!workspace || workspace_bytes < expanded_workspace(T, dtype) || !aligned(workspace, 256)) return KDA_ERR_WORKSPACE;
     const kda_host::ExpandedArgs a{q, k_nope, k_rope, v, cu_seqlens, cu_seqlens_k, q_stride, k_token_stride, k_head_stride,
                                    k_rope_stride, v_token_stride, v_head_stride, N, T, S, H, scale, causal != 0, dtype, o, lse,
                                    workspace, stream, kda_host::status_word()};
-    return from_cuda(kda_host::launch_expanded_attention_simt(a));
+    // TMA fetches rows that start on 16-byte boundaries, at strides below 2^40 bytes
+    auto fetchable = [](const void* p, int64_t s0, int64_t s1) {
+        constexpr int64_t kMost = (int64_t(1) << 39) - 8;
+        return aligned(p, 16) && s0 % 8 == 0 && s1 % 8 == 0 && s0 > 0 && s1 > 0 && s0 <= kMost && s1 <= kMost;
+    };
+    const bool tc = dtype == KDA_BF16 && S > 0 && fetchable(q, q_stride, 8) && fetchable(k_nope, k_token_stride, k_head_stride) &&
+                    fetchable(k_rope, k_rope_stride, 8) && fetchable(v, v_token_stride, v_head_stride);
+    return from_cuda(tc ? kda_host::launch_expanded_attention_tc(a) : kda_host::launch_expanded_attention_simt(a));
 }
 
 }  // extern "C"

@@ -38,7 +38,7 @@
 // if they found one (in both CTAs); the output then adds such elements to the rows that see them.
 #include <algorithm>
 
-#include "attention_tc.cuh"
+#include "attention_pair.cuh"
 #include "latent.cuh"
 
 namespace {
@@ -103,59 +103,6 @@ struct Tail {
 };
 static_assert(sizeof(Tail) <= kTailBytes, "tail");
 
-__device__ __forceinline__ uint32_t cluster_rank() {
-    uint32_t r;
-    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
-}
-// A shared-memory address of CTA `rank` of the cluster, at the place that p has here.
-__device__ __forceinline__ uint32_t at_rank(const void* p, uint32_t rank) {
-    uint32_t r;
-    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(kda::smem_u32(p)), "r"(rank));
-    return r;
-}
-__device__ __forceinline__ void cluster_sync() {
-    asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
-}
-__device__ __forceinline__ void arrive_remote(uint32_t bar) {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
-}
-__device__ __forceinline__ bool try_wait_cluster(uint64_t* bar, uint32_t parity) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(kda::smem_u32(bar)), "r"(parity)
-        : "memory");
-    return ok != 0;
-}
-// Tile load into this CTA's shared memory whose bytes are counted on CTA 0's barrier.
-__device__ __forceinline__ void load_pair(uint32_t dst, const void* tmap, int x, int y, int z, uint32_t bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%2, "
-        "%3, %4}], [%5];" ::"r"(dst),
-        "l"(tmap), "r"(x), "r"(y), "r"(z), "r"(bar)
-        : "memory");
-}
-__device__ __forceinline__ void mma_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
-        : "memory");
-}
-// Arrive once on the barrier at this place in both CTAs when the products issued so far are done.
-__device__ __forceinline__ void commit_pair(uint64_t* bar) {
-    asm volatile(
-        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
-            kda::smem_u32(bar)),
-        "h"((uint16_t)3)
-        : "memory");
-}
-
 // Adds to o[0..31] (channels c0 ..) the values that are not finite, of the keys that this row sees
 // among those that not all rows of the unit see.
 template <int LOG2>
@@ -190,9 +137,7 @@ kda_latent_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const _
 
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the merge may be set up; it waits for this grid
     if (w == kIssueWarp) {
-        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(kda::smem_u32(&tl.tmem))
-                     : "memory");
-        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+        alloc_pair(&tl.tmem);
     }
     if (tid == 0) {
         for (int i = 0; i < C::STAGES; ++i) {
@@ -539,22 +484,12 @@ kda_latent_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const _
                         uint4 x = make_uint4(0, 0, 0, 0);
                         if (key < si.hi) {
                             x = *at;
-                            uint32_t* y = reinterpret_cast<uint32_t*>(&x);
-                            int found = 0;
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                if ((y[i] & 0x7f80u) == 0x7f80u) { y[i] &= 0xffff0000u; found = 1; }
-                                if ((y[i] & 0x7f800000u) == 0x7f800000u) { y[i] &= 0x0000ffffu; found = 1; }
-                            }
-                            if (!found) continue;
+                            if (!take_odd(x)) continue;
                             odd = 1;
                         }
                         *at = x;
                     }
-                    if (odd) {
-                        for (uint32_t r = 0; r < 2; ++r)
-                            asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(at_rank(&tl.odd_values[k & 3], r)), "r"(1) : "memory");
-                    }
+                    if (odd) flag_pair(&tl.odd_values[k & 3]);
                 }
                 kda::fence_proxy_async_smem();
                 kda::tc_fence_before();
@@ -625,8 +560,7 @@ kda_latent_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const _
     }
     __syncthreads();
     cluster_sync();                                    // the other CTA is done with this one's memory and TMEM
-    if (w == kIssueWarp)
-        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+    if (w == kIssueWarp) dealloc_pair(tmem);
 }
 
 // ---- host
