@@ -20,19 +20,11 @@ __device__ __forceinline__ uint32_t at_rank(const void* p, uint32_t rank) {
 __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
 }
+// Arrives on a barrier of either CTA.  What it has to order is in this SM: stores to shared memory
+// (made visible to the tensor cores by fence.proxy.async) and TMEM (by tcgen05.wait and fence); release at cluster
+// scope would also wait for this thread's stores to global memory, half a microsecond each time.
 __device__ __forceinline__ void arrive_remote(uint32_t bar) {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
-}
-__device__ __forceinline__ bool try_wait_cluster(uint64_t* bar, uint32_t parity) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(kda::smem_u32(bar)), "r"(parity)
-        : "memory");
-    return ok != 0;
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 // Tile load into this CTA's shared memory whose bytes are counted on CTA 0's barrier.
 __device__ __forceinline__ void load_pair(uint32_t dst, const void* tmap, int x, int y, int z, uint32_t bar) {
@@ -87,10 +79,11 @@ __device__ __forceinline__ bool take_odd(uint4& x) {
     }
     return found;
 }
-// Sets an int of the shared memory of both CTAs to 1.
+// Sets an int of the shared memory of both CTAs to 1, before whatever this thread does next.
 __device__ __forceinline__ void flag_pair(int* flag) {
     for (uint32_t r = 0; r < 2; ++r)
         asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(at_rank(flag, r)), "r"(1) : "memory");
+    asm volatile("fence.acq_rel.cluster;" ::: "memory");
 }
 
 }  // namespace kda_tc

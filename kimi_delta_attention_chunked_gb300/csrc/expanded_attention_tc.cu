@@ -162,8 +162,8 @@ kda_expanded_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const
     // true once the phase is complete; false when this CTA gives up.  Called by all
     // lanes of a warp, with one answer for all of them, so that none leaves a loop alone
     auto wait = [&](uint64_t* b, uint32_t parity) -> bool {
-        if (__all_sync(0xffffffffu, try_wait_cluster(b, parity))) return true;
-        return wait_longer(b, parity, &tl.abort, status) && __all_sync(0xffffffffu, try_wait_cluster(b, parity));
+        if (__all_sync(0xffffffffu, kda::mbar_try_wait(b, parity))) return true;
+        return wait_longer(b, parity, &tl.abort, status);
     };
     auto read_unit = [&](int k, Unit& u) -> bool {
         if (!wait(&tl.u_full[k % kUnits], (k / kUnits) & 1)) return false;
