@@ -22,7 +22,7 @@
 // even and the odd ones and are joined at the end.
 //
 // Warps of each CTA: 0-3 and 4-7 softmax and output of half 0 and 1; 8 copies; 9 issues the
-// products (in CTA 0, for both); 10 walks the units.  Barriers of loads and of P are CTA 0's.
+// products (in CTA 0, for both); 10 walks the units; 11 copies queries.  Barriers of loads and of P are CTA 0's.
 //
 // Masked places.  A zero weight times a NaN or infinity in V is NaN.  So in a tile that not every row
 // of the unit sees whole, the softmax warps of its first step zero the rows of V that no row sees (the
@@ -45,7 +45,7 @@ using kda_paged::Piece;
 using kda_paged::Walker;
 
 constexpr int kThreads = 384;
-constexpr int kCopyWarp = 8, kIssueWarp = 9, kWalkWarp = 10;
+constexpr int kCopyWarp = 8, kIssueWarp = 9, kWalkWarp = 10, kQueryWarp = 11;
 constexpr int kKeys = 128, kKeysLog2 = 7;              // keys of a tile
 constexpr int kRows = 128;                             // rows of a CTA's part of a row tile
 constexpr int kTileTokens = 2 * kRows;                 // tokens of a row tile
@@ -136,7 +136,7 @@ kda_expanded_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const
         kda::mbar_init(&tl.join_b, 8);
         for (int i = 0; i < kUnits; ++i) {
             kda::mbar_init(&tl.u_full[i], 1);
-            kda::mbar_init(&tl.u_empty[i], rank == 0 ? 10 : 9);
+            kda::mbar_init(&tl.u_empty[i], rank == 0 ? 11 : 10);
         }
         kda::mbar_init(&tl.drain, 1);
         kda::fence_barrier_init();
@@ -147,6 +147,7 @@ kda_expanded_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const
         const CUtensorMap* m = lane == 0 ? &qmap : lane == 1 ? &nmap : lane == 2 ? &rmap : &vmap;
         asm volatile("prefetch.tensormap [%0];" ::"l"(m) : "memory");
     }
+    cluster_arrive();                                  // both CTAs' barriers will be there
     // this pair's piece of the work; both CTAs find the same
     auto* cost = reinterpret_cast<unsigned long long*>(sm + kK0);
     auto* red = cost + kda_paged::kMaxRequests;
@@ -155,7 +156,7 @@ kda_expanded_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const
     kda::fence_proxy_async_smem();                     // the scratch becomes the target of copies
     kda::tc_fence_before();
     __syncthreads();
-    cluster_sync();                                    // both CTAs' barriers are there
+    cluster_wait();
     kda::tc_fence_after();
     const uint32_t tmem = (uint32_t)uniform((int)tl.tmem);
     volatile int* abort_f = &tl.abort;
@@ -184,7 +185,8 @@ kda_expanded_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const
         walk.start(s, cu, cu_k, piece, cluster);
         for (int k = 0;; ++k) {
             Unit u;
-            const bool more = walk.next(s, cu, cu_k, u);
+            unsigned long long from;
+            const bool more = walk.step(s, cu, cu_k, u, from);
             if (k >= kUnits && !wait(&tl.u_empty[k % kUnits], (k / kUnits - 1) & 1)) break;
             __syncwarp();
             if (lane == 0) {
@@ -193,6 +195,7 @@ kda_expanded_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const
                 kda::mbar_arrive(&tl.u_full[k % kUnits]);
             }
             if (!more) break;
+            walk.share(s, u, from);
             if (lane == 0 && rank == 0) parts.describe(cluster, u);
         }
     } else if (w == kCopyWarp) {
@@ -201,7 +204,6 @@ kda_expanded_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const
         for (int k = 0; ok; ++k) {
             Unit u;
             if (!read_unit(k, u)) break;
-            const bool two = u.ntok > kTileTokens;
             const int key0 = first_row(u);
             for (int tile = u.tb; tile < u.te; ++tile) {
                 const int st = n_ld % kStages, at = key0 + (tile << kKeysLog2);
@@ -217,20 +219,6 @@ kda_expanded_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const
                     load_pair(dst + 2 * kKPanel, &rmap, 0, 0, y, bar);
                 }
                 __syncwarp();
-                if (tile == u.tb) {
-                    if (k > 0 && !wait(&tl.q_empty, (k - 1) & 1)) { ok = false; break; }
-                    __syncwarp();
-                    if (lane == 0) {
-                        if (rank == 0) kda::mbar_arrive_expect_tx(&tl.q_full, (two ? 4 : 2) * kQTile);
-                        const uint32_t bar = at_rank(&tl.q_full, 0);
-                        for (int i = 0; i < (two ? 2 : 1); ++i)
-                            for (int c = 0; c < kPanels; ++c)
-                                load_pair(kda::smem_u32(sm) + i * kQTile + c * kQPanel, &qmap, c * 64, u.qh0,
-                                          u.tok0 + i * kTileTokens + rank * kRows, bar);
-                    }
-                    ++n_q;
-                    __syncwarp();
-                }
                 if (n_ld >= kStages && !wait(&tl.v_empty[st], parity)) { ok = false; break; }
                 __syncwarp();
                 if (lane == 0) {
@@ -240,6 +228,23 @@ kda_expanded_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const
                 __syncwarp();
                 ++n_ld;
             }
+        }
+    } else if (w == kQueryWarp) {
+        // ---------------- this CTA's rows of the queries
+        for (int k = 0;; ++k) {
+            Unit u;
+            if (!read_unit(k, u)) break;
+            const int tiles = u.ntok > kTileTokens ? 2 : 1;
+            if (k > 0 && !wait(&tl.q_empty, (k - 1) & 1)) break;
+            __syncwarp();
+            if (lane == 0 && rank == 0) kda::mbar_arrive_expect_tx(&tl.q_full, 2 * tiles * kQTile);
+            __syncwarp();
+            if (lane < tiles * kPanels) {
+                const int i = lane / kPanels, c = lane % kPanels;
+                load_pair(kda::smem_u32(sm) + i * kQTile + c * kQPanel, &qmap, c * 64, u.qh0,
+                          u.tok0 + i * kTileTokens + rank * kRows, at_rank(&tl.q_full, 0));
+            }
+            ++n_q;
         }
     } else if (w == kIssueWarp) {
         // ---------------- products: CTA 0 issues for both.  All lanes wait, an elected one issues.
@@ -505,9 +510,9 @@ kda_expanded_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const
                                                 kda::pack_bf16x2(y[e + 4] * inv, y[e + 5] * inv),
                                                 kda::pack_bf16x2(y[e + 6] * inv, y[e + 7] * inv));
                 } else {
-                    float4* dst = reinterpret_cast<float4*>(parts.sums(cluster, which) + (size_t)tok * kValue + c0);
+                    float* dst = parts.sums(cluster, which) + (size_t)tok * kValue + c0;
 #pragma unroll
-                    for (int e = 0; e < 32; e += 4) dst[e / 4] = make_float4(y[e], y[e + 1], y[e + 2], y[e + 3]);
+                    for (int e = 0; e < 32; e += 8) store8(dst + e, y + e);
                 }
             };
             auto put_stats = [&](float r, float sum_l) {
@@ -591,15 +596,16 @@ kda_expanded_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const
     }
     kda::tc_fence_before();
     __syncthreads();
+    if (*abort_f && rank == 0 && w == kQueryWarp && n_q > 0)
+        (void)kda::mbar_wait(&tl.q_full, (n_q - 1) & 1, kda::kWaitCycles);
     if (*abort_f && rank == 0 && w == kCopyWarp) {     // no copy in flight into shared memory that is given up
         for (int i = max(0, n_ld - kStages); i <= n_ld; ++i) {
             (void)kda::mbar_wait(&tl.k_full[i % kStages], (i / kStages) & 1, i < n_ld ? kda::kWaitCycles : 10000000);
             (void)kda::mbar_wait(&tl.v_full[i % kStages], (i / kStages) & 1, i < n_ld ? kda::kWaitCycles : 10000000);
         }
-        if (n_q > 0) (void)kda::mbar_wait(&tl.q_full, (n_q - 1) & 1, kda::kWaitCycles);
     }
     __syncthreads();
-    cluster_sync();                                    // the other CTA is done with this one's memory and TMEM
+    cluster_leave();                                   // the other CTA is done with this one's memory and TMEM
     if (w == kIssueWarp) dealloc_pair(tmem);
 }
 

@@ -28,8 +28,8 @@
 // Every cache row comes from HBM once; the four panels fetched again come from L2.
 //
 // Warps of each CTA: 0-3 softmax and output (a thread has one row and one half of the keys and
-// of the channels); 4 copies tiles and queries; 5 copies the four panels anew; 6 issues the
-// products (in CTA 0, for both); 7 walks the units.  Barriers of loads and of P are CTA 0's, where the
+// of the channels); 4 copies tiles; 5 copies the four panels anew; 6 issues the products (in
+// CTA 0, for both); 7 walks the units; 8 copies queries.  Barriers of loads and of P are CTA 0's, where the
 // products are issued; a product's completion is told to both.
 //
 // Masked places.  A zero weight times a NaN or infinity in V is NaN.  So in a tile that not every
@@ -51,8 +51,8 @@ using kda_paged::Piece;
 using kda_paged::Shape;
 using kda_paged::Walker;
 
-constexpr int kThreads = 256;
-constexpr int kCopyWarp = 4, kSwapWarp = 5, kIssueWarp = 6, kWalkWarp = 7;
+constexpr int kThreads = 288;
+constexpr int kCopyWarp = 4, kSwapWarp = 5, kIssueWarp = 6, kWalkWarp = 7, kQueryWarp = 8;
 constexpr int kRows = 64;                              // rows of a CTA
 constexpr int kPanels = kRow / 64;                     // of a key
 constexpr int kQPanel = kRows * 128;                   // bytes of 64 rows x 64 channels
@@ -155,7 +155,7 @@ kda_latent_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const _
         }
         for (int i = 0; i < kUnits; ++i) {
             kda::mbar_init(&tl.u_full[i], 1);
-            kda::mbar_init(&tl.u_empty[i], rank == 0 ? 7 : 6);
+            kda::mbar_init(&tl.u_empty[i], rank == 0 ? 8 : 7);
         }
         kda::mbar_init(&tl.drain, 1);
         kda::fence_barrier_init();
@@ -166,6 +166,7 @@ kda_latent_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const _
         const CUtensorMap* m = lane == 0 ? &qmap : &kmap;
         asm volatile("prefetch.tensormap [%0];" ::"l"(m) : "memory");
     }
+    cluster_arrive();                                  // both CTAs' barriers will be there
     // this pair's piece of the work; both CTAs find the same
     auto* cost = reinterpret_cast<unsigned long long*>(sm + C::KV0);
     auto* red = cost + kda_paged::kMaxRequests;
@@ -174,7 +175,7 @@ kda_latent_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const _
     kda::fence_proxy_async_smem();                     // the scratch becomes the target of copies
     kda::tc_fence_before();
     __syncthreads();
-    cluster_sync();                                    // both CTAs' barriers are there
+    cluster_wait();
     kda::tc_fence_after();
     const uint32_t tmem = (uint32_t)uniform((int)tl.tmem);
     volatile int* abort_f = &tl.abort;
@@ -218,7 +219,8 @@ kda_latent_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const _
         walk.start(s, cu, seq_len, piece, cluster);
         for (int k = 0;; ++k) {
             Unit u;
-            const bool more = walk.next(s, cu, seq_len, u);
+            unsigned long long from;
+            const bool more = walk.step(s, cu, seq_len, u, from);
             if (k >= kUnits && !wait(&tl.u_empty[k % kUnits], (k / kUnits - 1) & 1)) break;
             __syncwarp();
             if (lane == 0) {
@@ -227,17 +229,15 @@ kda_latent_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const _
                 kda::mbar_arrive(&tl.u_full[k % kUnits]);
             }
             if (!more) break;
+            walk.share(s, u, from);
             if (lane == 0 && rank == 0) parts.describe(cluster, u);
         }
     } else if (w == kCopyWarp) {
-        // ---------------- this CTA's half of every tile, and its rows of the queries
+        // ---------------- this CTA's half of every tile
         bool ok = true;
-        const int q_bytes = kPanels * tiling.heads * tiling.tokens * 128;
-        const uint32_t q_bar = at_rank(&tl.q_full, 0);
         for (int k = 0; ok; ++k) {
             Unit u;
             if (!read_unit(k, u)) break;
-            const bool both = tiling.by_heads || u.ntok > tiling.tokens;      // the second CTA has rows too
             int next_page = page_of(u, u.tb, rank);
             for (int tile = u.tb; tile < u.te; ++tile) {
                 const int page = next_page, st = n_ld % C::STAGES, y = place_of(tile, rank);
@@ -251,18 +251,24 @@ kda_latent_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const _
                 for (int c = lane / pieces; c < kPanels; c += 32 / pieces)
                     load_pair(dst + c * C::PANEL, &kmap, c * 64, y, page, bar);
                 ++n_ld;
-                if (tile == u.tb) {
-                    if (k > 0 && !wait(&tl.q_empty, (k - 1) & 1)) { ok = false; break; }
-                    __syncwarp();
-                    if (lane == 0 && rank == 0) kda::mbar_arrive_expect_tx(&tl.q_full, (both ? 2 : 1) * q_bytes);
-                    __syncwarp();
-                    if ((rank == 0 || both) && lane < kPanels)
-                        load_pair(kda::smem_u32(sm) + lane * kQPanel, &qmap, lane * 64,
-                                  u.qh0 + (tiling.by_heads ? rank * tiling.heads : 0),
-                                  u.tok0 + (tiling.by_heads ? 0 : rank * tiling.tokens), q_bar);
-                    ++n_q;
-                }
             }
+        }
+    } else if (w == kQueryWarp) {
+        // ---------------- this CTA's rows of the queries
+        const int q_bytes = kPanels * tiling.heads * tiling.tokens * 128;
+        const uint32_t q_bar = at_rank(&tl.q_full, 0);
+        for (int k = 0;; ++k) {
+            Unit u;
+            if (!read_unit(k, u)) break;
+            const bool both = tiling.by_heads || u.ntok > tiling.tokens;      // the second CTA has rows too
+            if (k > 0 && !wait(&tl.q_empty, (k - 1) & 1)) break;
+            __syncwarp();
+            if (lane == 0 && rank == 0) kda::mbar_arrive_expect_tx(&tl.q_full, (both ? 2 : 1) * q_bytes);
+            __syncwarp();
+            if ((rank == 0 || both) && lane < kPanels)
+                load_pair(kda::smem_u32(sm) + lane * kQPanel, &qmap, lane * 64, u.qh0 + (tiling.by_heads ? rank * tiling.heads : 0),
+                          u.tok0 + (tiling.by_heads ? 0 : rank * tiling.tokens), q_bar);
+            ++n_q;
         }
     } else if (w == kSwapWarp) {
         // ---------------- once S is complete, the other half's keys in this CTA's channels over
@@ -530,9 +536,9 @@ kda_latent_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const _
                                                     kda::pack_bf16x2(y[e + 4] * inv, y[e + 5] * inv),
                                                     kda::pack_bf16x2(y[e + 6] * inv, y[e + 7] * inv));
                     } else {
-                        float4* dst = reinterpret_cast<float4*>(parts.sums(cluster, which) + (size_t)prow * kLatent + c0);
+                        float* dst = parts.sums(cluster, which) + (size_t)prow * kLatent + c0;
 #pragma unroll
-                        for (int e = 0; e < 32; e += 4) dst[e / 4] = make_float4(y[e], y[e + 1], y[e + 2], y[e + 3]);
+                        for (int e = 0; e < 32; e += 8) store8(dst + e, y + e);
                     }
                 }
                 if (valid && half == 0) {
@@ -552,14 +558,14 @@ kda_latent_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const _
         if (w == kCopyWarp) {
             for (int i = max(0, n_ld - C::STAGES); i < n_ld; ++i)
                 (void)kda::mbar_wait(&tl.kv_full[i % C::STAGES], (i / C::STAGES) & 1, kda::kWaitCycles);
-            if (n_q > 0) (void)kda::mbar_wait(&tl.q_full, (n_q - 1) & 1, kda::kWaitCycles);
         }
+        if (w == kQueryWarp && n_q > 0) (void)kda::mbar_wait(&tl.q_full, (n_q - 1) & 1, kda::kWaitCycles);
         if (w == kSwapWarp)
             for (int i = max(0, n_ld - C::STAGES); i < n_ld; ++i)
                 (void)kda::mbar_wait(&tl.sw_full[i % C::STAGES], (i / C::STAGES) & 1, kda::kWaitCycles);
     }
     __syncthreads();
-    cluster_sync();                                    // the other CTA is done with this one's memory and TMEM
+    cluster_leave();                                   // the other CTA is done with this one's memory and TMEM
     if (w == kIssueWarp) dealloc_pair(tmem);
 }
 

@@ -231,6 +231,7 @@ struct Walker {
     unsigned long long at, end, total;
     int ctas, c;
     int n, h, i, in;                               // next unit; places of it that lie before the piece
+    int whole_tiles;                               // of the unit whose part was handed out last, all parts together
     Req r;
     int units;
 
@@ -285,6 +286,17 @@ struct Walker {
     // The next part, or false at the end of the piece.
     template <class Sh>
     __device__ __forceinline__ bool next(const Sh& s, const int32_t* cu, const int32_t* seq_len, Unit& u) {
+        unsigned long long from;
+        const bool more = step(s, cu, seq_len, u, from);
+        if (more) share(s, u, from);
+        return more;
+    }
+
+    // The same without the CTAs that share the unit (share() adds them: divisions that a kernel may put off
+    // until it has handed the part on).  `from` is the unit's first place on the line.
+    template <class Sh>
+    __device__ __forceinline__ bool step(const Sh& s, const int32_t* cu, const int32_t* seq_len, Unit& u,
+                                         unsigned long long& from) {
         while (at < end) {
             while (i >= units) {
                 i = 0;
@@ -297,10 +309,11 @@ struct Walker {
             }
             int tb, te;
             unit_span(s, r, i, tb, te);
-            const int len = s.extra + te - tb;
+            whole_tiles = te - tb;
+            const int len = s.extra + whole_tiles;
             const int take = (int)min((unsigned long long)(len - in), end - at);
             const int t0 = max(in - s.extra, 0), t1 = max(in + take - s.extra, 0);    // tiles of this part
-            const unsigned long long fin = at - (unsigned)in + (unsigned)len;         // the unit's end
+            from = at - (unsigned)in;
             u.n = n;
             u.kvh = h / s.sub;
             u.qh0 = h * s.Gv;
@@ -312,25 +325,31 @@ struct Walker {
             u.te = tb + t1;
             u.first = t0 == 0;
             u.last = u.te == te;
-            // CTA c begins at total * c / ctas, so the last one that has a place below `fin` is
-            // ceil(fin * ctas / total) - 1
-            u.start = c;
-            u.parts = 1;
-            if (!u.first) {
-                u.start = -1;
-                if (u.ntok * s.Gv > kSpreadRows) {
-                    const unsigned long long tile0 = at - (unsigned)in + (unsigned)s.extra;
-                    u.start = (int)(((tile0 + 1) * (unsigned)ctas + total - 1) / total) - 1;
-                }
-            }
-            if (!u.last && u.start >= 0) u.parts = (int)((fin * (unsigned)ctas + total - 1) / total) - u.start;
-            else if (u.start >= 0) u.parts = c + 1 - u.start;
             at += (unsigned)take;
             in = 0;
             ++i;
             if (t1 > t0) return true;
         }
         return false;
+    }
+
+    // CTA c begins at total * c / ctas, so the last one that has a place below the unit's end `fin` is
+    // ceil(fin * ctas / total) - 1
+    template <class Sh>
+    __device__ __forceinline__ void share(const Sh& s, Unit& u, unsigned long long from) const {
+        u.start = c;
+        u.parts = 1;
+        if (!u.first) {
+            u.start = -1;
+            if (u.ntok * s.Gv > kSpreadRows)
+                u.start = (int)(((from + (unsigned)s.extra + 1) * (unsigned)ctas + total - 1) / total) - 1;
+        }
+        if (!u.last && u.start >= 0) {
+            const unsigned long long fin = from + (unsigned)(s.extra + whole_tiles);
+            u.parts = (int)((fin * (unsigned)ctas + total - 1) / total) - u.start;
+        } else if (u.start >= 0) {
+            u.parts = c + 1 - u.start;
+        }
     }
 };
 
