@@ -148,6 +148,7 @@ kda_expanded_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const
         asm volatile("prefetch.tensormap [%0];" ::"l"(m) : "memory");
     }
     cluster_arrive();                                  // both CTAs' barriers will be there
+    asm volatile("griddepcontrol.wait;" ::: "memory");   // the kernels before this one are complete
     // this pair's piece of the work; both CTAs find the same
     auto* cost = reinterpret_cast<unsigned long long*>(sm + kK0);
     auto* red = cost + kda_paged::kMaxRequests;
@@ -180,7 +181,7 @@ kda_expanded_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const
 
     if (w == kWalkWarp) {
         // ---------------- unit descriptions
-        if (lane == 0 && rank == 0) parts.clear(cluster);
+        if (lane == 0 && rank == 0) parts.clear_pair(cluster);
         Walker walk;
         walk.start(s, cu, cu_k, piece, cluster);
         for (int k = 0;; ++k) {
@@ -195,8 +196,8 @@ kda_expanded_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const
                 kda::mbar_arrive(&tl.u_full[k % kUnits]);
             }
             if (!more) break;
-            walk.share(s, u, from);
-            if (lane == 0 && rank == 0) parts.describe(cluster, u);
+            walk.share(s, u, from, 0);
+            if (lane == 0 && rank == 0) parts.describe_pair(cluster, u);
         }
     } else if (w == kCopyWarp) {
         // ---------------- copies: of each tile this CTA's keys, then its channels of the values
@@ -652,12 +653,12 @@ cudaError_t launch_expanded_attention_tc(const ExpandedArgs& a) {
     const cudaError_t e = once.run([&] { return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem); });
     if (e != cudaSuccess) return e;
     const int pairs = std::min(p.max_ctas, sm_count() / 2);
-    kern<<<2 * pairs, kThreads, kSmem, a.stream>>>(
-        qm, nm, rm, vm, Values{static_cast<const __nv_bfloat16*>(a.v), a.v_token, a.v_head}, a.cu_seqlens, a.cu_seqlens_k,
-        expanded_shape(a, p), a.scale * kLog2e, static_cast<__nv_bfloat16*>(a.o), a.lse, paged_partials(pa, p), a.status);
-    const cudaError_t err = cudaGetLastError();
+    const cudaError_t err = launch_overlapped(
+        kern, 2 * pairs, kThreads, kSmem, a.stream, 1, qm, nm, rm, vm,
+        Values{static_cast<const __nv_bfloat16*>(a.v), a.v_token, a.v_head}, a.cu_seqlens, a.cu_seqlens_k, expanded_shape(a, p),
+        a.scale * kLog2e, static_cast<__nv_bfloat16*>(a.o), a.lse, paged_partials(pa, p), a.status);
     if (err != cudaSuccess) return err;
-    return launch_paged_merge(pa, p, pairs);
+    return launch_pair_merge(pa, p, pairs);
 }
 
 }  // namespace kda_host

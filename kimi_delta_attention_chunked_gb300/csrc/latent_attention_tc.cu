@@ -167,6 +167,7 @@ kda_latent_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const _
         asm volatile("prefetch.tensormap [%0];" ::"l"(m) : "memory");
     }
     cluster_arrive();                                  // both CTAs' barriers will be there
+    asm volatile("griddepcontrol.wait;" ::: "memory");   // the kernels before this one are complete
     // this pair's piece of the work; both CTAs find the same
     auto* cost = reinterpret_cast<unsigned long long*>(sm + C::KV0);
     auto* red = cost + kda_paged::kMaxRequests;
@@ -214,7 +215,7 @@ kda_latent_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const _
 
     if (w == kWalkWarp) {
         // ---------------- unit descriptions
-        if (lane == 0 && rank == 0) parts.clear(cluster);
+        if (lane == 0 && rank == 0) parts.clear_pair(cluster);
         Walker walk;
         walk.start(s, cu, seq_len, piece, cluster);
         for (int k = 0;; ++k) {
@@ -229,8 +230,8 @@ kda_latent_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const _
                 kda::mbar_arrive(&tl.u_full[k % kUnits]);
             }
             if (!more) break;
-            walk.share(s, u, from);
-            if (lane == 0 && rank == 0) parts.describe(cluster, u);
+            walk.share(s, u, from, 0);
+            if (lane == 0 && rank == 0) parts.describe_pair(cluster, u);
         }
     } else if (w == kCopyWarp) {
         // ---------------- this CTA's half of every tile
@@ -626,12 +627,12 @@ cudaError_t launch_latent_attention_tc(const LatentArgs& a) {
     });
     if (e != cudaSuccess) return e;
     const int pairs = std::min(p.max_ctas, sm_count() / 2);
-    kern<<<2 * pairs, kThreads, Cfg<kKeys>::SMEM, a.stream>>>(
-        qm, km, static_cast<const __nv_bfloat16*>(a.cache), a.block_table, a.cu_seqlens, a.seq_len, latent_shape(a, p), t,
-        a.scale * kLog2e, static_cast<__nv_bfloat16*>(a.o), a.lse, paged_partials(pa, p), a.status);
-    const cudaError_t err = cudaGetLastError();
+    const cudaError_t err = launch_overlapped(
+        kern, 2 * pairs, kThreads, Cfg<kKeys>::SMEM, a.stream, 1, qm, km, static_cast<const __nv_bfloat16*>(a.cache),
+        a.block_table, a.cu_seqlens, a.seq_len, latent_shape(a, p), t, a.scale * kLog2e, static_cast<__nv_bfloat16*>(a.o), a.lse,
+        paged_partials(pa, p), a.status);
     if (err != cudaSuccess) return err;
-    return launch_paged_merge(pa, p, pairs);
+    return launch_pair_merge(pa, p, pairs);
 }
 
 }  // namespace kda_host

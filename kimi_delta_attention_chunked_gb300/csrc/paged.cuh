@@ -334,14 +334,14 @@ struct Walker {
     }
 
     // CTA c begins at total * c / ctas, so the last one that has a place below the unit's end `fin` is
-    // ceil(fin * ctas / total) - 1
+    // ceil(fin * ctas / total) - 1.  Where a unit that goes on here begins is asked for if it has more than `spread` rows.
     template <class Sh>
-    __device__ __forceinline__ void share(const Sh& s, Unit& u, unsigned long long from) const {
+    __device__ __forceinline__ void share(const Sh& s, Unit& u, unsigned long long from, int spread = kSpreadRows) const {
         u.start = c;
         u.parts = 1;
         if (!u.first) {
             u.start = -1;
-            if (u.ntok * s.Gv > kSpreadRows)
+            if (u.ntok * s.Gv > spread)
                 u.start = (int)(((from + (unsigned)s.extra + 1) * (unsigned)ctas + total - 1) / total) - 1;
         }
         if (!u.last && u.start >= 0) {
@@ -371,6 +371,12 @@ struct Partials {
     __device__ __forceinline__ void describe(int c, const Unit& u) const {
         if (!u.first) meta[2 * c] = make_int4(u.start, u.parts, 0, 0);
         else if (!u.last) meta[2 * c + 1] = make_int4(u.tok0, u.qh0, u.ntok, u.parts);
+    }
+    // As the merge of the pairs reads it: either slot's unit in full, (first token, first query head, tokens,
+    // CTA in which it begins << 16 | parts), parts = 0 where there is none.
+    __device__ __forceinline__ void clear_pair(int c) const { meta[2 * c] = meta[2 * c + 1] = make_int4(0, 0, 0, 0); }
+    __device__ __forceinline__ void describe_pair(int c, const Unit& u) const {
+        if (!u.first || !u.last) meta[2 * c + (u.first ? 1 : 0)] = make_int4(u.tok0, u.qh0, u.ntok, u.start << 16 | u.parts);
     }
     __device__ __forceinline__ size_t slot(int c, int which) const {
         return ((size_t)c * 2 + which) * (size_t)cap * (d + 2);
