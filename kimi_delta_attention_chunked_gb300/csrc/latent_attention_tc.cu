@@ -336,7 +336,13 @@ kda_latent_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const _
             const int tb = uniform(u.tb), te = uniform(u.te);
             for (int tile = tb; tile < te; ++tile, ++g) {
                 const int st = g % C::STAGES;
-                ok = wait(&tl.kv_full[st], (g / C::STAGES) & 1);
+                // the last product of a unit does not wait for the next one's queries, which are fetched
+                // when its last scores are done
+                if (due && tile == tb) {
+                    ok = values_step(g - 1);
+                    due = false;
+                }
+                ok = ok && wait(&tl.kv_full[st], (g / C::STAGES) & 1);
                 if (ok && tile == tb) ok = wait(&tl.q_full, k & 1);
                 if (!ok) break;
                 kda::tc_fence_after();
