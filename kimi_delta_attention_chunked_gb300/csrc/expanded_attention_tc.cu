@@ -22,7 +22,7 @@
 // even and the odd ones and are joined at the end.
 //
 // Warps of each CTA: 0-3 and 4-7 softmax and output of half 0 and 1; 8 copies; 9 issues the
-// products (in CTA 0, for both); 10 walks the units; 11 copies queries.  Barriers of loads and of P are CTA 0's.
+// products (in CTA 0, for both); 10 walks the units; 11 copies queries and tells of values that are there.  Barriers of loads and of P are CTA 0's.
 //
 // Masked places.  A zero weight times a NaN or infinity in V is NaN.  So in a tile that not every row
 // of the unit sees whole, the softmax warps of its first step zero the rows of V that no row sees (the
@@ -70,8 +70,8 @@ struct UnitSlot {
 };
 
 struct Tail {
-    uint64_t k_full[kStages], v_full[kStages], q_full, p_full[2];     // CTA 0's are used
-    uint64_t k_empty[kStages], v_empty[kStages], q_empty, s_full[2], o_full[2], landed[2];    // each CTA's own
+    uint64_t k_full[kStages], v_full[kStages], q_full, p_full[2][2];  // CTA 0's are used; P in two halves of its keys
+    uint64_t k_empty[kStages], v_empty[kStages], q_empty, s_full[2], o_full[2], landed[kStages];    // each CTA's own
     uint64_t join_a, join_b;
     uint64_t u_full[kUnits], u_empty[kUnits];
     uint64_t drain;
@@ -82,6 +82,13 @@ struct Tail {
     float2 stats[2][kRows];                            // (reference in octaves, sum of weights) of each half's rows
 };
 static_assert(sizeof(Tail) <= kTailBytes, "tail");
+
+// Key tiles of this part that row tile 0 of a unit of two takes: the rest hold no key that it sees.  One at
+// least, so that both halves have a step in every part.
+__device__ __forceinline__ int first_tiles(const Unit& u) {
+    const int hi = min(max(u.pos + kTileTokens, 0), u.kend);
+    return min(u.te - u.tb, max(((hi + kKeys - 1) >> kKeysLog2) - u.tb, 1));
+}
 
 // Where the values lie in global memory.
 struct Values {
@@ -123,14 +130,15 @@ kda_expanded_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const
             kda::mbar_init(&tl.v_full[i], 1);
             kda::mbar_init(&tl.k_empty[i], 1);
             kda::mbar_init(&tl.v_empty[i], 1);
+            kda::mbar_init(&tl.landed[i], 1);
         }
         kda::mbar_init(&tl.q_full, 1);
         kda::mbar_init(&tl.q_empty, 1);
         for (int i = 0; i < 2; ++i) {
             kda::mbar_init(&tl.s_full[i], 1);
-            kda::mbar_init(&tl.p_full[i], 8);
+            kda::mbar_init(&tl.p_full[i][0], 8);
+            kda::mbar_init(&tl.p_full[i][1], 8);
             kda::mbar_init(&tl.o_full[i], 1);
-            kda::mbar_init(&tl.landed[i], 1);
         }
         kda::mbar_init(&tl.join_a, 8);
         kda::mbar_init(&tl.join_b, 8);
@@ -232,6 +240,7 @@ kda_expanded_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const
         }
     } else if (w == kQueryWarp) {
         // ---------------- this CTA's rows of the queries
+        int n_v = 0;                                   // key tiles so far
         for (int k = 0;; ++k) {
             Unit u;
             if (!read_unit(k, u)) break;
@@ -246,6 +255,14 @@ kda_expanded_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const
                           u.tok0 + i * kTileTokens + rank * kRows, at_rank(&tl.q_full, 0));
             }
             ++n_q;
+            // tells both CTAs that a tile's values are there (CTA 1 cannot see it: its loads count on CTA 0's barriers)
+            bool ok = true;
+            for (int j = u.tb; ok && rank == 0 && j < u.te; ++j, ++n_v) {
+                ok = wait(&tl.v_full[n_v % kStages], (n_v / kStages) & 1);
+                if (ok && lane < 2) arrive_remote(at_rank(&tl.landed[n_v % kStages], lane));
+                __syncwarp();
+            }
+            if (!ok) break;
         }
     } else if (w == kIssueWarp) {
         // ---------------- products: CTA 0 issues for both.  All lanes wait, an elected one issues.
@@ -259,7 +276,7 @@ kda_expanded_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const
         uint32_t p_phase = 0;                          // bit h: parity of the next P_h
         bool issued = false, ok = rank == 0;
         // a step whose second product is due: flags, its tile's place in the ring
-        enum { kFirstUse = 1, kLastUse = 2, kAdd = 4, kFinal = 8, kDue = 16, kEdge = 32 };
+        enum { kFirstUse = 1, kLastUse = 2, kAdd = 4, kFinal = 8, kDue = 16 };
         struct Pending { int flags, at; };
         Pending older{0, 0}, newer{0, 0};              // of steps g - 2 and g - 1
         auto issue_scores = [&](int h, int tile, int at, int flags) {     // S_h = Q_tile K^T; one lane
@@ -272,30 +289,27 @@ kda_expanded_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const
             if (flags & kLastUse) commit_pair(&tl.k_empty[at % kStages]);
             if (flags & kFinal) commit_pair(&tl.q_empty);
         };
-        auto issue_values = [&](int h, const Pending& pv) {               // O_h += P_h V; one lane
+        // O_h += P_h V, the first half of the keys as soon as its weights are there
+        auto values_step = [&](int h, const Pending& pv) -> bool {
+            if ((pv.flags & kFirstUse) && !wait(&tl.v_full[pv.at % kStages], (pv.at / kStages) & 1)) return false;
             const uint64_t b = v_desc + kda::desc_step(pv.at % kStages * kVTile);
+            const uint32_t d = tmem + kTmemO + h * 128, a = tmem + h * 128;
+            if (!wait(&tl.p_full[h][0], (p_phase >> h) & 1)) return false;
+            kda::tc_fence_after();
+            if (elect_one()) {
 #pragma unroll
-            for (int i = 0; i < kKeys / 16; ++i)
-                mma_pair_ta(tmem + kTmemO + h * 128, tmem + h * 128 + 8 * i, b + kda::desc_step(i * 2048), id_o,
-                            (i > 0 || (pv.flags & kAdd)) ? 1u : 0u);
-            if (pv.flags & kLastUse) commit_pair(&tl.v_empty[pv.at % kStages]);
-            if (pv.flags & kFinal) commit_pair(&tl.o_full[h]);
-        };
-        // values there, weights there (and what has to be cleaned is)
-        auto take_values = [&](int h, const Pending& pv) -> bool {
-            if (pv.flags & kFirstUse) {
-                if (!wait(&tl.v_full[pv.at % kStages], (pv.at / kStages) & 1)) return false;
-                if ((pv.flags & kEdge) && lane < 2) arrive_remote(at_rank(&tl.landed[h], lane));
-                __syncwarp();
+                for (int i = 0; i < kKeys / 32; ++i)
+                    mma_pair_ta(d, a + 8 * i, b + kda::desc_step(i * 2048), id_o, (i > 0 || (pv.flags & kAdd)) ? 1u : 0u);
             }
-            if (!wait(&tl.p_full[h], (p_phase >> h) & 1)) return false;
+            if (!wait(&tl.p_full[h][1], (p_phase >> h) & 1)) return false;
             p_phase ^= 1u << h;
             kda::tc_fence_after();
-            return true;
-        };
-        auto values_step = [&](int h, const Pending& pv) -> bool {
-            if (!take_values(h, pv)) return false;
-            if (elect_one()) issue_values(h, pv);
+            if (elect_one()) {
+#pragma unroll
+                for (int i = kKeys / 32; i < kKeys / 16; ++i) mma_pair_ta(d, a + 8 * i, b + kda::desc_step(i * 2048), id_o, 1u);
+                if (pv.flags & kLastUse) commit_pair(&tl.v_empty[pv.at % kStages]);
+                if (pv.flags & kFinal) commit_pair(&tl.o_full[h]);
+            }
             __syncwarp();
             return true;
         };
@@ -308,13 +322,13 @@ kda_expanded_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const
             Unit u;
             if (!read_unit(k, u)) break;
             const int two = uniform(u.ntok > kTileTokens), tiles = uniform(u.te - u.tb), steps = tiles << two;
-            const int tb = uniform(u.tb);
-            const int whole = uniform(sight(u, 0, 0, u.ntok - 1).all_hi >> kKeysLog2);    // tiles below it: all rows see all
+            const int tiles0 = two ? uniform(first_tiles(u)) : tiles;
             auto due = [&](int t, int at) {            // the second product of step t
                 Pending pv;
                 pv.at = at;
-                pv.flags = kDue | (!two || !(t & 1) ? kFirstUse : 0) | (!two || (t & 1) ? kLastUse : 0) | (t >= 2 ? kAdd : 0) |
-                           (t >= steps - 2 ? kFinal : 0) | (tb + (t >> two) >= whole ? kEdge : 0);
+                const int j = t >> two;
+                pv.flags = kDue | (!two || !(t & 1) || j >= tiles0 ? kFirstUse : 0) | (!two || (t & 1) ? kLastUse : 0) |
+                           (t >= 2 ? kAdd : 0) | (t >= steps - 2 || (two && !(t & 1) && j == tiles0 - 1) ? kFinal : 0);
                 return pv;
             };
             // a unit of two row tiles past its first key tile goes through the loop below this one
@@ -338,24 +352,20 @@ kda_expanded_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const
             // the tensor cores' time is here: as few instructions between products as can be
             const int h0 = g & 1, h1 = h0 ^ 1;
             for (int j = 1; j < tiles; ++j, ++n_k) {
-                Pending pv{kDue | kFirstUse | (j > 1 ? kAdd : 0) | (tb + j - 1 >= whole ? kEdge : 0), n_k - 1};
-                ok = take_values(h0, pv);
+                Pending pv{kDue | kFirstUse | (j > 1 ? kAdd : 0) | (j == tiles0 ? kFinal : 0), n_k - 1};
+                if (j <= tiles0) ok = values_step(h0, pv);
+                ok = ok && take_keys(n_k);
                 if (!ok) break;
-                if (elect_one()) issue_values(h0, pv);
-                ok = take_keys(n_k);
+                if (j < tiles0 && elect_one()) issue_scores(h0, 0, n_k, 0);
+                pv.flags = kDue | kLastUse | (j > 1 ? kAdd : 0) | (j > tiles0 ? kFirstUse : 0);
+                ok = values_step(h1, pv);
                 if (!ok) break;
-                if (elect_one()) issue_scores(h0, 0, n_k, 0);
-                pv.flags = kDue | kLastUse | (j > 1 ? kAdd : 0);
-                ok = take_values(h1, pv);
-                if (!ok) break;
-                if (elect_one()) {
-                    issue_values(h1, pv);
-                    issue_scores(h1, 1, n_k, kLastUse | (j == tiles - 1 ? kFinal : 0));
-                }
+                if (elect_one()) issue_scores(h1, 1, n_k, kLastUse | (j == tiles - 1 ? kFinal : 0));
             }
             __syncwarp();
             g += steps - 2;
             older = due(steps - 2, n_k - 1);
+            if (tiles0 < tiles) older.flags = 0;
             newer = due(steps - 1, n_k - 1);
         }
         if (ok && (older.flags & kDue)) ok = values_step(g & 1, older);
@@ -370,8 +380,8 @@ kda_expanded_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const
         const int h = w >> 2, row = tid & 127;
         const uint32_t lane_off = (uint32_t)((w & 3) * 32) << 16;
         const uint32_t tS = tmem + lane_off + h * 128;
-        const uint32_t p_bar = at_rank(&tl.p_full[h], 0);
-        int n_s = 0, n_j = 0, g = 0, n_landed = 0, n_v = 0;               // n_v: key tiles of the units before
+        const uint32_t p_bar = at_rank(&tl.p_full[h][0], 0);
+        int n_s = 0, n_j = 0, g = 0, n_v = 0;          // n_v: key tiles of the units before
         uint32_t o_phase = 0;                          // bit h: parity of the next O_h
         bool ok = true;
         for (int k = 0; ok; ++k) {
@@ -387,87 +397,19 @@ kda_expanded_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const
             const int hi = valid ? min(max(pos + 1, 0), u.kend) : 0;
             const bool busy = __any_sync(0xffffffffu, valid);
             const Sight un = sight(u, 0, 0, u.ntok - 1);
-            const int mine = min(max(u.pos + first + 1, 0), u.kend);      // keys that all of this CTA's rows see
+            const int mine = min(max(u.pos + first + 1, 0), u.kend);      // keys that all of this CTA's rows see,
+            const int none = min(max(u.pos + first + kRows, 0), u.kend);  // and that none of them sees from here on
+            const int tiles0 = two ? first_tiles(u) : tiles, last = two && qi == 0 ? 2 * tiles0 : steps;
             float m = -INFINITY, l = 0.f;
-            for (int t = t0; t < steps; t += 2) {
+            for (int t = t0; t < last; t += 2) {
                 const int j = two ? t >> 1 : t, k0 = (u.tb + j) << kKeysLog2;
                 if (!wait(&tl.s_full[h], n_s & 1)) { ok = false; break; }
                 ++n_s;
                 kda::tc_fence_after();
-                if (busy) {
-                    if (k0 + kKeys > mine) {
-                        // scores of keys this row does not see become -inf, in place.  Rolled: these
-                        // tiles are few, and a short call's time goes into fetching instructions
-#pragma unroll 1
-                        for (int c = 0; c < kKeys; c += 32) {
-                            const int b = hi - k0 - c;
-                            const uint32_t seen = b >= 32 ? 0xffffffffu : (1u << max(b, 0)) - 1u;
-                            float y[32];
-                            kda::tmem_ld32(tS + c, y);
-                            kda::tmem_wait_ld();
-#pragma unroll
-                            for (int e = 0; e < 32; ++e) y[e] = (seen >> e) & 1 ? y[e] : -INFINITY;
-                            tmem_st32(tS + c, reinterpret_cast<const uint32_t*>(y));
-                        }
-                        kda::tmem_wait_st();
-                    }
-                    float x[128];
-#pragma unroll
-                    for (int c = 0; c < 128; c += 32) kda::tmem_ld32(tS + c, x + c);
-                    kda::tmem_wait_ld();
-                    float top[4] = {x[0], x[1], x[2], x[3]};
-#pragma unroll
-                    for (int c = 4; c < 128; c += 4)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) top[e] = fmaxf(top[e], x[c + e]);
-                    const float big = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
-                    if (t < 2) {
-                        m = big;
-                    } else {
-                        // S complete means that this half's product before it is too, so O stands still
-                        const bool grow = (big - m) * scale_log2 > kGrow;
-                        if (__any_sync(0xffffffffu, grow)) {
-                            const float f = grow ? ex2((m - big) * scale_log2) : 1.f;
-                            const uint32_t tO = tmem + lane_off + kTmemO + h * 128;
-#pragma unroll 1
-                            for (int c = 0; c < kValue; c += 16) {
-                                float y[16];
-                                kda::tmem_ld16(tO + c, y);
-                                kda::tmem_wait_ld();
-#pragma unroll
-                                for (int e = 0; e < 16; ++e) y[e] *= f;
-                                kda::tmem_st16(tO + c, y);
-                            }
-                            l *= f;
-                            if (grow) m = big;
-                        }
-                    }
-                    const float ref = m == -INFINITY ? 0.f : m * scale_log2;
-                    const uint64_t sc2 = pack2(scale_log2, scale_log2), off2 = pack2(-ref, -ref);
-                    uint64_t sum[2] = {0, 0};
-#pragma unroll
-                    for (int c0 = 0; c0 < 128; c0 += 64) {
-                        uint32_t p[32];
-#pragma unroll
-                        for (int c = 0; c < 64; c += 2) {
-                            float a, b;
-                            unpack2(fma2(pack2(x[c0 + c], x[c0 + c + 1]), sc2, off2), a, b);
-                            a = ex2(a);
-                            b = ex2(b);
-                            sum[(c >> 1) & 1] = add2(sum[(c >> 1) & 1], pack2(a, b));
-                            p[c >> 1] = kda::pack_bf16x2(a, b);
-                        }
-                        tmem_st32(tS + c0 / 2, p);
-                    }
-                    float sa, sb;
-                    unpack2(add2(sum[0], sum[1]), sa, sb);
-                    l += sa + sb;
-                    kda::tmem_wait_st();
-                }
-                if ((!two || !(t & 1)) && k0 + kKeys > un.all_hi) {
-                    // values that must not meet a zero weight (see the header)
-                    if (!wait(&tl.landed[h], n_landed & 1)) { ok = false; break; }
-                    ++n_landed;
+                // this half takes the tile first, and not all rows see it whole: clean its values
+                const bool clean = (!two || !(t & 1) || j >= tiles0) && k0 + kKeys > un.all_hi;
+                auto prepare_values = [&]() -> bool {  // values that must not meet a zero weight (see the header)
+                    if (!wait(&tl.landed[(n_v + j) % kStages], ((n_v + j) / kStages) & 1)) return false;
                     unsigned char* v = sm + kV0 + (n_v + j) % kStages * kVTile;
                     bool odd = false;
 #pragma unroll 1
@@ -485,10 +427,100 @@ kda_expanded_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const
                     }
                     if (odd) flag_pair(&tl.odd_values[k & 7]);
                     kda::fence_proxy_async_smem();
+                    return true;
+                };
+                auto arrive = [&](int part) {          // weights of that half of the keys are there
+                    kda::tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) arrive_remote(p_bar + part * 8);
+                };
+                if (!busy || k0 >= none) {             // no row here sees any key of the tile
+                    if (busy) {
+                        const uint32_t zero[32] = {};
+                        tmem_st32(tS, zero);
+                        tmem_st32(tS + 32, zero);
+                        kda::tmem_wait_st();
+                    }
+                    if (clean && !prepare_values()) { ok = false; break; }
+                    arrive(0);
+                    arrive(1);
+                    continue;
                 }
-                kda::tc_fence_before();
-                __syncwarp();
-                if (lane == 0) arrive_remote(p_bar);
+                if (k0 + kKeys > mine) {
+                    // scores of keys this row does not see become -inf, in place.  Rolled: these
+                    // tiles are few, and a short call's time goes into fetching instructions
+#pragma unroll 1
+                    for (int c = 0; c < kKeys; c += 32) {
+                        const int b = hi - k0 - c;
+                        const uint32_t seen = b >= 32 ? 0xffffffffu : (1u << max(b, 0)) - 1u;
+                        float y[32];
+                        kda::tmem_ld32(tS + c, y);
+                        kda::tmem_wait_ld();
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) y[e] = (seen >> e) & 1 ? y[e] : -INFINITY;
+                        tmem_st32(tS + c, reinterpret_cast<const uint32_t*>(y));
+                    }
+                    kda::tmem_wait_st();
+                }
+                float x[128];
+#pragma unroll
+                for (int c = 0; c < 128; c += 32) kda::tmem_ld32(tS + c, x + c);
+                kda::tmem_wait_ld();
+                float top[4] = {x[0], x[2], x[4], x[6]};
+#pragma unroll
+                for (int c = 0; c < 128; c += 8)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) top[e] = fmaxf(top[e], fmaxf(x[c + 2 * e], x[c + 2 * e + 1]));
+                const float big = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+                if (t < 2) {
+                    m = big;
+                } else {
+                    // S complete means that this half's product before it is too, so O stands still
+                    const bool grow = (big - m) * scale_log2 > kGrow;
+                    if (__any_sync(0xffffffffu, grow)) {
+                        const float f = grow ? ex2((m - big) * scale_log2) : 1.f;
+                        const uint32_t tO = tmem + lane_off + kTmemO + h * 128;
+#pragma unroll 1
+                        for (int c = 0; c < kValue; c += 16) {
+                            float y[16];
+                            kda::tmem_ld16(tO + c, y);
+                            kda::tmem_wait_ld();
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) y[e] *= f;
+                            kda::tmem_st16(tO + c, y);
+                        }
+                        l *= f;
+                        if (grow) m = big;
+                    }
+                }
+                const float ref = m == -INFINITY ? 0.f : m * scale_log2;
+                const uint64_t sc2 = pack2(scale_log2, scale_log2), off2 = pack2(-ref, -ref);
+                uint64_t sum[2] = {0, 0};
+                uint32_t p[32];
+                auto weigh = [&](int from, int to) {   // weights of keys [from, to), as pairs in p
+#pragma unroll
+                    for (int c = from; c < to; c += 2) {
+                        float a, b;
+                        unpack2(fma2(pack2(x[c], x[c + 1]), sc2, off2), a, b);
+                        a = ex2(a);
+                        b = ex2(b);
+                        sum[(c >> 1) & 1] = add2(sum[(c >> 1) & 1], pack2(a, b));
+                        p[(c >> 1) & 31] = kda::pack_bf16x2(a, b);
+                    }
+                };
+                weigh(0, 64);
+                tmem_st32(tS, p);
+                if (clean && !prepare_values()) { ok = false; break; }
+                weigh(64, 96);                         // while the first half is being stored
+                kda::tmem_wait_st();
+                arrive(0);
+                weigh(96, 128);
+                tmem_st32(tS + 32, p);
+                float sa, sb;
+                unpack2(add2(sum[0], sum[1]), sa, sb);
+                l += sa + sb;
+                kda::tmem_wait_st();
+                arrive(1);
             }
             if (!ok) break;
             // ---- output
