@@ -189,7 +189,7 @@ kda_expanded_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const
 
     if (w == kWalkWarp) {
         // ---------------- unit descriptions
-        if (lane == 0 && rank == 0) parts.clear_pair(cluster);
+        if (lane == 0 && rank == 0) parts.clear_both(cluster);
         Walker walk;
         walk.start(s, cu, cu_k, piece, cluster);
         for (int k = 0;; ++k) {
@@ -205,7 +205,7 @@ kda_expanded_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const
             }
             if (!more) break;
             walk.share(s, u, from, 0);
-            if (lane == 0 && rank == 0) parts.describe_pair(cluster, u);
+            if (lane == 0 && rank == 0) parts.describe_both(cluster, u);
         }
     } else if (w == kCopyWarp) {
         // ---------------- copies: of each tile this CTA's keys, then its channels of the values
@@ -690,7 +690,7 @@ cudaError_t launch_expanded_attention_tc(const ExpandedArgs& a) {
         Values{static_cast<const __nv_bfloat16*>(a.v), a.v_token, a.v_head}, a.cu_seqlens, a.cu_seqlens_k, expanded_shape(a, p),
         a.scale * kLog2e, static_cast<__nv_bfloat16*>(a.o), a.lse, paged_partials(pa, p), a.status);
     if (err != cudaSuccess) return err;
-    return launch_pair_merge(pa, p, pairs);
+    return launch_latent_merge(pa, p, pairs);
 }
 
 }  // namespace kda_host

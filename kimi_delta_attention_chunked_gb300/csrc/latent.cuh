@@ -86,7 +86,7 @@ kda_paged::Shape latent_shape(const LatentArgs& a, const PagedPlan& p);
 PagedArgs expanded_view(const ExpandedArgs& a);
 kda_paged::PackedShape expanded_shape(const ExpandedArgs& a, const PagedPlan& p);
 
-cudaError_t launch_pair_merge(const PagedArgs& a, const PagedPlan& p, int pairs);
+cudaError_t launch_latent_merge(const PagedArgs& a, const PagedPlan& p, int ctas);
 
 cudaError_t launch_rotary(const RotaryArgs& a);
 cudaError_t launch_latent_append(const LatentAppendArgs& a);

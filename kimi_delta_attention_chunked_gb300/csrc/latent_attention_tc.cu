@@ -215,7 +215,7 @@ kda_latent_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const _
 
     if (w == kWalkWarp) {
         // ---------------- unit descriptions
-        if (lane == 0 && rank == 0) parts.clear_pair(cluster);
+        if (lane == 0 && rank == 0) parts.clear_both(cluster);
         Walker walk;
         walk.start(s, cu, seq_len, piece, cluster);
         for (int k = 0;; ++k) {
@@ -231,7 +231,7 @@ kda_latent_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const _
             }
             if (!more) break;
             walk.share(s, u, from, 0);
-            if (lane == 0 && rank == 0) parts.describe_pair(cluster, u);
+            if (lane == 0 && rank == 0) parts.describe_both(cluster, u);
         }
     } else if (w == kCopyWarp) {
         // ---------------- this CTA's half of every tile
@@ -638,7 +638,7 @@ cudaError_t launch_latent_attention_tc(const LatentArgs& a) {
         a.block_table, a.cu_seqlens, a.seq_len, latent_shape(a, p), t, a.scale * kLog2e, static_cast<__nv_bfloat16*>(a.o), a.lse,
         paged_partials(pa, p), a.status);
     if (err != cudaSuccess) return err;
-    return launch_pair_merge(pa, p, pairs);
+    return launch_latent_merge(pa, p, pairs);
 }
 
 }  // namespace kda_host

@@ -8,7 +8,7 @@
 // cache and v_j its first 512 channels, so a tile is fetched once for both.
 //
 // This path is for fp32, whose accuracy the tensor cores' 16-bit operands do not reach, and
-// for bf16 rows that TMA cannot fetch.  A tile of 32 keys lies in shared memory as fp32; 256
+// for bf16 rows that TMA cannot fetch.  A tile of 16 or 32 keys lies in shared memory as fp32; 256
 // threads form 4 x 2 scores each (over a part of the channels: the parts are added up in the
 // softmax step), then DV / 4 column groups of 4 with ROWS / RPT row groups of RPT rows each.
 #include <algorithm>
@@ -31,14 +31,13 @@ using kda_paged::Unit;
 using kda_paged::Walker;
 
 constexpr int kThreads = 256;
-constexpr int kTileLog2 = 5, kTile = 1 << kTileLog2;
 constexpr float kLn2 = 0.69314718055994531f;
 constexpr float kLog2e = 1.44269504088896341f;
 
 // Where the keys and values of the absorbed form lie.
 template <typename T>
 struct Absorbed {
-    static constexpr int DK = kRow, DV = kLatent, ROWS = 16;
+    static constexpr int DK = kRow, DV = kLatent, ROWS = 16, LOG2 = 4;
     static constexpr bool kShared = true;              // values are the keys' first channels
     using Sh = Shape;
     const T* cache;
@@ -57,7 +56,7 @@ struct Absorbed {
 // And of the expanded one.
 template <typename T>
 struct Expanded {
-    static constexpr int DK = kKey, DV = kValue, ROWS = 32;
+    static constexpr int DK = kKey, DV = kValue, ROWS = 32, LOG2 = 5;
     static constexpr bool kShared = false;
     using Sh = PackedShape;
     const T *k_nope, *k_rope, *v;
@@ -76,6 +75,7 @@ struct Expanded {
 
 template <class Src>
 struct Smem {
+    static constexpr int kTile = 1 << Src::LOG2;       // keys of a tile
     float q[Src::ROWS][Src::DK];
     float k[kTile][Src::DK + 4];
     float v[Src::kShared ? 1 : kTile][Src::DV];
@@ -94,11 +94,11 @@ __device__ __forceinline__ void load4(const T* p, float* y) {
 
 // VEC: channels a load brings (1: rows off their 16-byte boundaries)
 template <class Src, typename T, int VEC>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kThreads, 2)
 kda_latent_simt_kernel(const T* __restrict__ q, Src src, const int32_t* __restrict__ cu,
                        const int32_t* __restrict__ lengths, long long q_stride, typename Src::Sh s, float scale_log2,
                        T* __restrict__ o, float* __restrict__ lse, Partials parts) {
-    constexpr int DK = Src::DK, DV = Src::DV, ROWS = Src::ROWS;
+    constexpr int DK = Src::DK, DV = Src::DV, ROWS = Src::ROWS, kTileLog2 = Src::LOG2, kTile = 1 << kTileLog2;
     extern __shared__ __align__(16) unsigned char smem_raw[];
     Smem<Src>& sm = *reinterpret_cast<Smem<Src>*>(smem_raw);
     __shared__ unsigned long long s_red[kThreads / 32];
@@ -113,7 +113,7 @@ kda_latent_simt_kernel(const T* __restrict__ q, Src src, const int32_t* __restri
                                                         reinterpret_cast<unsigned long long*>(smem_raw), s_red, &s_piece);
     Walker walk;
     if (w == 0) walk.start(s, cu, lengths, piece, blockIdx.x);
-    if (tid == 0) parts.clear(blockIdx.x);
+    if (tid == 0) parts.clear_both(blockIdx.x);
 
     constexpr int CG = DV / 4, RPT = ROWS * CG / kThreads;        // column groups; rows of a thread
     static_assert(RPT >= 4 && RPT % 4 == 0, "rows");
@@ -122,7 +122,9 @@ kda_latent_simt_kernel(const T* __restrict__ q, Src src, const int32_t* __restri
         __syncthreads();                               // the unit before is done with shared memory
         if (w == 0) {
             Unit nu;
-            const bool more = walk.next(s, cu, lengths, nu);
+            unsigned long long from;
+            const bool more = walk.step(s, cu, lengths, nu, from);
+            if (more) walk.share(s, nu, from, 0);
             if (lane == 0) {
                 s_unit = nu;
                 s_more = more;
@@ -167,7 +169,6 @@ kda_latent_simt_kernel(const T* __restrict__ q, Src src, const int32_t* __restri
             struct alignas(VEC * sizeof(T)) Chunk { T v[VEC]; };
             constexpr int KC = DK / VEC, VC = Src::kShared ? 0 : DV / VEC, BATCH = 4;
             constexpr int TOTAL = kTile * (KC + VC);
-            static_assert(TOTAL % (kThreads * BATCH) == 0 || VEC > 1, "tile");
 #pragma unroll 1
             for (int e0 = tid; e0 < TOTAL; e0 += kThreads * BATCH) {
                 Chunk x[BATCH];
@@ -201,18 +202,18 @@ kda_latent_simt_kernel(const T* __restrict__ q, Src src, const int32_t* __restri
             }
             if (tid < kTile && t + 1 < u.te) s_place[(t + 1) & 1][tid] = next_place;
             __syncthreads();
-            // scores over one part of the channels: rows 4 ty .. + 3, keys tx, tx + 16
+            // scores over one part of the channels: rows 4 ty .. + 3, keys tx, tx + KX
             {
-                constexpr int SPLIT = Smem<Src>::SPLIT, CP = DK / SPLIT;
+                constexpr int SPLIT = Smem<Src>::SPLIT, CP = DK / SPLIT, KX = kTile / 2;
                 static_assert(CP % 4 == 0, "channels");
-                const int tx = tid & 15, ty = (tid >> 4) % (ROWS / 4), part = tid / (16 * (ROWS / 4));
+                const int tx = tid % KX, ty = tid / KX % (ROWS / 4), part = tid / (KX * (ROWS / 4));
                 float a[4][2];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) a[i][0] = a[i][1] = 0.f;
 #pragma unroll 4
                 for (int c = part * CP; c < (part + 1) * CP; c += 4) {
                     const float4 k0 = *reinterpret_cast<const float4*>(&sm.k[tx][c]);
-                    const float4 k1 = *reinterpret_cast<const float4*>(&sm.k[tx + 16][c]);
+                    const float4 k1 = *reinterpret_cast<const float4*>(&sm.k[tx + KX][c]);
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const float4 x = *reinterpret_cast<const float4*>(&sm.q[4 * ty + i][c]);
@@ -223,7 +224,7 @@ kda_latent_simt_kernel(const T* __restrict__ q, Src src, const int32_t* __restri
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     sm.part[part][4 * ty + i][tx] = a[i][0];
-                    sm.part[part][4 * ty + i][tx + 16] = a[i][1];
+                    sm.part[part][4 * ty + i][tx + KX] = a[i][1];
                 }
             }
             __syncthreads();
@@ -318,7 +319,7 @@ kda_latent_simt_kernel(const T* __restrict__ q, Src src, const int32_t* __restri
                 if (cg == 0) parts.stats(blockIdx.x, which)[r] = make_float2(rm, rl);
             }
         }
-        if (tid == 0) parts.describe(blockIdx.x, u);
+        if (tid == 0) parts.describe_both(blockIdx.x, u);
     }
 }
 
@@ -333,12 +334,12 @@ cudaError_t launch(const Src& src, const void* q, int64_t q_stride, const int32_
         return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
     });
     if (e != cudaSuccess) return e;
-    const int ctas = std::min(p.max_ctas, kda_host::sm_count());
+    const int ctas = std::min(p.max_ctas, 2 * kda_host::sm_count());
     const cudaError_t err = kda_host::launch_overlapped(kern, ctas, kThreads, smem, pa.stream, 1, static_cast<const T*>(q), src,
                                                         cu, lengths, q_stride, s, scale * kLog2e, static_cast<T*>(pa.o),
                                                         pa.lse, kda_host::paged_partials(pa, p));
     if (err != cudaSuccess) return err;
-    return kda_host::launch_paged_merge(pa, p, ctas);
+    return kda_host::launch_latent_merge(pa, p, ctas);
 }
 
 template <typename T>
@@ -380,8 +381,8 @@ PagedPlan latent_plan_simt(int T, int H) {
     p.Gv = (H + groups - 1) / groups;
     p.U = kRows / p.Gv;
     p.rows = paged_slot_rows(p.U, T, p.Gv);
-    p.tile_log2 = kTileLog2;
-    p.max_ctas = 160;
+    p.tile_log2 = Absorbed<float>::LOG2;
+    p.max_ctas = 304;
     p.extra = 0;
     return p;
 }
@@ -391,8 +392,8 @@ PagedPlan expanded_plan_simt(int T) {
     p.Gv = 1;
     p.U = Expanded<float>::ROWS;
     p.rows = paged_slot_rows(p.U, T, 1);
-    p.tile_log2 = kTileLog2;
-    p.max_ctas = 160;
+    p.tile_log2 = Expanded<float>::LOG2;
+    p.max_ctas = 304;
     p.extra = 0;
     return p;
 }

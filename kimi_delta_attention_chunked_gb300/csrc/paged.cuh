@@ -372,10 +372,10 @@ struct Partials {
         if (!u.first) meta[2 * c] = make_int4(u.start, u.parts, 0, 0);
         else if (!u.last) meta[2 * c + 1] = make_int4(u.tok0, u.qh0, u.ntok, u.parts);
     }
-    // As the merge of the pairs reads it: either slot's unit in full, (first token, first query head, tokens,
+    // As latent attention's merge reads it: either slot's unit in full, (first token, first query head, tokens,
     // CTA in which it begins << 16 | parts), parts = 0 where there is none.
-    __device__ __forceinline__ void clear_pair(int c) const { meta[2 * c] = meta[2 * c + 1] = make_int4(0, 0, 0, 0); }
-    __device__ __forceinline__ void describe_pair(int c, const Unit& u) const {
+    __device__ __forceinline__ void clear_both(int c) const { meta[2 * c] = meta[2 * c + 1] = make_int4(0, 0, 0, 0); }
+    __device__ __forceinline__ void describe_both(int c, const Unit& u) const {
         if (!u.first || !u.last) meta[2 * c + (u.first ? 1 : 0)] = make_int4(u.tok0, u.qh0, u.ntok, u.start << 16 | u.parts);
     }
     __device__ __forceinline__ size_t slot(int c, int which) const {

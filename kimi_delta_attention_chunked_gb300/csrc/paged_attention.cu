@@ -367,7 +367,7 @@ kda_paged_merge_kernel(Partials parts, int Gv, int Hq, T* __restrict__ o, float*
                 add(st, v);
             }
         }
-        if (r0 + grp / share >= rows || me.y + r % Gv >= Hq) continue;     // a last group of fewer heads
+        if (r0 + grp / share >= rows) continue;
         const float inv = l == 0.f ? 0.f : 1.f / l;
         const size_t at = (size_t)(me.x + r / Gv) * Hq + me.y + r % Gv;
         T* dst = o + at * D + 4 * x;
@@ -496,7 +496,6 @@ cudaError_t launch_paged_merge(const PagedArgs& a, const PagedPlan& p, int ctas)
         case 32: return wide ? launch_merge<32, __nv_bfloat16>(a, p, ctas) : launch_merge<32, float>(a, p, ctas);
         case 64: return wide ? launch_merge<64, __nv_bfloat16>(a, p, ctas) : launch_merge<64, float>(a, p, ctas);
         case 128: return wide ? launch_merge<128, __nv_bfloat16>(a, p, ctas) : launch_merge<128, float>(a, p, ctas);
-        case 512: return wide ? launch_merge<512, __nv_bfloat16>(a, p, ctas) : launch_merge<512, float>(a, p, ctas);
     }
     return cudaErrorNotSupported;
 }

@@ -64,68 +64,84 @@ constexpr int kThreads = 256;
 struct RotarySizes {
     long long xt, xh, ot, oh;                          // strides in elements
     int T, H, d, rot, tokens;                          // tokens of a block
-    int turned_items, items;                           // pieces of a head: turned ones, then copied ones
+    int turned_items, copy_items, items;               // threads of a row: turned pieces, then copied ones
 };
 
 // A block takes `tokens` tokens: the cosines and sines of all their pairs once, into shared
-// memory, then the heads.  A thread keeps one piece of a head's channels and goes through the
-// rows (token, head) with it: VEC neighbouring channels of an interleaved head, VEC and their VEC
-// partners of the other layout, or VEC channels that are copied.
-// Bound: HBM for long prompts, the launch and two dependent reads for decode steps.
+// memory, then the rows (token, head).  A thread goes through them with one piece of the head's channels: VEC
+// neighbouring channels of an interleaved head, VEC and their VEC partners of the other layout, or up to twice VEC
+// channels that are copied (with one piece of those to a thread, 20,001 tokens x 32 heads of 128, half of
+// them turned, took 75 us instead of 58).  The first row is fetched ahead of the table.  Bound: HBM for long prompts
+// (0.83 of the copy rate there; two or four heads a thread 59 and 87 us: fewer threads fit; blocks of 16 and 32
+// tokens 59 and 63 us), the launch and two dependent reads for decode steps (2.2 us).
 template <typename T, int VEC, bool WIDE, bool INTERLEAVED>
 __global__ void __launch_bounds__(kThreads)
 kda_rotary_kernel(const T* x, const int32_t* __restrict__ positions, const float* __restrict__ inv_freq, RotarySizes s,
                   float factor, T* out) {
-    extern __shared__ float2 table[];                  // [tokens][rot / 2]
+    extern __shared__ __align__(16) float2 table[];    // [tokens][rot / 2]
     kda_paged::wait_for_stream();
     const int half = s.rot >> 1, tid = threadIdx.x;
     const int t0 = blockIdx.x * s.tokens, n = min(s.tokens, s.T - t0);
+    struct alignas(WIDE ? VEC * sizeof(T) : sizeof(T)) Piece { T v[VEC]; };
+    const int per = kThreads / s.items, item = tid % s.items;             // rows at once
+    const bool turns = item < s.turned_items;
+    // first channels of the two pieces; the second may not be there
+    const int c = turns ? item * VEC : s.rot + (item - s.turned_items) * VEC;
+    const int c2 = turns ? half + c : c + s.copy_items * VEC;
+    const bool two = turns ? !INTERLEAVED : c2 < s.d;
+    const int len = WIDE ? VEC : min(VEC, s.d - c), len2 = WIDE ? VEC : min(VEC, s.d - c2);      // shorter at an odd end
+    Piece p, q;
+    auto load_piece = [&](Piece& y, const T* src, int m) {
+        if (m == VEC) y = *reinterpret_cast<const Piece*>(src);
+        else
+            for (int i = 0; i < m; ++i) y.v[i] = src[i];
+    };
+    auto store_piece = [&](T* dst, const Piece& y, int m) {
+        if (m == VEC) *reinterpret_cast<Piece*>(dst) = y;
+        else
+            for (int i = 0; i < m; ++i) dst[i] = y.v[i];
+    };
+    const int rows = n * s.H;
+    auto load = [&](int row) {
+        const int t = row / s.H, h = row - t * s.H;
+        const T* src = x + (t0 + t) * s.xt + h * s.xh;
+        load_piece(p, src + c, len);
+        if (two) load_piece(q, src + c2, len2);
+    };
+    int row = tid / s.items < per ? tid / s.items : rows;
+    if (row < rows) load(row);
     for (int e = tid; e < n * half; e += kThreads) {
-        const int t = e / half;
-        table[e] = turned(inv_freq[e - t * half], positions[t0 + t], factor);
+        const int k = e / half;
+        table[e] = turned(inv_freq[e - k * half], positions[t0 + k], factor);
     }
     __syncthreads();
-    struct alignas(WIDE ? VEC * sizeof(T) : sizeof(T)) Piece { T v[VEC]; };
-    const int per = kThreads / s.items, item = tid % s.items, row0 = tid / s.items;    // rows at once
-    if (row0 >= per) return;
-    const int rows = n * s.H;
-    int t = row0 / s.H, h = row0 - t * s.H;
-    for (int row = row0; row < rows; row += per) {
-        const T* src = x + (t0 + t) * s.xt + h * s.xh;
+    for (; row < rows; row += per) {
+        const int t = row / s.H, h = row - t * s.H;
         T* dst = out + (t0 + t) * s.ot + h * s.oh;
-        if (item < s.turned_items) {
-            const int c = item * VEC;
-            const float2* cs = table + t * half;
+        if (turns) {
+            const float2* cs = table + t * half + (INTERLEAVED ? c >> 1 : c);
             if constexpr (INTERLEAVED) {
-                Piece p = *reinterpret_cast<const Piece*>(src + c);
 #pragma unroll
-                for (int i = 0; i < VEC; i += 2) turn(p.v[i], p.v[i + 1], cs[(c + i) >> 1]);
-                *reinterpret_cast<Piece*>(dst + c) = p;
+                for (int i = 0; i < VEC; i += 2) turn(p.v[i], p.v[i + 1], cs[i >> 1]);
             } else {
-                Piece p = *reinterpret_cast<const Piece*>(src + c), q = *reinterpret_cast<const Piece*>(src + half + c);
 #pragma unroll
-                for (int i = 0; i < VEC; ++i) turn(p.v[i], q.v[i], cs[c + i]);
-                *reinterpret_cast<Piece*>(dst + c) = p;
-                *reinterpret_cast<Piece*>(dst + half + c) = q;
-            }
-        } else {
-            const int c = s.rot + (item - s.turned_items) * VEC;
-            if (WIDE || c + VEC <= s.d) {
-                *reinterpret_cast<Piece*>(dst + c) = *reinterpret_cast<const Piece*>(src + c);
-            } else {
-                for (int i = c; i < s.d; ++i) dst[i] = src[i];
+                for (int i = 0; i < VEC; ++i) turn(p.v[i], q.v[i], cs[i]);
             }
         }
-        for (h += per; h >= s.H; h -= s.H) ++t;
+        store_piece(dst + c, p, len);
+        if (two) store_piece(dst + c2, q, len2);
+        if (row + per < rows) load(row + per);
     }
 }
 
 template <typename T, int VEC, bool WIDE, bool INTERLEAVED>
 cudaError_t rotary(const kda_host::RotaryArgs& a) {
-    RotarySizes s{a.x_token, a.x_head, a.out_token, a.out_head, a.T, a.H, a.d, a.rot, 1, 0, 0};
+    RotarySizes s{a.x_token, a.x_head, a.out_token, a.out_head, a.T, a.H, a.d, a.rot, 1, 0, 0, 0};
     s.turned_items = (INTERLEAVED ? a.rot : a.rot / 2) / VEC;
     const bool in_place = a.x == a.out;                // with the same strides: the other channels stay
-    s.items = s.turned_items + (in_place ? 0 : (a.d - a.rot + VEC - 1) / VEC);
+    const int copied = in_place ? 0 : (a.d - a.rot + VEC - 1) / VEC;
+    s.copy_items = (copied + 1) / 2;
+    s.items = s.turned_items + s.copy_items;
     // a block's tokens share the set-up, and their rows hide each other's loads, as long as every SM
     // has a few blocks
     const int sms = kda_host::sm_count();
@@ -165,26 +181,20 @@ kda_latent_append_kernel(const T* __restrict__ c, const T* __restrict__ k_rope, 
     const int step = gridDim.x * (kThreads / 32);
     for (int t = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5); t < n_tokens; t += step) {
         const long long slot = slot_map[t];
-        if (slot < 0 || slot >= n_slots) continue;
+        const int pos = inv_freq ? positions[t] : 0;
         const T* src = c + t * c_stride;
         const T* rope = k_rope + t * r_stride;
         T* dst = cache + slot * kRow;
         T x = rope[a], y = rope[b];
-        if constexpr (WIDE) {
-            constexpr int N = kLatent / VEC / 32;
-            uint4 p[N];
+        struct alignas(WIDE ? 16 : sizeof(T)) Piece { T v[WIDE ? VEC : 1]; };
+        constexpr int N = kLatent / 32 / (WIDE ? VEC : 1);
+        Piece p[N];
 #pragma unroll
-            for (int i = 0; i < N; ++i) p[i] = reinterpret_cast<const uint4*>(src)[lane + 32 * i];
+        for (int i = 0; i < N; ++i) p[i] = reinterpret_cast<const Piece*>(src)[lane + 32 * i];
+        if (slot < 0 || slot >= n_slots) continue;
 #pragma unroll
-            for (int i = 0; i < N; ++i) reinterpret_cast<uint4*>(dst)[lane + 32 * i] = p[i];
-        } else {
-            T p[kLatent / 32];
-#pragma unroll
-            for (int i = 0; i < kLatent / 32; ++i) p[i] = src[lane + 32 * i];
-#pragma unroll
-            for (int i = 0; i < kLatent / 32; ++i) dst[lane + 32 * i] = p[i];
-        }
-        if (inv_freq) turn(x, y, turned(f, positions[t], factor));
+        for (int i = 0; i < N; ++i) reinterpret_cast<Piece*>(dst)[lane + 32 * i] = p[i];
+        if (inv_freq) turn(x, y, turned(f, pos, factor));
         dst[kLatent + a] = x;
         dst[kLatent + b] = y;
     }
