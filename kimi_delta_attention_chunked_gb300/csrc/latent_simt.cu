@@ -8,10 +8,11 @@
 // cache and v_j its first 512 channels, so a tile is fetched once for both.
 //
 // This path is for fp32, whose accuracy the tensor cores' 16-bit operands do not reach, and
-// for bf16 rows that TMA cannot fetch.  A tile of 16 or 32 keys lies in shared memory as fp32; 256
+// for bf16 rows that TMA cannot fetch.  A tile of 32 keys lies in shared memory as fp32; the
 // threads form 4 x 2 scores each (over a part of the channels: the parts are added up in the
 // softmax step), then DV / 4 column groups of 4 with ROWS / RPT row groups of RPT rows each.
 #include <algorithm>
+#include <type_traits>
 
 #include "latent.cuh"
 
@@ -30,14 +31,13 @@ using kda_paged::Shape;
 using kda_paged::Unit;
 using kda_paged::Walker;
 
-constexpr int kThreads = 256;
 constexpr float kLn2 = 0.69314718055994531f;
 constexpr float kLog2e = 1.44269504088896341f;
 
 // Where the keys and values of the absorbed form lie.
 template <typename T>
 struct Absorbed {
-    static constexpr int DK = kRow, DV = kLatent, ROWS = 16, LOG2 = 4;
+    static constexpr int DK = kRow, DV = kLatent, ROWS = 16, LOG2 = 5, THREADS = 512, BLOCKS = 1;
     static constexpr bool kShared = true;              // values are the keys' first channels
     using Sh = Shape;
     const T* cache;
@@ -56,7 +56,7 @@ struct Absorbed {
 // And of the expanded one.
 template <typename T>
 struct Expanded {
-    static constexpr int DK = kKey, DV = kValue, ROWS = 32, LOG2 = 5;
+    static constexpr int DK = kKey, DV = kValue, ROWS = 32, LOG2 = 5, THREADS = 256, BLOCKS = 2;
     static constexpr bool kShared = false;
     using Sh = PackedShape;
     const T *k_nope, *k_rope, *v;
@@ -79,7 +79,7 @@ struct Smem {
     float q[Src::ROWS][Src::DK];
     float k[kTile][Src::DK + 4];
     float v[Src::kShared ? 1 : kTile][Src::DV];
-    static constexpr int SPLIT = kThreads / (Src::ROWS / 4 * (kTile / 2));    // parts of the channels
+    static constexpr int SPLIT = Src::THREADS / (Src::ROWS / 4 * (kTile / 2));    // parts of the channels
     float part[SPLIT][Src::ROWS][kTile + 1];
     float p[kTile][Src::ROWS];                         // weights; -1 where the row does not see the key
     float scale[Src::ROWS];                            // factor of the earlier sums
@@ -94,11 +94,12 @@ __device__ __forceinline__ void load4(const T* p, float* y) {
 
 // VEC: channels a load brings (1: rows off their 16-byte boundaries)
 template <class Src, typename T, int VEC>
-__global__ void __launch_bounds__(kThreads, 2)
+__global__ void __launch_bounds__(Src::THREADS, Src::BLOCKS)
 kda_latent_simt_kernel(const T* __restrict__ q, Src src, const int32_t* __restrict__ cu,
                        const int32_t* __restrict__ lengths, long long q_stride, typename Src::Sh s, float scale_log2,
                        T* __restrict__ o, float* __restrict__ lse, Partials parts) {
     constexpr int DK = Src::DK, DV = Src::DV, ROWS = Src::ROWS, kTileLog2 = Src::LOG2, kTile = 1 << kTileLog2;
+    constexpr int kThreads = Src::THREADS;
     extern __shared__ __align__(16) unsigned char smem_raw[];
     Smem<Src>& sm = *reinterpret_cast<Smem<Src>*>(smem_raw);
     __shared__ unsigned long long s_red[kThreads / 32];
@@ -134,6 +135,7 @@ kda_latent_simt_kernel(const T* __restrict__ q, Src src, const int32_t* __restri
         if (!s_more) break;
         const Unit u = s_unit;
         const int rows = u.ntok * s.Gv;
+#pragma unroll 12
         for (int e = tid; e < ROWS * DK; e += kThreads) {
             const int r = e / DK, c = e % DK, head = u.qh0 + r % s.Gv;
             float x = 0.f;
@@ -167,8 +169,8 @@ kda_latent_simt_kernel(const T* __restrict__ q, Src src, const int32_t* __restri
             if (tid < kTile && t + 1 < u.te) next_place = place_of(t + 1);
             // places without a key become zero
             struct alignas(VEC * sizeof(T)) Chunk { T v[VEC]; };
-            constexpr int KC = DK / VEC, VC = Src::kShared ? 0 : DV / VEC, BATCH = 4;
-            constexpr int TOTAL = kTile * (KC + VC);
+            constexpr int KC = DK / VEC, VC = Src::kShared ? 0 : DV / VEC, TOTAL = kTile * (KC + VC);
+            constexpr int BATCH = TOTAL / kThreads < 10 ? (TOTAL + kThreads - 1) / kThreads : 10;    // loads in flight
 #pragma unroll 1
             for (int e0 = tid; e0 < TOTAL; e0 += kThreads * BATCH) {
                 Chunk x[BATCH];
@@ -229,6 +231,7 @@ kda_latent_simt_kernel(const T* __restrict__ q, Src src, const int32_t* __restri
             }
             __syncthreads();
             // softmax statistics of row sr
+            int hidden;                                // some row does not see some key of the tile
             {
                 float x[KPT];
                 float top = -INFINITY;
@@ -251,7 +254,7 @@ kda_latent_simt_kernel(const T* __restrict__ q, Src src, const int32_t* __restri
                 float sum = 0.f;
 #pragma unroll
                 for (int i = 0; i < KPT; ++i) {
-                    const float p = (seen >> i) & 1 ? exp2f(x[i] - ref) : -1.f;
+                    const float p = (seen >> i) & 1 ? exp2f(x[i] - ref) : sr < rows ? -1.f : 0.f;
                     if ((seen >> i) & 1) sum += p;
                     sm.p[sx + TPR * i][sr] = p;
                 }
@@ -260,17 +263,20 @@ kda_latent_simt_kernel(const T* __restrict__ q, Src src, const int32_t* __restri
                 l = fmaf(l, f, sum);
                 m = mn;
                 if (sx == 0) sm.scale[sr] = f;
+                hidden = sr < rows && seen != (1u << KPT) - 1;
             }
-            __syncthreads();
-            // weighted sums; a masked key is passed over, not multiplied by zero, so that what
-            // stands there stays out
+            hidden = __syncthreads_or(hidden);
+            // weighted sums
 #pragma unroll
             for (int a = 0; a < RPT; ++a) {
                 const float f = sm.scale[r0 + a];
 #pragma unroll
                 for (int c = 0; c < 4; ++c) acc[a][c] *= f;
             }
-            if (r0 < rows) {
+            // A masked key is passed over, not multiplied by zero, so that what stands there stays out.  Its
+            // branches cost more than the products (16 rows x 16 keys x 512: 5 us), so tiles that all rows see whole
+            // do without
+            auto weigh = [&](auto masked) {
 #pragma unroll 4
                 for (int j = 0; j < kTile; ++j) {
                     const float4 v = *reinterpret_cast<const float4*>(Src::kShared ? &sm.k[j][4 * cg]
@@ -281,7 +287,7 @@ kda_latent_simt_kernel(const T* __restrict__ q, Src src, const int32_t* __restri
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
                             const float p = i == 0 ? p4.x : i == 1 ? p4.y : i == 2 ? p4.z : p4.w;
-                            if (p != -1.f) {
+                            if (!decltype(masked)::value || p != -1.f) {
                                 acc[a0 + i][0] = fmaf(p, v.x, acc[a0 + i][0]);
                                 acc[a0 + i][1] = fmaf(p, v.y, acc[a0 + i][1]);
                                 acc[a0 + i][2] = fmaf(p, v.z, acc[a0 + i][2]);
@@ -290,6 +296,10 @@ kda_latent_simt_kernel(const T* __restrict__ q, Src src, const int32_t* __restri
                         }
                     }
                 }
+            };
+            if (r0 < rows) {
+                if (hidden) weigh(std::true_type{});
+                else weigh(std::false_type{});
             }
         }
         __syncthreads();
@@ -334,8 +344,8 @@ cudaError_t launch(const Src& src, const void* q, int64_t q_stride, const int32_
         return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
     });
     if (e != cudaSuccess) return e;
-    const int ctas = std::min(p.max_ctas, 2 * kda_host::sm_count());
-    const cudaError_t err = kda_host::launch_overlapped(kern, ctas, kThreads, smem, pa.stream, 1, static_cast<const T*>(q), src,
+    const int ctas = std::min(p.max_ctas, Src::BLOCKS * kda_host::sm_count());
+    const cudaError_t err = kda_host::launch_overlapped(kern, ctas, Src::THREADS, smem, pa.stream, 1, static_cast<const T*>(q), src,
                                                         cu, lengths, q_stride, s, scale * kLog2e, static_cast<T*>(pa.o),
                                                         pa.lse, kda_host::paged_partials(pa, p));
     if (err != cudaSuccess) return err;
@@ -384,6 +394,7 @@ PagedPlan latent_plan_simt(int T, int H) {
     p.tile_log2 = Absorbed<float>::LOG2;
     p.max_ctas = 304;
     p.extra = 0;
+    p.least_log2 = 0;
     return p;
 }
 
@@ -395,6 +406,7 @@ PagedPlan expanded_plan_simt(int T) {
     p.tile_log2 = Expanded<float>::LOG2;
     p.max_ctas = 304;
     p.extra = 0;
+    p.least_log2 = 0;
     return p;
 }
 

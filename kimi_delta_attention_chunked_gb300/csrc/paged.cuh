@@ -42,6 +42,7 @@ struct Shape {
     int blocks, page_log2, n_pages, window;
     int U, tile_log2;                              // tokens per unit, keys per tile
     int extra;                                     // places on the line before a unit's tiles
+    int least_log2;                                // a CTA that has a piece has 2^least_log2 places at least (but the only one)
 };
 
 // The same over packed keys: those of request n lie at rows cu_k[n] .. cu_k[n + 1] - 1 of [S, ...]
@@ -188,7 +189,7 @@ __device__ __forceinline__ Piece find_piece(const Sh& s, const int32_t* __restri
         total += t;
     }
     incl += before;
-    const int ctas = (int)min((unsigned long long)C, total);
+    const int ctas = (int)min((unsigned long long)C, total > 0 ? max(total >> s.least_log2, 1ull) : 0ull);
     if (c < ctas) {
         const unsigned long long begin = total * (unsigned)c / (unsigned)ctas;
         const unsigned long long excl = incl - mine;
@@ -500,6 +501,7 @@ inline int heads_per_unit(int group, int most) {
 // Partial-row geometry of an attention call: rows of a slot, most CTAs.
 struct PagedPlan {
     int Gv, U, rows, tile_log2, max_ctas, extra;
+    int least_log2 = 0;
 };
 bool paged_tc_supported(int d, kda_dtype dt);
 PagedPlan paged_plan_tc(int T, int Hq, int Hkv);
