@@ -2,8 +2,8 @@
 // cores (bf16), by pairs of CTAs.
 //
 // A cache row of 576 channels is the key of every head and its first 512 channels the
-// value.  A unit (paged.cuh) is up to 128 rows (a token and a query head each), 64 in either
-// CTA of a cluster of two.  Per tile of KEYS keys, with cta_group::2 products of M = 128:
+// value.  A unit (paged.cuh) is up to 128 rows (a token and a query head each), up to 64 in either
+// CTA of a cluster of two: half of the heads of the same tokens.  Per tile of KEYS keys, with cta_group::2 products of M = 128:
 //     S = Q K^T     (128 x KEYS over 576 channels, both operands in shared memory)
 //     P = 2^(scale log2(e) S - m)   (registers; bf16 to shared memory)
 //     O += P V      (128 x 512 over KEYS keys, two products of N = 256)
@@ -76,11 +76,10 @@ struct Cfg {
     static_assert(KEYS == 64, "the layout of P has one panel");
 };
 
-// How a unit's rows lie in the two CTAs.
+// A CTA's rows of a unit: `heads` heads (the second CTA has the ones behind the first's) of `tokens` tokens.  The
+// CTAs share the heads and not the tokens, so that a single token gives both of them the same work.
 struct Tiling {
-    int heads;                                         // heads of a row tile
-    int tokens;                                        // tokens of a row tile
-    int by_heads;                                      // the CTAs share a token's heads; else they share the tokens
+    int heads, tokens;
 };
 
 struct UnitSlot {
@@ -124,7 +123,8 @@ __device__ __forceinline__ void add_odd_values(float* o, int c0, const Unit& u, 
 
 template <int KEYS>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
-kda_latent_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
+kda_latent_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap qmap1,
+                               const __grid_constant__ CUtensorMap kmap,
                                const __nv_bfloat16* __restrict__ cache, const int32_t* __restrict__ table,
                                const int32_t* __restrict__ cu, const int32_t* __restrict__ seq_len, Shape s, Tiling tiling,
                                float scale_log2, __nv_bfloat16* __restrict__ o, float* __restrict__ lse, Partials parts,
@@ -162,8 +162,8 @@ kda_latent_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const _
         tl.abort = 0;
         for (int i = 0; i < 4; ++i) tl.odd_values[i] = 0;
     }
-    if (w == kCopyWarp && lane < 2) {
-        const CUtensorMap* m = lane == 0 ? &qmap : &kmap;
+    if (w == kCopyWarp && lane < 3) {
+        const CUtensorMap* m = lane == 0 ? &qmap : lane == 1 ? &qmap1 : &kmap;
         asm volatile("prefetch.tensormap [%0];" ::"l"(m) : "memory");
     }
     cluster_arrive();                                  // both CTAs' barriers will be there
@@ -256,19 +256,19 @@ kda_latent_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const _
         }
     } else if (w == kQueryWarp) {
         // ---------------- this CTA's rows of the queries
-        const int q_bytes = kPanels * tiling.heads * tiling.tokens * 128;
         const uint32_t q_bar = at_rank(&tl.q_full, 0);
         for (int k = 0;; ++k) {
             Unit u;
             if (!read_unit(k, u)) break;
-            const bool both = tiling.by_heads || u.ntok > tiling.tokens;      // the second CTA has rows too
+            const bool one = u.ntok == 1;              // its rows alone: a fourth and less of what the box of all tokens brings
+            const int bytes = kPanels * tiling.heads * (one ? 1 : tiling.tokens) * 128;
             if (k > 0 && !wait(&tl.q_empty, (k - 1) & 1)) break;
             __syncwarp();
-            if (lane == 0 && rank == 0) kda::mbar_arrive_expect_tx(&tl.q_full, (both ? 2 : 1) * q_bytes);
+            if (lane == 0 && rank == 0) kda::mbar_arrive_expect_tx(&tl.q_full, 2 * bytes);
             __syncwarp();
-            if ((rank == 0 || both) && lane < kPanels)
-                load_pair(kda::smem_u32(sm) + lane * kQPanel, &qmap, lane * 64, u.qh0 + (tiling.by_heads ? rank * tiling.heads : 0),
-                          u.tok0 + (tiling.by_heads ? 0 : rank * tiling.tokens), q_bar);
+            if (lane < kPanels)
+                load_pair(kda::smem_u32(sm) + lane * kQPanel, one ? &qmap1 : &qmap, lane * 64, u.qh0 + rank * tiling.heads, u.tok0,
+                          q_bar);
             ++n_q;
         }
     } else if (w == kSwapWarp) {
@@ -375,8 +375,7 @@ kda_latent_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const _
         // ---------------- softmax and output: row, half of the keys and of each product's channels
         const int row = tid & 63, half = tid >> 6;
         const uint32_t lane_off = (uint32_t)(w * 32) << 16;
-        const int tok_in = tiling.by_heads ? 0 : rank * tiling.tokens + row / tiling.heads;
-        const int head_in = tiling.by_heads ? rank * tiling.heads + row : row % tiling.heads;
+        const int tok_in = row / tiling.heads, head_in = rank * tiling.heads + row % tiling.heads;
         const bool in_tile = row < tiling.heads * tiling.tokens;
         const uint32_t p_bar = at_rank(&tl.p_full, 0);
         int g = 0, n_landed = 0, n_join = 0;
@@ -523,7 +522,7 @@ kda_latent_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const _
                 const bool whole = u.first && u.last;
                 const int which = u.first ? 1 : 0;
                 const size_t at = (size_t)(u.tok0 + tok_in) * s.Hq + u.qh0 + head_in;
-                const int prow = rank * tiling.heads * tiling.tokens + row;          // row of a partial slot
+                const int prow = tok_in * 2 * tiling.heads + head_in;                // row of a partial slot
                 const float inv = l == 0.f ? 0.f : 1.f / l;
                 const bool add = *(volatile int*)&tl.odd_values[k & 3] != 0 && valid;
 #pragma unroll 1
@@ -578,11 +577,10 @@ kda_latent_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const _
 
 // ---- host
 Tiling tiling_of(int H) {
-    const int groups = kda_host::latent_groups(H, kRows);
+    const int groups = kda_host::latent_groups(H, 2 * kRows);        // of a unit's heads each
     Tiling t;
-    t.heads = (H + groups - 1) / groups;
-    t.by_heads = groups > 1;
-    t.tokens = t.by_heads ? 1 : kRows / t.heads;
+    t.heads = ((H + groups - 1) / groups + 1) / 2;
+    t.tokens = kRows / t.heads;
     return t;
 }
 
@@ -607,8 +605,8 @@ namespace kda_host {
 PagedPlan latent_plan_tc(int T, int H) {
     const Tiling t = tiling_of(H);
     PagedPlan p;
-    p.Gv = t.by_heads ? 2 * t.heads : t.heads;         // heads of a unit
-    p.U = t.by_heads ? 1 : 2 * t.tokens;
+    p.Gv = 2 * t.heads;                                // heads of a unit
+    p.U = t.tokens;
     p.rows = paged_slot_rows(p.U, T, p.Gv);
     p.tile_log2 = Cfg<kKeys>::LOG2;
     p.max_ctas = 80;                                   // pairs
@@ -621,9 +619,10 @@ cudaError_t launch_latent_attention_tc(const LatentArgs& a) {
     const PagedArgs pa = latent_view(a);
     const Tiling t = tiling_of(a.H);
     if (!tensor_map_encoder()) return cudaErrorNotSupported;
-    CUtensorMap qm, km;
+    CUtensorMap qm, qm1, km;
     constexpr cuuint64_t row = kRow * 2;
     if (!make_map(&qm, a.q, a.H, a.T, row, (cuuint64_t)a.q_stride * 2, t.heads, t.tokens) ||
+        !make_map(&qm1, a.q, a.H, a.T, row, (cuuint64_t)a.q_stride * 2, t.heads, 1) ||
         !make_map(&km, a.cache, a.page_size, a.n_pages, row, row * a.page_size, std::min(a.page_size, Cfg<kKeys>::HALF), 1))
         return cudaErrorInvalidValue;
     auto kern = kda_latent_attention_tc_kernel<kKeys>;
@@ -634,7 +633,7 @@ cudaError_t launch_latent_attention_tc(const LatentArgs& a) {
     if (e != cudaSuccess) return e;
     const int pairs = std::min(p.max_ctas, sm_count() / 2);
     const cudaError_t err = launch_overlapped(
-        kern, 2 * pairs, kThreads, Cfg<kKeys>::SMEM, a.stream, 1, qm, km, static_cast<const __nv_bfloat16*>(a.cache),
+        kern, 2 * pairs, kThreads, Cfg<kKeys>::SMEM, a.stream, 1, qm, qm1, km, static_cast<const __nv_bfloat16*>(a.cache),
         a.block_table, a.cu_seqlens, a.seq_len, latent_shape(a, p), t, a.scale * kLog2e, static_cast<__nv_bfloat16*>(a.o), a.lse,
         paged_partials(pa, p), a.status);
     if (err != cudaSuccess) return err;

@@ -148,6 +148,8 @@ struct Piece {
     unsigned long long off;                        // begin - first place of request n
     unsigned long long len;                        // length of request n for one head
     int n, ctas;                                   // first request; CTAs that have a piece
+    int known;                                     // its lengths are in r
+    Req r;
 };
 
 // Finds the piece of CTA `c` of `C`.  Every thread of the block (NT of them)
@@ -159,14 +161,15 @@ __device__ __forceinline__ Piece find_piece(const Sh& s, const int32_t* __restri
                                             unsigned long long* red, Piece* shared) {
     constexpr int NW = NT / 32;
     const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
+    Req r{0, 0, 0, 0};
     for (int base = 0; base < s.n_req; base += NT) {
         const int n = base + tid;
-        Req r{0, 0, 0, 0};
+        r = Req{0, 0, 0, 0};
         if (n < s.n_req) r = load_req(s, cu, seq_len, n);
         const unsigned long long x = request_places(s, r);
         if (n < s.n_req) cost[n] = x;
     }
-    if (tid == 0) *shared = Piece{0, 0, 0, 0, 0, 0, 0};
+    if (tid == 0) *shared = Piece{};
     __syncthreads();
     // each thread takes `per` consecutive requests of the running sum
     const int per = (s.n_req + NT - 1) / NT, n0 = min(tid * per, s.n_req), n1 = min(n0 + per, s.n_req);
@@ -208,6 +211,8 @@ __device__ __forceinline__ Piece find_piece(const Sh& s, const int32_t* __restri
             shared->len = cost[n];
             shared->n = n;
             shared->ctas = ctas;
+            shared->known = s.n_req <= NT;             // a thread has one request, this one this
+            shared->r = r;
         }
     }
     __syncthreads();
@@ -246,14 +251,14 @@ struct Walker {
         ctas = p.ctas;
         n = p.n;
         if (at >= end) return;
-        r = load_req(s, cu, seq_len, n);
+        r = p.known ? p.r : load_req(s, cu, seq_len, n);
         first_unit(s, p.off, p.len);
     }
 
     // Head, unit and place that lie `off` places behind the start of request n, whose heads have `len` each.
     __device__ __forceinline__ void first_unit(const Shape& s, unsigned long long off, unsigned long long len) {
         units = n_units(s, r);
-        h = (int)(off / len);
+        h = s.Hv == 1 ? 0 : (int)(off / len);
         unsigned long long left = off - (unsigned long long)h * len;
         i = 0;
         in = (int)left;
