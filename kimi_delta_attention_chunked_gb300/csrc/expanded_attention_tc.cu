@@ -476,7 +476,7 @@ kda_expanded_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const
                     m = big;
                 } else {
                     // S complete means that this half's product before it is too, so O stands still
-                    const bool grow = (big - m) * scale_log2 > kGrow;
+                    const bool grow = valid && (big - m) * scale_log2 > kGrow;
                     if (__any_sync(0xffffffffu, grow)) {
                         const float f = grow ? ex2((m - big) * scale_log2) : 1.f;
                         const uint32_t tO = tmem + lane_off + kTmemO + h * 128;

@@ -437,7 +437,7 @@ kda_latent_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const _
                     if (tile == u.tb) {
                         m = big;
                     } else {
-                        const bool grow = (big - m) * scale_log2 > kGrow;
+                        const bool grow = valid && (big - m) * scale_log2 > kGrow;
                         if (__any_sync(0xffffffffu, grow)) {
                             if (!wait_before()) { ok = false; break; }
                             kda::tc_fence_after();
