@@ -25,12 +25,6 @@ __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.w
 __device__ __forceinline__ void cluster_leave() {
     asm volatile("barrier.cluster.arrive.relaxed;\n\tbarrier.cluster.wait;" ::: "memory");
 }
-// 32 bytes to a 32-byte boundary of global memory: a whole sector of each lane's row.
-__device__ __forceinline__ void store8(float* p, const float* y) {
-    asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "f"(y[0]), "f"(y[1]), "f"(y[2]), "f"(y[3]),
-                 "f"(y[4]), "f"(y[5]), "f"(y[6]), "f"(y[7])
-                 : "memory");
-}
 // Arrives on a barrier of either CTA.  What it has to order is in this SM: stores to shared memory
 // (made visible to the tensor cores by fence.proxy.async) and TMEM (by tcgen05.wait and fence); release at cluster
 // scope would also wait for this thread's stores to global memory, half a microsecond each time.

@@ -543,9 +543,9 @@ kda_expanded_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const
                                                 kda::pack_bf16x2(y[e + 4] * inv, y[e + 5] * inv),
                                                 kda::pack_bf16x2(y[e + 6] * inv, y[e + 7] * inv));
                 } else {
-                    float* dst = parts.sums(cluster, which) + (size_t)tok * kValue + c0;
+                    float4* dst = reinterpret_cast<float4*>(parts.sums4(cluster, which, tok, c0));
 #pragma unroll
-                    for (int e = 0; e < 32; e += 8) store8(dst + e, y + e);
+                    for (int e = 0; e < 32; e += 4) dst[e / 4 * parts.cap] = make_float4(y[e], y[e + 1], y[e + 2], y[e + 3]);
                 }
             };
             auto put_stats = [&](float r, float sum_l) {

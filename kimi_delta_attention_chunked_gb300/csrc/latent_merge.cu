@@ -2,10 +2,11 @@
 // with M the largest of the parts' references m_i,
 //     o = sum_i 2^(m_i - M) o_i / sum_i 2^(m_i - M) l_i,   lse = (M + log2 of the divisor) ln 2.
 //
-// The rows of a unit are shared out over the blocks of all CTAs that hold a part of it.  D / 4
-// threads take a row; units of few parts, which most are, several rows at once.  A part's weight is
-// formed by one lane of each warp; the sums are read beside the statistics.  Bound: latency
-// (description, then statistics and sums) and, with hundreds of rows in every slot, L2.
+// A slot's sums lie four channels wide, [D / 4][rows][4]: the threads of the attention kernels hold a row
+// each, so a warp's store and a warp's load here are whole lines (by rows, 128 of 512 channels took a pair of
+// CTAs 5,700 cycles to write).  A warp takes 16 channels of 32 rows, or, where there are more than
+// four parts, of 8 rows with four lanes to a row; the warps of all CTAs that hold a part of a unit share it out.  Bound: latency (description, then statistics and sums) and, with hundreds of rows in
+// every slot, L2.
 #include <algorithm>
 
 #include "latent.cuh"
@@ -15,7 +16,8 @@ namespace {
 using kda_paged::Partials;
 
 constexpr int kThreads = 128, kBlocks = 12;
-constexpr int kMostParts = 304;                        // CTAs or pairs of a call
+constexpr int kWide = 16;                              // channels of a warp's work
+constexpr int kBatch = 4;                              // parts read at once
 
 __device__ __forceinline__ float ex2(float x) {
     float y;
@@ -23,107 +25,135 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
+// Weighted sums of parts first, first + stride, ... of rows r (one a lane), 16 channels from 16 `wide` on.
+struct Sum {
+    float4 acc[kWide / 4];
+    float top, l;                                      // reference; sum of the weights
+    __device__ __forceinline__ void take(const Partials& parts, int c0, int n, int first, int stride, int r, int wide) {
+        auto stats = [&](int i) { return i < n ? parts.stats(c0 + i, i == 0 ? 1 : 0)[r] : make_float2(-INFINITY, 0.f); };
+        float4 v[kBatch][kWide / 4];
+        float2 st[kBatch];
+        auto load = [&](int i0) {
+#pragma unroll
+            for (int e = 0; e < kBatch; ++e) {
+                const int i = i0 + e * stride;
+                st[e] = stats(i);
+                if (i < n) {
+                    const float4* src =
+                        reinterpret_cast<const float4*>(parts.sums4(c0 + i, i == 0 ? 1 : 0, r, wide * kWide));
+#pragma unroll
+                    for (int x = 0; x < kWide / 4; ++x) v[e][x] = src[(size_t)x * parts.cap];
+                }
+            }
+        };
+        load(first);
+        top = -INFINITY;
+        l = 0.f;
+#pragma unroll
+        for (int e = 0; e < kBatch; ++e) top = fmaxf(top, st[e].x);
+        for (int i = first + kBatch * stride; i < n; i += stride) top = fmaxf(top, stats(i).x);
+        const float ref = top == -INFINITY ? 0.f : top;
+#pragma unroll
+        for (int x = 0; x < kWide / 4; ++x) acc[x] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+        for (int i0 = first;;) {
+#pragma unroll
+            for (int e = 0; e < kBatch; ++e) {
+                const float f = st[e].y == 0.f ? 0.f : ex2(st[e].x - ref);
+                l = fmaf(f, st[e].y, l);
+                if (f != 0.f) {                        // a part that saw no key does not enter
+#pragma unroll
+                    for (int x = 0; x < kWide / 4; ++x) add(acc[x], f, v[e][x]);
+                }
+            }
+            i0 += kBatch * stride;
+            if (i0 >= n) break;
+            load(i0);
+        }
+    }
+    static __device__ __forceinline__ void add(float4& a, float f, const float4& v) {
+        a.x = fmaf(f, v.x, a.x); a.y = fmaf(f, v.y, a.y); a.z = fmaf(f, v.z, a.z); a.w = fmaf(f, v.w, a.w);
+    }
+};
+
+__device__ __forceinline__ void store4(__nv_bfloat16* p, const float4& v, float f) {
+    *reinterpret_cast<uint2*>(p) = make_uint2(kda::pack_bf16x2(v.x * f, v.y * f), kda::pack_bf16x2(v.z * f, v.w * f));
+}
+__device__ __forceinline__ void store4(float* p, const float4& v, float f) {
+    *reinterpret_cast<float4*>(p) = make_float4(v.x * f, v.y * f, v.z * f, v.w * f);
+}
+
 // One unit: rows of q from u.x, heads from u.y, parts in slots of the CTAs c0, c0 + 1, ...
 template <typename T>
-struct Join {
+struct Unit {
     int4 u;
     int n, c0, rows, Gv, Hq;
     T* o;
     float* lse;
 };
 
-// Rows first, first + step, ... in groups of R, whose parts are read PARTS at a time.  ALL: PARTS are all that a unit has.
-template <int D, int R, int PARTS, bool ALL, typename T>
-__device__ __forceinline__ void join_rows(const Partials& parts, const Join<T>& j, int first, int step, float* w) {
-    constexpr int TPR = D / 4;
-    const int x = threadIdx.x % TPR, lane = threadIdx.x & 31;
-    auto sums = [&](int r, int i) {
-        return i < j.n ? reinterpret_cast<const float4*>(parts.sums(j.c0 + i, i == 0 ? 1 : 0) + (size_t)r * D)[x]
-                       : make_float4(0.f, 0.f, 0.f, 0.f);
-    };
-    auto stats = [&](int r, int i) {
-        return i < j.n ? parts.stats(j.c0 + i, i == 0 ? 1 : 0)[r] : make_float2(-INFINITY, 0.f);
-    };
-    auto weight = [](const float2& st, float ref) { return st.y == 0.f ? 0.f : ex2(st.x - ref); };    // 0: the part saw no key
+// A warp's share of a unit: 32 / SHARE rows at a time, each row's parts shared by SHARE lanes.
+template <int D, int SHARE, typename T>
+__device__ __forceinline__ void join(const Partials& parts, const Unit<T>& j, int first, int step) {
+    constexpr int ROWS = 32 / SHARE;
+    const int lane = threadIdx.x & 31, blocks = (j.rows + ROWS - 1) / ROWS, items = blocks * (D / kWide);
 #pragma unroll 1
-    for (int r0 = first; r0 < j.rows; r0 += R * step) {
-        float4 v[R][PARTS];
-        float2 st[R];
-        int r[R];
+    for (int item = first; item < items; item += step) {
+        const int wide = item / blocks, row = (item - wide * blocks) * ROWS + lane % ROWS, r = min(row, j.rows - 1);
+        Sum sum;
+        sum.take(parts, j.c0, j.n, lane / ROWS, SHARE, r, wide);
+        float top = sum.top, l = sum.l;
+        if constexpr (SHARE > 1) {
 #pragma unroll
-        for (int a = 0; a < R; ++a) {
-            r[a] = min(r0 + a * step, j.rows - 1);
-            st[a] = stats(r[a], lane);
+            for (int d = ROWS; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+            const float f = l == 0.f ? 0.f : ex2(sum.top - top);
+            l *= f;
 #pragma unroll
-            for (int e = 0; e < PARTS; ++e) v[a][e] = sums(r[a], e);
-        }
+            for (int x = 0; x < kWide / 4; ++x) {
+                float* y = &sum.acc[x].x;
 #pragma unroll
-        for (int a = 0; a < R; ++a) {
-            float top = st[a].x;
-            if (!ALL)
-                for (int i = lane + 32; i < j.n; i += 32) top = fmaxf(top, stats(r[a], i).x);
+                for (int e = 0; e < 4; ++e) {
+                    y[e] = f == 0.f ? 0.f : y[e] * f;
 #pragma unroll
-            for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-            const float ref = top == -INFINITY ? 0.f : top, f = weight(st[a], ref);
-            float l = f * st[a].y;
-            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-            auto add = [&](float g, const float4& y) {
-                if (g != 0.f) {                        // a part that saw no key does not enter
-                    acc.x = fmaf(g, y.x, acc.x); acc.y = fmaf(g, y.y, acc.y);
-                    acc.z = fmaf(g, y.z, acc.z); acc.w = fmaf(g, y.w, acc.w);
-                }
-            };
-            if constexpr (ALL) {
-#pragma unroll
-                for (int e = 0; e < PARTS; ++e) add(__shfl_sync(0xffffffffu, f, e), v[a][e]);
-            } else {
-                __syncwarp();                          // the row before has been read
-                w[lane] = f;
-                for (int i = lane + 32; i < j.n; i += 32) {
-                    const float2 more = stats(r[a], i);
-                    w[i] = weight(more, ref);
-                    l = fmaf(w[i], more.y, l);
-                }
-                __syncwarp();
-#pragma unroll 1
-                for (int i0 = 0; i0 < j.n; i0 += PARTS) {
-#pragma unroll
-                    for (int e = 0; e < PARTS; ++e) add(i0 + e < j.n ? w[i0 + e] : 0.f, v[a][e]);
-#pragma unroll
-                    for (int e = 0; e < PARTS; ++e) v[a][e] = sums(r[a], i0 + PARTS + e);
+                    for (int d = ROWS; d < 32; d <<= 1) y[e] += __shfl_xor_sync(0xffffffffu, y[e], d);
                 }
             }
 #pragma unroll
-            for (int d = 16; d > 0; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
-            const int head = j.u.y + r[a] % j.Gv;
-            if (r0 + a * step >= j.rows || head >= j.Hq) continue;            // a last group of fewer heads
-            const float inv = l == 0.f ? 0.f : 1.f / l;
-            const size_t at = (size_t)(j.u.x + r[a] / j.Gv) * j.Hq + head;
-            T* dst = j.o + at * D + 4 * x;
-            if constexpr (sizeof(T) == 2)
-                *reinterpret_cast<uint2*>(dst) =
-                    make_uint2(kda::pack_bf16x2(acc.x * inv, acc.y * inv), kda::pack_bf16x2(acc.z * inv, acc.w * inv));
-            else
-                *reinterpret_cast<float4*>(dst) = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
-            if (j.lse && x == 0) j.lse[at] = l == 0.f ? -INFINITY : (top + log2f(l)) * 0.69314718055994531f;
+            for (int d = ROWS; d < 32; d <<= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
         }
+        const int head = j.u.y + r % j.Gv;
+        if (row >= j.rows || head >= j.Hq) continue;   // a last group may have fewer heads
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        const size_t at = (size_t)(j.u.x + r / j.Gv) * j.Hq + head;
+        T* dst = j.o + at * D + wide * kWide;
+        if constexpr (SHARE > 1) {                     // a lane of the row stores four channels
+            static_assert(SHARE == kWide / 4, "channels");
+            const int x = lane / ROWS;
+            float4 v = sum.acc[0];
+#pragma unroll
+            for (int e = 1; e < kWide / 4; ++e)
+                if (x == e) v = sum.acc[e];
+            store4(dst + 4 * x, v, inv);
+        } else {
+#pragma unroll
+            for (int x = 0; x < kWide / 4; ++x) store4(dst + 4 * x, sum.acc[x], inv);
+        }
+        if (j.lse && wide == 0 && lane < ROWS) j.lse[at] = l == 0.f ? -INFINITY : (top + log2f(l)) * 0.69314718055994531f;
     }
 }
 
 template <int D, typename T>
-__global__ void __launch_bounds__(kThreads, 8)
+__global__ void __launch_bounds__(kThreads, 4)
 kda_latent_merge_kernel(Partials parts, int Gv, int Hq, T* __restrict__ o, float* __restrict__ lse) {
-    constexpr int ROWS = kThreads / (D / 4);           // rows of a pass
-    __shared__ float s_w[kThreads / 32][kMostParts];   // weights of a row's parts: every warp forms its row's itself
+    constexpr int WARPS = kThreads / 32;
     kda_paged::wait_for_stream();
     const int c = blockIdx.x;
     const int4 u = parts.meta[2 * c + 1 - blockIdx.z]; // z = 0: the unit that begins here, 1: the one that goes on here
-    const Join<T> j{u, u.w & 0xffff, u.w >> 16, u.z * Gv, Gv, Hq, o, lse};
+    const Unit<T> j{u, u.w & 0xffff, u.w >> 16, u.z * Gv, Gv, Hq, o, lse};
     if (j.n == 0) return;
-    const int first = ((c - j.c0) * kBlocks + blockIdx.y) * ROWS + (int)threadIdx.x / (D / 4), step = j.n * kBlocks * ROWS;
-    if (j.n <= 2) join_rows<D, 2, 2, true>(parts, j, first, step, nullptr);
-    else if (j.n <= 4) join_rows<D, 2, 4, true>(parts, j, first, step, nullptr);
-    else join_rows<D, 1, 8, false>(parts, j, first, step, s_w[threadIdx.x >> 5]);
+    const int first = ((c - j.c0) * kBlocks + blockIdx.y) * WARPS + (int)(threadIdx.x >> 5), step = j.n * kBlocks * WARPS;
+    if (j.n <= kBatch) join<D, 1>(parts, j, first, step);
+    else join<D, 4>(parts, j, first, step);
 }
 
 template <int D, typename T>
@@ -150,7 +180,6 @@ cudaError_t merge_of(const kda_host::PagedArgs& a, const kda_host::PagedPlan& p,
 namespace kda_host {
 
 cudaError_t launch_latent_merge(const PagedArgs& a, const PagedPlan& p, int ctas) {
-    if (ctas > kMostParts) return cudaErrorInvalidValue;
     return a.d == kda_latent::kLatent ? merge_of<kda_latent::kLatent>(a, p, ctas) : merge_of<kda_latent::kValue>(a, p, ctas);
 }
 

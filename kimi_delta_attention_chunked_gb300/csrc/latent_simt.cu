@@ -324,7 +324,7 @@ kda_latent_simt_kernel(const T* __restrict__ q, Src src, const int32_t* __restri
                         make_float4(acc[a][0] * inv, acc[a][1] * inv, acc[a][2] * inv, acc[a][3] * inv);
                 if (lse && cg == 0) lse[at] = rl == 0.f ? -INFINITY : (rm + log2f(rl)) * kLn2;
             } else {
-                *reinterpret_cast<float4*>(parts.sums(blockIdx.x, which) + (size_t)r * DV + 4 * cg) =
+                *reinterpret_cast<float4*>(parts.sums4(blockIdx.x, which, r, 4 * cg)) =
                     make_float4(acc[a][0], acc[a][1], acc[a][2], acc[a][3]);
                 if (cg == 0) parts.stats(blockIdx.x, which)[r] = make_float2(rm, rl);
             }

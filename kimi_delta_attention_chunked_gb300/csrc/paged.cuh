@@ -388,6 +388,10 @@ struct Partials {
         return ((size_t)c * 2 + which) * (size_t)cap * (d + 2);
     }
     __device__ __forceinline__ float* sums(int c, int which) const { return rows + slot(c, which); }
+    // Latent attention's slots hold their sums four channels wide, [d / 4][cap][4].
+    __device__ __forceinline__ float* sums4(int c, int which, int row, int channel) const {
+        return rows + slot(c, which) + ((size_t)(channel >> 2) * cap + row) * 4;
+    }
     __device__ __forceinline__ float2* stats(int c, int which) const {
         return reinterpret_cast<float2*>(rows + slot(c, which) + (size_t)cap * d);
     }
