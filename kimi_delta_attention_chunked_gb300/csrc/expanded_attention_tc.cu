@@ -666,7 +666,9 @@ PagedPlan expanded_plan_tc(int T) {
     p.rows = paged_slot_rows(p.U, T, 1);
     p.tile_log2 = kKeysLog2;
     p.max_ctas = 80;                                   // pairs
-    p.extra = 3;
+    p.half_unit = kTileTokens;
+    p.extra = 5;
+    p.extra_two = 12;
     return p;
 }
 

@@ -610,7 +610,7 @@ PagedPlan latent_plan_tc(int T, int H) {
     p.rows = paged_slot_rows(p.U, T, p.Gv);
     p.tile_log2 = Cfg<kKeys>::LOG2;
     p.max_ctas = 80;                                   // pairs
-    p.extra = 4;
+    p.extra = 5;
     return p;
 }
 

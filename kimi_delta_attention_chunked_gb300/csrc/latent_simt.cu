@@ -394,7 +394,6 @@ PagedPlan latent_plan_simt(int T, int H) {
     p.tile_log2 = Absorbed<float>::LOG2;
     p.max_ctas = 304;
     p.extra = 0;
-    p.least_log2 = 0;
     return p;
 }
 
@@ -406,7 +405,6 @@ PagedPlan expanded_plan_simt(int T) {
     p.tile_log2 = Expanded<float>::LOG2;
     p.max_ctas = 304;
     p.extra = 0;
-    p.least_log2 = 0;
     return p;
 }
 
@@ -454,6 +452,8 @@ kda_paged::PackedShape expanded_shape(const ExpandedArgs& a, const PagedPlan& p)
     static_cast<kda_paged::Shape&>(s) = paged_shape(expanded_view(a), p);
     s.S = a.S;
     s.causal = a.causal;
+    s.half_unit = p.half_unit > 0 ? p.half_unit : p.U;
+    s.extra_two = p.extra_two;
     return s;
 }
 

@@ -42,7 +42,6 @@ struct Shape {
     int blocks, page_log2, n_pages, window;
     int U, tile_log2;                              // tokens per unit, keys per tile
     int extra;                                     // places on the line before a unit's tiles
-    int least_log2;                                // a CTA that has a piece has 2^least_log2 places at least (but the only one)
 };
 
 // The same over packed keys: those of request n lie at rows cu_k[n] .. cu_k[n + 1] - 1 of [S, ...]
@@ -51,6 +50,9 @@ struct Shape {
 struct PackedShape : Shape {
     int S;                                         // rows of the keys
     int causal;                                    // 0: every row sees all keys of its request
+    // Units of more than half_unit tokens take two steps a tile, and so two places, with extra_two ahead of them
+    // (half_unit = U: there are none).
+    int half_unit, extra_two;
 };
 
 // One request's lengths, inside the buffers whatever the device arrays hold.
@@ -95,6 +97,18 @@ __host__ __device__ __forceinline__ int first_key(int pos, int window) {
 
 __device__ __forceinline__ int n_units(const Shape& s, const Req& r) { return (r.len + s.U - 1) / s.U; }
 
+// log2 of the places of a tile of unit i, and the places before its tiles.
+__device__ __forceinline__ int unit_shift(const Shape&, const Req&, int) { return 0; }
+__device__ __forceinline__ int unit_shift(const PackedShape& s, const Req& r, int i) { return r.len - i * s.U > s.half_unit ? 1 : 0; }
+// CTAs that may have a piece.  Where a tile may have two places, a piece has two at least, so that one that lies
+// among a unit's tiles holds the first place of one of them.
+__device__ __forceinline__ unsigned long long most_pieces(const Shape&, unsigned long long total) { return total; }
+__device__ __forceinline__ unsigned long long most_pieces(const PackedShape&, unsigned long long total) {
+    return total > 1 ? total >> 1 : total;
+}
+__device__ __forceinline__ int unit_extra(const Shape& s, int) { return s.extra; }
+__device__ __forceinline__ int unit_extra(const PackedShape& s, int shift) { return shift ? s.extra_two : s.extra; }
+
 // Tiles [tb, te) of unit i: those that hold a key some row sees, and one tile
 // where no row sees any (its rows are written as empty).
 __device__ __forceinline__ void unit_span(const Shape& s, const Req& r, int i, int& tb, int& te) {
@@ -106,18 +120,24 @@ __device__ __forceinline__ void unit_span(const Shape& s, const Req& r, int i, i
     if (te <= tb) te = tb + 1;
 }
 
+// Places of unit i.
+template <class Sh>
+__device__ __forceinline__ unsigned unit_places(const Sh& s, const Req& r, int i) {
+    int tb, te;
+    unit_span(s, r, i, tb, te);
+    const int shift = unit_shift(s, r, i);
+    return (unsigned)(te - tb << shift) + (unsigned)unit_extra(s, shift);
+}
+
 // Length of all units of a request, for one head.  A thread counts a request of
 // few units by itself; the lanes of a warp share out one of many.
-__device__ __forceinline__ unsigned long long request_places(const Shape& s, const Req& r) {
+template <class Sh>
+__device__ __forceinline__ unsigned long long request_places(const Sh& s, const Req& r) {
     constexpr int kAlone = 8;
     const int units = n_units(s, r);
     unsigned long long cost = 0;
     if (units <= kAlone) {
-        for (int i = 0; i < units; ++i) {
-            int tb, te;
-            unit_span(s, r, i, tb, te);
-            cost += te - tb + s.extra;
-        }
+        for (int i = 0; i < units; ++i) cost += unit_places(s, r, i);
     }
     unsigned many = __ballot_sync(0xffffffffu, units > kAlone);
     while (many) {
@@ -130,11 +150,7 @@ __device__ __forceinline__ unsigned long long request_places(const Shape& s, con
         q.kend = __shfl_sync(0xffffffffu, r.kend, src);
         const int total = n_units(s, q);
         unsigned long long part = 0;
-        for (int i = threadIdx.x & 31; i < total; i += 32) {
-            int tb, te;
-            unit_span(s, q, i, tb, te);
-            part += te - tb + s.extra;
-        }
+        for (int i = threadIdx.x & 31; i < total; i += 32) part += unit_places(s, q, i);
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) part += __shfl_xor_sync(0xffffffffu, part, o);
         if ((int)(threadIdx.x & 31) == src) cost = part;
@@ -192,7 +208,7 @@ __device__ __forceinline__ Piece find_piece(const Sh& s, const int32_t* __restri
         total += t;
     }
     incl += before;
-    const int ctas = (int)min((unsigned long long)C, total > 0 ? max(total >> s.least_log2, 1ull) : 0ull);
+    const int ctas = (int)min((unsigned long long)C, most_pieces(s, total));
     if (c < ctas) {
         const unsigned long long begin = total * (unsigned)c / (unsigned)ctas;
         const unsigned long long excl = incl - mine;
@@ -237,7 +253,8 @@ struct Walker {
     unsigned long long at, end, total;
     int ctas, c;
     int n, h, i, in;                               // next unit; places of it that lie before the piece
-    int whole_tiles;                               // of the unit whose part was handed out last, all parts together
+    int ahead, last_place;                         // of the unit whose part was handed out last: places before its
+                                                   // tiles, place of its last tile
     Req r;
     int units;
 
@@ -256,7 +273,8 @@ struct Walker {
     }
 
     // Head, unit and place that lie `off` places behind the start of request n, whose heads have `len` each.
-    __device__ __forceinline__ void first_unit(const Shape& s, unsigned long long off, unsigned long long len) {
+    template <class Sh>
+    __device__ __forceinline__ void first_unit(const Sh& s, unsigned long long off, unsigned long long len) {
         units = n_units(s, r);
         h = s.Hv == 1 ? 0 : (int)(off / len);
         unsigned long long left = off - (unsigned long long)h * len;
@@ -267,11 +285,7 @@ struct Walker {
 #pragma unroll 1
         for (int base = 0; base < units; base += 32) {
             unsigned x = 0;
-            if (base + lane < units) {
-                int tb, te;
-                unit_span(s, r, base + lane, tb, te);
-                x = te - tb + s.extra;
-            }
+            if (base + lane < units) x = unit_places(s, r, base + lane);
             unsigned incl = x;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -315,10 +329,14 @@ struct Walker {
             }
             int tb, te;
             unit_span(s, r, i, tb, te);
-            whole_tiles = te - tb;
-            const int len = s.extra + whole_tiles;
+            const int shift = unit_shift(s, r, i);
+            ahead = unit_extra(s, shift);
+            last_place = ahead + (te - tb - 1 << shift);
+            const int len = ahead + (te - tb << shift);
             const int take = (int)min((unsigned long long)(len - in), end - at);
-            const int t0 = max(in - s.extra, 0), t1 = max(in + take - s.extra, 0);    // tiles of this part
+            // tiles of this part: those whose first place is in it
+            const int t0 = max(in - ahead, 0) + (1 << shift) - 1 >> shift;
+            const int t1 = max(in + take - ahead, 0) + (1 << shift) - 1 >> shift;
             from = at - (unsigned)in;
             u.n = n;
             u.kvh = h / s.sub;
@@ -339,8 +357,7 @@ struct Walker {
         return false;
     }
 
-    // CTA c begins at total * c / ctas, so the last one that has a place below the unit's end `fin` is
-    // ceil(fin * ctas / total) - 1.  Where a unit that goes on here begins is asked for if it has more than `spread` rows.
+    // CTA c begins at total * c / ctas, so the one that has place x is ceil((x + 1) * ctas / total) - 1.  Where a unit that goes on here begins is asked for if it has more than `spread` rows.
     template <class Sh>
     __device__ __forceinline__ void share(const Sh& s, Unit& u, unsigned long long from, int spread = kSpreadRows) const {
         u.start = c;
@@ -348,10 +365,10 @@ struct Walker {
         if (!u.first) {
             u.start = -1;
             if (u.ntok * s.Gv > spread)
-                u.start = (int)(((from + (unsigned)s.extra + 1) * (unsigned)ctas + total - 1) / total) - 1;
+                u.start = (int)(((from + (unsigned)ahead + 1) * (unsigned)ctas + total - 1) / total) - 1;
         }
         if (!u.last && u.start >= 0) {
-            const unsigned long long fin = from + (unsigned)(s.extra + whole_tiles);
+            const unsigned long long fin = from + (unsigned)last_place + 1;
             u.parts = (int)((fin * (unsigned)ctas + total - 1) / total) - u.start;
         } else if (u.start >= 0) {
             u.parts = c + 1 - u.start;
@@ -510,7 +527,7 @@ inline int heads_per_unit(int group, int most) {
 // Partial-row geometry of an attention call: rows of a slot, most CTAs.
 struct PagedPlan {
     int Gv, U, rows, tile_log2, max_ctas, extra;
-    int least_log2 = 0;
+    int half_unit = 0, extra_two = 0;                  // of packed keys (PackedShape); 0: every unit takes one step a tile
 };
 bool paged_tc_supported(int d, kda_dtype dt);
 PagedPlan paged_plan_tc(int T, int Hq, int Hkv);

@@ -478,7 +478,6 @@ kda_paged::Shape paged_shape(const PagedArgs& a, const PagedPlan& p) {
     s.U = p.U;
     s.tile_log2 = p.tile_log2;
     s.extra = p.extra;
-    s.least_log2 = p.least_log2;
     return s;
 }
 
