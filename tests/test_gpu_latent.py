@@ -554,3 +554,124 @@ def test_forms_agree(dt):
     ds = mag * (3 * half + 580 * 2.0 ** -24)
     assert float((lse[tail].double() - joint).abs().max()) < 2 * ds
     assert float((absorbed[tail] - expanded).abs().max()) < (4 * ds + 4 * half) * float(v.abs().max())
+
+
+# ------------------------------------------------------------------ chance sizes, long offsets, order of calls
+@pytest.mark.parametrize("seed", range(16))
+def test_absorbed_chance(seed):
+    """Lengths, heads and pages by chance: units of every kind, cut wherever the division puts its borders."""
+    import random
+    rng = random.Random(seed)
+    dt = rng.choice([BF16, BF16, BF16, FP32])
+    H, page, n = rng.choice([1, 2, 3, 7, 16, 33, 48, 64, 100, 128, 129, 200]), rng.choice([16, 32, 64, 128, 256]), rng.randint(1, 40)
+    lens = [(rng.choice([0, 1, rng.randint(0, 900)]), rng.choice([0, 1, 1, 1, 2, rng.randint(0, 12)])) for _ in range(n)]
+    if sum(m for _, m in lens) == 0:
+        lens.append((5, 1))
+    check_absorbed(*absorbed_case(lens, H, page, dt, seed=seed))
+
+
+@pytest.mark.parametrize("seed", range(16))
+def test_expanded_chance(seed):
+    import random
+    rng = random.Random(100 + seed)
+    dt, H, n = rng.choice([BF16, BF16, BF16, FP32]), rng.choice([1, 1, 2, 3, 5]), rng.randint(1, 12)
+    lens = [(rng.choice([0, 1, 255, 256, 257, 512, 513, rng.randint(0, 700)]), rng.choice([0, 1, rng.randint(0, 300), rng.randint(0, 900)]))
+            for _ in range(n)]
+    if sum(m for m, _ in lens) == 0:
+        lens.append((5, 1))
+    check_expanded(expanded_case(lens, H, dt, seed=seed), causal=rng.random() < 0.6)
+
+
+@pytest.mark.parametrize("tokens", [1, 257, 513])
+@pytest.mark.parametrize("keys", [1, 2, 129, 300])
+def test_expanded_few_places(tokens, keys):
+    """Fewer tiles than CTAs, with row tiles that take one place and two."""
+    for n in (1, 3):
+        check_expanded(expanded_case([(tokens, keys)] * n, 1, BF16, seed=tokens + keys), causal=False)
+
+
+@pytest.mark.parametrize("dt", DTYPES)
+def test_offsets_past_32_bits(dt):
+    """A cache of more than 2^32 bytes and 2^31 elements with the pages of a request at its end."""
+    page, n_pages = 256, 16000                          # 2.36e9 channels
+    gen = torch.Generator().manual_seed(0)
+    small = rnd(gen, 3, page, 576, dt=dt)
+    cache = torch.zeros(n_pages, page, 576, dtype=dt, device="cuda")
+    q = rnd(gen, 2, 8, 576, dt=dt)
+    table, cu, seq = torch.tensor([[2, 0, 1]], dtype=torch.int32), torch.tensor([0, 2], dtype=torch.int32), torch.tensor([600], dtype=torch.int32)
+    ref, lref, bo, bl = absorbed_ref(q, small, table, cu, seq, SCALE)
+    slot = torch.arange(3 * page, device="cuda") + (n_pages - 3) * page
+    rows = small.reshape(-1, 576).cuda()
+    kda.kda_latent_append(rows[:, :512], rows[:, 512:], cache, slot)
+    assert torch.equal(cache[-3:].cpu(), small) and not cache[:-3].any()
+    o, lse = run_absorbed(q, cache, table + (n_pages - 3), cu, seq)
+    assert_close(o, ref, bo, "o")
+    assert_close(lse, lref, bl, "lse")
+
+
+def test_expanded_strides_past_32_bits():
+    """Tokens of the keys 2^24 elements apart: their offsets pass 2^31."""
+    case = expanded_case([(40, 150)], 2, BF16)
+    ref, lref, bo, bl = expanded_ref(*case, SCALE, True)
+    q, kn, kr, v, cu, cu_k = on_gpu(case)
+    far = torch.empty(150 * (1 << 24), dtype=BF16, device="cuda")
+    view = far.as_strided((150, 2, 256), (1 << 24, 256, 1))
+    view[..., :128], view[..., 128:] = kn, v
+    o, lse = kda.kda_expanded_attention(q, view[..., :128], kr, view[..., 128:], cu, cu_k, want_lse=True)
+    assert_close(o, ref, bo, "o")
+    assert_close(lse, lref, bl, "lse")
+
+
+def test_rotary_strides_past_32_bits():
+    gen = torch.Generator().manual_seed(1)
+    x, pos = rnd(gen, 200, 2, 64, dt=BF16), torch.arange(200, dtype=torch.int32)
+    freq, _ = kda.rotary_frequencies(64, device="cpu")
+    ref, bound = turned(x, pos, freq, 1.0, False)
+    far = torch.empty(200 * (1 << 24), dtype=BF16, device="cuda").as_strided((200, 2, 64), (1 << 24, 64, 1))
+    far.copy_(x.cuda())
+    assert_close(kda.kda_rotary(far, pos.cuda(), freq.cuda(), out=far), ref, bound, "rotary")
+
+
+def test_calls_in_a_row_share_a_workspace():
+    """Calls of both forms one behind the other on one stream, with one workspace and other inputs each time."""
+    size = max(kda.kda_latent_attention_workspace_size(4, 32, BF16), kda.kda_expanded_attention_workspace_size(60, 2, BF16))
+    ws = torch.empty(size, dtype=torch.uint8, device="cuda")
+    a = [[x.cuda() for x in absorbed_case([(300 * i, 2), (50, 1)], 32, 32, BF16, seed=i)] for i in range(4)]
+    e = [on_gpu(expanded_case([(30, 400 * i), (20, 20)], 2, BF16, seed=i)) for i in range(4)]
+    want_a, want_e = [kda.kda_latent_attention(*c, SCALE) for c in a], [kda.kda_expanded_attention(*c) for c in e]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        got = [(kda.kda_latent_attention(*a[i], SCALE, workspace=ws), kda.kda_expanded_attention(*e[i], workspace=ws)) for i in range(4)]
+        torch.cuda.synchronize()
+        for i in range(4):
+            assert torch.equal(got[i][0], want_a[i]) and torch.equal(got[i][1], want_e[i])
+
+
+def test_other_stream():
+    """A call on another stream than the current one; what it makes is that stream's memory."""
+    gen = torch.Generator().manual_seed(2)
+    x, pos = rnd(gen, 500, 4, 64, dt=BF16).cuda(), torch.arange(500, dtype=torch.int32, device="cuda")
+    freq, _ = kda.rotary_frequencies(64)
+    case = on_gpu(expanded_case([(200, 300)], 4, BF16))
+    want, want_o = kda.kda_rotary(x, pos, freq), kda.kda_expanded_attention(*case)
+    cache, none = torch.zeros(40, 16, 576, dtype=BF16, device="cuda"), torch.zeros(500, 512, dtype=BF16, device="cuda")
+    at = torch.arange(500, device="cuda")
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(10):
+        got, got_o = kda.kda_rotary(x, pos, freq, stream=s), kda.kda_expanded_attention(*case, stream=s)
+        kda.kda_latent_append(none, x[:, 0], cache, at, pos, freq, stream=s)
+        torch.cuda.current_stream().wait_stream(s)
+        assert torch.equal(got, want) and torch.equal(got_o, want_o)
+        assert torch.equal(cache.reshape(-1, 576)[:500, 512:], want[:, 0])
+        s.wait_stream(torch.cuda.current_stream())
+
+
+@pytest.mark.parametrize("dt", DTYPES)
+def test_append_slot_named_twice(dt):
+    """Each piece of the slot's row is one of the two rows'."""
+    rows = torch.arange(1, 3, dtype=torch.float32)[:, None].expand(2, 576).to(dt).cuda()
+    cache = torch.zeros(1, 16, 576, dtype=dt, device="cuda")
+    kda.kda_latent_append(rows[:, :512], rows[:, 512:], cache, torch.tensor([5, 5], device="cuda"))
+    got = cache[0, 5].float()
+    assert bool(((got == 1) | (got == 2)).all()) and not cache[0, :5].any() and not cache[0, 6:].any()
