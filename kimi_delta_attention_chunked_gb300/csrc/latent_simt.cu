@@ -9,7 +9,7 @@
 //
 // This path is for fp32, whose accuracy the tensor cores' 16-bit operands do not reach, and
 // for bf16 rows that TMA cannot fetch.  A tile of 32 keys lies in shared memory as fp32; the
-// threads form 4 x 2 scores each (over a part of the channels: the parts are added up in the
+// threads form 4 x 4 scores each (over a part of the channels: the parts are added up in the
 // softmax step), then DV / 4 column groups of 4 with ROWS / RPT row groups of RPT rows each.
 #include <algorithm>
 #include <type_traits>
@@ -76,10 +76,10 @@ struct Expanded {
 template <class Src>
 struct Smem {
     static constexpr int kTile = 1 << Src::LOG2;       // keys of a tile
-    float q[Src::ROWS][Src::DK];
+    float q[Src::ROWS][Src::DK + 4];                   // rows of q and k 16 bytes on in the banks from one to the next
     float k[kTile][Src::DK + 4];
     float v[Src::kShared ? 1 : kTile][Src::DV];
-    static constexpr int SPLIT = Src::THREADS / (Src::ROWS / 4 * (kTile / 2));    // parts of the channels
+    static constexpr int SPLIT = Src::THREADS / (Src::ROWS / 4 * (kTile / 4));    // parts of the channels
     float part[SPLIT][Src::ROWS][kTile + 1];
     float p[kTile][Src::ROWS];                         // weights; -1 where the row does not see the key
     float scale[Src::ROWS];                            // factor of the earlier sums
@@ -96,7 +96,7 @@ __device__ __forceinline__ void load4(const T* p, float* y) {
 template <class Src, typename T, int VEC>
 __global__ void __launch_bounds__(Src::THREADS, Src::BLOCKS)
 kda_latent_simt_kernel(const T* __restrict__ q, Src src, const int32_t* __restrict__ cu,
-                       const int32_t* __restrict__ lengths, long long q_stride, typename Src::Sh s, float scale_log2,
+                       const int32_t* __restrict__ lengths, long long q_stride, bool q_wide, typename Src::Sh s, float scale_log2,
                        T* __restrict__ o, float* __restrict__ lse, Partials parts) {
     constexpr int DK = Src::DK, DV = Src::DV, ROWS = Src::ROWS, kTileLog2 = Src::LOG2, kTile = 1 << kTileLog2;
     constexpr int kThreads = Src::THREADS;
@@ -135,14 +135,34 @@ kda_latent_simt_kernel(const T* __restrict__ q, Src src, const int32_t* __restri
         if (!s_more) break;
         const Unit u = s_unit;
         const int rows = u.ntok * s.Gv;
-#pragma unroll 12
-        for (int e = tid; e < ROWS * DK; e += kThreads) {
-            const int r = e / DK, c = e % DK, head = u.qh0 + r % s.Gv;
-            float x = 0.f;
-            if (r < rows && head < s.Hq)
-                x = kda::io<T>::ld(q + (long long)(u.tok0 + r / s.Gv) * q_stride + (long long)head * DK + c);
-            sm.q[r][c] = x * scale_log2;
-        }
+        // queries, in 16-byte pieces where their rows start on such boundaries
+        auto load_q = [&](auto vec) {
+            constexpr int V = decltype(vec)::value, CH = DK / V, N = (ROWS * CH + kThreads - 1) / kThreads;
+            struct alignas(V * sizeof(T)) Chunk { T v[V]; };
+            constexpr int B = N < 6 ? N : 6;           // loads in flight
+#pragma unroll 1
+            for (int e0 = tid; e0 < ROWS * CH; e0 += B * kThreads) {
+                Chunk x[B];
+#pragma unroll
+                for (int i = 0; i < B; ++i) {
+                    const int e = e0 + i * kThreads, r = e / CH, c = e % CH * V, tok = (int)((unsigned)r / (unsigned)s.Gv);
+                    const int head = u.qh0 + r - tok * s.Gv;
+#pragma unroll
+                    for (int y = 0; y < V; ++y) kda::io<T>::st(&x[i].v[y], 0.f);
+                    if (r < rows && head < s.Hq)       // rows end before ROWS
+                        x[i] = *reinterpret_cast<const Chunk*>(q + (u.tok0 + tok) * q_stride + (long long)head * DK + c);
+                }
+#pragma unroll
+                for (int i = 0; i < B; ++i) {
+                    const int e = e0 + i * kThreads;
+                    if (e >= ROWS * CH) continue;
+#pragma unroll
+                    for (int y = 0; y < V; ++y) sm.q[e / CH][e % CH * V + y] = kda::io<T>::ld(&x[i].v[y]) * scale_log2;
+                }
+            }
+        };
+        if (q_wide) load_q(std::integral_constant<int, 16 / sizeof(T)>{});
+        else load_q(std::integral_constant<int, 1>{});
         // softmax state: 256 / ROWS threads share a row
         constexpr int TPR = kThreads / ROWS, KPT = kTile / TPR;
         const int sr = tid / TPR, sx = tid % TPR;
@@ -204,30 +224,34 @@ kda_latent_simt_kernel(const T* __restrict__ q, Src src, const int32_t* __restri
             }
             if (tid < kTile && t + 1 < u.te) s_place[(t + 1) & 1][tid] = next_place;
             __syncthreads();
-            // scores over one part of the channels: rows 4 ty .. + 3, keys tx, tx + KX
+            // scores over one part of the channels: rows ty, ty + ROWS / 4, ..., keys tx, tx + KX, ...  (neighbouring
+            // threads neighbouring rows of both, so that no two meet in a bank)
             {
-                constexpr int SPLIT = Smem<Src>::SPLIT, CP = DK / SPLIT, KX = kTile / 2;
+                constexpr int SPLIT = Smem<Src>::SPLIT, CP = DK / SPLIT, KX = kTile / 4;
                 static_assert(CP % 4 == 0, "channels");
                 const int tx = tid % KX, ty = tid / KX % (ROWS / 4), part = tid / (KX * (ROWS / 4));
-                float a[4][2];
+                float a[4][4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) a[i][0] = a[i][1] = 0.f;
-#pragma unroll 4
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) a[i][e] = 0.f;
+#pragma unroll 3
                 for (int c = part * CP; c < (part + 1) * CP; c += 4) {
-                    const float4 k0 = *reinterpret_cast<const float4*>(&sm.k[tx][c]);
-                    const float4 k1 = *reinterpret_cast<const float4*>(&sm.k[tx + KX][c]);
+                    float4 k[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) k[e] = *reinterpret_cast<const float4*>(&sm.k[tx + e * KX][c]);
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        const float4 x = *reinterpret_cast<const float4*>(&sm.q[4 * ty + i][c]);
-                        a[i][0] = fmaf(x.x, k0.x, fmaf(x.y, k0.y, fmaf(x.z, k0.z, fmaf(x.w, k0.w, a[i][0]))));
-                        a[i][1] = fmaf(x.x, k1.x, fmaf(x.y, k1.y, fmaf(x.z, k1.z, fmaf(x.w, k1.w, a[i][1]))));
+                        const float4 x = *reinterpret_cast<const float4*>(&sm.q[ty + i * (ROWS / 4)][c]);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            a[i][e] = fmaf(x.x, k[e].x, fmaf(x.y, k[e].y, fmaf(x.z, k[e].z, fmaf(x.w, k[e].w, a[i][e]))));
                     }
                 }
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    sm.part[part][4 * ty + i][tx] = a[i][0];
-                    sm.part[part][4 * ty + i][tx + KX] = a[i][1];
-                }
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) sm.part[part][ty + i * (ROWS / 4)][tx + e * KX] = a[i][e];
             }
             __syncthreads();
             // softmax statistics of row sr
@@ -344,9 +368,10 @@ cudaError_t launch(const Src& src, const void* q, int64_t q_stride, const int32_
         return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
     });
     if (e != cudaSuccess) return e;
+    const bool q_wide = reinterpret_cast<uintptr_t>(q) % 16 == 0 && q_stride * sizeof(T) % 16 == 0;
     const int ctas = std::min(p.max_ctas, Src::BLOCKS * kda_host::sm_count());
     const cudaError_t err = kda_host::launch_overlapped(kern, ctas, Src::THREADS, smem, pa.stream, 1, static_cast<const T*>(q), src,
-                                                        cu, lengths, q_stride, s, scale * kLog2e, static_cast<T*>(pa.o),
+                                                        cu, lengths, q_stride, q_wide, s, scale * kLog2e, static_cast<T*>(pa.o),
                                                         pa.lse, kda_host::paged_partials(pa, p));
     if (err != cudaSuccess) return err;
     return kda_host::launch_latent_merge(pa, p, ctas);
