@@ -22,11 +22,11 @@
 // even and the odd ones and are joined at the end.
 //
 // Warps of each CTA: 0-3 and 4-7 softmax and output of half 0 and 1; 8 copies; 9 issues the
-// products (in CTA 0, for both); 10 walks the units; 11 copies queries and tells of values that are there.  Barriers of loads and of P are CTA 0's.
+// products (in CTA 0, for both); 10 walks the units; 11 cleans masked values.  Barriers of loads and of P are CTA 0's.
 //
 // Masked places.  A zero weight times a NaN or infinity in V is NaN.  So in a tile that not every row
-// of the unit sees whole, the softmax warps of its first step zero the rows of V that no row sees (the
-// next request's), and in the rows that some see and some do not take out the elements that are not
+// of the unit sees whole, a warp of each CTA zeroes the rows of V that no row sees (the next
+// request's), and in the rows that some see and some do not takes out the elements that are not
 // finite; the output adds such elements to the rows that see them.
 #include <algorithm>
 
@@ -45,7 +45,7 @@ using kda_paged::Piece;
 using kda_paged::Walker;
 
 constexpr int kThreads = 384;
-constexpr int kCopyWarp = 8, kIssueWarp = 9, kWalkWarp = 10, kQueryWarp = 11;
+constexpr int kCopyWarp = 8, kIssueWarp = 9, kWalkWarp = 10, kCleanWarp = 11;
 constexpr int kKeys = 128, kKeysLog2 = 7;              // keys of a tile
 constexpr int kRows = 128;                             // rows of a CTA's part of a row tile
 constexpr int kTileTokens = 2 * kRows;                 // tokens of a row tile
@@ -70,7 +70,7 @@ struct UnitSlot {
 };
 
 struct Tail {
-    uint64_t k_full[kStages], v_full[kStages], q_full, p_full[2][2];  // CTA 0's are used; P in two halves of its keys
+    uint64_t k_full[kStages], v_full[kStages], v_ready[kStages], q_full, p_full[2][2];  // CTA 0's are used; P in halves of its keys
     uint64_t k_empty[kStages], v_empty[kStages], q_empty, s_full[2], o_full[2], landed[kStages];    // each CTA's own
     uint64_t join_a, join_b;
     uint64_t u_full[kUnits], u_empty[kUnits];
@@ -131,6 +131,7 @@ kda_expanded_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const
             kda::mbar_init(&tl.k_empty[i], 1);
             kda::mbar_init(&tl.v_empty[i], 1);
             kda::mbar_init(&tl.landed[i], 1);
+            kda::mbar_init(&tl.v_ready[i], 2);
         }
         kda::mbar_init(&tl.q_full, 1);
         kda::mbar_init(&tl.q_empty, 1);
@@ -228,6 +229,19 @@ kda_expanded_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const
                     load_pair(dst + 2 * kKPanel, &rmap, 0, 0, y, bar);
                 }
                 __syncwarp();
+                if (tile == u.tb) {
+                    const int tiles = u.ntok > kTileTokens ? 2 : 1;
+                    if (k > 0 && !wait(&tl.q_empty, (k - 1) & 1)) { ok = false; break; }
+                    __syncwarp();
+                    if (lane == 0 && rank == 0) kda::mbar_arrive_expect_tx(&tl.q_full, 2 * tiles * kQTile);
+                    __syncwarp();
+                    if (lane < tiles * kPanels) {
+                        const int i = lane / kPanels, c = lane % kPanels;
+                        load_pair(kda::smem_u32(sm) + i * kQTile + c * kQPanel, &qmap, c * 64, u.qh0,
+                                  u.tok0 + i * kTileTokens + rank * kRows, at_rank(&tl.q_full, 0));
+                    }
+                    ++n_q;
+                }
                 if (n_ld >= kStages && !wait(&tl.v_empty[st], parity)) { ok = false; break; }
                 __syncwarp();
                 if (lane == 0) {
@@ -238,31 +252,41 @@ kda_expanded_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const
                 ++n_ld;
             }
         }
-    } else if (w == kQueryWarp) {
-        // ---------------- this CTA's rows of the queries
+    } else if (w == kCleanWarp) {
+        // ---------------- values that must not meet a zero weight (see the header).  CTA 1's loads count on CTA 0's
+        // barriers, so it is told of them; the products wait for both CTAs
         int n_v = 0;                                   // key tiles so far
-        for (int k = 0;; ++k) {
+        bool ok = true;
+        for (int k = 0; ok; ++k) {
             Unit u;
             if (!read_unit(k, u)) break;
-            const int tiles = u.ntok > kTileTokens ? 2 : 1;
-            if (k > 0 && !wait(&tl.q_empty, (k - 1) & 1)) break;
-            __syncwarp();
-            if (lane == 0 && rank == 0) kda::mbar_arrive_expect_tx(&tl.q_full, 2 * tiles * kQTile);
-            __syncwarp();
-            if (lane < tiles * kPanels) {
-                const int i = lane / kPanels, c = lane % kPanels;
-                load_pair(kda::smem_u32(sm) + i * kQTile + c * kQPanel, &qmap, c * 64, u.qh0,
-                          u.tok0 + i * kTileTokens + rank * kRows, at_rank(&tl.q_full, 0));
-            }
-            ++n_q;
-            // tells both CTAs that a tile's values are there (CTA 1 cannot see it: its loads count on CTA 0's barriers)
-            bool ok = true;
-            for (int j = u.tb; ok && rank == 0 && j < u.te; ++j, ++n_v) {
-                ok = wait(&tl.v_full[n_v % kStages], (n_v / kStages) & 1);
-                if (ok && lane < 2) arrive_remote(at_rank(&tl.landed[n_v % kStages], lane));
+            const Sight un = sight(u, 0, 0, u.ntok - 1);
+            for (int tile = u.tb; tile < u.te; ++tile, ++n_v) {
+                const int st = n_v % kStages, k0 = tile << kKeysLog2;
+                ok = wait(rank == 0 ? &tl.v_full[st] : &tl.landed[st], (n_v / kStages) & 1);
+                if (!ok) break;
+                if (rank == 0 && lane == 0) arrive_remote(at_rank(&tl.landed[st], 1));
+                if (k0 + kKeys > un.all_hi) {          // not every row sees it whole
+                    unsigned char* v = sm + kV0 + st * kVTile;
+                    const int from = max(un.all_hi - k0, 0), to = min(max(un.hi - k0, 0), kKeys);
+                    bool odd = false;
+#pragma unroll 4
+                    for (int e = from * 8 + lane; e < to * 8; e += 32) {     // some rows see them: what is not finite is taken out
+                        uint4* at = reinterpret_cast<uint4*>(v + e * 16);
+                        uint4 x = *at;
+                        if (take_odd(x)) {
+                            *at = x;
+                            odd = true;
+                        }
+                    }
+                    for (int e = max(from, to) * 8 + lane; e < kKeys * 8; e += 32)            // no row sees them
+                        *reinterpret_cast<uint4*>(v + e * 16) = make_uint4(0, 0, 0, 0);
+                    if (odd) flag_pair(&tl.odd_values[k & 7]);
+                    kda::fence_proxy_async_smem();
+                }
                 __syncwarp();
+                if (lane == 0) arrive_remote(at_rank(&tl.v_ready[st], 0));
             }
-            if (!ok) break;
         }
     } else if (w == kIssueWarp) {
         // ---------------- products: CTA 0 issues for both.  All lanes wait, an elected one issues.
@@ -291,7 +315,7 @@ kda_expanded_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const
         };
         // O_h += P_h V, the first half of the keys as soon as its weights are there
         auto values_step = [&](int h, const Pending& pv) -> bool {
-            if ((pv.flags & kFirstUse) && !wait(&tl.v_full[pv.at % kStages], (pv.at / kStages) & 1)) return false;
+            if ((pv.flags & kFirstUse) && !wait(&tl.v_ready[pv.at % kStages], (pv.at / kStages) & 1)) return false;
             const uint64_t b = v_desc + kda::desc_step(pv.at % kStages * kVTile);
             const uint32_t d = tmem + kTmemO + h * 128, a = tmem + h * 128;
             if (!wait(&tl.p_full[h][0], (p_phase >> h) & 1)) return false;
@@ -381,7 +405,7 @@ kda_expanded_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const
         const uint32_t lane_off = (uint32_t)((w & 3) * 32) << 16;
         const uint32_t tS = tmem + lane_off + h * 128;
         const uint32_t p_bar = at_rank(&tl.p_full[h][0], 0);
-        int n_s = 0, n_j = 0, g = 0, n_v = 0;          // n_v: key tiles of the units before
+        int n_s = 0, n_j = 0, g = 0;
         uint32_t o_phase = 0;                          // bit h: parity of the next O_h
         bool ok = true;
         for (int k = 0; ok; ++k) {
@@ -406,29 +430,6 @@ kda_expanded_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const
                 if (!wait(&tl.s_full[h], n_s & 1)) { ok = false; break; }
                 ++n_s;
                 kda::tc_fence_after();
-                // this half takes the tile first, and not all rows see it whole: clean its values
-                const bool clean = (!two || !(t & 1) || j >= tiles0) && k0 + kKeys > un.all_hi;
-                auto prepare_values = [&]() -> bool {  // values that must not meet a zero weight (see the header)
-                    if (!wait(&tl.landed[(n_v + j) % kStages], ((n_v + j) / kStages) & 1)) return false;
-                    unsigned char* v = sm + kV0 + (n_v + j) % kStages * kVTile;
-                    bool odd = false;
-#pragma unroll 1
-                    for (int e = row; e < kKeys * 8; e += 128) {
-                        const int key = k0 + (e >> 3);
-                        if (key < un.all_hi) continue;
-                        uint4* at = reinterpret_cast<uint4*>(v + e * 16);
-                        uint4 x = make_uint4(0, 0, 0, 0);
-                        if (key < un.hi) {
-                            x = *at;
-                            if (!take_odd(x)) continue;
-                            odd = true;
-                        }
-                        *at = x;
-                    }
-                    if (odd) flag_pair(&tl.odd_values[k & 7]);
-                    kda::fence_proxy_async_smem();
-                    return true;
-                };
                 auto arrive = [&](int part) {          // weights of that half of the keys are there
                     kda::tc_fence_before();
                     __syncwarp();
@@ -441,31 +442,19 @@ kda_expanded_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const
                         tmem_st32(tS + 32, zero);
                         kda::tmem_wait_st();
                     }
-                    if (clean && !prepare_values()) { ok = false; break; }
                     arrive(0);
                     arrive(1);
                     continue;
-                }
-                if (k0 + kKeys > mine) {
-                    // scores of keys this row does not see become -inf, in place.  Rolled: these
-                    // tiles are few, and a short call's time goes into fetching instructions
-#pragma unroll 1
-                    for (int c = 0; c < kKeys; c += 32) {
-                        const int b = hi - k0 - c;
-                        const uint32_t seen = b >= 32 ? 0xffffffffu : (1u << max(b, 0)) - 1u;
-                        float y[32];
-                        kda::tmem_ld32(tS + c, y);
-                        kda::tmem_wait_ld();
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) y[e] = (seen >> e) & 1 ? y[e] : -INFINITY;
-                        tmem_st32(tS + c, reinterpret_cast<const uint32_t*>(y));
-                    }
-                    kda::tmem_wait_st();
                 }
                 float x[128];
 #pragma unroll
                 for (int c = 0; c < 128; c += 32) kda::tmem_ld32(tS + c, x + c);
                 kda::tmem_wait_ld();
+                if (k0 + kKeys > mine) {               // keys that this row does not see
+                    const int b = hi - k0;
+#pragma unroll
+                    for (int c = 0; c < 128; ++c) x[c] = c < b ? x[c] : -INFINITY;
+                }
                 float top[4] = {x[0], x[2], x[4], x[6]};
 #pragma unroll
                 for (int c = 0; c < 128; c += 8)
@@ -510,7 +499,6 @@ kda_expanded_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const
                 };
                 weigh(0, 64);
                 tmem_st32(tS, p);
-                if (clean && !prepare_values()) { ok = false; break; }
                 weigh(64, 96);                         // while the first half is being stored
                 kda::tmem_wait_st();
                 arrive(0);
@@ -529,19 +517,14 @@ kda_expanded_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const
             const size_t at = (size_t)(u.tok0 + tok) * s.Hq + u.qh0;
             const float ref = m == -INFINITY ? -INFINITY : m * scale_log2;
             const int key0 = first_row(u);
+            const bool wide = ((uintptr_t)o & 31) == 0;
             // writes 32 columns of this row: o, or unnormalised sums
             auto put = [&](float* y, int c0, float sum_l) {
                 if (*(volatile int*)&tl.odd_values[k & 7] && valid) add_odd_values(y, c0, u, un, hi, key0, values);
                 if (!valid) return;
                 if (whole) {
                     const float inv = sum_l == 0.f ? 0.f : 1.f / sum_l;
-                    uint4* dst = reinterpret_cast<uint4*>(o + at * kValue + c0);
-#pragma unroll
-                    for (int e = 0; e < 32; e += 8)
-                        dst[e / 8] = make_uint4(kda::pack_bf16x2(y[e] * inv, y[e + 1] * inv),
-                                                kda::pack_bf16x2(y[e + 2] * inv, y[e + 3] * inv),
-                                                kda::pack_bf16x2(y[e + 4] * inv, y[e + 5] * inv),
-                                                kda::pack_bf16x2(y[e + 6] * inv, y[e + 7] * inv));
+                    store_row(o + at * kValue + c0, y, inv, wide);
                 } else {
                     float4* dst = reinterpret_cast<float4*>(parts.sums4(cluster, which, tok, c0));
 #pragma unroll
@@ -624,18 +607,16 @@ kda_expanded_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const
             // the one four back (every unit takes all warps of one half, and the halves meet within two)
             if (tid == 0) tl.odd_values[(k + 4) & 7] = 0;
             g += steps;
-            n_v += tiles;
         }
     }
     kda::tc_fence_before();
     __syncthreads();
-    if (*abort_f && rank == 0 && w == kQueryWarp && n_q > 0)
-        (void)kda::mbar_wait(&tl.q_full, (n_q - 1) & 1, kda::kWaitCycles);
     if (*abort_f && rank == 0 && w == kCopyWarp) {     // no copy in flight into shared memory that is given up
         for (int i = max(0, n_ld - kStages); i <= n_ld; ++i) {
             (void)kda::mbar_wait(&tl.k_full[i % kStages], (i / kStages) & 1, i < n_ld ? kda::kWaitCycles : 10000000);
             (void)kda::mbar_wait(&tl.v_full[i % kStages], (i / kStages) & 1, i < n_ld ? kda::kWaitCycles : 10000000);
         }
+        if (n_q > 0) (void)kda::mbar_wait(&tl.q_full, (n_q - 1) & 1, kda::kWaitCycles);
     }
     __syncthreads();
     cluster_leave();                                   // the other CTA is done with this one's memory and TMEM

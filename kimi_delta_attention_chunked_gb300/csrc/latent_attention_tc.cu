@@ -534,13 +534,7 @@ kda_latent_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const _
                     if (add) add_odd_values<C::LOG2>(y, c0, u, si, hi, s, cache, table);
                     if (!valid) continue;
                     if (whole) {
-                        uint4* dst = reinterpret_cast<uint4*>(o + at * kLatent + c0);
-#pragma unroll
-                        for (int e = 0; e < 32; e += 8)
-                            dst[e / 8] = make_uint4(kda::pack_bf16x2(y[e] * inv, y[e + 1] * inv),
-                                                    kda::pack_bf16x2(y[e + 2] * inv, y[e + 3] * inv),
-                                                    kda::pack_bf16x2(y[e + 4] * inv, y[e + 5] * inv),
-                                                    kda::pack_bf16x2(y[e + 6] * inv, y[e + 7] * inv));
+                        store_row(o + at * kLatent + c0, y, inv, ((uintptr_t)o & 31) == 0);
                     } else {
                         float4* dst = reinterpret_cast<float4*>(parts.sums4(cluster, which, prow, c0));
 #pragma unroll
