@@ -470,7 +470,7 @@ KDA_API size_t kda_latent_attention_workspace_size(int T, int H, kda_dtype dtype
  * seq_len     [N] int32 device array
  * scale       > 0 and at most 2^127 (of the expanded head: usually 192^-1/2)
  * max_blocks  at most KDA_MAX_STEP_POSITIONS / page_size
- * o           [T, H, 512] dtype, 16-byte aligned;  lse [T, H] float or NULL
+ * o           [T, H, 512] dtype, 32-byte aligned;  lse [T, H] float or NULL
  * workspace   kda_latent_attention_workspace_size bytes, 256-byte aligned; a call has it to
  *             itself until it is complete
  * The scores, their statistics and the sums are fp32.
@@ -506,7 +506,7 @@ KDA_API size_t kda_expanded_attention_workspace_size(int T, int H, kda_dtype dty
  *               not written
  * S + T         at most KDA_MAX_STEP_POSITIONS
  * scale         > 0 and at most 2^127
- * o             [T, H, 128] dtype, 16-byte aligned;  lse [T, H] float or NULL
+ * o             [T, H, 128] dtype, 32-byte aligned;  lse [T, H] float or NULL
  * workspace     kda_expanded_attention_workspace_size bytes, 256-byte aligned; a call has it
  *               to itself until it is complete
  * The scores, their statistics and the sums are fp32.

@@ -25,22 +25,14 @@ __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.w
 __device__ __forceinline__ void cluster_leave() {
     asm volatile("barrier.cluster.arrive.relaxed;\n\tbarrier.cluster.wait;" ::: "memory");
 }
-// 32 values times f to 64 bytes of a row, as bf16.  A lane has a row, so an instruction touches 32 rows: 32 bytes of
-// each (where the rows start on such boundaries: `wide`) take half as long as 16 at a time.
-__device__ __forceinline__ void store_row(__nv_bfloat16* p, const float* y, float f, bool wide) {
-    uint32_t x[16];
+// 16 values to 32 bytes of a row, as bf16: a whole sector, on a 32-byte boundary.
+__device__ __forceinline__ void store16(__nv_bfloat16* p, const float* y) {
+    uint32_t x[8];
 #pragma unroll
-    for (int e = 0; e < 16; ++e) x[e] = kda::pack_bf16x2(y[2 * e] * f, y[2 * e + 1] * f);
-    if (wide) {
-#pragma unroll
-        for (int e = 0; e < 16; e += 8)
-            asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p + 2 * e), "r"(x[e]), "r"(x[e + 1]),
-                         "r"(x[e + 2]), "r"(x[e + 3]), "r"(x[e + 4]), "r"(x[e + 5]), "r"(x[e + 6]), "r"(x[e + 7])
-                         : "memory");
-    } else {
-#pragma unroll
-        for (int e = 0; e < 16; e += 4) *reinterpret_cast<uint4*>(p + 2 * e) = make_uint4(x[e], x[e + 1], x[e + 2], x[e + 3]);
-    }
+    for (int e = 0; e < 8; ++e) x[e] = kda::pack_bf16x2(y[2 * e], y[2 * e + 1]);
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(x[0]), "r"(x[1]), "r"(x[2]), "r"(x[3]),
+                 "r"(x[4]), "r"(x[5]), "r"(x[6]), "r"(x[7])
+                 : "memory");
 }
 // Arrives on a barrier of either CTA.  What it has to order is in this SM: stores to shared memory
 // (made visible to the tensor cores by fence.proxy.async) and TMEM (by tcgen05.wait and fence); release at cluster

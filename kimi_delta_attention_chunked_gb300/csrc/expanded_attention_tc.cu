@@ -96,19 +96,17 @@ struct Values {
     long long token, head;
 };
 
-// Adds to o[0..31] (channels c0 ..) the values that are not finite, of the keys that this row sees
-// among those that not all rows of the unit see.
-__device__ __forceinline__ void add_odd_values(float* o, int c0, const Unit& u, const Sight& un, int hi, int key0,
-                                               const Values& vs) {
-    const int b = min(min(un.hi, hi), u.te << kKeysLog2);
-    for (int key = max(un.all_hi, u.tb << kKeysLog2); key < b; ++key) {
-        const __nv_bfloat16* v = vs.v + (key0 + (long long)key) * vs.token + u.kvh * vs.head + c0;
-#pragma unroll
-        for (int c = 0; c < 32; ++c) {
-            const float x = __bfloat162float(v[c]);
-            if ((__float_as_uint(x) & 0x7f800000u) == 0x7f800000u) o[c] += x;
+// Adds to a row's output or partial sums, channels from .. to - 1, the values that are not finite, of the keys [first, last)
+// among those that not all rows of the unit see: rare, and so out of the way of what every unit fetches.
+__device__ __noinline__ void add_odd_values(__nv_bfloat16* o, float* sums, int cap, int from, int to, const __nv_bfloat16* v,
+                                            long long token, int first, int last) {
+    for (int key = first; key < last; ++key)
+        for (int c = from; c < to; ++c) {
+            const float x = __bfloat162float(v[key * token + c]);
+            if ((__float_as_uint(x) & 0x7f800000u) != 0x7f800000u) continue;
+            if (o) o[c] = __float2bfloat16_rn(__bfloat162float(o[c]) + x);
+            else sums[(size_t)(c >> 2) * cap * 4 + (c & 3)] += x;
         }
-    }
 }
 
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
@@ -511,49 +509,19 @@ kda_expanded_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const
                 arrive(1);
             }
             if (!ok) break;
-            // ---- output
+            // ---- output: one short loop for every kind of unit, since it is fetched anew each time
+            const float ref = m == -INFINITY ? -INFINITY : m * scale_log2;
+            const size_t at = (size_t)(u.tok0 + tok) * s.Hq + u.qh0;
             const bool whole = u.first && u.last;
             const int which = u.first ? 1 : 0;
-            const size_t at = (size_t)(u.tok0 + tok) * s.Hq + u.qh0;
-            const float ref = m == -INFINITY ? -INFINITY : m * scale_log2;
-            const int key0 = first_row(u);
-            const bool wide = ((uintptr_t)o & 31) == 0;
-            // writes 32 columns of this row: o, or unnormalised sums
-            auto put = [&](float* y, int c0, float sum_l) {
-                if (*(volatile int*)&tl.odd_values[k & 7] && valid) add_odd_values(y, c0, u, un, hi, key0, values);
-                if (!valid) return;
-                if (whole) {
-                    const float inv = sum_l == 0.f ? 0.f : 1.f / sum_l;
-                    store_row(o + at * kValue + c0, y, inv, wide);
-                } else {
-                    float4* dst = reinterpret_cast<float4*>(parts.sums4(cluster, which, tok, c0));
-#pragma unroll
-                    for (int e = 0; e < 32; e += 4) dst[e / 4 * parts.cap] = make_float4(y[e], y[e + 1], y[e + 2], y[e + 3]);
-                }
-            };
-            auto put_stats = [&](float r, float sum_l) {
-                if (!valid) return;
-                if (whole) {
-                    if (lse) lse[at] = sum_l == 0.f ? -INFINITY : (r + log2f(sum_l)) * kLn2;
-                } else {
-                    parts.stats(cluster, which)[tok] = make_float2(r, sum_l);
-                }
-            };
+            // sources in TMEM and their factors, columns of this thread, statistics of the row
+            uint32_t src0 = kTmemO + h * 128, src1 = src0;
+            float f0 = l == 0.f ? 0.f : 1.f, f1 = 0.f, top = ref, sum_l = l;
+            int from = 0, to = kValue;
             if (two) {
                 ok = wait(&tl.o_full[h], (o_phase >> h) & 1);
                 o_phase ^= 3;
                 if (!ok) break;
-                kda::tc_fence_after();
-                if (busy) {
-#pragma unroll 1
-                    for (int c = 0; c < kValue; c += 32) {
-                        float y[32];
-                        kda::tmem_ld32(tmem + lane_off + kTmemO + h * 128 + c, y);
-                        kda::tmem_wait_ld();
-                        put(y, c, l);
-                    }
-                    put_stats(ref, l);
-                }
             } else {
                 // the halves hold the sums over every second key tile: each joins half of the columns
                 const bool has[2] = {(g & 1) == 0 || steps > 1, (g & 1) == 1 || steps > 1};
@@ -568,34 +536,53 @@ kda_expanded_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const
                     o_phase ^= 1u << e;
                 }
                 if (!ok) break;
-                kda::tc_fence_after();
-                if (busy) {
-                    const float2 st = tl.stats[h ^ 1][row];
-                    const float top = fmaxf(ref, st.x), base = top == -INFINITY ? 0.f : top;
-                    const float fm = l == 0.f ? 0.f : ex2(ref - base), fo = st.y == 0.f ? 0.f : ex2(st.x - base);
-                    const float f0 = h == 0 ? fm : fo, f1 = h == 0 ? fo : fm;
-                    const float sum_l = fmaf(fm, l, fo * st.y);
+                const float2 st = tl.stats[h ^ 1][row];
+                top = fmaxf(ref, st.x);
+                const float base = top == -INFINITY ? 0.f : top;
+                f0 = l == 0.f ? 0.f : ex2(ref - base);
+                f1 = st.y == 0.f ? 0.f : ex2(st.x - base);
+                sum_l = fmaf(f0, l, f1 * st.y);
+                src1 = kTmemO + (h ^ 1) * 128;
+                from = h * (kValue / 2);
+                to = from + kValue / 2;
+            }
+            kda::tc_fence_after();
+            if (busy) {
+                const float inv = !whole ? 1.f : sum_l == 0.f ? 0.f : 1.f / sum_l;
+                f0 *= inv;
+                f1 *= inv;
+                __nv_bfloat16* const dst = o + at * kValue;
+                float4* const part = reinterpret_cast<float4*>(parts.sums4(cluster, which, valid ? tok : 0, 0));
 #pragma unroll 1
-                    for (int c = h * 64; c < h * 64 + 64; c += 32) {
-                        float y[32];
+                for (int c = from; c < to; c += 16) {
+                    float y[16], z[16];
+                    kda::tmem_ld16(tmem + lane_off + src0 + c, y);
+                    kda::tmem_ld16(tmem + lane_off + src1 + c, z);
+                    kda::tmem_wait_ld();
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) y[e] = 0.f;
+                    for (int e = 0; e < 16; ++e)       // a half without a sum holds anything
+                        y[e] = (f0 == 0.f ? 0.f : f0 * y[e]) + (f1 == 0.f ? 0.f : f1 * z[e]);
+                    if (!valid) continue;
+                    if (whole) {
+                        store16(dst + c, y);
+                    } else {
 #pragma unroll
-                        for (int b = 0; b < 2; ++b) {
-                            if (!has[b]) continue;
-                            float z[32];
-                            kda::tmem_ld32(tmem + lane_off + kTmemO + b * 128 + c, z);
-                            kda::tmem_wait_ld();
-                            const float f = b == 0 ? f0 : f1;
-                            if (f != 0.f) {
-#pragma unroll
-                                for (int e = 0; e < 32; ++e) y[e] = fmaf(f, z[e], y[e]);
-                            }
-                        }
-                        put(y, c, sum_l);
+                        for (int e = 0; e < 4; ++e)
+                            part[(c / 4 + e) * parts.cap] = make_float4(y[4 * e], y[4 * e + 1], y[4 * e + 2], y[4 * e + 3]);
                     }
-                    if (h == 0) put_stats(top, sum_l);
                 }
+                if (valid && (two || h == 0)) {
+                    if (!whole) parts.stats(cluster, which)[tok] = make_float2(top, sum_l);
+                    else if (lse) lse[at] = sum_l == 0.f ? -INFINITY : (top + log2f(sum_l)) * kLn2;
+                }
+                if (valid && *(volatile int*)&tl.odd_values[k & 7]) {
+                    const int key0 = first_row(u);
+                    add_odd_values(whole ? dst : nullptr, reinterpret_cast<float*>(part), parts.cap, from, to,
+                                   values.v + key0 * values.token + u.kvh * values.head, values.token,
+                                   max(un.all_hi, u.tb << kKeysLog2), min(min(un.hi, hi), u.te << kKeysLog2));
+                }
+            }
+            if (!two) {
                 kda::tc_fence_before();
                 __syncwarp();
                 if (lane == 0) kda::mbar_arrive(&tl.join_b);

@@ -94,7 +94,7 @@ kda_status kda_latent_attention(const void* q, const void* cache, const int32_t*
     if (T == 0 || N == 0) return KDA_OK;
     if (!q || !cu_seqlens || !seq_len || !o) return KDA_ERR_INVALID_ARG;
     if ((n_pages > 0 && !cache) || (max_blocks > 0 && !block_table)) return KDA_ERR_INVALID_ARG;
-    if (!aligned(cache, 16) || !aligned(o, 16) || !aligned(q, element_size(dtype))) return KDA_ERR_INVALID_ARG;
+    if (!aligned(cache, 16) || !aligned(o, 32) || !aligned(q, element_size(dtype))) return KDA_ERR_INVALID_ARG;
     if (o == q || o == cache) return KDA_ERR_INVALID_ARG;
     if (!workspace || workspace_bytes < latent_workspace(T, H, dtype) || !aligned(workspace, 256)) return KDA_ERR_WORKSPACE;
     const kda_host::LatentArgs a{q, cache, block_table, cu_seqlens, seq_len, q_stride, N, T, H, page_size, max_blocks, n_pages,
@@ -131,7 +131,7 @@ kda_status kda_expanded_attention(const void* q, const void* k_nope, const void*
     if (!q || !cu_seqlens || !cu_seqlens_k || !o) return KDA_ERR_INVALID_ARG;
     if (S > 0 && (!k_nope || !k_rope || !v)) return KDA_ERR_INVALID_ARG;
     const int size = element_size(dtype);
-    if (!aligned(q, size) || !aligned(k_nope, size) || !aligned(k_rope, size) || !aligned(v, size) || !aligned(o, 16))
+    if (!aligned(q, size) || !aligned(k_nope, size) || !aligned(k_rope, size) || !aligned(v, size) || !aligned(o, 32))
         return KDA_ERR_INVALID_ARG;
     if (o == q || o == k_nope || o == k_rope || o == v) return KDA_ERR_INVALID_ARG;
     if (!workspace || workspace_bytes < expanded_workspace(T, dtype) || !aligned(workspace, 256)) return KDA_ERR_WORKSPACE;

@@ -102,21 +102,20 @@ struct Tail {
 };
 static_assert(sizeof(Tail) <= kTailBytes, "tail");
 
-// Adds to o[0..31] (channels c0 ..) the values that are not finite, of the keys that this row sees
-// among those that not all rows of the unit see.
-template <int LOG2>
-__device__ __forceinline__ void add_odd_values(float* o, int c0, const Unit& u, const Sight& un, int hi, const Shape& s,
-                                               const __nv_bfloat16* cache, const int32_t* table) {
-    const int b = min(min(un.hi, hi), u.te << LOG2);
-    for (int key = max(un.all_hi, u.tb << LOG2); key < b; ++key) {
-        const int page = table[(size_t)u.n * s.blocks + (key >> s.page_log2)];
+// Adds to a row's output or partial sums, 128 channels from each of c0 and c0 + 256 on, the values that are not finite, of the
+// keys [first, last) among those that not all rows of the unit see: rare, and so out of the way of what every unit fetches.
+__device__ __noinline__ void add_odd_values(__nv_bfloat16* o, float* sums, int cap, int c0, const Shape& s,
+                                            const __nv_bfloat16* cache, const int32_t* pages, int first, int last) {
+    for (int key = first; key < last; ++key) {
+        const int page = pages[key >> s.page_log2];
         if (page < 0 || page >= s.n_pages) continue;
-        const __nv_bfloat16* v =
-            cache + (((size_t)page << s.page_log2) + (key & ((1 << s.page_log2) - 1))) * kRow + c0;
-#pragma unroll
-        for (int c = 0; c < 32; ++c) {
+        const __nv_bfloat16* v = cache + (((size_t)page << s.page_log2) + (key & ((1 << s.page_log2) - 1))) * kRow;
+        for (int i = 0; i < 256; ++i) {
+            const int c = c0 + (i & 127) + (i & 128) * 2;
             const float x = __bfloat162float(v[c]);
-            if ((__float_as_uint(x) & 0x7f800000u) == 0x7f800000u) o[c] += x;
+            if ((__float_as_uint(x) & 0x7f800000u) != 0x7f800000u) continue;
+            if (o) o[c] = __float2bfloat16_rn(__bfloat162float(o[c]) + x);
+            else sums[(size_t)(c >> 2) * cap * 4 + (c & 3)] += x;
         }
     }
 }
@@ -524,23 +523,29 @@ kda_latent_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const _
                 const size_t at = (size_t)(u.tok0 + tok_in) * s.Hq + u.qh0 + head_in;
                 const int prow = tok_in * 2 * tiling.heads + head_in;                // row of a partial slot
                 const float inv = l == 0.f ? 0.f : 1.f / l;
-                const bool add = *(volatile int*)&tl.odd_values[k & 3] != 0 && valid;
+                __nv_bfloat16* const dst = o + at * kLatent;
+                float4* const part = reinterpret_cast<float4*>(parts.sums4(cluster, which, valid ? prow : 0, 0));
 #pragma unroll 1
-                for (int c = 0; c < 256; c += 32) {
-                    float y[32];
-                    kda::tmem_ld32(tmem + lane_off + c, y);
+                for (int c = 0; c < 256; c += 16) {
+                    float y[16];
+                    kda::tmem_ld16(tmem + lane_off + c, y);
                     kda::tmem_wait_ld();
-                    const int c0 = (c & 128) * 2 + half * 128 + (c & 127);          // channel
-                    if (add) add_odd_values<C::LOG2>(y, c0, u, si, hi, s, cache, table);
                     if (!valid) continue;
+                    const int c0 = (c & 128) * 2 + half * 128 + (c & 127);          // channel
                     if (whole) {
-                        store_row(o + at * kLatent + c0, y, inv, ((uintptr_t)o & 31) == 0);
-                    } else {
-                        float4* dst = reinterpret_cast<float4*>(parts.sums4(cluster, which, prow, c0));
 #pragma unroll
-                        for (int e = 0; e < 32; e += 4) dst[e / 4 * parts.cap] = make_float4(y[e], y[e + 1], y[e + 2], y[e + 3]);
+                        for (int e = 0; e < 16; ++e) y[e] *= inv;
+                        store16(dst + c0, y);
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            part[(c0 / 4 + e) * parts.cap] = make_float4(y[4 * e], y[4 * e + 1], y[4 * e + 2], y[4 * e + 3]);
                     }
                 }
+                if (valid && *(volatile int*)&tl.odd_values[k & 3])
+                    add_odd_values(whole ? dst : nullptr, reinterpret_cast<float*>(part), parts.cap, half * 128, s, cache,
+                                   table + (size_t)u.n * s.blocks, max(si.all_hi, u.tb << C::LOG2),
+                                   min(min(si.hi, hi), u.te << C::LOG2));
                 if (valid && half == 0) {
                     const float ref = m == -INFINITY ? -INFINITY : m * scale_log2;
                     if (!whole) parts.stats(cluster, which)[prow] = make_float2(ref, l);

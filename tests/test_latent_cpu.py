@@ -76,7 +76,7 @@ def absorbed(lib, **kw):  # noqa: F811
     (dict(scale=2.0 ** 127 * 1.5), E.KDA_ERR_INVALID_ARG), (dict(qs=8 * 576 - 1), E.KDA_ERR_INVALID_ARG),
     (dict(q=None), E.KDA_ERR_INVALID_ARG), (dict(cache=None), E.KDA_ERR_INVALID_ARG), (dict(table=None), E.KDA_ERR_INVALID_ARG),
     (dict(cu=None), E.KDA_ERR_INVALID_ARG), (dict(seq=None), E.KDA_ERR_INVALID_ARG), (dict(o=None), E.KDA_ERR_INVALID_ARG),
-    (dict(o=P(0x1000)), E.KDA_ERR_INVALID_ARG), (dict(o=P(0x2000)), E.KDA_ERR_INVALID_ARG), (dict(o=P(0x7008)), E.KDA_ERR_INVALID_ARG),
+    (dict(o=P(0x1000)), E.KDA_ERR_INVALID_ARG), (dict(o=P(0x2000)), E.KDA_ERR_INVALID_ARG), (dict(o=P(0x7010)), E.KDA_ERR_INVALID_ARG),
     (dict(cache=P(0x2008)), E.KDA_ERR_INVALID_ARG), (dict(q=P(0x1001)), E.KDA_ERR_INVALID_ARG), (dict(ws=None), E.KDA_ERR_WORKSPACE),
     (dict(ws=P(0x10010)), E.KDA_ERR_WORKSPACE), (dict(bytes=0), E.KDA_ERR_WORKSPACE), (dict(T=0), E.KDA_OK), (dict(N=0), E.KDA_OK),
 ])
@@ -103,7 +103,7 @@ def expanded(lib, **kw):  # noqa: F811
     (dict(vt=0), E.KDA_ERR_INVALID_ARG), (dict(vh=-256), E.KDA_ERR_INVALID_ARG), (dict(q=None), E.KDA_ERR_INVALID_ARG),
     (dict(kn=None), E.KDA_ERR_INVALID_ARG), (dict(kr=None), E.KDA_ERR_INVALID_ARG), (dict(v=None), E.KDA_ERR_INVALID_ARG),
     (dict(cu=None), E.KDA_ERR_INVALID_ARG), (dict(cuk=None), E.KDA_ERR_INVALID_ARG), (dict(o=None), E.KDA_ERR_INVALID_ARG),
-    (dict(o=P(0x4000)), E.KDA_ERR_INVALID_ARG), (dict(o=P(0x7008)), E.KDA_ERR_INVALID_ARG), (dict(v=P(0x4001)), E.KDA_ERR_INVALID_ARG),
+    (dict(o=P(0x4000)), E.KDA_ERR_INVALID_ARG), (dict(o=P(0x7010)), E.KDA_ERR_INVALID_ARG), (dict(v=P(0x4001)), E.KDA_ERR_INVALID_ARG),
     (dict(kr=P(0x3002), dt=E.KDA_FP32), E.KDA_ERR_INVALID_ARG), (dict(ws=None), E.KDA_ERR_WORKSPACE), (dict(bytes=0), E.KDA_ERR_WORKSPACE),
     (dict(ws=P(0x10080)), E.KDA_ERR_WORKSPACE), (dict(T=0), E.KDA_OK), (dict(N=0), E.KDA_OK),
 ])
