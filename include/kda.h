@@ -437,7 +437,8 @@ KDA_API kda_status kda_rotary(const void* x, const int32_t* positions, const flo
  * n_pages * page_size are skipped.
  *
  * c          [T, 512] dtype, k_rope [T, 64] dtype: consecutive tokens are c_stride
- *            and k_rope_stride elements apart (both may be slices of one projection)
+ *            and k_rope_stride elements apart (both may be slices of one projection, but
+ *            not of the cache)
  * slot_map   [T] int64.  What a slot named by two tokens holds is unspecified: each
  *            piece of its row is either one's.
  * positions  [T] int32, inv_freq [32] float; both NULL: the key part is copied
@@ -473,7 +474,9 @@ KDA_API size_t kda_latent_attention_workspace_size(int T, int H, kda_dtype dtype
  * o           [T, H, 512] dtype, 32-byte aligned;  lse [T, H] float or NULL
  * workspace   kda_latent_attention_workspace_size bytes, 256-byte aligned; a call has it to
  *             itself until it is complete
- * The scores, their statistics and the sums are fp32.
+ * The scores, their statistics and the sums are fp32; on the tensor-core path (bf16, q
+ * 16-byte aligned with a stride that is a multiple of 8) the weights enter the second product
+ * as bf16.  fp32 tensors, and bf16 with other rows of q, run in fp32 on CUDA cores.
  */
 KDA_API kda_status kda_latent_attention(const void* q, const void* cache, const int32_t* block_table,
                                 const int32_t* cu_seqlens, const int32_t* seq_len, int64_t q_stride, int N, int T, int H,
@@ -509,7 +512,9 @@ KDA_API size_t kda_expanded_attention_workspace_size(int T, int H, kda_dtype dty
  * o             [T, H, 128] dtype, 32-byte aligned;  lse [T, H] float or NULL
  * workspace     kda_expanded_attention_workspace_size bytes, 256-byte aligned; a call has it
  *               to itself until it is complete
- * The scores, their statistics and the sums are fp32.
+ * The scores, their statistics and the sums are fp32; on the tensor-core path (bf16, all rows
+ * on 16-byte boundaries) the weights enter the second product as bf16.  fp32 tensors, and bf16
+ * with other rows, run in fp32 on CUDA cores.
  */
 KDA_API kda_status kda_expanded_attention(const void* q, const void* k_nope, const void* k_rope, const void* v,
                                   const int32_t* cu_seqlens, const int32_t* cu_seqlens_k, int64_t q_stride,

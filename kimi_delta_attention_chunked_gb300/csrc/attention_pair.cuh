@@ -48,20 +48,13 @@ __device__ __forceinline__ void load_pair(uint32_t dst, const void* tmap, int x,
         "l"(tmap), "r"(x), "r"(y), "r"(z), "r"(bar)
         : "memory");
 }
+// D[tmem] (+)= A[smem] * B[smem] of both CTAs; issued by one thread of CTA 0.
 __device__ __forceinline__ void mma_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
     asm volatile(
         "{\n\t.reg .pred p;\n\t"
         "setp.ne.b32 p, %4, 0;\n\t"
         "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
         "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
-        : "memory");
-}
-// Arrive once on the barrier at this place in both CTAs when the products issued so far are done.
-__device__ __forceinline__ void commit_pair(uint64_t* bar) {
-    asm volatile(
-        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
-            kda::smem_u32(bar)),
-        "h"((uint16_t)3)
         : "memory");
 }
 // The same with A in TMEM (each CTA's rows in its own).
@@ -71,6 +64,14 @@ __device__ __forceinline__ void mma_pair_ta(uint32_t d, uint32_t a, uint64_t b, 
         "setp.ne.b32 p, %4, 0;\n\t"
         "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
         "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+// Arrive once on the barrier at this place in both CTAs when the products issued so far are done.
+__device__ __forceinline__ void commit_pair(uint64_t* bar) {
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+            kda::smem_u32(bar)),
+        "h"((uint16_t)3)
         : "memory");
 }
 // All of TMEM, in both CTAs: one warp of each calls these.

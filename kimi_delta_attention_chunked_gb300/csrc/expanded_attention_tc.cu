@@ -28,6 +28,17 @@
 // of the unit sees whole, a warp of each CTA zeroes the rows of V that no row sees (the next
 // request's), and in the rows that some see and some do not takes out the elements that are not
 // finite; the output adds such elements to the rows that see them.
+//
+// Bound, and what it measured (GPU time with the merge; cuBLAS 1888 TFLOP/s).  A prompt of 8192 tokens, 32 heads: 418 us, 1.64
+// PFLOP/s of the products that a causal mask leaves (floor 364): a tile of two steps takes 2970 cycles, 2560 of them products, and a unit's
+// end (its last two tiles have one row tile, its output) 10 k cycles of 60 k to 190 k.  12 requests of 1 to 700 tokens over up
+// to 3200 keys, 16 heads: 46 us (floor 10.6): 2 to 6 short units a pair at 7 to 8 k cycles each.
+// What it took: arrivals at the other CTA without a fence of global memory (684 -> 528 us); the weights in two halves, so that
+// the first half's products run while the second is formed, no steps of a row tile behind its last key, values cleaned off
+// the softmax warps' path (518 -> 427); places of the division that count steps (444 -> 427); one short output loop (424 -> 418).
+// Queries of lone row tiles fetched a unit ahead gained nothing.
+// Rounding: P enters its product as bf16, the type of V; the output's error against 64 bits is 2.0e-3 (2-norm), 1.5e-3
+// of it its own rounding to bf16.
 #include <algorithm>
 
 #include "attention_pair.cuh"

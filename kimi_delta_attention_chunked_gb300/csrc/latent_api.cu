@@ -35,6 +35,12 @@ size_t expanded_workspace(int T, kda_dtype dt) {
     return std::max(simt, kda_host::paged_plan_bytes(kda_host::expanded_plan_tc(T), kValue));
 }
 
+// TMA fetches bf16 rows that start on 16-byte boundaries, at strides below 2^40 bytes.
+bool fetchable(const void* p, int64_t s0, int64_t s1 = 8) {
+    constexpr int64_t kMost = (int64_t(1) << 39) - 8;
+    return aligned(p, 16) && s0 % 8 == 0 && s1 % 8 == 0 && s0 > 0 && s1 > 0 && s0 <= kMost && s1 <= kMost;
+}
+
 }  // namespace
 
 extern "C" {
@@ -99,9 +105,8 @@ kda_status kda_latent_attention(const void* q, const void* cache, const int32_t*
     if (!workspace || workspace_bytes < latent_workspace(T, H, dtype) || !aligned(workspace, 256)) return KDA_ERR_WORKSPACE;
     const kda_host::LatentArgs a{q, cache, block_table, cu_seqlens, seq_len, q_stride, N, T, H, page_size, max_blocks, n_pages,
                                  scale, dtype, o, lse, workspace, stream, kda_host::status_word()};
-    // the tensor-core path fetches q by TMA, whose rows start on 16-byte boundaries, and
-    // describes the cache to it, which an empty one cannot be
-    const bool tc = dtype == KDA_BF16 && aligned(q, 16) && q_stride % 8 == 0 && n_pages > 0 && max_blocks > 0;
+    // the tensor-core path fetches q by TMA and describes the cache to it, which an empty one cannot be
+    const bool tc = dtype == KDA_BF16 && fetchable(q, q_stride) && n_pages > 0 && max_blocks > 0;
     return from_cuda(tc ? kda_host::launch_latent_attention_tc(a) : kda_host::launch_latent_attention_simt(a));
 }
 
@@ -138,13 +143,8 @@ kda_status kda_expanded_attention(const void* q, const void* k_nope, const void*
     const kda_host::ExpandedArgs a{q, k_nope, k_rope, v, cu_seqlens, cu_seqlens_k, q_stride, k_token_stride, k_head_stride,
                                    k_rope_stride, v_token_stride, v_head_stride, N, T, S, H, scale, causal != 0, dtype, o, lse,
                                    workspace, stream, kda_host::status_word()};
-    // TMA fetches rows that start on 16-byte boundaries, at strides below 2^40 bytes
-    auto fetchable = [](const void* p, int64_t s0, int64_t s1) {
-        constexpr int64_t kMost = (int64_t(1) << 39) - 8;
-        return aligned(p, 16) && s0 % 8 == 0 && s1 % 8 == 0 && s0 > 0 && s1 > 0 && s0 <= kMost && s1 <= kMost;
-    };
-    const bool tc = dtype == KDA_BF16 && S > 0 && fetchable(q, q_stride, 8) && fetchable(k_nope, k_token_stride, k_head_stride) &&
-                    fetchable(k_rope, k_rope_stride, 8) && fetchable(v, v_token_stride, v_head_stride);
+    const bool tc = dtype == KDA_BF16 && S > 0 && fetchable(q, q_stride) && fetchable(k_nope, k_token_stride, k_head_stride) &&
+                    fetchable(k_rope, k_rope_stride) && fetchable(v, v_token_stride, v_head_stride);
     return from_cuda(tc ? kda_host::launch_expanded_attention_tc(a) : kda_host::launch_expanded_attention_simt(a));
 }
 

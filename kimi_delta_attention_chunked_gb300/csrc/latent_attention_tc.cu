@@ -10,7 +10,7 @@
 //
 // Why a pair.  128 rows of 512 sums are the whole TMEM of an SM.  With M = 128 over two CTAs
 // each holds 64 rows, and those use all 128 lanes: lanes 0-63 the first half of a product's N
-// columns, lanes 64-127 the second.  So O takes 256 columns of TMEM and S KEYS / 2, S is double
+// columns, lanes 64-127 the second.  So O takes 256 columns of TMEM and S KEYS / 2 (KEYS = 64), S is double
 // buffered, and the tensor cores run at their full rate.  64 rows in a CTA alone would pay
 // twice the tensor time for the same rows: half of the lanes stay idle there.
 //
@@ -36,6 +36,19 @@
 // row sees whole, once S is complete, the softmax warps zero the rows of V that no row of the unit
 // sees, and in rows that some see and some do not take out the elements that are not finite.  They note
 // if they found one (in both CTAs); the output then adds such elements to the rows that see them.
+//
+// Bound, and what it measured (GPU time with the merge; HBM 6790 GB/s, cuBLAS 1888 TFLOP/s).  While it streams, HBM: a 64-key
+// tile of a pair takes 0.85 us of the 0.83 that the copy rate allows, for any number of rows up to 128; with the cache in L2 (many
+// units of a request), the tensor cores: 0.79 us of the 0.72 that cuBLAS's rate allows.  64 requests of 1 K to 16 K keys, 32
+// heads: 82 us (floor 61).  24 requests of 2 K to 32 K keys, 128 heads: 73 us (46).  32 x 8 tokens, 32 heads, 0.7 K to 8 K keys:
+// 61 us (29).  4 requests of 90 to 1500 keys: 14.3 us.  Above the floors: 5 us before a pair's first product (its piece, the
+// first unit, the page table, the first tile: a good part fetching instructions), 1.5 to 3 us to write a unit's sums, 5 to 10
+// for the merge.
+// What it took, in the order of its worth: arrivals at the other CTA without a fence of global memory (136 -> 89 us in the
+// first case); a merge of its own and partial sums in whole lines (verify 71 -> 61); a unit's last product not behind the next unit's
+// queries; padding rows that do not move references; the heads of a token shared by both CTAs.
+// Rounding: P enters its product as bf16, the type of V (both operands have one type); the output's error against 64 bits is
+// 2.0e-3 (2-norm), 1.7e-3 of it its own rounding to bf16.
 #include <algorithm>
 
 #include "attention_pair.cuh"
@@ -59,10 +72,9 @@ constexpr int kQPanel = kRows * 128;                   // bytes of 64 rows x 64 
 constexpr int kUnits = 4;                              // unit descriptions in flight
 constexpr int kTailBytes = 3 * 1024;
 
-template <int KEYS>
-struct Cfg {
+struct C {
+    static constexpr int KEYS = 64, LOG2 = 6;          // keys of a tile: four tiles fit beside the queries
     static constexpr int HALF = KEYS / 2;              // keys that a CTA loads of a tile
-    static constexpr int LOG2 = KEYS == 128 ? 7 : 6;
     static constexpr int PANEL = HALF * 128;
     static constexpr int TILE = kPanels * PANEL;
     static constexpr int STAGES = 4;
@@ -73,7 +85,6 @@ struct Cfg {
     static constexpr uint32_t TMEM_S = 256;            // columns: O from 0, the two S behind it
     static_assert(SMEM <= 227 * 1024, "shared memory");
     static_assert(STAGES * TILE >= kda_paged::kMaxRequests * 8 + 512, "scratch of find_piece");
-    static_assert(KEYS == 64, "the layout of P has one panel");
 };
 
 // A CTA's rows of a unit: `heads` heads (the second CTA has the ones behind the first's) of `tokens` tokens.  The
@@ -120,7 +131,6 @@ __device__ __noinline__ void add_odd_values(__nv_bfloat16* o, float* sums, int c
     }
 }
 
-template <int KEYS>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 kda_latent_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap qmap1,
                                const __grid_constant__ CUtensorMap kmap,
@@ -128,7 +138,6 @@ kda_latent_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const _
                                const int32_t* __restrict__ cu, const int32_t* __restrict__ seq_len, Shape s, Tiling tiling,
                                float scale_log2, __nv_bfloat16* __restrict__ o, float* __restrict__ lse, Partials parts,
                                int* status) {
-    using C = Cfg<KEYS>;
     extern __shared__ __align__(1024) unsigned char sm[];
     Tail& tl = *reinterpret_cast<Tail*>(sm + C::TAIL);
     const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
@@ -297,7 +306,7 @@ kda_latent_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const _
         n_ld = g;
     } else if (w == kIssueWarp) {
         // ---------------- products: CTA 0 issues for both.  All lanes wait, an elected one issues
-        const uint32_t id_s = kda::idesc_bf16(128, KEYS, 0, 0), id_o = kda::idesc_bf16(128, 256, 0, 1);
+        const uint32_t id_s = kda::idesc_bf16(128, C::KEYS, 0, 0), id_o = kda::idesc_bf16(128, 256, 0, 1);
         const uint64_t q_desc = kda::sw128_desc(kda::smem_u32(sm), 16, 1024);
         const uint64_t k_desc = kda::sw128_desc(kda::smem_u32(sm + C::KV0), 16, 1024);
         const uint64_t v_desc = kda::sw128_desc(kda::smem_u32(sm + C::KV0), C::PANEL, 1024);
@@ -317,7 +326,7 @@ kda_latent_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const _
 #pragma unroll
                 for (int j = 0; j < 2; ++j)
 #pragma unroll
-                    for (int i = 0; i < KEYS / 16; ++i) {
+                    for (int i = 0; i < C::KEYS / 16; ++i) {
                         const int hi = i >= C::HALF / 16;          // second half of the keys: two places on
                         mma_pair(tmem + j * 128, p_desc + kda::desc_step(i * 32),
                                  b + kda::desc_step((4 * j + 2 * hi) * C::PANEL + (i - hi * (C::HALF / 16)) * 2048), id_o,
@@ -595,8 +604,6 @@ bool make_map(CUtensorMap* m, const void* base, cuuint64_t d1, cuuint64_t d2, cu
                                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-constexpr int kKeys = 64;
-
 }  // namespace
 
 namespace kda_host {
@@ -607,7 +614,7 @@ PagedPlan latent_plan_tc(int T, int H) {
     p.Gv = 2 * t.heads;                                // heads of a unit
     p.U = t.tokens;
     p.rows = paged_slot_rows(p.U, T, p.Gv);
-    p.tile_log2 = Cfg<kKeys>::LOG2;
+    p.tile_log2 = C::LOG2;
     p.max_ctas = 80;                                   // pairs
     p.extra = 5;
     return p;
@@ -622,17 +629,17 @@ cudaError_t launch_latent_attention_tc(const LatentArgs& a) {
     constexpr cuuint64_t row = kRow * 2;
     if (!make_map(&qm, a.q, a.H, a.T, row, (cuuint64_t)a.q_stride * 2, t.heads, t.tokens) ||
         !make_map(&qm1, a.q, a.H, a.T, row, (cuuint64_t)a.q_stride * 2, t.heads, 1) ||
-        !make_map(&km, a.cache, a.page_size, a.n_pages, row, row * a.page_size, std::min(a.page_size, Cfg<kKeys>::HALF), 1))
+        !make_map(&km, a.cache, a.page_size, a.n_pages, row, row * a.page_size, std::min(a.page_size, C::HALF), 1))
         return cudaErrorInvalidValue;
-    auto kern = kda_latent_attention_tc_kernel<kKeys>;
+    auto kern = kda_latent_attention_tc_kernel;
     static OncePerDevice once;
     const cudaError_t e = once.run([&] {
-        return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<kKeys>::SMEM);
+        return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
     });
     if (e != cudaSuccess) return e;
     const int pairs = std::min(p.max_ctas, sm_count() / 2);
     const cudaError_t err = launch_overlapped(
-        kern, 2 * pairs, kThreads, Cfg<kKeys>::SMEM, a.stream, 1, qm, qm1, km, static_cast<const __nv_bfloat16*>(a.cache),
+        kern, 2 * pairs, kThreads, C::SMEM, a.stream, 1, qm, qm1, km, static_cast<const __nv_bfloat16*>(a.cache),
         a.block_table, a.cu_seqlens, a.seq_len, latent_shape(a, p), t, a.scale * kLog2e, static_cast<__nv_bfloat16*>(a.o), a.lse,
         paged_partials(pa, p), a.status);
     if (err != cudaSuccess) return err;
