@@ -176,12 +176,15 @@ kda_latent_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const _
     }
     cluster_arrive();                                  // both CTAs' barriers will be there
     asm volatile("griddepcontrol.wait;" ::: "memory");   // the kernels before this one are complete
-    // this pair's piece of the work; both CTAs find the same
+    // this pair's piece of the work; both CTAs find the same.  Few requests: the walking warp does, below
     auto* cost = reinterpret_cast<unsigned long long*>(sm + C::KV0);
-    auto* red = cost + kda_paged::kMaxRequests;
-    const Piece piece = kda_paged::find_piece<kThreads>(s, cu, seq_len, cluster, gridDim.x >> 1, cost, red,
-                                                        reinterpret_cast<Piece*>(red + kThreads / 32));
-    kda::fence_proxy_async_smem();                     // the scratch becomes the target of copies
+    Piece piece{};
+    if (s.n_req > kda_paged::kWarpRequests) {
+        auto* red = cost + kda_paged::kMaxRequests;
+        piece = kda_paged::find_piece<kThreads>(s, cu, seq_len, cluster, gridDim.x >> 1, cost, red,
+                                                reinterpret_cast<Piece*>(red + kThreads / 32));
+        kda::fence_proxy_async_smem();                 // the scratch becomes the target of copies
+    }
     kda::tc_fence_before();
     __syncthreads();
     cluster_wait();
@@ -224,6 +227,10 @@ kda_latent_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const _
     if (w == kWalkWarp) {
         // ---------------- unit descriptions
         if (lane == 0 && rank == 0) parts.clear_both(cluster);
+        if (s.n_req <= kda_paged::kWarpRequests) {
+            piece = kda_paged::find_piece_warp(s, cu, seq_len, cluster, gridDim.x >> 1, cost);
+            kda::fence_proxy_async_smem();
+        }
         Walker walk;
         walk.start(s, cu, seq_len, piece, cluster);
         for (int k = 0;; ++k) {

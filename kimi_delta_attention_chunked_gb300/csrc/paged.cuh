@@ -235,6 +235,60 @@ __device__ __forceinline__ Piece find_piece(const Sh& s, const int32_t* __restri
     return *shared;
 }
 
+// The same by one warp alone, for up to kWarpRequests requests: fewer instructions and no barrier of the block,
+// so the other warps go on to their parts meanwhile.  `cost` holds n_req words of shared memory.
+constexpr int kWarpRequests = 512;
+template <class Sh>
+__device__ __forceinline__ Piece find_piece_warp(const Sh& s, const int32_t* __restrict__ cu,
+                                                 const int32_t* __restrict__ seq_len, int c, int C, unsigned long long* cost) {
+    const int lane = threadIdx.x & 31;
+    Piece p{};
+    unsigned long long total = 0;
+#pragma unroll 1
+    for (int base = 0; base < s.n_req; base += 32) {
+        p.r = Req{0, 0, 0, 0};
+        if (base + lane < s.n_req) p.r = load_req(s, cu, seq_len, base + lane);
+        const unsigned long long x = request_places(s, p.r);
+        if (base + lane < s.n_req) cost[base + lane] = x;
+        total += x;
+    }
+    __syncwarp();
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+    p.total = total * (unsigned)s.Hv;
+    p.ctas = (int)min((unsigned long long)C, most_pieces(s, p.total));
+    if (c >= p.ctas) return p;
+    p.begin = p.total * (unsigned)c / (unsigned)p.ctas;
+    p.end = p.total * (unsigned)(c + 1) / (unsigned)p.ctas;
+    p.off = p.begin;
+#pragma unroll 1
+    for (int base = 0; base < s.n_req; base += 32) {
+        const unsigned long long x = base + lane < s.n_req ? cost[base + lane] : 0;
+        unsigned long long incl = x * (unsigned)s.Hv;
+        const unsigned long long mine = incl;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const unsigned long long t = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += t;
+        }
+        const unsigned hit = __ballot_sync(0xffffffffu, p.off < incl);
+        if (hit) {
+            const int src = __ffs((int)hit) - 1;
+            p.off -= __shfl_sync(0xffffffffu, incl - mine, src);
+            p.len = __shfl_sync(0xffffffffu, x, src);
+            p.n = base + src;
+            p.known = s.n_req <= 32;                   // a lane has one request
+            p.r.tok0 = __shfl_sync(0xffffffffu, p.r.tok0, src);
+            p.r.len = __shfl_sync(0xffffffffu, p.r.len, src);
+            p.r.pos0 = __shfl_sync(0xffffffffu, p.r.pos0, src);
+            p.r.kend = __shfl_sync(0xffffffffu, p.r.kend, src);
+            return p;
+        }
+        p.off -= __shfl_sync(0xffffffffu, incl, 31);
+    }
+    return p;
+}
+
 // A cut unit of more rows than this is joined by the blocks of all its CTAs (if they are many).
 constexpr int kSpreadRows = 64;
 

@@ -178,6 +178,12 @@ def test_absorbed_many_requests(dt):
     check_absorbed(*absorbed_case([(17 * i % 301, 1 + i % 3) for i in range(400)], 4, 16, dt))
 
 
+def test_thousands_of_requests():
+    """More requests than one warp looks through alone."""
+    check_absorbed(*absorbed_case([(7 * i % 90, i % 3) for i in range(1500)], 2, 16, BF16))
+    check_expanded(expanded_case([(i % 4, 5 * i % 70) for i in range(1300)], 1, BF16))
+
+
 @pytest.mark.parametrize("dt", DTYPES)
 @pytest.mark.parametrize("bad", [-1, "n_pages", 2 ** 31 - 1, -2 ** 31])
 def test_absorbed_missing_pages(bad, dt):
