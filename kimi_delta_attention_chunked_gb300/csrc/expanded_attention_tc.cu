@@ -29,16 +29,18 @@
 // request's), and in the rows that some see and some do not takes out the elements that are not
 // finite; the output adds such elements to the rows that see them.
 //
-// Bound, and what it measured (GPU time with the merge; cuBLAS 1888 TFLOP/s).  A prompt of 8192 tokens, 32 heads: 418 us, 1.64
-// PFLOP/s of the products that a causal mask leaves (floor 364): a tile of two steps takes 2970 cycles, 2560 of them products, and a unit's
-// end (its last two tiles have one row tile, its output) 10 k cycles of 60 k to 190 k.  12 requests of 1 to 700 tokens over up
-// to 3200 keys, 16 heads: 46 us (floor 10.6): 2 to 6 short units a pair at 7 to 8 k cycles each.
-// What it took: arrivals at the other CTA without a fence of global memory (684 -> 528 us); the weights in two halves, so that
-// the first half's products run while the second is formed, no steps of a row tile behind its last key, values cleaned off
-// the softmax warps' path (518 -> 427); places of the division that count steps (444 -> 427); one short output loop (424 -> 418).
-// Queries of lone row tiles fetched a unit ahead gained nothing.
-// Rounding: P enters its product as bf16, the type of V; the output's error against 64 bits is 2.0e-3 (2-norm), 1.5e-3
-// of it its own rounding to bf16.
+// Bound, and what it measured (GPU time with the merge; cuBLAS 1888 TFLOP/s).  A prompt of 8192 tokens,
+// 32 heads: 418 us, 1.64 PFLOP/s of the products that a causal mask leaves (floor 364): a tile of two steps
+// takes 2970 cycles, 2560 of them products, and a unit's end (its last two tiles have one row tile, its
+// output) 10 k cycles of 60 k to 190 k.  12 requests of 1 to 700 tokens over up to 3200 keys, 16 heads: 46 us
+// (floor 10.6): 2 to 6 short units a pair at 7 to 8 k cycles each.
+// What it took: arrivals at the other CTA without a fence of global memory (684 -> 528 us); the weights in two
+// halves, so that the first half's products run while the second is formed, and no steps of a row tile
+// behind its last key (518 -> 440); places of the division that count steps (444 -> 427); values cleaned off
+// the softmax warps' path, one short output loop (431 -> 418).  Queries of lone row tiles fetched a unit
+// ahead gained nothing.
+// Rounding: P enters its product as bf16, the type of V; the output's error against 64 bits is 2.0e-3
+// (2-norm), 1.5e-3 of it its own rounding to bf16.
 #include <algorithm>
 
 #include "attention_pair.cuh"
@@ -81,7 +83,8 @@ struct UnitSlot {
 };
 
 struct Tail {
-    uint64_t k_full[kStages], v_full[kStages], v_ready[kStages], q_full, p_full[2][2];  // CTA 0's are used; P in halves of its keys
+    uint64_t k_full[kStages], v_full[kStages], v_ready[kStages], q_full;             // CTA 0's are used
+    uint64_t p_full[2][2];                             // too; P in halves of its keys
     uint64_t k_empty[kStages], v_empty[kStages], q_empty, s_full[2], o_full[2], landed[kStages];    // each CTA's own
     uint64_t join_a, join_b;
     uint64_t u_full[kUnits], u_empty[kUnits];
@@ -107,8 +110,9 @@ struct Values {
     long long token, head;
 };
 
-// Adds to a row's output or partial sums, channels from .. to - 1, the values that are not finite, of the keys [first, last)
-// among those that not all rows of the unit see: rare, and so out of the way of what every unit fetches.
+// Adds to a row's output or partial sums, channels from .. to - 1, the values that are not finite, of the keys
+// [first, last) among those that not all rows of the unit see: rare, and so out of the way of what every unit
+// fetches.
 __device__ __noinline__ void add_odd_values(__nv_bfloat16* o, float* sums, int cap, int from, int to, const __nv_bfloat16* v,
                                             long long token, int first, int last) {
     for (int key = first; key < last; ++key)
@@ -287,7 +291,7 @@ kda_expanded_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const
                     const int from = max(un.all_hi - k0, 0), to = min(max(un.hi - k0, 0), kKeys);
                     bool odd = false;
 #pragma unroll 4
-                    for (int e = from * 8 + lane; e < to * 8; e += 32) {     // some rows see them: what is not finite is taken out
+                    for (int e = from * 8 + lane; e < to * 8; e += 32) {     // some rows see them
                         uint4* at = reinterpret_cast<uint4*>(v + e * 16);
                         uint4 x = *at;
                         if (take_odd(x)) {
@@ -427,6 +431,10 @@ kda_expanded_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const
         for (int k = 0; ok; ++k) {
             Unit u;
             if (!read_unit(k, u)) break;
+            // the flag of the unit after the next three.  Nobody sets it yet: its values come into the ring when those of
+            // the next unit are done with, which takes this warp's part in this one; and nobody reads it any more for
+            // the unit four back
+            if (tid == 0) tl.odd_values[(k + 4) & 7] = 0;
             const bool two = u.ntok > kTileTokens;
             const int tiles = u.te - u.tb, steps = tiles << (two ? 1 : 0);
             const int t0 = (h ^ g) & 1;                // this half's first step
@@ -608,9 +616,6 @@ kda_expanded_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const
                 ++n_j;
                 if (!ok) break;
             }
-            // for the unit after the next three: no warp of either CTA is there yet, and none is still at
-            // the one four back (every unit takes all warps of one half, and the halves meet within two)
-            if (tid == 0) tl.odd_values[(k + 4) & 7] = 0;
             g += steps;
         }
     }

@@ -3,7 +3,8 @@
 //
 // A cache row of 576 channels is the key of every head and its first 512 channels the
 // value.  A unit (paged.cuh) is up to 128 rows (a token and a query head each), up to 64 in either
-// CTA of a cluster of two: half of the heads of the same tokens.  Per tile of KEYS keys, with cta_group::2 products of M = 128:
+// CTA of a cluster of two: half of the heads of the same tokens.  Per tile of KEYS keys, with cta_group::2
+// products of M = 128:
 //     S = Q K^T     (128 x KEYS over 576 channels, both operands in shared memory)
 //     P = 2^(scale log2(e) S - m)   (registers; bf16 to shared memory)
 //     O += P V      (128 x 512 over KEYS keys, two products of N = 256)
@@ -37,18 +38,19 @@
 // sees, and in rows that some see and some do not take out the elements that are not finite.  They note
 // if they found one (in both CTAs); the output then adds such elements to the rows that see them.
 //
-// Bound, and what it measured (GPU time with the merge; HBM 6790 GB/s, cuBLAS 1888 TFLOP/s).  While it streams, HBM: a 64-key
-// tile of a pair takes 0.85 us of the 0.83 that the copy rate allows, for any number of rows up to 128; with the cache in L2 (many
-// units of a request), the tensor cores: 0.79 us of the 0.72 that cuBLAS's rate allows.  64 requests of 1 K to 16 K keys, 32
-// heads: 82 us (floor 61).  24 requests of 2 K to 32 K keys, 128 heads: 73 us (46).  32 x 8 tokens, 32 heads, 0.7 K to 8 K keys:
-// 61 us (29).  4 requests of 90 to 1500 keys: 14.3 us.  Above the floors: 5 us before a pair's first product (its piece, the
-// first unit, the page table, the first tile: a good part fetching instructions), 1.5 to 3 us to write a unit's sums, 5 to 10
-// for the merge.
-// What it took, in the order of its worth: arrivals at the other CTA without a fence of global memory (136 -> 89 us in the
-// first case); a merge of its own and partial sums in whole lines (verify 71 -> 61); a unit's last product not behind the next unit's
-// queries; padding rows that do not move references; the heads of a token shared by both CTAs.
-// Rounding: P enters its product as bf16, the type of V (both operands have one type); the output's error against 64 bits is
-// 2.0e-3 (2-norm), 1.7e-3 of it its own rounding to bf16.
+// Bound, and what it measured (GPU time with the merge; HBM 6790 GB/s, cuBLAS 1888 TFLOP/s).  While it streams,
+// HBM: a 64-key tile of a pair takes 0.85 us of the 0.83 that the copy rate allows, for any number of rows up to
+// 128; with the cache in L2 (many units of a request), the tensor cores: 0.79 us of the 0.72 that cuBLAS's rate
+// allows.  64 requests of 1 K to 16 K keys, 32 heads: 82 us (floor 61).  24 requests of 2 K to 32 K keys, 128
+// heads: 73 us (46).  32 x 8 tokens, 32 heads, 0.7 K to 8 K keys: 60 us (29).  4 requests of 90 to 1500 keys:
+// 14.2 us.  Above the floors: 5 us before a pair's first product (its piece, the first unit, the page table, the
+// first tile: a good part fetching instructions), 1.5 to 3 us to write a unit's sums, 5 to 10 for the merge.
+// What it took, in the order of its worth: arrivals at the other CTA without a fence of global memory (136 ->
+// 89 us in the first case); a merge of its own and partial sums in whole lines (verify 71 -> 61); a unit's last
+// product not behind the next unit's queries; padding rows that do not move references; the heads of a token
+// shared by both CTAs; the piece found by one warp.
+// Rounding: P enters its product as bf16, the type of V (both operands have one type); the output's error
+// against 64 bits is 2.0e-3 (2-norm), 1.7e-3 of it its own rounding to bf16.
 #include <algorithm>
 
 #include "attention_pair.cuh"
@@ -113,8 +115,9 @@ struct Tail {
 };
 static_assert(sizeof(Tail) <= kTailBytes, "tail");
 
-// Adds to a row's output or partial sums, 128 channels from each of c0 and c0 + 256 on, the values that are not finite, of the
-// keys [first, last) among those that not all rows of the unit see: rare, and so out of the way of what every unit fetches.
+// Adds to a row's output or partial sums, 128 channels from each of c0 and c0 + 256 on, the values that are not
+// finite, of the keys [first, last) among those that not all rows of the unit see: rare, and so out of the way of
+// what every unit fetches.
 __device__ __noinline__ void add_odd_values(__nv_bfloat16* o, float* sums, int cap, int c0, const Shape& s,
                                             const __nv_bfloat16* cache, const int32_t* pages, int first, int last) {
     for (int key = first; key < last; ++key) {

@@ -5,8 +5,9 @@
 // A slot's sums lie four channels wide, [D / 4][rows][4]: the threads of the attention kernels hold a row
 // each, so a warp's store and a warp's load here are whole lines (by rows, 128 of 512 channels took a pair of
 // CTAs 5,700 cycles to write).  A warp takes 16 channels of 32 rows, or, where there are more than
-// four parts, of 8 rows with four lanes to a row; the warps of all CTAs that hold a part of a unit share it out.  Bound: latency (description, then statistics and sums: 5 us
-// for units of a few rows) and, with 128 and more rows in every slot, L2 (40 MB: 8 to 10 us).
+// four parts, of 8 rows with four lanes to a row; the warps of all CTAs that hold a part of a unit share it
+// out.  Bound: latency (description, then statistics and sums: 5 us for units of a few rows) and, with 128 and
+// more rows in every slot, L2 (40 MB: 8 to 10 us).  Two parts at once and twice the blocks: 2 us slower.
 #include <algorithm>
 
 #include "latent.cuh"

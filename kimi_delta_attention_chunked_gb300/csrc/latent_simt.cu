@@ -12,8 +12,8 @@
 // threads form 4 x 4 scores each (over a part of the channels: the parts are added up in the
 // softmax step), then DV / 4 column groups of 4 with ROWS / RPT row groups of RPT rows each.
 // Bound: latency of a tile's loads and steps, then shared memory (a 16-byte load of a warp takes four cycles,
-// whatever its addresses): 6 requests of 1 to 9 tokens over 17 to 2100 keys, 5 heads, absorbed, 20.6 us with the merge; 5 prompts
-// of 3 to 260 tokens over up to 860 keys, 5 heads, expanded, 40 us.
+// whatever its addresses): 6 requests of 1 to 9 tokens over 17 to 2100 keys, 5 heads, absorbed, 20.6 us with the
+// merge; 5 prompts of 3 to 260 tokens over up to 860 keys, 5 heads, expanded, 40 us.
 #include <algorithm>
 #include <type_traits>
 
