@@ -681,3 +681,57 @@ def test_append_slot_named_twice(dt):
     kda.kda_latent_append(rows[:, :512], rows[:, 512:], cache, torch.tensor([5, 5], device="cuda"))
     got = cache[0, 5].float()
     assert bool(((got == 1) | (got == 2)).all()) and not cache[0, :5].any() and not cache[0, 6:].any()
+
+
+@pytest.mark.parametrize("H", [257, 700])
+def test_absorbed_hundreds_of_heads(H):
+    """More heads than one unit holds, and a last group with fewer of them."""
+    check_absorbed(*absorbed_case([(150, 2), (0, 1), (333, 1)], H, 64, BF16, seed=H))
+
+
+def test_two_threads():
+    """Calls at once from two host threads, each on its own stream."""
+    import threading
+    cases = [[x.cuda() for x in absorbed_case([(500 + 90 * i, 2), (33, 1)], 16, 32, BF16, seed=i)] for i in range(2)]
+    packed = [on_gpu(expanded_case([(150, 300 + 70 * i), (5, 9)], 3, BF16, seed=i)) for i in range(2)]
+    want = [(kda.kda_latent_attention(*cases[i], SCALE), kda.kda_expanded_attention(*packed[i])) for i in range(2)]
+    torch.cuda.synchronize()
+    wrong = []
+
+    def work(i):
+        stream = torch.cuda.Stream()
+        with torch.cuda.stream(stream):
+            for _ in range(25):
+                got = kda.kda_latent_attention(*cases[i], SCALE), kda.kda_expanded_attention(*packed[i])
+                stream.synchronize()
+                if not all(torch.equal(a, b) for a, b in zip(got, want[i])):
+                    wrong.append(i)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong
+    assert kda.kda_get_last_device_status() == 0
+
+
+def test_absorbed_beside_other_kernels():
+    """On another stream the recurrent layer's prefill holds shared memory and TMEM of the same SMs."""
+    from kimi_delta_attention_chunked_gb300 import inputs
+    w = inputs.Workload("beside", "prefill", H=32, dk=128, dv=128, dtype=BF16, chunk=64)
+    d = inputs.make_prefill(w, device=torch.device("cuda", 0), seed=0, lengths=[2048])
+    run = lambda: kda.kda_prefill(d["q"], d["k"], d["v"], d["log_alpha"], d["beta"], cu_seqlens=d["cu_seqlens"],  # noqa: E731
+                                  cu_seqlens_host=d["cu_seqlens_host"], chunk=64)
+    case = [x.cuda() for x in absorbed_case([(2000, 1), (700, 3)], 32, 64, BF16)]
+    packed = on_gpu(expanded_case([(600, 900)], 4, BF16))
+    want, want_e, want_p = kda.kda_latent_attention(*case, SCALE), kda.kda_expanded_attention(*packed), run()
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for _ in range(10):
+        with torch.cuda.stream(side):
+            got_p = [run() for _ in range(3)]
+        got = [(kda.kda_latent_attention(*case, SCALE), kda.kda_expanded_attention(*packed)) for _ in range(3)]
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, want) and torch.equal(b, want_e) for a, b in got)
+        assert all(torch.equal(a[0], want_p[0]) and torch.equal(a[1], want_p[1]) for a in got_p)
