@@ -66,12 +66,13 @@ __device__ __forceinline__ void mma_pair_ta(uint32_t d, uint32_t a, uint64_t b, 
         "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
         : "memory");
 }
-// Arrive once on the barrier at this place in both CTAs when the products issued so far are done.
-__device__ __forceinline__ void commit_pair(uint64_t* bar) {
+// Arrive once on the barrier at this place in both CTAs (or those of `mask`) when the products issued so far are done.
+// Nothing may arrive at a CTA that has left: each one waits for, or for something behind, every arrival that it gets.
+__device__ __forceinline__ void commit_pair(uint64_t* bar, uint16_t mask = 3) {
     asm volatile(
         "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
             kda::smem_u32(bar)),
-        "h"((uint16_t)3)
+        "h"(mask)
         : "memory");
 }
 // All of TMEM, in both CTAs: one warp of each calls these.

@@ -415,7 +415,7 @@ kda_expanded_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const
         if (ok && (older.flags & kDue)) ok = values_step(g & 1, older);
         if (ok && (newer.flags & kDue)) ok = values_step((g + 1) & 1, newer);
         if (issued) {                                  // no product in flight when TMEM is freed
-            if (elect_one()) commit_pair(&tl.drain);
+            if (elect_one()) commit_pair(&tl.drain, 1);
             __syncwarp();
             (void)kda::mbar_wait(&tl.drain, 0, kda::kWaitCycles);
         }

@@ -385,7 +385,7 @@ kda_latent_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const _
         }
         if (ok && due) ok = values_step(g - 1);
         if (issued) {                                  // no product in flight when TMEM is freed
-            if (elect_one()) commit_pair(&tl.drain);
+            if (elect_one()) commit_pair(&tl.drain, 1);
             __syncwarp();
             (void)kda::mbar_wait(&tl.drain, 0, kda::kWaitCycles);
         }
