@@ -72,7 +72,7 @@ constexpr int kRows = 64;                              // rows of a CTA
 constexpr int kPanels = kRow / 64;                     // of a key
 constexpr int kQPanel = kRows * 128;                   // bytes of 64 rows x 64 channels
 constexpr int kUnits = 4;                              // unit descriptions in flight
-constexpr int kTailBytes = 3 * 1024;
+constexpr int kTailBytes = 2 * 1024;
 
 struct C {
     static constexpr int KEYS = 64, LOG2 = 6;          // keys of a tile: four tiles fit beside the queries
