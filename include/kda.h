@@ -463,7 +463,8 @@ KDA_API size_t kda_latent_attention_workspace_size(int T, int H, kda_dtype dtype
  * A row that sees no key gives o = 0, lse = -inf.  Keys whose block_table entry names
  * no page of the cache are left out, as are keys past max_blocks * page_size.  What
  * stands in the cache at places that a row does not see, NaN among it, does not reach
- * that row.
+ * that row.  A latent channel that is not finite makes that channel NaN in the rows
+ * that see it, and the whole row unless the key scores -inf (its weight is then 0).
  *
  * q           [T, H, 576] dtype, consecutive tokens q_stride elements apart
  * cu_seqlens  [N + 1] int32 device array, 0 = cu[0] <= ... <= cu[N] <= T;
@@ -498,7 +499,9 @@ KDA_API size_t kda_expanded_attention_workspace_size(int T, int H, kda_dtype dty
  *     o = sum_j exp(z_j - lse) v[j, h],   lse = ln sum_j exp(z_j)
  *
  * A row that sees no key gives o = 0, lse = -inf.  What stands in the keys and values at
- * places that a row does not see, NaN among it, does not reach that row.
+ * places that a row does not see, NaN among it, does not reach that row.  A value that is
+ * not finite makes its channel infinite or NaN in the rows that see it (either, where its
+ * weight is 0 in fp32).
  *
  * q             [T, H, 192] dtype, consecutive tokens q_stride elements apart
  * k_nope, v     [S, H, 128] dtype, token and head strides in elements (both may be slices of

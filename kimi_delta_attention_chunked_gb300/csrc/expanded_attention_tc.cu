@@ -542,7 +542,8 @@ kda_expanded_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const
             const int which = u.first ? 1 : 0;
             // sources in TMEM and their factors, columns of this thread, statistics of the row
             uint32_t src0 = kTmemO + h * 128, src1 = src0;
-            float f0 = l == 0.f ? 0.f : 1.f, f1 = 0.f, top = ref, sum_l = l;
+            float f0 = 1.f, f1 = 0.f, top = ref, sum_l = l;
+            bool use0 = true, use1 = false;            // sums that a product wrote; the others hold anything
             int from = 0, to = kValue;
             if (two) {
                 ok = wait(&tl.o_full[h], (o_phase >> h) & 1);
@@ -565,6 +566,8 @@ kda_expanded_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const
                 const float2 st = tl.stats[h ^ 1][row];
                 top = fmaxf(ref, st.x);
                 const float base = top == -INFINITY ? 0.f : top;
+                use0 = steps > 1 || (g & 1) == h;
+                use1 = steps > 1 || (g & 1) != h;
                 f0 = l == 0.f ? 0.f : ex2(ref - base);
                 f1 = st.y == 0.f ? 0.f : ex2(st.x - base);
                 sum_l = fmaf(f0, l, f1 * st.y);
@@ -586,8 +589,8 @@ kda_expanded_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const
                     kda::tmem_ld16(tmem + lane_off + src1 + c, z);
                     kda::tmem_wait_ld();
 #pragma unroll
-                    for (int e = 0; e < 16; ++e)       // a half without a sum holds anything
-                        y[e] = (f0 == 0.f ? 0.f : f0 * y[e]) + (f1 == 0.f ? 0.f : f1 * z[e]);
+                    for (int e = 0; e < 16; ++e)       // a weight of 0 does not hide a sum that is not finite
+                        y[e] = (use0 ? f0 * y[e] : 0.f) + (use1 ? f1 * z[e] : 0.f);
                     if (!valid) continue;
                     if (whole) {
                         store16(dst + c, y);

@@ -36,7 +36,8 @@
 // Masked places.  A zero weight times a NaN or infinity in V is NaN.  So in a tile that not every
 // row sees whole, once S is complete, the softmax warps zero the rows of V that no row of the unit
 // sees, and in rows that some see and some do not take out the elements that are not finite.  They note
-// if they found one (in both CTAs); the output then adds such elements to the rows that see them.
+// if they found one (in both CTAs); the output then makes those channels NaN in the rows that see them.  NaN for an
+// infinity too: the channel is one of the key's as well, so its score is NaN, or infinite and the weight NaN or 0.
 //
 // Bound, and what it measured (GPU time with the merge; HBM 6790 GB/s, cuBLAS 1888 TFLOP/s).  While it streams,
 // HBM: a 64-key tile of a pair takes 0.85 us of the 0.83 that the copy rate allows, for any number of rows up to
@@ -115,10 +116,10 @@ struct Tail {
 };
 static_assert(sizeof(Tail) <= kTailBytes, "tail");
 
-// Adds to a row's output or partial sums, 128 channels from each of c0 and c0 + 256 on, the values that are not
-// finite, of the keys [first, last) among those that not all rows of the unit see: rare, and so out of the way of
-// what every unit fetches.
-__device__ __noinline__ void add_odd_values(__nv_bfloat16* o, float* sums, int cap, int c0, const Shape& s,
+// Makes NaN, in a row's output or partial sums, those of 128 channels from each of c0 and c0 + 256 on in which a key
+// of [first, last), among those that not all rows of the unit see, is not finite: rare, and so out of the way of what
+// every unit fetches.
+__device__ __noinline__ void mark_odd_values(__nv_bfloat16* o, float* sums, int cap, int c0, const Shape& s,
                                             const __nv_bfloat16* cache, const int32_t* pages, int first, int last) {
     for (int key = first; key < last; ++key) {
         const int page = pages[key >> s.page_log2];
@@ -126,10 +127,9 @@ __device__ __noinline__ void add_odd_values(__nv_bfloat16* o, float* sums, int c
         const __nv_bfloat16* v = cache + (((size_t)page << s.page_log2) + (key & ((1 << s.page_log2) - 1))) * kRow;
         for (int i = 0; i < 256; ++i) {
             const int c = c0 + (i & 127) + (i & 128) * 2;
-            const float x = __bfloat162float(v[c]);
-            if ((__float_as_uint(x) & 0x7f800000u) != 0x7f800000u) continue;
-            if (o) o[c] = __float2bfloat16_rn(__bfloat162float(o[c]) + x);
-            else sums[(size_t)(c >> 2) * cap * 4 + (c & 3)] += x;
+            if ((__float_as_uint(__bfloat162float(v[c])) & 0x7f800000u) != 0x7f800000u) continue;
+            if (o) o[c] = __float2bfloat16_rn(NAN);
+            else sums[(size_t)(c >> 2) * cap * 4 + (c & 3)] = NAN;
         }
     }
 }
@@ -562,9 +562,9 @@ kda_latent_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const _
                     }
                 }
                 if (valid && *(volatile int*)&tl.odd_values[k & 3])
-                    add_odd_values(whole ? dst : nullptr, reinterpret_cast<float*>(part), parts.cap, half * 128, s, cache,
-                                   table + (size_t)u.n * s.blocks, max(si.all_hi, u.tb << C::LOG2),
-                                   min(min(si.hi, hi), u.te << C::LOG2));
+                    mark_odd_values(whole ? dst : nullptr, reinterpret_cast<float*>(part), parts.cap, half * 128, s, cache,
+                                    table + (size_t)u.n * s.blocks, max(si.all_hi, u.tb << C::LOG2),
+                                    min(min(si.hi, hi), u.te << C::LOG2));
                 if (valid && half == 0) {
                     const float ref = m == -INFINITY ? -INFINITY : m * scale_log2;
                     if (!whole) parts.stats(cluster, which)[prow] = make_float2(ref, l);

@@ -62,7 +62,7 @@ struct Sum {
             for (int e = 0; e < kBatch; ++e) {
                 const float f = st[e].y == 0.f ? 0.f : ex2(st[e].x - ref);
                 l = fmaf(f, st[e].y, l);
-                if (f != 0.f) {                        // a part that saw no key does not enter
+                if (i0 + e * stride < n) {             // at a weight of 0 too: 0 * NaN is NaN, wherever keys are cut
 #pragma unroll
                     for (int x = 0; x < kWide / 4; ++x) add(acc[x], f, v[e][x]);
                 }
@@ -114,7 +114,7 @@ __device__ __forceinline__ void join(const Partials& parts, const Unit<T>& j, in
                 float* y = &sum.acc[x].x;
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    y[e] = f == 0.f ? 0.f : y[e] * f;
+                    y[e] *= f;
 #pragma unroll
                     for (int d = ROWS; d < 32; d <<= 1) y[e] += __shfl_xor_sync(0xffffffffu, y[e], d);
                 }

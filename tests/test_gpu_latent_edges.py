@@ -1,0 +1,95 @@
+"""Latent attention on the GPU at the ends of its numbers, strides and division."""
+import math
+
+import pytest
+import torch
+
+import kimi_delta_attention_chunked_gb300 as kda
+from _gpu import need_gpu
+from _latent import LATENT, NOPE, ROPE, assert_close, rows_ref
+from test_gpu_latent import DTYPES, SCALE, absorbed_case, expanded_case, on_gpu, run_absorbed
+
+pytestmark = pytest.mark.gpu
+
+INF = float("inf")
+
+
+@pytest.fixture(scope="module", autouse=True)
+def gpu():
+    return need_gpu()
+
+
+def same_kind(got, want, bound, what):
+    """`want` within `bound` where it is finite; not finite where it is not."""
+    got = got.double().cpu()
+    odd = ~torch.isfinite(want)
+    assert not torch.isfinite(got[odd]).any(), f"{what}: {int(torch.isfinite(got[odd]).sum())} finite of {int(odd.sum())}"
+    assert_close(torch.where(odd, torch.zeros_like(got), got), torch.where(odd, torch.zeros_like(want), want), bound, what)
+
+
+# ------------------------------------------------------------------ values that are not finite, seen at a weight of zero
+# (earlier tokens, new ones) of the requests; the keys of each whose channel becomes infinite
+SEEN = {
+    "at the edge of one tile": ([(57, 6)], lambda n: [60]),
+    "in and behind whole tiles": ([(130, 2)] * 160, lambda n: [10] if n % 3 == 0 else [131] if n % 3 == 1 else []),
+    "all keys of a part": ([(5000, 2)], lambda n: list(range(64, 192)) + [5001]),
+}
+
+
+@pytest.mark.parametrize("dt", DTYPES)
+@pytest.mark.parametrize("where", list(SEEN))
+def test_absorbed_infinities_of_no_weight(where, dt):
+    """An infinite latent against a query of the other sign scores -inf: its key weighs nothing, and 0 * inf makes
+    that channel NaN for the rows that see it, wherever its tile lies and however the keys are divided."""
+    lens, odd = SEEN[where]
+    H = 3
+    q, cache, table, cu, seq = absorbed_case(lens, H, 64, dt, seed=1)
+    q[..., 7] = -q[..., 7].abs() - 1.0
+    T = q.shape[0]
+    o = torch.zeros(T, H, LATENT, dtype=torch.float64)
+    lse, bo, bl = torch.zeros(T, H, dtype=torch.float64), torch.zeros_like(o), torch.zeros(T, H, dtype=torch.float64)
+    for n, (ctx, m) in enumerate(lens):
+        keys, bad = ctx + m, torch.tensor(odd(n), dtype=torch.long)
+        rows = cache[table[n].long().repeat_interleave(64)[:keys], torch.arange(keys) % 64].double()
+        good = torch.ones(keys, dtype=torch.bool)
+        good[bad] = False
+        for i in range(m):
+            K = rows[:ctx + i + 1][good[:ctx + i + 1]][:, None]
+            t = int(cu[n]) + i
+            o[t], lse[t], bo[t], bl[t] = rows_ref(q[t].double(), K, K[..., :LATENT], SCALE, dt)
+            if bool((bad <= ctx + i).any()):
+                o[t, :, 7] = math.nan
+        for j in bad.tolist():
+            cache[table[n, j // 64], j % 64, 7] = INF
+    got, gl = run_absorbed(q, cache, table, cu, seq)
+    same_kind(got, o, bo, "o")
+    assert bool(torch.isnan(got.cpu()[..., 7][torch.isnan(o[..., 7])]).all())
+    assert_close(gl, lse, bl, "lse")
+
+
+@pytest.mark.parametrize("dt", DTYPES)
+@pytest.mark.parametrize("lens,keys", [([(40, 60)], [45]), ([(300, 700)], [3, 690]), ([(2, 5000)], list(range(128, 384))),
+                                       ([(300, 2000)], list(range(128, 640))), ([(100, 256)], list(range(128, 256)))])
+def test_expanded_infinities_of_no_weight(lens, keys, dt):
+    """The same of keys that score -inf in the expanded form: the channel is not finite for the rows that see the key,
+    the others are as without it."""
+    H = 2
+    q, kn, kr, v, cu, cu_k = case = expanded_case(lens, H, dt, seed=2)
+    q[..., NOPE] = -q[..., NOPE].abs() - 1.0
+    (m, s), bad = lens[0], torch.tensor(keys)
+    good = torch.ones(s, dtype=torch.bool)
+    good[bad] = False
+    K = torch.cat([kn, kr[:, None].expand(s, H, ROPE)], 2).double()
+    V = v.double()
+    o = torch.zeros(m, H, 128, dtype=torch.float64)
+    lse, bo, bl = torch.zeros(m, H, dtype=torch.float64), torch.zeros_like(o), torch.zeros(m, H, dtype=torch.float64)
+    for i in range(m):
+        g = good[:s - m + i + 1]
+        o[i], lse[i], bo[i], bl[i] = rows_ref(q[i].double(), K[:len(g)][g], V[:len(g)][g], SCALE, dt)
+        if not bool(g.all()):
+            o[i, 1, 9] = math.nan
+    kr[bad, 0] = INF
+    v[bad, 1, 9] = INF
+    got, gl = kda.kda_expanded_attention(*on_gpu(case), scale=SCALE, want_lse=True)
+    same_kind(got, o, bo, "o")
+    assert_close(gl, lse, bl, "lse")
