@@ -470,7 +470,9 @@ KDA_API size_t kda_latent_attention_workspace_size(int T, int H, kda_dtype dtype
  * cu_seqlens  [N + 1] int32 device array, 0 = cu[0] <= ... <= cu[N] <= T;
  *             rows of q at and past cu[N] are padding, their o is not written
  * seq_len     [N] int32 device array
- * scale       > 0 and at most 2^127 (of the expanded head: usually 192^-1/2)
+ * scale       > 0 and at most 2^127 (of the expanded head: usually 192^-1/2).  A row whose
+ *             largest score, times log2(e), is past the range of fp32 becomes NaN, on the
+ *             tensor-core path one whose largest is 2^29 or more from 0
  * max_blocks  at most KDA_MAX_STEP_POSITIONS / page_size
  * o           [T, H, 512] dtype, 32-byte aligned;  lse [T, H] float or NULL
  * workspace   kda_latent_attention_workspace_size bytes, 256-byte aligned; a call has it to
@@ -511,7 +513,9 @@ KDA_API size_t kda_expanded_attention_workspace_size(int T, int H, kda_dtype dty
  *               at the end; rows of q at and past cu_seqlens[N] are padding, their o is
  *               not written
  * S + T         at most KDA_MAX_STEP_POSITIONS
- * scale         > 0 and at most 2^127
+ * scale         > 0 and at most 2^127.  A row whose largest score, times log2(e), is past the
+ *               range of fp32 becomes NaN, on the tensor-core path one whose largest is 2^29
+ *               or more from 0
  * o             [T, H, 128] dtype, 32-byte aligned;  lse [T, H] float or NULL
  * workspace     kda_expanded_attention_workspace_size bytes, 256-byte aligned; a call has it
  *               to itself until it is complete

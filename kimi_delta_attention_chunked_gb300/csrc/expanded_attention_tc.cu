@@ -506,7 +506,7 @@ kda_expanded_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const
                         if (grow) m = big;
                     }
                 }
-                const float ref = m == -INFINITY ? 0.f : m * scale_log2;
+                const float ref = kda_paged::reference(m, scale_log2);
                 const uint64_t sc2 = pack2(scale_log2, scale_log2), off2 = pack2(-ref, -ref);
                 uint64_t sum[2] = {0, 0};
                 uint32_t p[32];
@@ -536,7 +536,9 @@ kda_expanded_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const
             }
             if (!ok) break;
             // ---- output: one short loop for every kind of unit, since it is fetched anew each time
-            const float ref = m == -INFINITY ? -INFINITY : m * scale_log2;
+            const float2 mine_st = kda_paged::row_stats(m, l, scale_log2);
+            const float ref = mine_st.x;
+            l = mine_st.y;
             const size_t at = (size_t)(u.tok0 + tok) * s.Hq + u.qh0;
             const bool whole = u.first && u.last;
             const int which = u.first ? 1 : 0;
@@ -577,6 +579,7 @@ kda_expanded_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const
             }
             kda::tc_fence_after();
             if (busy) {
+                if (whole) sum_l = kda_paged::whole_sum(top, sum_l);
                 const float inv = !whole ? 1.f : sum_l == 0.f ? 0.f : 1.f / sum_l;
                 f0 *= inv;
                 f1 *= inv;

@@ -474,7 +474,7 @@ kda_latent_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const _
                             if (grow) m = big;
                         }
                     }
-                    const float ref = m == -INFINITY ? 0.f : m * scale_log2;
+                    const float ref = kda_paged::reference(m, scale_log2);
                     const uint64_t sc2 = pack2(scale_log2, scale_log2), off2 = pack2(-ref, -ref);
                     uint64_t sum[2] = {0, 0};
 #pragma unroll
@@ -534,6 +534,7 @@ kda_latent_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const _
                 if (!join()) break;
                 l += tl.sum[half ^ 1][row];
             }
+            const float2 st = kda_paged::row_stats(m, l, scale_log2);
             if (!wait(&tl.kv_empty[last % C::STAGES], (last / C::STAGES) & 1)) break;
             kda::tc_fence_after();
             if (busy) {
@@ -541,7 +542,7 @@ kda_latent_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const _
                 const int which = u.first ? 1 : 0;
                 const size_t at = (size_t)(u.tok0 + tok_in) * s.Hq + u.qh0 + head_in;
                 const int prow = tok_in * 2 * tiling.heads + head_in;                // row of a partial slot
-                const float inv = l == 0.f ? 0.f : 1.f / l;
+                const float sum_l = kda_paged::whole_sum(st.x, st.y), inv = sum_l == 0.f ? 0.f : 1.f / sum_l;
                 __nv_bfloat16* const dst = o + at * kLatent;
                 float4* const part = reinterpret_cast<float4*>(parts.sums4(cluster, which, valid ? prow : 0, 0));
 #pragma unroll 1
@@ -566,9 +567,8 @@ kda_latent_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const _
                                     table + (size_t)u.n * s.blocks, max(si.all_hi, u.tb << C::LOG2),
                                     min(min(si.hi, hi), u.te << C::LOG2));
                 if (valid && half == 0) {
-                    const float ref = m == -INFINITY ? -INFINITY : m * scale_log2;
-                    if (!whole) parts.stats(cluster, which)[prow] = make_float2(ref, l);
-                    else if (lse) lse[at] = l == 0.f ? -INFINITY : (ref + log2f(l)) * kLn2;
+                    if (!whole) parts.stats(cluster, which)[prow] = st;
+                    else if (lse) lse[at] = sum_l == 0.f ? -INFINITY : (st.x + log2f(sum_l)) * kLn2;
                 }
             }
             // no CTA is at the unit after the next before this one has arrived for the next

@@ -124,6 +124,7 @@ __device__ __forceinline__ void join(const Partials& parts, const Unit<T>& j, in
         }
         const int head = j.u.y + r % j.Gv;
         if (row >= j.rows || head >= j.Hq) continue;   // a last group may have fewer heads
+        l = kda_paged::whole_sum(top, l);
         const float inv = l == 0.f ? 0.f : 1.f / l;
         const size_t at = (size_t)(j.u.x + r / j.Gv) * j.Hq + head;
         T* dst = j.o + at * D + wide * kWide;

@@ -2,9 +2,10 @@
 // over the paged latent cache, expanded over packed keys and values.
 //
 // Per row (a new token and a query head), over the keys it sees, in one pass:
-//     m' = max(m, max_j s_j),  l' = l 2^(m - m') + sum_j 2^(s_j - m'),
-//     o' = o 2^(m - m') + sum_j 2^(s_j - m') v_j,   s_j = scale log2(e) q.k_j
-// and o / l at the end; lse = (m + log2 l) ln 2.  In the absorbed form k_j is a row of the
+//     m' = max(m, max_j s_j),  l' = l 2^(c (m - m')) + sum_j 2^(c (s_j - m')),
+//     o' = o 2^(c (m - m')) + sum_j 2^(c (s_j - m')) v_j,   s_j = q.k_j,  c = scale log2(e)
+// and o / l at the end; lse = (c m + log2 l) ln 2.  The factor comes last, so that no product of a query is out of
+// fp32's range where the scores are not.  In the absorbed form k_j is a row of the
 // cache and v_j its first 512 channels, so a tile is fetched once for both.
 //
 // This path is for fp32, whose accuracy the tensor cores' 16-bit operands do not reach, and
@@ -160,7 +161,7 @@ kda_latent_simt_kernel(const T* __restrict__ q, Src src, const int32_t* __restri
                     const int e = e0 + i * kThreads;
                     if (e >= ROWS * CH) continue;
 #pragma unroll
-                    for (int y = 0; y < V; ++y) sm.q[e / CH][e % CH * V + y] = kda::io<T>::ld(&x[i].v[y]) * scale_log2;
+                    for (int y = 0; y < V; ++y) sm.q[e / CH][e % CH * V + y] = kda::io<T>::ld(&x[i].v[y]);
                 }
             }
         };
@@ -277,11 +278,11 @@ kda_latent_simt_kernel(const T* __restrict__ q, Src src, const int32_t* __restri
 #pragma unroll
                 for (int d = TPR / 2; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
                 const float mn = fmaxf(m, top), ref = mn == -INFINITY ? 0.f : mn;
-                const float f = m == -INFINITY ? (l == 0.f ? 0.f : 1.f) : exp2f(m - ref);
+                const float f = m == -INFINITY ? (l == 0.f ? 0.f : 1.f) : exp2f((m - ref) * scale_log2);
                 float sum = 0.f;
 #pragma unroll
                 for (int i = 0; i < KPT; ++i) {
-                    const float p = (seen >> i) & 1 ? exp2f(x[i] - ref) : sr < rows ? -1.f : 0.f;
+                    const float p = (seen >> i) & 1 ? exp2f((x[i] - ref) * scale_log2) : sr < rows ? -1.f : 0.f;
                     if ((seen >> i) & 1) sum += p;
                     sm.p[sx + TPR * i][sr] = p;
                 }
@@ -330,7 +331,7 @@ kda_latent_simt_kernel(const T* __restrict__ q, Src src, const int32_t* __restri
             }
         }
         __syncthreads();
-        if (sx == 0) sm.stats[sr] = make_float2(m, l);
+        if (sx == 0) sm.stats[sr] = kda_paged::row_stats(m, l, scale_log2, INFINITY);
         __syncthreads();
         const bool whole = u.first && u.last;
         const int which = u.first ? 1 : 0;
@@ -338,8 +339,10 @@ kda_latent_simt_kernel(const T* __restrict__ q, Src src, const int32_t* __restri
         for (int a = 0; a < RPT; ++a) {
             const int r = r0 + a, head = u.qh0 + r % s.Gv;
             if (r >= rows || head >= s.Hq) continue;
-            const float rm = sm.stats[r].x, rl = sm.stats[r].y;
+            const float rm = sm.stats[r].x;
+            float rl = sm.stats[r].y;
             if (whole) {
+                rl = kda_paged::whole_sum(rm, rl);
                 const float inv = rl == 0.f ? 0.f : 1.f / rl;
                 const size_t at = (size_t)(u.tok0 + r / s.Gv) * s.Hq + head;
                 T* dst = o + at * DV + 4 * cg;

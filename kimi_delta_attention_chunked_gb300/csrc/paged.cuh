@@ -20,6 +20,8 @@
 // on the device: no plan is made on the host, and no extra launch is needed.
 #pragma once
 
+#include <float.h>
+
 #include <atomic>
 
 #include "common.cuh"
@@ -288,6 +290,28 @@ __device__ __forceinline__ Piece find_piece_warp(const Sh& s, const int32_t* __r
     }
     return p;
 }
+
+// Large scores.  A row's reference is its largest score m times c = scale log2(e), rounded, and on the tensor-core
+// paths a weight is 2^(c x - reference) in one fused step: the reference's rounding enters all of them alike and the
+// sum takes it out again, while it is no more than some octaves (|m c| < 2^29).  From there on the reference is moved up,
+// so that weights end at 0 and not at infinity, and the row, or the part of it, has a reference above -inf and no sum:
+// it does not pass for one that sees no key (-inf, 0), weighs nothing beside a part that is in range, and is NaN where
+// it is the largest.  (2^(c (x - m)) would give such rows their values; it took the expanded prompt from 424 to 435 us.)
+constexpr float kMostOctaves = 0x1p29f;
+__device__ __forceinline__ float reference(float m, float c) {
+    const float r = fmaxf(m * c, -FLT_MAX);
+    return fabsf(r) < kMostOctaves ? r : fmaf(fabsf(r), 0x1p-22f, r);
+}
+// (reference, sum of weights) of a row or a part of it, from its largest score and what its weights came to.  On CUDA
+// cores, where the difference of the scores is formed first, `most` is the range of fp32.
+__device__ __forceinline__ float2 row_stats(float m, float l, float c, float most = kMostOctaves) {
+    if (m == -INFINITY) return make_float2(-INFINITY, l);
+    const float r = m * c;
+    if (fabsf(r) >= most && !isinf(m) && l == l) l = 0.f;
+    return make_float2(fmaxf(r, -FLT_MAX), l);
+}
+// The sum to divide by: 0 for a row that sees no key.
+__device__ __forceinline__ float whole_sum(float top, float l) { return l == 0.f && top > -INFINITY ? NAN : l; }
 
 // A cut unit of more rows than this is joined by the blocks of all its CTAs (if they are many).
 constexpr int kSpreadRows = 64;

@@ -7,7 +7,7 @@ import torch
 import kimi_delta_attention_chunked_gb300 as kda
 from _gpu import need_gpu
 from _latent import LATENT, NOPE, ROPE, assert_close, rows_ref
-from test_gpu_latent import DTYPES, SCALE, absorbed_case, expanded_case, on_gpu, run_absorbed
+from test_gpu_latent import BF16, DTYPES, SCALE, absorbed_case, expanded_case, on_gpu, run_absorbed
 
 pytestmark = pytest.mark.gpu
 
@@ -93,3 +93,69 @@ def test_expanded_infinities_of_no_weight(lens, keys, dt):
     got, gl = kda.kda_expanded_attention(*on_gpu(case), scale=SCALE, want_lse=True)
     same_kind(got, o, bo, "o")
     assert_close(gl, lse, bl, "lse")
+
+
+# ------------------------------------------------------------------ scores past the range of fp32
+FACTORS = [0.125, 4.0, -0.125, -4.0]                       # of the heads' queries
+
+
+def sharp(keys, falls, dt, gen):
+    """Keys whose first channel has distinct values from 1/2 to 1 in any order, exact in bf16, and 2^-6 of such in the
+    second half of the keys if `falls`; the second channel is 0."""
+    b = (128 + torch.randperm(128, generator=gen)[torch.arange(keys) % 128].float()) / 256
+    if falls:
+        b[keys // 2:] *= 2.0 ** -6
+    rows = torch.zeros(keys, 2)
+    rows[:, 0] = b
+    return b.double(), rows.to(dt)
+
+
+def check_sharp(o, lse, b, values, seen, scale):
+    """Row by row.  At these scales (2^24 and more: neighbours are at least 2^-17 2^24 apart, e^-128) the largest score
+    has all the weight, in bf16 a rounded one and a rounded output; past fp32's range, or 2^29 on the tensor cores,
+    the row is NaN."""
+    rel, most = (2.0 ** -7, 2.0 ** 29) if o.dtype == BF16 else (4 * 2.0 ** -24, 2.0 ** 128)
+    o, lse = o.double().cpu(), lse.double().cpu()
+    for t, n in enumerate(seen):
+        for h, a in enumerate(FACTORS):
+            j = int((a * b[:n]).argmax())
+            top = scale * a * float(b[j])
+            if int((b[:n] == b[j]).sum()) > 1:         # two keys share the weight
+                continue
+            if abs(top * math.log2(math.e)) >= most:
+                assert bool(torch.isnan(o[t, h]).all()) and not bool(torch.isfinite(lse[t, h])), (t, h, o[t, h, :4], lse[t, h])
+            else:
+                want = values(j, h).double()
+                assert bool(((o[t, h] - want).abs() <= rel * want.abs()).all()), (t, h)
+                assert abs(float(lse[t, h]) - top) <= 4 * 2.0 ** -24 * abs(top), (t, h)
+
+
+@pytest.mark.parametrize("dt", DTYPES)
+@pytest.mark.parametrize("scale", [2.0 ** 127, 2.0 ** 60, 2.0 ** 32, 2.0 ** 28, 2.0 ** 24])
+@pytest.mark.parametrize("ctx,m,falls", [(50, 3, False), (117, 3, False), (20, 1, False), (50, 3, True), (130, 2, True), (250, 6, True)])
+def test_absorbed_large_scales(ctx, m, falls, scale, dt):
+    gen = torch.Generator().manual_seed(3)
+    q, cache, table, cu, seq = absorbed_case([(ctx, m)], len(FACTORS), 16, dt, seed=3)
+    b, rows = sharp(ctx + m, falls, dt, gen)
+    q.zero_()
+    q[..., 0], q[..., 1] = torch.tensor(FACTORS, dtype=dt), 8.0
+    at = table[0].long().repeat_interleave(16)[:ctx + m], torch.arange(ctx + m) % 16
+    for c in range(2):
+        cache[at[0], at[1], c] = rows[:, c]
+    flat = cache[at]
+    o, lse = run_absorbed(q, cache, table, cu, seq, scale=scale)
+    check_sharp(o, lse, b, lambda j, h: flat[j, :LATENT], [ctx + i + 1 for i in range(m)], scale)
+
+
+@pytest.mark.parametrize("dt", DTYPES)
+@pytest.mark.parametrize("scale", [2.0 ** 127, 2.0 ** 60, 2.0 ** 32, 2.0 ** 28, 2.0 ** 24])
+@pytest.mark.parametrize("m,s,falls", [(3, 53, False), (40, 120, False), (1, 100, False), (3, 53, True), (40, 250, True), (300, 600, True)])
+def test_expanded_large_scales(m, s, falls, scale, dt):
+    gen = torch.Generator().manual_seed(4)
+    q, kn, kr, v, cu, cu_k = case = expanded_case([(m, s)], len(FACTORS), dt, seed=4)
+    b, rows = sharp(s, falls, dt, gen)
+    q.zero_()
+    q[..., 0], q[..., 1] = torch.tensor(FACTORS, dtype=dt), 8.0
+    kn[..., :2] = rows[:, None]
+    o, lse = kda.kda_expanded_attention(*on_gpu(case), scale=scale, want_lse=True)
+    check_sharp(o, lse, b, lambda j, h: v[j, h], [s - m + i + 1 for i in range(m)], scale)
