@@ -2,9 +2,10 @@
 // the merge of units that were cut between CTAs (paged.cuh).
 //
 // Per row (a new token and query head), over the keys it sees, in one pass:
-//     m' = max(m, max_j s_j),  l' = l 2^(m - m') + sum_j 2^(s_j - m'),
-//     o' = o 2^(m - m') + sum_j 2^(s_j - m') v_j,   s_j = scale log2(e) q.k_j
-// and o / l at the end; lse = (m + log2 l) ln 2.
+//     m' = max(m, max_j s_j),  l' = l 2^(c (m - m')) + sum_j 2^(c (s_j - m')),
+//     o' = o 2^(c (m - m')) + sum_j 2^(c (s_j - m')) v_j,   s_j = q.k_j,  c = scale log2(e)
+// and o / l at the end; lse = (c m + log2 l) ln 2.  The factor comes last, so that no product of a query is out of
+// fp32's range where the scores are not.
 //
 // This path is for fp32 (whose accuracy the tensor cores' 16-bit operands do
 // not reach) and for rows of q that TMA cannot fetch.  A unit
@@ -88,7 +89,7 @@ kda_paged_attention_simt_kernel(const T* __restrict__ q, const T* __restrict__ k
             float x = 0.f;
             if (r < rows)
                 x = kda::io<T>::ld(q + (long long)(u.tok0 + r / s.Gv) * q_stride + (long long)(u.qh0 + r % s.Gv) * D + c);
-            sm.q[r][c] = x * scale_log2;
+            sm.q[r][c] = x;
         }
         // softmax state: 8 threads share a row
         const int sr = tid >> 3, sx = tid & 7;
@@ -198,11 +199,11 @@ kda_paged_attention_simt_kernel(const T* __restrict__ q, const T* __restrict__ k
 #pragma unroll
                 for (int d = 4; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
                 const float mn = fmaxf(m, top), ref = mn == -INFINITY ? 0.f : mn;
-                const float f = m == -INFINITY ? (l == 0.f ? 0.f : 1.f) : exp2f(m - ref);
+                const float f = m == -INFINITY ? (l == 0.f ? 0.f : 1.f) : exp2f((m - ref) * scale_log2);
                 float sum = 0.f;
 #pragma unroll
                 for (int i = 0; i < kTile / 8; ++i) {
-                    const float p = (seen >> i) & 1 ? exp2f(x[i] - ref) : -1.f;
+                    const float p = (seen >> i) & 1 ? exp2f((x[i] - ref) * scale_log2) : -1.f;
                     if ((seen >> i) & 1) sum += p;
                     sm.p[sr][sx + 8 * i] = p;
                 }
@@ -246,8 +247,9 @@ kda_paged_attention_simt_kernel(const T* __restrict__ q, const T* __restrict__ k
         // the row's statistics to the threads that hold its sums
         __syncthreads();
         if (sx == 0) {
-            sm.p[sr][0] = m;
-            sm.p[sr][1] = l;
+            const float2 st = kda_paged::row_stats(m, l, scale_log2, INFINITY);
+            sm.p[sr][0] = st.x;
+            sm.p[sr][1] = st.y;
         }
         __syncthreads();
         const bool whole = u.first && u.last;
@@ -256,8 +258,10 @@ kda_paged_attention_simt_kernel(const T* __restrict__ q, const T* __restrict__ k
         for (int a = 0; a < 4; ++a) {
             const int r = 4 * w + a;
             if (r >= rows) continue;
-            const float rm = sm.p[r][0], rl = sm.p[r][1];
+            const float rm = sm.p[r][0];
+            float rl = sm.p[r][1];
             if (whole) {
+                rl = kda_paged::whole_sum(rm, rl);
                 const float inv = rl == 0.f ? 0.f : 1.f / rl;
                 const size_t at = (size_t)(u.tok0 + r / s.Gv) * s.Hq + u.qh0 + r % s.Gv;
 #pragma unroll
@@ -368,6 +372,7 @@ kda_paged_merge_kernel(Partials parts, int Gv, int Hq, T* __restrict__ o, float*
             }
         }
         if (r0 + grp / share >= rows) continue;
+        l = kda_paged::whole_sum(top, l);
         const float inv = l == 0.f ? 0.f : 1.f / l;
         const size_t at = (size_t)(me.x + r / Gv) * Hq + me.y + r % Gv;
         T* dst = o + at * D + 4 * x;

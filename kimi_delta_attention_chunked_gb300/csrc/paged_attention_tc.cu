@@ -551,7 +551,7 @@ kda_paged_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __
                             if (grow) m = big;
                         }
                     }
-                    const float ref = m == -INFINITY ? 0.f : m * scale_log2;
+                    const float ref = kda_paged::reference(m, scale_log2);
                     const uint64_t sc2 = pack2(scale_log2, scale_log2), off2 = pack2(-ref, -ref);
                     uint64_t sum[2] = {0, 0};
 #pragma unroll
@@ -584,7 +584,9 @@ kda_paged_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __
             const size_t at = (size_t)(u.tok0 + tok) * s.Hq + u.qh0 + head_in;
             const int prow = qi * rows_tile + row;     // row of a partial slot
             const Sight un = sight(u, s.window, 0, u.ntok - 1);
-            float ref = m == -INFINITY ? -INFINITY : m * scale_log2;
+            const float2 own_stats = kda_paged::row_stats(m, l, scale_log2);
+            const float ref = own_stats.x;
+            l = own_stats.y;
             // writes 32 columns of this row: o, or unnormalised sums
             auto put = [&](float* y, int c0, float sum_l) {
                 if (tl.odd_values[k & 3] && valid) add_odd_values<D>(y, c0, u, un, lo, hi, s, vc, table);
@@ -617,6 +619,7 @@ kda_paged_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __
                 o_phase ^= 3;
                 if (!ok) break;
                 kda::tc_fence_after();
+                if (whole) l = kda_paged::whole_sum(ref, l);
                 if (busy) {
 #pragma unroll 1
                     for (int c = 0; c < D; c += 32) {
@@ -648,7 +651,8 @@ kda_paged_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __
                     const float top = fmaxf(ref, st.x), base = top == -INFINITY ? 0.f : top;
                     const float fm = l == 0.f ? 0.f : ex2(ref - base), fo = st.y == 0.f ? 0.f : ex2(st.x - base);
                     const float f0 = h == 0 ? fm : fo, f1 = h == 0 ? fo : fm;
-                    const float sum_l = fmaf(fm, l, fo * st.y);
+                    float sum_l = fmaf(fm, l, fo * st.y);
+                    if (whole) sum_l = kda_paged::whole_sum(top, sum_l);
 #pragma unroll 1
                     for (int c = h * kShare; c < min((h + 1) * kShare, D); c += 32) {
                         float y[32];
