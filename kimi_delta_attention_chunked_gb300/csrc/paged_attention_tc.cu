@@ -664,11 +664,9 @@ kda_paged_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __
                             float z[32];
                             kda::tmem_ld32(tmem + lane_off + C::TMEM_O + b * D + c, z);
                             kda::tmem_wait_ld();
-                            const float f = b == 0 ? f0 : f1;
-                            if (f != 0.f) {
+                            const float f = b == 0 ? f0 : f1;    // at 0 too: 0 * NaN is NaN, whichever half a tile goes to
 #pragma unroll
-                                for (int e = 0; e < 32; ++e) y[e] = fmaf(f, z[e], y[e]);
-                            }
+                            for (int e = 0; e < 32; ++e) y[e] = fmaf(f, z[e], y[e]);
                         }
                         put(y, c, sum_l);
                     }

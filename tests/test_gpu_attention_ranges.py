@@ -45,3 +45,27 @@ def test_attention_large_scales(ctx, m, falls, scale, dtype, d):
             elif int((see == b[j]).sum()) == 1:
                 assert bool(((o[t, h] - values[j]).abs() <= rel * values[j].abs()).all()), (t, h)
                 assert abs(float(lse[t, h]) - top) <= 4 * 2.0 ** -24 * abs(top), (t, h)
+
+
+@pytest.mark.parametrize("dtype,d", [(BF, 128), (BF, 64), (F32, 64)])
+@pytest.mark.parametrize("n", [1, 200])
+def test_attention_infinities_of_no_weight(n, dtype, d):
+    """Keys that score -inf in every second tile, with infinite values: 0 * inf makes that channel NaN, in units of one
+    CTA as in cut ones; the other channels are as without them."""
+    dev = need_gpu()
+    c = make([(511, 1)] * n, 4, 4, d, 64, dtype, dev, seed=4)
+    c["q"][..., 0] = -1.0
+    finite = on(c, dev)
+    for r in range(n):
+        for lo in (128, 384):
+            pages = c["table"][r, lo // 64:lo // 64 + 2].long()
+            c["k"][pages, :, :, 0] = math.inf
+            c["v"][pages, :, :, 9] = math.inf
+    o, lse = (x.double().cpu() for x in kda.kda_paged_attention(*on(c, dev), want_lse=True))
+    # the reference: tables without those pages
+    finite[3][:, 2:4] = finite[3][:, 6:8] = -1
+    ref, rl = (x.double().cpu() for x in kda.kda_paged_attention(*finite, want_lse=True))
+    assert not torch.isfinite(o[..., 9]).any()
+    keep = torch.arange(d) != 9
+    assert torch.allclose(o[..., keep], ref[..., keep], rtol=0, atol=2.0 ** -8 if dtype == BF else 1e-5)
+    assert torch.allclose(lse, rl, rtol=0, atol=1e-5)
