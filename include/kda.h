@@ -418,8 +418,10 @@ KDA_API kda_status kda_paged_attention(const void* q, const void* k_cache, const
  * rot / 2 pairs: pair i of a token at position p, with angle w = p * inv_freq[i],
  *     (a, b) -> factor (a cos w - b sin w, b cos w + a sin w)
  * is channels (2 i, 2 i + 1) when `interleaved`, else (i, i + rot / 2).  The other
- * channels are copied.  The angle is formed to 2^-32 turns for every int32 position and
- * frequency below 1 (radians a position); sine, cosine and products are fp32.
+ * channels are copied.  For every int32 position and frequency below 1 (radians a
+ * position) the angle is formed to 2^-33 turns, and what is left of it beside the nearest
+ * quarter turn is rounded to fp32 (2^-24 of it, 2^-28 turns at most); sine, cosine and
+ * products are fp32.
  *
  * x, out     [T, H, d] dtype, strides in elements, the channels contiguous.  out may be
  *            x itself with the same strides (the other channels then stay as they

@@ -10,9 +10,9 @@
 // matters of it is its part of a turn, and that is exact in integers: F = f / (2 pi)
 // as a 64-bit fraction of a turn (f has 24 bits, 1 / (2 pi) enters with 128), then p F
 // modulo 2^64 is the angle, off by less than p 2^-64 turns.  The nearest quarter turn
-// is taken off in integers too, so that the rest, at most an eighth of a turn, goes to
-// fp32 with a relative error of 2^-24, and sincospif gets an argument it has no
-// reduction to do for.
+// is taken off in integers too, and the rest, at most an eighth of a turn, is converted
+// from all its 64 bits: with a relative error of 2^-24, however small it is.  sincospif
+// gets an argument it has no reduction to do for.
 #include <algorithm>
 
 #include "latent.cuh"
@@ -47,7 +47,7 @@ __device__ __forceinline__ float2 turned(float f, int p, float factor) {
     const uint32_t quarter = (uint32_t)((phase + (1ull << 61)) >> 62);
     const int64_t rest = (int64_t)(phase - ((uint64_t)quarter << 62));                // [-2^61, 2^61)
     float s, c;
-    sincospif((float)(int32_t)(rest >> 30) * 0x1p-33f, &s, &c);                       // units of 2^-34 turns
+    sincospif((float)rest * 0x1p-63f, &s, &c);                                        // in half turns
     const float x = quarter & 1 ? s : c, y = quarter & 1 ? c : s;                     // cos, sin up to their signs
     return make_float2(factor * ((quarter + 1) & 2 ? -x : x), factor * (quarter & 2 ? -y : y));
 }

@@ -7,7 +7,7 @@ import torch
 import kimi_delta_attention_chunked_gb300 as kda
 from _gpu import need_gpu
 from _latent import LATENT, NOPE, ROPE, assert_close, rows_ref
-from test_gpu_latent import BF16, DTYPES, SCALE, absorbed_case, expanded_case, on_gpu, run_absorbed
+from test_gpu_latent import BF16, DTYPES, FP32, SCALE, absorbed_case, expanded_case, on_gpu, run_absorbed
 
 pytestmark = pytest.mark.gpu
 
@@ -159,3 +159,18 @@ def test_expanded_large_scales(m, s, falls, scale, dt):
     kn[..., :2] = rows[:, None]
     o, lse = kda.kda_expanded_attention(*on_gpu(case), scale=scale, want_lse=True)
     check_sharp(o, lse, b, lambda j, h: v[j, h], [s - m + i + 1 for i in range(m)], scale)
+
+
+# ------------------------------------------------------------------ angles
+def test_rotary_small_angles():
+    """The sine of a small angle keeps fp32's relative accuracy: half a step of the angle's conversion, sincospi's own
+    step, and the frequency's fixed point (2^-64 turns of a position: 2^-30 of the least angle here)."""
+    freq = torch.tensor([1e-9, 3.3e-8, 1e-6, 1e-5, 7e-4, 0.02, 0.3, 0.77], dtype=FP32)
+    pos = torch.tensor([1, -1, 3, 100], dtype=torch.int32)
+    x = torch.zeros(len(pos), 1, 16)
+    x[..., :8] = 1.0
+    got = kda.kda_rotary(x.cuda(), pos.cuda(), freq.cuda()).double().cpu()
+    w = pos.double()[:, None] * freq.double()
+    near = w.abs() < 0.78                                  # an eighth of a turn: behind it a quarter is taken off
+    err = (got[:, 0, 8:] - w.sin()).abs() / w.sin().abs()
+    assert bool((err <= 4 * 2.0 ** -24)[near].all()), err
