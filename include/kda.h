@@ -441,8 +441,8 @@ KDA_API kda_status kda_rotary(const void* x, const int32_t* positions, const flo
  * n_pages * page_size are skipped.
  *
  * c          [T, 512] dtype, k_rope [T, 64] dtype: consecutive tokens are c_stride
- *            and k_rope_stride elements apart (both may be slices of one projection, but
- *            not of the cache)
+ *            and k_rope_stride elements apart, at least 512 and 64 (both may be slices of
+ *            one projection, but not of the cache)
  * slot_map   [T] int64.  What a slot named by two tokens holds is unspecified: each
  *            piece of its row is either one's.
  * positions  [T] int32, inv_freq [32] float; both NULL: the key part is copied
@@ -470,7 +470,7 @@ KDA_API size_t kda_latent_attention_workspace_size(int T, int H, kda_dtype dtype
  * that row.  A latent channel that is not finite makes that channel NaN in the rows
  * that see it, and the whole row unless the key scores -inf (its weight is then 0).
  *
- * q           [T, H, 576] dtype, consecutive tokens q_stride elements apart
+ * q           [T, H, 576] dtype, consecutive tokens q_stride elements apart, at least H * 576
  * cu_seqlens  [N + 1] int32 device array, 0 = cu[0] <= ... <= cu[N] <= T;
  *             rows of q at and past cu[N] are padding, their o is not written
  * seq_len     [N] int32 device array
@@ -509,10 +509,11 @@ KDA_API size_t kda_expanded_attention_workspace_size(int T, int H, kda_dtype dty
  * not finite makes its channel infinite or NaN in the rows that see it (either, where its
  * weight is 0 in fp32).
  *
- * q             [T, H, 192] dtype, consecutive tokens q_stride elements apart
+ * q             [T, H, 192] dtype, consecutive tokens q_stride elements apart, at least H * 192
  * k_nope, v     [S, H, 128] dtype, token and head strides in elements (both may be slices of
- *               one projection; tokens and heads may lie in either order);
- *               k_rope [S, 64] dtype, tokens k_rope_stride elements apart
+ *               one projection; tokens and heads may lie in either order).  Rows may not
+ *               overlap, but a head stride of 0 gives all heads the same ones;
+ *               k_rope [S, 64] dtype, tokens k_rope_stride elements apart, at least 64
  * cu_seqlens, cu_seqlens_k  [N + 1] int32 device arrays, rising from 0, at most T and S
  *               at the end; rows of q at and past cu_seqlens[N] are padding, their o is
  *               not written

@@ -94,8 +94,8 @@ def kda_expanded_attention_workspace_size(T: int, H: int, dtype) -> int:
 def kda_expanded_attention(q, k_nope, k_rope, v, cu_seqlens, cu_seqlens_k, scale=None, causal=True, o=None, lse=None,
                            want_lse=False, workspace=None, stream=None):
     """Expanded attention of q [T, H, 192] over packed keys and values (include/kda.h): k_nope [S, H, 128],
-    k_rope [S, 64] shared by the heads, v [S, H, 128], views with free token and head strides;
-    cu_seqlens and cu_seqlens_k int32 [N+1] on the device.  scale defaults to 192 ** -0.5.  Returns
+    k_rope [S, 64] shared by the heads, v [S, H, 128], views with free token and head strides whose rows
+    do not overlap (expanded over the heads: one row for all of them, on CUDA cores); cu_seqlens and cu_seqlens_k int32 [N+1] on the device.  scale defaults to 192 ** -0.5.  Returns
     o [T, H, 128], or (o, lse [T, H] float32) where ``lse`` is passed in or ``want_lse`` is set."""
     return (_paged._binding or _paged._load()).expanded_attention(q, k_nope, k_rope, v, cu_seqlens, cu_seqlens_k, scale, causal,
                                                                   o, lse, want_lse, workspace, stream)

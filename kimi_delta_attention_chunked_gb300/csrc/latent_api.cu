@@ -127,8 +127,9 @@ kda_status kda_expanded_attention(const void* q, const void* k_nope, const void*
     if ((int64_t)S + T > KDA_MAX_STEP_POSITIONS) return KDA_ERR_UNSUPPORTED;
     if (!(scale > 0.f) || !(scale <= 0x1p127f)) return KDA_ERR_INVALID_ARG;
     if (q_stride < (int64_t)H * kKey || k_rope_stride < kRope) return KDA_ERR_INVALID_ARG;
-    if (!rows_apart(S, k_token_stride, H, k_head_stride, kNope) || !rows_apart(S, v_token_stride, H, v_head_stride, kValue))
-        return KDA_ERR_INVALID_ARG;
+    // rows of their own, or at a head stride of 0 the same ones for all heads (which TMA does not fetch)
+    auto rows_ok = [&](int64_t token, int64_t head, int width) { return rows_apart(S, token, head == 0 ? 1 : H, head, width); };
+    if (!rows_ok(k_token_stride, k_head_stride, kNope) || !rows_ok(v_token_stride, v_head_stride, kValue)) return KDA_ERR_INVALID_ARG;
     // the stride of a dim of one has no meaning
     if (S <= 1) k_token_stride = v_token_stride = (int64_t)H * (kNope + kValue);
     if (H == 1) k_head_stride = v_head_stride = kNope;

@@ -6,7 +6,7 @@ import torch
 
 import kimi_delta_attention_chunked_gb300 as kda
 from _gpu import need_gpu
-from _latent import LATENT, NOPE, ROPE, assert_close, rows_ref
+from _latent import LATENT, NOPE, ROPE, assert_close, expanded_ref, rows_ref
 from test_gpu_latent import BF16, DTYPES, FP32, SCALE, absorbed_case, expanded_case, on_gpu, run_absorbed
 
 pytestmark = pytest.mark.gpu
@@ -174,3 +174,22 @@ def test_rotary_small_angles():
     near = w.abs() < 0.78                                  # an eighth of a turn: behind it a quarter is taken off
     err = (got[:, 0, 8:] - w.sin()).abs() / w.sin().abs()
     assert bool((err <= 4 * 2.0 ** -24)[near].all()), err
+
+
+# ------------------------------------------------------------------ views
+@pytest.mark.parametrize("dt", DTYPES)
+@pytest.mark.parametrize("shared", ["v", "k", "both"])
+def test_expanded_heads_share_keys_and_values(shared, dt):
+    """One head's keys or values for all of them: views with a head stride of 0."""
+    q, kn, kr, v, cu, cu_k = expanded_case([(30, 90), (140, 150)], 4, dt)
+    if shared != "v":
+        kn = kn[:, :1].expand(-1, 4, -1)
+    if shared != "k":
+        v = v[:, :1].expand(-1, 4, -1)
+    ref, lref, bo, bl = expanded_ref(q, kn, kr, v, cu, cu_k, SCALE, True)
+    put = lambda x: x[:, :1].cuda().expand(-1, 4, -1) if x.stride(1) == 0 else x.cuda()  # noqa: E731
+    kd, vd = put(kn), put(v)
+    assert (kd.stride(1) == 0) == (shared != "v") and (vd.stride(1) == 0) == (shared != "k")
+    o, lse = kda.kda_expanded_attention(q.cuda(), kd, kr.cuda(), vd, cu.cuda(), cu_k.cuda(), want_lse=True)
+    assert_close(o, ref, bo, "o")
+    assert_close(lse, lref, bl, "lse")
