@@ -14,7 +14,7 @@
 // softmax step), then DV / 4 column groups of 4 with ROWS / RPT row groups of RPT rows each.
 // Bound: latency of a tile's loads and steps, then shared memory (a 16-byte load of a warp takes four cycles,
 // whatever its addresses): 6 requests of 1 to 9 tokens over 17 to 2100 keys, 5 heads, absorbed, 20.6 us with the
-// merge; 5 prompts of 3 to 260 tokens over up to 860 keys, 5 heads, expanded, 40 us.
+// merge; 5 prompts of 3 to 260 tokens over up to 860 keys, 5 heads, expanded, 37 us; 4 of 200 over 2000, 8 heads, 360.
 #include <algorithm>
 #include <type_traits>
 
@@ -483,7 +483,9 @@ kda_paged::PackedShape expanded_shape(const ExpandedArgs& a, const PagedPlan& p)
     static_cast<kda_paged::Shape&>(s) = paged_shape(expanded_view(a), p);
     s.S = a.S;
     s.causal = a.causal;
-    s.half_unit = p.half_unit > 0 ? p.half_unit : p.U;
+    // In a call of at most half_unit tokens no unit has two steps a tile, and its pieces may have one place: a prompt
+    // of 20 tokens over 3000 keys 12.9 -> 11.9 us, 2 of 100 over 1000 12.4 -> 11.9, 200 over 200 with 16 heads 13.5 -> 13.7.
+    s.half_unit = p.half_unit > 0 && a.T > p.half_unit ? p.half_unit : p.U;
     s.extra_two = p.extra_two;
     return s;
 }

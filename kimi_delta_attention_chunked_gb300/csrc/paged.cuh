@@ -101,12 +101,14 @@ __device__ __forceinline__ int n_units(const Shape& s, const Req& r) { return (r
 
 // log2 of the places of a tile of unit i, and the places before its tiles.
 __device__ __forceinline__ int unit_shift(const Shape&, const Req&, int) { return 0; }
-__device__ __forceinline__ int unit_shift(const PackedShape& s, const Req& r, int i) { return r.len - i * s.U > s.half_unit ? 1 : 0; }
+__device__ __forceinline__ int unit_shift(const PackedShape& s, const Req& r, int i) {
+    return min(s.U, r.len - i * s.U) > s.half_unit ? 1 : 0;
+}
 // CTAs that may have a piece.  Where a tile may have two places, a piece has two at least, so that one that lies
 // among a unit's tiles holds the first place of one of them.
 __device__ __forceinline__ unsigned long long most_pieces(const Shape&, unsigned long long total) { return total; }
-__device__ __forceinline__ unsigned long long most_pieces(const PackedShape&, unsigned long long total) {
-    return total > 1 ? total >> 1 : total;
+__device__ __forceinline__ unsigned long long most_pieces(const PackedShape& s, unsigned long long total) {
+    return total > 1 && s.half_unit < s.U ? total >> 1 : total;
 }
 __device__ __forceinline__ int unit_extra(const Shape& s, int) { return s.extra; }
 __device__ __forceinline__ int unit_extra(const PackedShape& s, int shift) { return shift ? s.extra_two : s.extra; }

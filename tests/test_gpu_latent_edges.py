@@ -193,3 +193,36 @@ def test_expanded_heads_share_keys_and_values(shared, dt):
     o, lse = kda.kda_expanded_attention(q.cuda(), kd, kr.cuda(), vd, cu.cuda(), cu_k.cuda(), want_lse=True)
     assert_close(o, ref, bo, "o")
     assert_close(lse, lref, bl, "lse")
+
+
+# ------------------------------------------------------------------ division
+def test_expanded_on_cuda_cores_uses_every_place():
+    """300 tiles, each of one place, go to 300 CTAs where so many fit: the unit that CTA 0 begins has as many parts."""
+    props = torch.cuda.get_device_properties(0)
+    ctas = min(304, 2 * props.multi_processor_count, 300)
+    case = on_gpu(expanded_case([(32, 300 * 32)], 1, FP32))
+    ws = torch.zeros(kda.kda_expanded_attention_workspace_size(32, 1, FP32), dtype=torch.uint8, device="cuda")
+    kda.kda_expanded_attention(*case, causal=False, workspace=ws)
+    meta = ws[:32].view(torch.int32).tolist()              # of CTA 0's two slots
+    assert meta[4:7] == [0, 0, 32] and meta[7] & 0xffff == ctas
+
+
+def test_expanded_of_single_row_tiles_uses_every_place():
+    """24 key tiles and 5 places for their fixed cost, for 24 pairs: calls of up to 256 tokens have no unit of two steps a
+    tile, for which a piece must have two places."""
+    if torch.cuda.get_device_properties(0).multi_processor_count < 2 * 29:
+        pytest.skip("fewer pairs than places")
+    case = on_gpu(expanded_case([(20, 24 * 128)], 1, BF16))
+    ws = torch.zeros(kda.kda_expanded_attention_workspace_size(20, 1, BF16), dtype=torch.uint8, device="cuda")
+    kda.kda_expanded_attention(*case, causal=False, workspace=ws)
+    meta = ws[:2 * 80 * 16].view(torch.int32).view(80, 2, 4)   # of each pair's two slots
+    assert meta[5, 1].tolist() == [0, 0, 20, 5 << 16 | 24]
+
+
+def test_expanded_on_cuda_cores_counts_steps():
+    """Two units of 32 tokens and ten tiles each, every tile one place: ten CTAs to either."""
+    case = on_gpu(expanded_case([(64, 320)], 1, FP32))
+    ws = torch.zeros(kda.kda_expanded_attention_workspace_size(64, 1, FP32), dtype=torch.uint8, device="cuda")
+    kda.kda_expanded_attention(*case, causal=False, workspace=ws)
+    meta = ws[:2 * 304 * 16].view(torch.int32).view(304, 2, 4)
+    assert meta[0, 1].tolist() == [0, 0, 32, 10] and meta[10, 1].tolist() == [32, 0, 32, 10 << 16 | 10]
