@@ -226,3 +226,21 @@ def test_expanded_on_cuda_cores_counts_steps():
     kda.kda_expanded_attention(*case, causal=False, workspace=ws)
     meta = ws[:2 * 304 * 16].view(torch.int32).view(304, 2, 4)
     assert meta[0, 1].tolist() == [0, 0, 32, 10] and meta[10, 1].tolist() == [32, 0, 32, 10 << 16 | 10]
+
+
+@pytest.mark.parametrize("lens,H", [([(1500, 9000)], 1), ([(1024, 6000)], 40), ([(256, 6000), (700, 5000)], 24)])
+def test_expanded_long_runs_of_tiles(lens, H):
+    """Units of dozens of key tiles, in one piece and with borders inside them; a sample of rows and heads is checked."""
+    q, kn, kr, v, cu, cu_k = case = expanded_case(lens, H, BF16, seed=H)
+    o, lse = kda.kda_expanded_attention(*on_gpu(case), scale=SCALE, want_lse=True)
+    o, lse = o.cpu(), lse.cpu()
+    gen = torch.Generator().manual_seed(5)
+    for n, (m, s) in enumerate(lens):
+        t0, k0 = int(cu[n]), int(cu_k[n])
+        for i in [0, m - 1] + torch.randint(0, m, (30,), generator=gen).tolist():
+            hs = torch.randperm(H, generator=gen)[:3]
+            sees = slice(k0, k0 + s - m + i + 1)
+            K = torch.cat([kn[sees][:, hs], kr[sees][:, None].expand(-1, len(hs), -1)], 2).double()
+            ref, lref, bo, bl = rows_ref(q[t0 + i, hs].double(), K, v[sees][:, hs].double(), SCALE, BF16)
+            assert_close(o[t0 + i, hs], ref, bo, f"o of token {i}")
+            assert_close(lse[t0 + i, hs], lref, bl, f"lse of token {i}")
