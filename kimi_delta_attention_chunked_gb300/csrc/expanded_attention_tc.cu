@@ -30,10 +30,11 @@
 // finite; the output adds such elements to the rows that see them.
 //
 // Bound, and what it measured (GPU time with the merge; cuBLAS 1888 TFLOP/s).  A prompt of 8192 tokens,
-// 32 heads: 418 us, 1.64 PFLOP/s of the products that a causal mask leaves (floor 364): a tile of two steps
+// 32 heads: 418 to 427 us, 1.61 to 1.64 PFLOP/s of the products that a causal mask leaves (floor 364): a tile of two steps
 // takes 2970 cycles, 2560 of them products, and a unit's end (its last two tiles have one row tile, its
-// output) 10 k cycles of 60 k to 190 k.  12 requests of 1 to 700 tokens over up to 3200 keys, 16 heads: 46 us
-// (floor 10.6): 2 to 6 short units a pair at 7 to 8 k cycles each.
+// output) 10 k cycles of 60 k to 190 k.  A chunk of 4096 tokens behind 24576 others, 16 heads: 588 us, 1.90 PFLOP/s
+// (floor 592: long units, few ends).  12 requests of 1 to 700 tokens over up to 3200 keys, 16 heads: 43 to 47 us
+// (floor 10.6): 2 to 6 short units a pair at 7 to 8 k cycles each; 16 prompts of 16 to 300 tokens, 16 heads: 36 us (4.5).
 // What it took: arrivals at the other CTA without a fence of global memory (684 -> 528 us); the weights in two
 // halves, so that the first half's products run while the second is formed, and no steps of a row tile
 // behind its last key (518 -> 440); places of the division that count steps (444 -> 427); values cleaned off
@@ -664,6 +665,8 @@ PagedPlan expanded_plan_tc(int T) {
     p.tile_log2 = kKeysLog2;
     p.max_ctas = 80;                                   // pairs
     p.half_unit = kTileTokens;
+    // places for the fixed cost of a unit of one row tile and of two; with 0 and 0, 2 and 6, 5 and 5, 5 and 12, 8 and 18: a
+    // prompt of 8192 tokens 445, 429, 431, 423 and 434 us, 12 requests of 1 to 700 tokens 88, 54, 45, 47 and 47
     p.extra = 5;
     p.extra_two = 12;
     return p;

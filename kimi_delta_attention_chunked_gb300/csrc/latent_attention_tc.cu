@@ -44,7 +44,9 @@
 // 128; with the cache in L2 (many units of a request), the tensor cores: 0.79 us of the 0.72 that cuBLAS's rate
 // allows.  64 requests of 1 K to 16 K keys, 32 heads: 82 us (floor 61).  24 requests of 2 K to 32 K keys, 128
 // heads: 73 us (46).  32 x 8 tokens, 32 heads, 0.7 K to 8 K keys: 60 us (29).  4 requests of 90 to 1500 keys:
-// 14.2 us.  Above the floors: 5 us before a pair's first product (its piece, the first unit, the page table, the
+// 14.2 us.  Chunks, which are all tensor cores: 512 tokens over 8192 keys, 128 heads 700 us, 1.62 PFLOP/s of what the mask
+// leaves (floor 600), 16 heads 107 us, 1.33 (75: three to four units a pair), 2048 over 32768, 16 heads 1365 us, 1.66 (1199).
+// Above the floors: 5 us before a pair's first product (its piece, the first unit, the page table, the
 // first tile: a good part fetching instructions), 1.5 to 3 us to write a unit's sums, 5 to 10 for the merge.
 // What it took, in the order of its worth: arrivals at the other CTA without a fence of global memory (136 ->
 // 89 us in the first case); a merge of its own and partial sums in whole lines (verify 71 -> 61); a unit's last
@@ -626,6 +628,8 @@ PagedPlan latent_plan_tc(int T, int H) {
     p.rows = paged_slot_rows(p.U, T, p.Gv);
     p.tile_log2 = C::LOG2;
     p.max_ctas = 80;                                   // pairs
+    // places for a unit's fixed cost; with 0, 2, 5, 8 and 12: 64 decode requests 87.3, 83.9, 83.2, 84.8 and 87.0 us,
+    // verification 68.2, 63.7, 60.9, 62.1 and 64.1, 128 heads 75.6, 73.9, 73.0, 73.5 and 74.0
     p.extra = 5;
     return p;
 }

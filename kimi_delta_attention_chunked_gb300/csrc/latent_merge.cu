@@ -2,12 +2,14 @@
 // with M the largest of the parts' references m_i,
 //     o = sum_i 2^(m_i - M) o_i / sum_i 2^(m_i - M) l_i,   lse = (M + log2 of the divisor) ln 2.
 //
-// A slot's sums lie four channels wide, [D / 4][rows][4]: the threads of the attention kernels hold a row
-// each, so a warp's store and a warp's load here are whole lines (by rows, 128 of 512 channels took a pair of
-// CTAs 5,700 cycles to write).  A warp takes 16 channels of 32 rows, or, where there are more than
+// A slot's sums lie four channels wide, [D / 4][rows][4]: the threads of the tensor-core kernels hold a row
+// each, so a warp's store there and a warp's load here are whole lines (by rows, 128 of 512 channels took a pair of
+// CTAs 5,700 cycles to write).  A warp of the CUDA-core kernel holds four rows of 32 such columns and writes 64 bytes of
+// each; by rows instead, its stores would be whole lines and the loads here not: 34 -> 41 us where 300 CTAs share a
+// unit, 20.6 -> 21.7 in the absorbed fp32 case, 40.7 -> 40.3 in the expanded one.  A warp takes 16 channels of 32 rows, or, where there are more than
 // four parts, of 8 rows with four lanes to a row; the warps of all CTAs that hold a part of a unit share it
 // out.  Bound: latency (description, then statistics and sums: 5 us for units of a few rows) and, with 128 and
-// more rows in every slot, L2 (40 MB: 8 to 10 us).  Two parts at once and twice the blocks: 2 us slower.
+// more rows in every slot, L2 (40 MB: 8 to 10 us).
 #include <algorithm>
 
 #include "latent.cuh"
@@ -16,9 +18,12 @@ namespace {
 
 using kda_paged::Partials;
 
+// Blocks that a CTA's slot is shared out to; with 4, 8, 12 and 20: 128 heads 77.4, 73.3, 73.0 and 72.7 us, verification 62.6,
+// 61.7, 60.9 and 61.3, few requests 14.2, 13.9, 14.2 and 14.7, 12 expanded requests 48, 44, 43 to 47 and 43.
 constexpr int kThreads = 128, kBlocks = 12;
 constexpr int kWide = 16;                              // channels of a warp's work
-constexpr int kBatch = 4;                              // parts read at once
+constexpr int kBatch = 4;                              // parts read at once (2, with twice the blocks on an SM: few requests
+                                                       // 14.2 -> 16.2 us, verification 60.9 -> 69)
 
 __device__ __forceinline__ float ex2(float x) {
     float y;

@@ -14,7 +14,9 @@
 // softmax step), then DV / 4 column groups of 4 with ROWS / RPT row groups of RPT rows each.
 // Bound: latency of a tile's loads and steps, then shared memory (a 16-byte load of a warp takes four cycles,
 // whatever its addresses): 6 requests of 1 to 9 tokens over 17 to 2100 keys, 5 heads, absorbed, 20.6 us with the
-// merge; 5 prompts of 3 to 260 tokens over up to 860 keys, 5 heads, expanded, 37 us; 4 of 200 over 2000, 8 heads, 360.
+// merge; 5 prompts of 3 to 260 tokens over up to 860 keys, 5 heads, expanded, 34 to 37 us; 4 of 200
+// over 2000, 8 heads, 360.  Long contexts are bound by shared memory, not by HBM: 64 requests of one token over 8192
+// keys, 16 heads, absorbed, 683 us (bytes: 179), 16 prompts of 32 over 4032, 16 heads, expanded, 848 us (160).
 #include <algorithm>
 #include <type_traits>
 
@@ -167,7 +169,7 @@ kda_latent_simt_kernel(const T* __restrict__ q, Src src, const int32_t* __restri
         };
         if (q_wide) load_q(std::integral_constant<int, 16 / sizeof(T)>{});
         else load_q(std::integral_constant<int, 1>{});
-        // softmax state: 256 / ROWS threads share a row
+        // softmax state: kThreads / ROWS threads share a row
         constexpr int TPR = kThreads / ROWS, KPT = kTile / TPR;
         const int sr = tid / TPR, sx = tid % TPR;
         const int my_pos = u.pos + sr / s.Gv;
@@ -301,9 +303,9 @@ kda_latent_simt_kernel(const T* __restrict__ q, Src src, const int32_t* __restri
 #pragma unroll
                 for (int c = 0; c < 4; ++c) acc[a][c] *= f;
             }
-            // A masked key is passed over, not multiplied by zero, so that what stands there stays out.  Its
-            // branches cost more than the products (16 rows x 16 keys x 512: 5 us), so tiles that all rows see whole
-            // do without
+            // A masked key is passed over, not multiplied by zero, so that what stands there stays out.  Tiles that all
+            // rows see whole do without the branches (with them everywhere: 4 prompts of 200 tokens over 2000 keys
+            // 360 -> 364 us, the absorbed case 20.7 -> 20.9, the expanded one as it is)
             auto weigh = [&](auto masked) {
 #pragma unroll 4
                 for (int j = 0; j < kTile; ++j) {
