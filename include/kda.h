@@ -525,8 +525,8 @@ KDA_API size_t kda_expanded_attention_workspace_size(int T, int H, kda_dtype dty
  * workspace     kda_expanded_attention_workspace_size bytes, 256-byte aligned; a call has it
  *               to itself until it is complete
  * The scores, their statistics and the sums are fp32; on the tensor-core path (bf16, all rows
- * on 16-byte boundaries) the weights enter the second product as bf16.  fp32 tensors, and bf16
- * with other rows, run in fp32 on CUDA cores.
+ * on 16-byte boundaries, each head its own) the weights enter the second product as bf16.  fp32
+ * tensors, and bf16 with other rows, run in fp32 on CUDA cores.
  */
 KDA_API kda_status kda_expanded_attention(const void* q, const void* k_nope, const void* k_rope, const void* v,
                                   const int32_t* cu_seqlens, const int32_t* cu_seqlens_k, int64_t q_stride,
