@@ -7,7 +7,7 @@ import torch
 import kimi_delta_attention_chunked_gb300 as kda
 from _gpu import need_gpu
 from _latent import LATENT, NOPE, ROPE, assert_close, expanded_ref, rows_ref
-from test_gpu_latent import BF16, DTYPES, FP32, SCALE, absorbed_case, expanded_case, on_gpu, run_absorbed
+from test_gpu_latent import BF16, DTYPES, FP32, SCALE, absorbed_case, check_expanded, expanded_case, on_gpu, run_absorbed
 
 pytestmark = pytest.mark.gpu
 
@@ -244,3 +244,18 @@ def test_expanded_long_runs_of_tiles(lens, H):
             ref, lref, bo, bl = rows_ref(q[t0 + i, hs].double(), K, v[sees][:, hs].double(), SCALE, BF16)
             assert_close(o[t0 + i, hs], ref, bo, f"o of token {i}")
             assert_close(lse[t0 + i, hs], lref, bl, f"lse of token {i}")
+
+
+@pytest.mark.parametrize("seed", range(16))
+def test_expanded_chance_of_few_tokens(seed):
+    """Calls of up to 256 tokens over long keys by chance: pieces of one place, borders wherever they fall."""
+    import random
+    rng = random.Random(500 + seed)
+    dt, H, left, lens = rng.choice([BF16, BF16, FP32]), rng.choice([1, 1, 2, 3]), 256, []
+    for _ in range(rng.randint(1, 6)):
+        m = rng.choice([0, 1, rng.randint(0, 40), rng.randint(0, 250)])
+        if m <= left:
+            lens.append((m, rng.choice([0, 1, rng.randint(0, 300), rng.randint(0, 3000)])))
+            left -= m
+    lens.append((left, rng.randint(0, 1500)) if rng.random() < 0.3 else (min(left, 1), 700))
+    check_expanded(expanded_case(lens, H, dt, seed=seed), causal=rng.random() < 0.6)
